@@ -413,6 +413,142 @@ pkv_status pkv_multi_query_attention(const void* q, int32_t batch, int32_t q_len
                                      void* workspace, size_t workspace_bytes,
                                      int32_t split_tokens, pkv_stream_t stream);
 
+/*
+ * Attention of ragged chunks of new tokens — every sequence's new tokens, one
+ * or thousands, attend its paged K/V causally ([SC] "9. Failure modes and
+ * limitations", item 3, Chunked Prefill beside decode steps; chunks of one
+ * token are decode steps), with the scores as models define them.
+ *
+ *   q              bf16 [n_tokens, num_q_heads, head_dim], 16-byte aligned: the
+ *                  new tokens of all sequences, one sequence after another.
+ *   q_starts       int32 [batch + 1] (device), not decreasing: sequence b owns
+ *                  rows [q_starts[b], q_starts[b + 1]) of q and out (none: it
+ *                  has no new tokens).  Rows of no sequence are left as they
+ *                  were in out.
+ *   max_q_len      host-side upper bound on the new tokens of a sequence.
+ *   context_lens   int32 [batch]: tokens of sequence b, its new tokens included
+ *                  (they must already be appended).  Query i of n sits at
+ *                  position pos = context_lens[b] - n + i.
+ *   mods           what the scores are besides scale * q.k (NULL: nothing), in
+ *                  this order:
+ *     softcap      > 0: z := softcap * tanh(z / softcap); 0: no cap.
+ *     slopes       float32 [num_q_heads] (device) or NULL:
+ *                  z := z + slopes[hq] * (t - pos) for key t.
+ *     window       > 0: query pos sees keys t > pos - window; 0: all behind it.
+ *     prefix_lens  int32 [batch] (device) or NULL: the first prefix_lens[b]
+ *                  tokens are seen by every placed query of the sequence, before
+ *                  the window and ahead of the query too.
+ *                  Key t < context_lens[b] is seen iff t < prefix or
+ *                  pos - window < t <= pos.  A query before position 0 (a
+ *                  context shorter than its new tokens) gives zeros.
+ *   scale          finite, > 0.
+ *   out            bf16 [n_tokens, num_q_heads, head_dim], 16-byte aligned.
+ *                  The weights are rounded to the cache's 16-bit type (bf16, or
+ *                  f16 for E4M3 caches, whose q is taken as f16 too: finite
+ *                  below 65520) and sums are binary32.
+ *   k_scale, v_scale  as pkv_decode_attention; positive.
+ *   split_tokens   0 = automatic, else visible tokens per split (a multiple of
+ *                  128, at most 1024 * block_size).
+ *   workspace      device scratch of plan.workspace_bytes from pkv_chunk_plan
+ *                  with the same arguments, 256-byte aligned; may be NULL when
+ *                  that is 0.  Overlapping calls must not share one.
+ *   Other arguments as pkv_decode_attention; block tables need only hold the
+ *   blocks that some new token sees (blocks behind every window may be freed;
+ *   their entries are not read).  K and V of tokens at or past
+ *   context_lens[b] may hold anything; those before it that a query does not
+ *   see must be finite.
+ * A sequence whose row range leaves [0, n_tokens] or exceeds max_q_len is
+ * recorded (PKV_DEVERR_CONTEXT_LEN) and skipped.  batch == 0 or n_tokens == 0
+ * is a no-op.
+ *
+ * pkv_chunk_plan (host only): mode 4; split_tokens / max_splits as for decode;
+ * workers = 1 when row tiles of up to 16 rows run (max_q_len x G <= 16), 0
+ * when the tcgen05 kernel runs.  `window` and `has_prefix` as in the call (they
+ * bound the visible tokens).
+ */
+typedef struct {
+  float softcap;
+  int32_t window;
+  const float* slopes;
+  const int32_t* prefix_lens;
+} pkv_score_mods;
+
+pkv_status pkv_chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_t num_q_heads,
+                          const pkv_cache_desc* cache, int32_t max_context_len, int32_t window,
+                          int32_t has_prefix, int32_t split_tokens, int32_t num_sms,
+                          pkv_decode_plan_t* plan);
+
+pkv_status pkv_chunk_attention(const void* q, int32_t n_tokens, const int32_t* q_starts, int32_t batch,
+                               int32_t max_q_len, int32_t num_q_heads, const void* k_cache,
+                               const void* v_cache, const pkv_cache_desc* cache,
+                               const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               const int32_t* context_lens, int32_t max_context_len, float scale,
+                               const pkv_score_mods* mods, void* out, const float* k_scale,
+                               const float* v_scale, int64_t scale_row_stride, void* workspace,
+                               size_t workspace_bytes, int32_t split_tokens, pkv_stream_t stream);
+
+/*
+ * pkv_rotary_append — rotary positions and append in one pass: the new tokens'
+ * queries and keys are turned by their positions' angles, the queries written
+ * to q_out, the keys and values into their slots as pkv_append writes them.
+ *
+ *   q, k, v        [n_tokens, heads, head_dim] of src_dtype (PKV_BF16 or
+ *                  PKV_F32), num_q_heads / num_kv_heads / num_kv_heads heads;
+ *                  tokens q_stride / k_stride / v_stride elements apart (so
+ *                  slices of one fused projection do), 16-byte aligned.
+ *   positions      int64 [n_tokens], any value.
+ *   inv_freq       float64 [rotary_dim / 2] (device), finite: radians per
+ *                  position of each pair.
+ *   magnitude      finite: factor on sine and cosine (1: a rotation).
+ *   rotary_dim     a multiple of 16, 16..head_dim: elements of a head that
+ *                  turn, from its first; the others pass through.
+ *   interleaved    0: pair i is elements (i, i + rotary_dim / 2); 1: (2i, 2i + 1).
+ *   slot_mapping, caches, scales  as pkv_append (a negative slot skips the
+ *                  token's K/V rows; its query is still turned).
+ *   q_out          bf16 [n_tokens, num_q_heads, head_dim], tokens out_stride
+ *                  elements apart; may be q itself (same strides, bf16).
+ * Sines and cosines are binary32 of the angle pos * inv_freq taken modulo one
+ * turn without rounding; a turned element is rounded once, to bf16 or to the
+ * code of x / scale.  n_tokens == 0 is a no-op.
+ */
+pkv_status pkv_rotary_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, int32_t src_dtype, int64_t n_tokens, int32_t num_q_heads,
+                             const int64_t* positions, const double* inv_freq, int32_t rotary_dim,
+                             int32_t interleaved, float magnitude, const int64_t* slot_mapping, void* k_cache,
+                             void* v_cache, const pkv_cache_desc* cache, const float* k_scale,
+                             const float* v_scale, int64_t scale_row_stride, void* q_out, int64_t out_stride,
+                             pkv_stream_t stream);
+
+/*
+ * pkv_compact_tokens — in-place compaction: entry j of sequence b moves K and V
+ * rows of logical position keep[keep_starts[b] + j] to logical position
+ * dst_start[b] + j ([UI] "Predictive Prefetching and Attention-Salience
+ * Eviction Policy": evicted tokens leave the cache; [SC] "7. Practical
+ * applications", item 3: a draft's accepted tokens stay).  The result is as if
+ * every row were read before any is written.
+ *
+ *   keep           int32 [n_keep] (device): logical positions; entry j needs
+ *                  keep >= dst_start[b] + j (any list of increasing positions
+ *                  from dst_start[b] on does).  An entry that breaks this or
+ *                  lies past the table is recorded (PKV_DEVERR_CONTEXT_LEN) and
+ *                  its row not moved.
+ *   keep_starts    int32 [batch + 1] (device): sequence b owns entries
+ *                  [keep_starts[b], keep_starts[b + 1]); a range outside
+ *                  [0, n_keep] or longer than max_keep is recorded and skipped.
+ *   dst_start      int32 [batch] (device), >= 0, or NULL: 0 for every sequence.
+ *   max_keep       host-side upper bound on a sequence's entries.
+ *   block_tables, caches  as pkv_append / pkv_decode_attention.  A block that
+ *                  two sequences share by reference is changed for both: copy
+ *                  it first.  Two sequences of one call must not share blocks
+ *                  that either of them writes.
+ * Shorten the sequences afterwards (pkv_bm_truncate frees the blocks).
+ * batch == 0 or n_keep == 0 is a no-op.
+ */
+pkv_status pkv_compact_tokens(void* k_cache, void* v_cache, const pkv_cache_desc* cache,
+                              const int32_t* block_tables, int32_t max_blocks_per_seq, int32_t batch,
+                              const int32_t* keep, int32_t n_keep, const int32_t* keep_starts,
+                              const int32_t* dst_start, int32_t max_keep, pkv_stream_t stream);
+
 /* Device error codes (first one recorded wins). */
 enum {
   PKV_DEVERR_NONE = 0,
@@ -457,7 +593,8 @@ int32_t pkv_abi_version(void);
  * pkv_trace_read synchronises those events and returns, per kernel kind,
  * the number of launches and their summed device time; it then clears the
  * buffer.  Kinds: 0 append, 1 decode split, 2 combine, 3 cascade prefix,
- * 4 block copy, 5 multi-token query, 6 slot mapping.
+ * 4 block copy, 5 multi-token query, 6 slot mapping, 7 chunk attention,
+ * 8 rotary append, 9 token compaction.
  */
 typedef struct {
   int32_t kind;

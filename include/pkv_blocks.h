@@ -72,6 +72,13 @@ pkv_status pkv_bm_fork(pkv_block_manager* bm, int64_t parent_id, int64_t child_i
 /* Drop a sequence and one reference from each of its blocks. */
 pkv_status pkv_bm_free_sequence(pkv_block_manager* bm, int64_t seq_id);
 
+/* Shorten a sequence to its first `new_len` tokens (0 <= new_len <= its
+ * length): the blocks past them leave its table, each losing one reference
+ * (blocks of the host tier return to the host pool).  For tokens a draft
+ * proposed and verification rejected, and after pkv_compact_tokens.  A shared
+ * last block stays shared; the next append copies it first. */
+pkv_status pkv_bm_truncate(pkv_block_manager* bm, int64_t seq_id, int64_t new_len);
+
 /*
  * Reserve n_new[i] token slots at the end of sequence seq_ids[i], for i in
  * [0, n_seqs) in that order (ids distinct, n_new[i] >= 0).

@@ -9,27 +9,35 @@ memory and streams.
     decode_attention(q, k_cache, v_cache, block_tables, context_lens, scale
                      [, k_scale, v_scale]) -> out (float32)
 
+    rotary_append(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache) -> q turned (bf16)
+    chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_starts, scale) -> out (bf16)
+    compact_tokens(k_cache, v_cache, block_tables, keep, keep_starts)
+
 Cache tensors are [num_blocks, H_kv, block_size, head_dim], bf16 or E4M3
 (torch.uint8 or torch.float8_e4m3fn storage).
 """
 
 import ctypes
+import functools
+import math
 
 import numpy as np
 import torch
 
 from . import _lib
 from ._lib import (PKV_BF16, PKV_E4M3, PKV_F32, CacheDesc, DecodePlan, PkvError,  # noqa: F401
-                   TraceEntry)
+                   ScoreMods, TraceEntry)
 
 __all__ = ["append", "decode_attention", "decode_plan", "cache_desc", "slot_mapping",
            "cascade_plan", "cascade_decode_attention", "multi_query_plan", "multi_query_attention",
+           "chunk_plan", "chunk_attention", "rotary_frequencies", "rotary_append", "compact_tokens",
            "BlockManager", "OutOfBlocks", "copy_blocks",
            "host_pool_like", "copy_blocks_between",
            "device_error", "trace_enable", "trace_read", "library", "PkvError"]
 
 KERNEL_KINDS = {0: "append", 1: "decode_split", 2: "combine", 3: "cascade_prefix", 4: "block_copy",
-                5: "multi_query", 6: "slot_mapping"}
+                5: "multi_query", 6: "slot_mapping", 7: "chunk_attention", 8: "rotary_append",
+                9: "compact_tokens"}
 
 
 def library():
@@ -314,6 +322,283 @@ def multi_query_attention(q, k_cache, v_cache, block_tables, context_lens, scale
     return out
 
 
+class _OnDevice:
+    """torch.cuda.device(dev) that costs nothing when dev is already current."""
+    __slots__ = ("_guard",)
+
+    def __init__(self, dev):
+        self._guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+@functools.lru_cache(maxsize=None)
+def _num_sms(index):
+    return torch.cuda.get_device_properties(index).multi_processor_count
+
+
+def _scale_stride(k_scale, v_scale, rows, heads, dev, stride):
+    """Row stride of an E4M3 cache's scales, [rows, H_kv] or [H_kv] each."""
+    if k_scale is None or v_scale is None:
+        raise ValueError("E4M3 cache needs k_scale and v_scale")
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _contig(t, torch.float32, name, dev)
+        if stride is None and tuple(t.shape) not in ((rows, heads), (heads,)):
+            raise ValueError(f"{name} must be [{rows}, {heads}] or [{heads}]")
+    if k_scale.shape != v_scale.shape:
+        raise ValueError("k_scale and v_scale differ in shape")
+    if stride is None:
+        return heads if k_scale.dim() == 2 else 0
+    stride = int(stride)
+    if stride < 0 or (rows > 0 and k_scale.numel() < stride * (rows - 1) + heads):
+        raise ValueError("scale_row_stride reaches past the scales")
+    return stride
+
+
+def _check_tables(block_tables, context_lens, b, dev):
+    _contig(block_tables, torch.int32, "block_tables", dev)
+    _contig(context_lens, torch.int32, "context_lens", dev)
+    if block_tables.dim() != 2 or block_tables.shape[0] != b or context_lens.shape != (b,):
+        raise ValueError("block_tables must be [B, MB] and context_lens [B]")
+
+
+def chunk_plan(n_tokens, batch, max_q_len, num_q_heads, k_cache_or_desc, max_context_len, window=0,
+               has_prefix=False, split_tokens=0, num_sms=0):
+    """Plan of a chunk_attention call (host only): visible tokens per split,
+    splits, workspace bytes; workers 1 for the mma.sync kernel, 0 for tcgen05."""
+    desc = k_cache_or_desc if isinstance(k_cache_or_desc, CacheDesc) else cache_desc(k_cache_or_desc)
+    plan = DecodePlan()
+    _lib.check(library().pkv_chunk_plan(int(n_tokens), int(batch), int(max_q_len), int(num_q_heads),
+                                        ctypes.byref(desc), int(max_context_len), int(window), int(bool(has_prefix)),
+                                        int(split_tokens), int(num_sms), ctypes.byref(plan)), "pkv_chunk_plan")
+    return plan
+
+
+@functools.lru_cache(maxsize=4096)
+def _chunk_workspace(n_tokens, batch, max_q_len, num_q_heads, desc, max_context_len, window, has_prefix,
+                     split_tokens, num_sms):
+    """Workspace bytes of a chunk_plan (a function of these numbers alone)."""
+    return int(chunk_plan(n_tokens, batch, max_q_len, num_q_heads, CacheDesc(*desc), max_context_len, window,
+                          has_prefix, split_tokens, num_sms).workspace_bytes)
+
+
+def chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_starts, scale, max_q_len=None,
+                    max_context_len=None, k_scale=None, v_scale=None, softcap=0.0, window=0, slopes=None,
+                    prefix_lens=None, out=None, workspace=None, split_tokens=0, scale_row_stride=None):
+    """Causal attention of every sequence's new tokens over its paged K/V.
+
+    q [T, H_q, D] bf16 holds the new tokens of all sequences, sequence b's in
+    rows q_starts[b] .. q_starts[b + 1] - 1 (q_starts int32 [B + 1], on the
+    device); they are the last tokens of its context_lens[b] and must already
+    be in the cache.  Returns out [T, H_q, D] bf16; rows of no sequence are
+    not written.  `max_q_len` and `max_context_len` are host bounds (default: T
+    and the tables' capacity; tighter ones plan better).
+
+    Scores: z = scale * q.k; softcap * tanh(z / softcap) if softcap > 0; plus
+    slopes[hq] * (t - pos) with slopes (float32 [H_q]).  A query at position
+    pos sees key t iff t < prefix_lens[b] (int32 [B]) or pos - window < t <=
+    pos (window 0: t <= pos).  E4M3 caches take k_scale / v_scale float32 [B,
+    H_kv] or [H_kv].
+    """
+    lib = library()
+    _check_pair(k_cache, v_cache)
+    dev = k_cache.device
+    desc = cache_desc(k_cache)
+    _contig(q, torch.bfloat16, "q", dev)
+    if q.dim() != 3 or q.shape[2] != desc.head_dim:
+        raise ValueError("q must be [T, H_q, head_dim]")
+    t, hq, d = q.shape
+    _contig(q_starts, torch.int32, "q_starts", dev)
+    if q_starts.dim() != 1 or q_starts.shape[0] < 1:
+        raise ValueError("q_starts must be [B + 1]")
+    b = q_starts.shape[0] - 1
+    _check_tables(block_tables, context_lens, b, dev)
+    mb = block_tables.shape[1]
+    max_q_len = max(t, 1) if max_q_len is None else int(max_q_len)
+    max_context_len = mb * desc.block_size if max_context_len is None else int(max_context_len)
+    split_tokens, window = int(split_tokens), int(window)
+    if out is None:
+        out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _contig(out, torch.bfloat16, "out", dev)
+        if out.shape != q.shape:
+            raise ValueError("out must be [T, H_q, D]")
+    stride = 0
+    if desc.dtype == PKV_E4M3:
+        stride = _scale_stride(k_scale, v_scale, b, desc.num_kv_heads, dev, scale_row_stride)
+    if slopes is not None:
+        _contig(slopes, torch.float32, "slopes", dev)
+        if slopes.shape != (hq,):
+            raise ValueError("slopes must be [H_q]")
+    if prefix_lens is not None:
+        _contig(prefix_lens, torch.int32, "prefix_lens", dev)
+        if prefix_lens.shape != (b,):
+            raise ValueError("prefix_lens must be [B]")
+    mods = ScoreMods(softcap, window, None if slopes is None else slopes.data_ptr(),
+                     None if prefix_lens is None else prefix_lens.data_ptr())
+    with _OnDevice(dev):
+        # planned for this device's SMs, as the library plans the call itself
+        need = _chunk_workspace(t, b, max_q_len, hq, (desc.num_blocks, desc.block_size, desc.num_kv_heads,
+                                                      desc.head_dim, desc.dtype), max_context_len, window,
+                                prefix_lens is not None, split_tokens, _num_sms(dev.index))
+        have = 0
+        if need > 0:
+            if workspace is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            _contig(workspace, torch.uint8, "workspace", dev)
+            have = workspace.numel()
+        st = lib.pkv_chunk_attention(
+            q.data_ptr(), t, q_starts.data_ptr(), b, max_q_len, hq, k_cache.data_ptr(), v_cache.data_ptr(),
+            ctypes.byref(desc), block_tables.data_ptr(), mb, context_lens.data_ptr(), max_context_len, float(scale),
+            ctypes.byref(mods), out.data_ptr(), _ptr(k_scale), _ptr(v_scale), stride,
+            workspace.data_ptr() if have else None, have, split_tokens, _stream(dev))
+    _lib.check(st, "pkv_chunk_attention")
+    return out
+
+
+def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_len=None, beta_fast=32.0,
+                       beta_slow=1.0, device=None):
+    """Rotary frequencies (radians per position, float64 [rotary_dim / 2]):
+    base^(-2i / rotary_dim), for contexts `factor` times the original_len a
+    model was trained on changed by `scaling`:
+
+      "linear"    every frequency divided by factor (positions interpolated)
+      "ntk"       base * factor^(rotary_dim / (rotary_dim - 2)): the lowest
+                  frequency divided by factor, the highest kept
+      "by_parts"  frequencies that turn more than beta_fast times over
+                  original_len kept, those below beta_slow turns divided by
+                  factor, linear in the turns between
+    """
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even")
+    if not (base > 0 and factor > 0):
+        raise ValueError("base and factor must be positive")
+    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
+    if scaling == "ntk":
+        if rotary_dim < 4:
+            raise ValueError("ntk scaling needs rotary_dim >= 4")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    f = float(base) ** (-i / rotary_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "by_parts":
+        if original_len is None or original_len <= 0 or not beta_fast > beta_slow:
+            raise ValueError("by_parts scaling needs original_len > 0 and beta_fast > beta_slow")
+        keep = ((original_len * f / (2.0 * math.pi) - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+        f = f * (keep + (1.0 - keep) / factor)
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.to(device) if device is not None else f
+
+
+def _token_rows(t, name, dtype, heads, d, n, dev):
+    """[N, heads, D] tensor whose tokens may lie further apart than their rows
+    (a slice of a fused projection); returns the elements between tokens."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if tuple(t.shape) != (n, heads, d):
+        raise ValueError(f"{name} must be [{n}, {heads}, {d}]")
+    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.stride(0) if n > 1 else heads * d
+
+
+def rotary_append(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=None,
+                  magnitude=1.0, interleaved=False, out=None, scale_row_stride=None):
+    """Turn new tokens' queries and keys by their rotary angles, append keys
+    and values to their slots, and return the queries (bf16 [N, H_q, D]).
+
+    q [N, H_q, D], k and v [N, H_kv, D] of one dtype (bf16 or float32), each
+    token's heads contiguous; positions int64 [N]; inv_freq float64
+    [rotary_dim / 2] on the device (rotary_frequencies); pairs are elements (i,
+    i + rotary_dim / 2) of a head, or (2i, 2i + 1) if interleaved; elements past
+    rotary_dim pass through.  slot_mapping and scales as `append` (a negative
+    slot stores nothing; its query is still returned).  `out` may be q itself.
+    """
+    lib = library()
+    _check_pair(k_cache, v_cache)
+    dev = k_cache.device
+    desc = cache_desc(k_cache)
+    if q.dim() != 3:
+        raise ValueError("q must be [N, H_q, D]")
+    n, hq, d = q.shape
+    hkv = desc.num_kv_heads
+    if d != desc.head_dim:
+        raise ValueError("q's head_dim does not match the cache")
+    if q.dtype == torch.bfloat16:
+        src = PKV_BF16
+    elif q.dtype == torch.float32:
+        src = PKV_F32
+    else:
+        raise TypeError(f"q dtype {q.dtype}: expected bfloat16 or float32")
+    qs = _token_rows(q, "q", q.dtype, hq, d, n, dev)
+    ks = _token_rows(k, "k", q.dtype, hkv, d, n, dev)
+    vs = _token_rows(v, "v", q.dtype, hkv, d, n, dev)
+    _contig(positions, torch.int64, "positions", dev)
+    _contig(slot_mapping, torch.int64, "slot_mapping", dev)
+    if positions.shape != (n,) or slot_mapping.shape != (n,):
+        raise ValueError("positions and slot_mapping must have one entry per token")
+    _contig(inv_freq, torch.float64, "inv_freq", dev)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rotary_dim / 2]")
+    if out is None:
+        out = torch.empty((n, hq, d), dtype=torch.bfloat16, device=dev)
+    os_ = _token_rows(out, "out", torch.bfloat16, hq, d, n, dev)
+    stride = 0
+    if desc.dtype == PKV_E4M3:
+        stride = _scale_stride(k_scale, v_scale, n, hkv, dev, scale_row_stride)
+    with _OnDevice(dev):
+        st = lib.pkv_rotary_append(
+            q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, src, n, hq, positions.data_ptr(),
+            inv_freq.data_ptr(), 2 * inv_freq.shape[0], int(bool(interleaved)), float(magnitude),
+            slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ctypes.byref(desc), _ptr(k_scale),
+            _ptr(v_scale), stride, out.data_ptr(), os_, _stream(dev))
+    _lib.check(st, "pkv_rotary_append")
+    return out
+
+
+def compact_tokens(k_cache, v_cache, block_tables, keep, keep_starts, dst_start=None, max_keep=None):
+    """Move the tokens a sequence keeps towards its front, in place.
+
+    Sequence b keeps logical positions keep[keep_starts[b] : keep_starts[b + 1]]
+    (keep int32 [N], keep_starts int32 [B + 1], on the device); the j-th of them
+    moves to position dst_start[b] + j (dst_start int32 [B]; default 0) and
+    must not lie before it.  `max_keep` is a host bound on a sequence's entries
+    (default N).  Shorten the sequences afterwards (BlockManager.truncate).
+    """
+    lib = library()
+    _check_pair(k_cache, v_cache)
+    dev = k_cache.device
+    desc = cache_desc(k_cache)
+    _contig(block_tables, torch.int32, "block_tables", dev)
+    _contig(keep, torch.int32, "keep", dev)
+    _contig(keep_starts, torch.int32, "keep_starts", dev)
+    if block_tables.dim() != 2 or keep.dim() != 1:
+        raise ValueError("block_tables must be [B, MB] and keep 1-D")
+    b = block_tables.shape[0]
+    if keep_starts.shape != (b + 1,):
+        raise ValueError("keep_starts must be [B + 1]")
+    if dst_start is not None:
+        _contig(dst_start, torch.int32, "dst_start", dev)
+        if dst_start.shape != (b,):
+            raise ValueError("dst_start must be [B]")
+    n = keep.numel()
+    with _OnDevice(dev):
+        st = lib.pkv_compact_tokens(
+            k_cache.data_ptr(), v_cache.data_ptr(), ctypes.byref(desc), block_tables.data_ptr(),
+            max(1, block_tables.shape[1]), b, keep.data_ptr(), n, keep_starts.data_ptr(), _ptr(dst_start),
+            n if max_keep is None else int(max_keep), _stream(dev))
+    _lib.check(st, "pkv_compact_tokens")
+
+
 def slot_mapping(block_tables, positions, k_cache, seq_index=None, out=None):
     """Flat cache slots (int64, on the cache's device) of new tokens at logical
     `positions` (int64; < 0 = padding, slot -1) of sequences `seq_index`
@@ -367,8 +652,8 @@ def trace_enable(on=True):
 
 def trace_read():
     """{kernel name: (launches, total_ms)} since the last read; clears the trace."""
-    buf = (TraceEntry * 8)()
-    n = library().pkv_trace_read(buf, 8)
+    buf = (TraceEntry * 16)()
+    n = library().pkv_trace_read(buf, 16)
     if n < 0:
         raise RuntimeError("pkv_trace_read failed")
     return {KERNEL_KINDS[buf[i].kind]: (buf[i].launches, buf[i].total_ms) for i in range(n)}
@@ -435,6 +720,11 @@ class BlockManager:
 
     def free_sequence(self, seq_id):
         _bm_check(library().pkv_bm_free_sequence(self._h, int(seq_id)), "pkv_bm_free_sequence")
+
+    def truncate(self, seq_id, new_len):
+        """Shorten a sequence to its first new_len tokens; its blocks past them
+        lose one reference each."""
+        _bm_check(library().pkv_bm_truncate(self._h, int(seq_id), int(new_len)), "pkv_bm_truncate")
 
     def blocks_needed(self, seq_ids, n_new):
         ids = np.ascontiguousarray(seq_ids, dtype=np.int64)

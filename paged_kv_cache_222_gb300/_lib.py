@@ -38,6 +38,11 @@ class DecodePlan(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class ScoreMods(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("slopes", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p)]
+
+
 class TraceEntry(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("launches", ctypes.c_int32), ("total_ms", ctypes.c_double)]
 
@@ -69,6 +74,14 @@ SIGNATURES = {
                                     ctypes.POINTER(DecodePlan)]),
     "pkv_multi_query_attention": (_I32, [_P, _I32, _I32, _I32, _P, _P, ctypes.POINTER(CacheDesc), _P, _I32,
                                          _P, _I32, _F, _P, _P, ctypes.c_size_t, _I32, _P]),
+    "pkv_chunk_plan": (_I32, [_I32, _I32, _I32, _I32, ctypes.POINTER(CacheDesc), _I32, _I32, _I32, _I32, _I32,
+                              ctypes.POINTER(DecodePlan)]),
+    "pkv_chunk_attention": (_I32, [_P, _I32, _P, _I32, _I32, _I32, _P, _P, ctypes.POINTER(CacheDesc), _P, _I32, _P,
+                                   _I32, _F, ctypes.POINTER(ScoreMods), _P, _P, _P, _I64, _P, ctypes.c_size_t,
+                                   _I32, _P]),
+    "pkv_rotary_append": (_I32, [_P, _I64, _P, _I64, _P, _I64, _I32, _I64, _I32, _P, _P, _I32, _I32, _F, _P, _P, _P,
+                                 ctypes.POINTER(CacheDesc), _P, _P, _I64, _P, _I64, _P]),
+    "pkv_compact_tokens": (_I32, [_P, _P, ctypes.POINTER(CacheDesc), _P, _I32, _I32, _P, _I32, _P, _P, _I32, _P]),
     "pkv_copy_blocks": (_I32, [_P, _P, ctypes.POINTER(CacheDesc), _P, _P, _I32, _P]),
     "pkv_bm_create": (_I32, [_I64, _I32, ctypes.POINTER(_P)]),
     "pkv_bm_destroy": (None, [_P]),
@@ -79,6 +92,7 @@ SIGNATURES = {
     "pkv_bm_add_sequence": (_I32, [_P, _I64]),
     "pkv_bm_fork": (_I32, [_P, _I64, _I64]),
     "pkv_bm_free_sequence": (_I32, [_P, _I64]),
+    "pkv_bm_truncate": (_I32, [_P, _I64, _I64]),
     "pkv_bm_append": (_I32, [_P, _I32, _P, _P, _P, _P, _P, _I32, ctypes.POINTER(_I32)]),
     "pkv_bm_blocks_needed": (_I32, [_P, _I32, _P, _P, ctypes.POINTER(_I64)]),
     "pkv_bm_block_tables": (_I32, [_P, _I32, _P, _I32, _P, _P]),

@@ -1221,6 +1221,310 @@ extern "C" pkv_status pkv_multi_query_attention(
 }
 
 // ---------------------------------------------------------------------------
+// Ragged chunk attention, rotary append, token compaction.
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// Rows (new tokens x query heads of a KV head) of one row tile: the mma.sync
+// kernel when every sequence's rows fit one of its tiles, else the tcgen05
+// kernel's 256.
+bool chunk_small(int32_t max_q_len, int32_t group) {
+  return static_cast<int64_t>(max_q_len) * group <= pkv::kChunkSmallRows;
+}
+
+int32_t chunk_tile_q(int32_t max_q_len, int32_t group) {
+  return pkv::kChunkSmallRows / group;
+}
+
+pkv_status chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_t num_q_heads,
+                      const pkv_cache_desc* c, int32_t max_ctx, int32_t window, bool has_prefix,
+                      int32_t split_tokens, int32_t sms, pkv_decode_plan_t* out) {
+  pkv_status s = check_cache(c);
+  if (s != PKV_OK) return s;
+  if (n_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "n_tokens %d", n_tokens);
+  if (batch < 0 || batch > 65535) return fail(PKV_ERR_INVALID_ARG, "batch %d", batch);
+  if (max_q_len < 1) return fail(PKV_ERR_INVALID_ARG, "max_q_len %d", max_q_len);
+  if (num_q_heads < 1 || num_q_heads % c->num_kv_heads != 0)
+    return fail(PKV_ERR_INVALID_ARG, "num_q_heads %d not a multiple of num_kv_heads %d", num_q_heads,
+                c->num_kv_heads);
+  const int32_t group = num_q_heads / c->num_kv_heads;
+  if (group > 16) return fail(PKV_ERR_UNSUPPORTED, "group size %d > 16", group);
+  if (max_ctx < 0) return fail(PKV_ERR_INVALID_ARG, "max_context_len %d", max_ctx);
+  if (window < 0) return fail(PKV_ERR_INVALID_ARG, "window %d", window);
+  const int64_t max_st = static_cast<int64_t>(pkv::kChunkMaxSplitBlocks) * c->block_size;
+  if (split_tokens < 0 || (split_tokens > 0 && (split_tokens % 128 != 0 || split_tokens > max_st)))
+    return fail(PKV_ERR_INVALID_ARG, "split_tokens %d (0, or a multiple of 128 up to %lld)", split_tokens,
+                static_cast<long long>(max_st));
+  if (sms <= 0) sms = kDefaultSms;
+  const bool small = true;
+  const int64_t tile_q = chunk_tile_q(max_q_len, group), nk = 64;
+  // visible keys of one row tile, in tiles of nk
+  int64_t tiles = ceil_div(max_ctx, nk);
+  if (window > 0 && !has_prefix) {
+    const int64_t span = static_cast<int64_t>(window) + (max_q_len < tile_q ? max_q_len : tile_q) - 1;
+    const int64_t w = ceil_div(span, nk) + 1;
+    tiles = tiles < w ? tiles : w;
+  }
+  if (tiles < 1) tiles = 1;
+  const int64_t row_tiles = ceil_div(n_tokens, tile_q) > batch ? ceil_div(n_tokens, tile_q) : batch;
+  const int64_t units = row_tiles * c->num_kv_heads;
+  int64_t st = split_tokens;
+  if (st == 0) {
+    // the longest split that still gives every SM work: three CTAs per SM and
+    // about six waves of them on the mma.sync kernel (as for decode), two
+    // units per SM on the tcgen05 kernel
+    const int64_t want = static_cast<int64_t>(sms) * (small ? 18 : 2);
+    st = small ? 4096 : max_st;
+    while (st > 256 && units * ceil_div(tiles * nk, st) < want) st /= 2;
+    if (units >= want && small) st = ceil_div(tiles * nk, 128) * 128;
+    if (st > max_st) st = max_st;
+  }
+  if (small && c->num_kv_heads * ceil_div(max_q_len, tile_q) > 65535)
+    return fail(PKV_ERR_UNSUPPORTED, "num_kv_heads x row tiles beyond the grid");
+  const int64_t splits = ceil_div(tiles * nk, st);
+  if (splits > 65535) return fail(PKV_ERR_UNSUPPORTED, "%lld splits", static_cast<long long>(splits));
+  *out = pkv_decode_plan_t{};
+  out->mode = 4;
+  out->split_tokens = static_cast<int32_t>(st);
+  out->max_splits = static_cast<int32_t>(splits);
+  out->workers = small ? 1 : 0;
+  if (splits > 1) {
+    const int64_t n = static_cast<int64_t>(n_tokens) * num_q_heads * splits;
+    out->workspace_bytes = align256(n * c->head_dim * 4) + n * 2 * 4;
+  }
+  return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" pkv_status pkv_chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_t num_q_heads,
+                                     const pkv_cache_desc* cache, int32_t max_context_len, int32_t window,
+                                     int32_t has_prefix, int32_t split_tokens, int32_t num_sms,
+                                     pkv_decode_plan_t* plan) {
+  if (plan == nullptr) return fail(PKV_ERR_INVALID_ARG, "plan output is NULL");
+  return chunk_plan(n_tokens, batch, max_q_len, num_q_heads, cache, max_context_len, window, has_prefix != 0,
+                    split_tokens, num_sms, plan);
+}
+
+extern "C" pkv_status pkv_chunk_attention(
+    const void* q, int32_t n_tokens, const int32_t* q_starts, int32_t batch, int32_t max_q_len,
+    int32_t num_q_heads, const void* k_cache, const void* v_cache, const pkv_cache_desc* cache,
+    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+    int32_t max_context_len, float scale, const pkv_score_mods* mods, void* out, const float* k_scale,
+    const float* v_scale, int64_t scale_row_stride, void* workspace, size_t workspace_bytes,
+    int32_t split_tokens, pkv_stream_t stream) {
+  // an empty call has no tensors to look at
+  const int32_t some = n_tokens > 0 ? batch : (batch < 0 || n_tokens < 0 ? -1 : 0);
+  DecodeArgs a = {q, some, num_q_heads, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
+                  context_lens, max_context_len, scale, static_cast<float*>(out), k_scale, v_scale,
+                  scale_row_stride};
+  pkv_status s = check_decode(a);
+  if (s != PKV_OK) return s;
+  if (!(scale > 0.f)) return fail(PKV_ERR_INVALID_ARG, "scale must be positive");
+  pkv_score_mods m = {};
+  if (mods != nullptr) m = *mods;
+  if (!std::isfinite(m.softcap) || m.softcap < 0.f) return fail(PKV_ERR_INVALID_ARG, "softcap must be finite and >= 0");
+  if (!aligned(m.slopes, 4) || !aligned(m.prefix_lens, 4) || !aligned(q_starts, 4))
+    return fail(PKV_ERR_INVALID_ARG, "slopes, prefix_lens and q_starts must be 4-byte aligned");
+  pkv_decode_plan_t pl;
+  s = chunk_plan(n_tokens, batch, max_q_len, num_q_heads, cache, max_context_len, m.window,
+                 m.prefix_lens != nullptr, split_tokens, kDefaultSms, &pl);
+  if (s != PKV_OK) return s;
+  if (batch == 0 || n_tokens == 0) return PKV_OK;
+  if (q_starts == nullptr) return fail(PKV_ERR_INVALID_ARG, "NULL q_starts");
+  int dev;
+  DeviceState* st;
+  s = current_device(&dev, &st);
+  if (s != PKV_OK) return s;
+  if (split_tokens == 0 && st->sms != kDefaultSms) {
+    s = chunk_plan(n_tokens, batch, max_q_len, num_q_heads, cache, max_context_len, m.window,
+                   m.prefix_lens != nullptr, 0, st->sms, &pl);
+    if (s != PKV_OK) return s;
+  }
+  if (pl.workspace_bytes > 0) {
+    if (workspace == nullptr || workspace_bytes < static_cast<size_t>(pl.workspace_bytes))
+      return fail(PKV_ERR_WORKSPACE, "workspace %zu bytes, need %lld", workspace_bytes,
+                  static_cast<long long>(pl.workspace_bytes));
+    if (!aligned(workspace, 256)) return fail(PKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  }
+  const pkv_cache_desc& c = *cache;
+  const int32_t group = num_q_heads / c.num_kv_heads;
+  CUtensorMap tk, tv;
+  s = make_cache_tmap(&tk, k_cache, c, pkv::kTileTokens);
+  if (s != PKV_OK) return s;
+  s = make_cache_tmap(&tv, v_cache, c, pkv::kTileTokens);
+  if (s != PKV_OK) return s;
+  pkv::ChunkParams p = {};
+  p.q = q;
+  p.out = out;
+  p.q_starts = q_starts;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.slopes = m.slopes;
+  p.prefix_lens = m.prefix_lens;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.scale_stride = scale_row_stride;
+  p.num_blocks = c.num_blocks;
+  if (pl.max_splits > 1) {
+    const int64_t n = static_cast<int64_t>(n_tokens) * num_q_heads * pl.max_splits;
+    p.ws_o = static_cast<float*>(workspace);
+    p.ws_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(n * c.head_dim * 4));
+  }
+  p.n_tokens = n_tokens;
+  p.batch = batch;
+  p.max_q_len = max_q_len;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = c.num_kv_heads;
+  p.group = group;
+  p.head_dim = c.head_dim;
+  p.block_size = c.block_size;
+  p.max_blocks = max_blocks_per_seq;
+  p.max_ctx = max_context_len;
+  p.window = m.window;
+  p.split_tokens = pl.split_tokens;
+  p.max_splits = pl.max_splits;
+  p.tile_q = chunk_tile_q(max_q_len, group);
+  constexpr float kLog2e = 1.4426950408889634f;
+  p.qk_log2 = m.softcap > 0.f ? 2.f * kLog2e * (scale / m.softcap) : scale * kLog2e;
+  p.cap_log2 = m.softcap * kLog2e;
+  p.cache_dtype = c.dtype;
+  p.err = st->err;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = traced(pkv::kKindChunk, cs, [&] { return pkv::launch_chunk_small(p, tk, tv, cs); });
+  if (e == cudaSuccess && pl.max_splits > 1)
+    e = traced(pkv::kKindCombine, cs, [&] { return pkv::launch_chunk_combine(p, cs); });
+  if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
+  return PKV_OK;
+}
+
+extern "C" pkv_status pkv_rotary_append(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+    int32_t src_dtype, int64_t n_tokens, int32_t num_q_heads, const int64_t* positions, const double* inv_freq,
+    int32_t rotary_dim, int32_t interleaved, float magnitude, const int64_t* slot_mapping, void* k_cache,
+    void* v_cache, const pkv_cache_desc* cache, const float* k_scale, const float* v_scale,
+    int64_t scale_row_stride, void* q_out, int64_t out_stride, pkv_stream_t stream) {
+  pkv_status s = check_cache(cache);
+  if (s != PKV_OK) return s;
+  const pkv_cache_desc& c = *cache;
+  if (src_dtype != PKV_BF16 && src_dtype != PKV_F32)
+    return fail(PKV_ERR_INVALID_ARG, "src_dtype %d (want PKV_BF16 or PKV_F32)", src_dtype);
+  if (n_tokens < 0 || n_tokens > 0x7FFFFFFFll) return fail(PKV_ERR_INVALID_ARG, "n_tokens %lld", static_cast<long long>(n_tokens));
+  if (num_q_heads < 1 || num_q_heads > 65535) return fail(PKV_ERR_INVALID_ARG, "num_q_heads %d", num_q_heads);
+  if (rotary_dim < 16 || rotary_dim > c.head_dim || rotary_dim % 16 != 0)
+    return fail(PKV_ERR_UNSUPPORTED, "rotary_dim %d (a multiple of 16 up to head_dim %d)", rotary_dim, c.head_dim);
+  if (interleaved != 0 && interleaved != 1) return fail(PKV_ERR_INVALID_ARG, "interleaved %d", interleaved);
+  if (!std::isfinite(magnitude)) return fail(PKV_ERR_INVALID_ARG, "magnitude is not finite");
+  const int64_t esz = src_dtype == PKV_BF16 ? 2 : 4;
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * c.head_dim, kv_row = static_cast<int64_t>(c.num_kv_heads) * c.head_dim;
+  if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row || out_stride < q_row)
+    return fail(PKV_ERR_INVALID_ARG, "a token stride is smaller than the token's heads");
+  if (q_stride * esz % 16 || k_stride * esz % 16 || v_stride * esz % 16 || out_stride * 2 % 16)
+    return fail(PKV_ERR_INVALID_ARG, "token strides must be multiples of 16 bytes");
+  const bool fp8 = c.dtype == PKV_E4M3;
+  if (fp8 && (k_scale == nullptr || v_scale == nullptr))
+    return fail(PKV_ERR_INVALID_ARG, "E4M3 cache needs k_scale and v_scale");
+  if (!fp8 && (k_scale != nullptr || v_scale != nullptr))
+    return fail(PKV_ERR_INVALID_ARG, "scales given for a bf16 cache");
+  if (scale_row_stride < 0) return fail(PKV_ERR_INVALID_ARG, "scale_row_stride < 0");
+  if (n_tokens == 0) return PKV_OK;
+  if (q == nullptr || k == nullptr || v == nullptr || q_out == nullptr || positions == nullptr ||
+      inv_freq == nullptr || slot_mapping == nullptr || k_cache == nullptr || v_cache == nullptr)
+    return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16))
+    return fail(PKV_ERR_INVALID_ARG, "q, k, v, q_out and the caches must be 16-byte aligned");
+  if (!aligned(positions, 8) || !aligned(inv_freq, 8) || !aligned(slot_mapping, 8))
+    return fail(PKV_ERR_INVALID_ARG, "positions, inv_freq and slot_mapping must be 8-byte aligned");
+  if (fp8 && (!aligned(k_scale, 4) || !aligned(v_scale, 4)))
+    return fail(PKV_ERR_INVALID_ARG, "scales must be 4-byte aligned");
+  if (q == q_out && (src_dtype != PKV_BF16 || q_stride != out_stride))
+    return fail(PKV_ERR_INVALID_ARG, "q turned in place needs bf16 and equal strides");
+  int dev;
+  DeviceState* st;
+  s = current_device(&dev, &st);
+  if (s != PKV_OK) return s;
+  pkv::RotaryParams p = {};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_out = q_out;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.out_stride = out_stride;
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  p.magnitude = magnitude;
+  p.slots = slot_mapping;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.scale_stride = scale_row_stride;
+  p.n_tokens = n_tokens;
+  p.num_slots = c.num_blocks * c.block_size;
+  p.block_size = c.block_size;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = c.num_kv_heads;
+  p.head_dim = c.head_dim;
+  p.rotary_dim = rotary_dim;
+  p.interleaved = interleaved;
+  p.src_dtype = src_dtype == PKV_BF16 ? pkv::kEncBF16 : pkv::kEncF32;
+  p.cache_dtype = fp8 ? pkv::kEncE4M3 : pkv::kEncBF16;
+  p.err = st->err;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = traced(pkv::kKindRotary, cs, [&] { return pkv::launch_rotary(p, cs); });
+  if (e != cudaSuccess) return cuda_fail(e, "rotary append launch");
+  return PKV_OK;
+}
+
+extern "C" pkv_status pkv_compact_tokens(void* k_cache, void* v_cache, const pkv_cache_desc* cache,
+                                         const int32_t* block_tables, int32_t max_blocks_per_seq, int32_t batch,
+                                         const int32_t* keep, int32_t n_keep, const int32_t* keep_starts,
+                                         const int32_t* dst_start, int32_t max_keep, pkv_stream_t stream) {
+  pkv_status s = check_cache(cache);
+  if (s != PKV_OK) return s;
+  const pkv_cache_desc& c = *cache;
+  if (batch < 0) return fail(PKV_ERR_INVALID_ARG, "batch %d", batch);
+  if (n_keep < 0 || max_keep < 0) return fail(PKV_ERR_INVALID_ARG, "n_keep %d, max_keep %d", n_keep, max_keep);
+  if (max_blocks_per_seq < 1) return fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq %d", max_blocks_per_seq);
+  if (c.num_kv_heads > 8191) return fail(PKV_ERR_UNSUPPORTED, "num_kv_heads %d beyond the grid", c.num_kv_heads);
+  if (batch == 0 || n_keep == 0) return PKV_OK;
+  if (k_cache == nullptr || v_cache == nullptr || block_tables == nullptr || keep == nullptr || keep_starts == nullptr)
+    return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return fail(PKV_ERR_INVALID_ARG, "caches must be 16-byte aligned");
+  if (!aligned(block_tables, 4) || !aligned(keep, 4) || !aligned(keep_starts, 4) || !aligned(dst_start, 4))
+    return fail(PKV_ERR_INVALID_ARG, "index arrays must be 4-byte aligned");
+  int dev;
+  DeviceState* st;
+  s = current_device(&dev, &st);
+  if (s != PKV_OK) return s;
+  pkv::CompactParams p = {};
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.block_tables = block_tables;
+  p.keep = keep;
+  p.keep_starts = keep_starts;
+  p.dst_start = dst_start;
+  p.num_blocks = c.num_blocks;
+  p.n_keep = n_keep;
+  p.batch = batch;
+  p.max_keep = max_keep;
+  p.max_blocks = max_blocks_per_seq;
+  p.block_size = c.block_size;
+  p.num_kv_heads = c.num_kv_heads;
+  p.row_bytes = c.head_dim * (c.dtype == PKV_E4M3 ? 1 : 2);
+  p.err = st->err;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = traced(pkv::kKindCompact, cs, [&] { return pkv::launch_compact(p, cs); });
+  if (e != cudaSuccess) return cuda_fail(e, "token compaction launch");
+  return PKV_OK;
+}
+
+// ---------------------------------------------------------------------------
 // Decode attention that allocates nothing.
 //
 // The split-KV partials live in a fixed array in device memory that belongs to

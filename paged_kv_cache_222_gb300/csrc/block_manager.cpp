@@ -206,6 +206,34 @@ pkv_status pkv_bm_free_sequence(pkv_block_manager* bm, int64_t seq_id) {
   return PKV_OK;
 }
 
+pkv_status pkv_bm_truncate(pkv_block_manager* bm, int64_t seq_id, int64_t new_len) {
+  if (bm == nullptr) return fail(PKV_ERR_INVALID_ARG, "manager is NULL");
+  std::lock_guard<std::mutex> lk(bm->mu);
+  auto it = bm->seqs.find(seq_id);
+  if (it == bm->seqs.end())
+    return fail(PKV_ERR_INVALID_ARG, "unknown sequence %lld", static_cast<long long>(seq_id));
+  Manager::Seq& sq = it->second;
+  if (new_len < 0 || new_len > sq.len)
+    return fail(PKV_ERR_INVALID_ARG, "new_len %lld outside [0, %lld]", static_cast<long long>(new_len),
+                static_cast<long long>(sq.len));
+  const size_t keep = static_cast<size_t>((new_len + bm->block_size - 1) / bm->block_size);
+  for (size_t j = keep; j < sq.blocks.size(); ++j) {
+    const int32_t b = sq.blocks[j];
+    if (sq.on_host[j]) {
+      bm->host_free.push_back(b);
+      sq.host_entries -= 1;
+      continue;
+    }
+    int32_t& r = bm->ref[static_cast<size_t>(b)];
+    r -= 1;
+    if (r == 0) bm->free_stack.push_back(b);
+  }
+  sq.blocks.resize(keep);
+  sq.on_host.resize(keep);
+  sq.len = new_len;
+  return PKV_OK;
+}
+
 pkv_status pkv_bm_blocks_needed(pkv_block_manager* bm, int32_t n_seqs, const int64_t* seq_ids,
                                 const int32_t* n_new, int64_t* blocks_needed) {
   if (bm == nullptr || blocks_needed == nullptr) return fail(PKV_ERR_INVALID_ARG, "NULL argument");

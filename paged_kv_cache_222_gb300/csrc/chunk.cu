@@ -1,0 +1,452 @@
+// Attention of ragged chunks of new tokens over the paged cache ([SC] "LLM
+// inference: prefill, decode, KV cache", "9. Failure modes and limitations",
+// item 3: chunked prefill beside decode steps; "4. Internal workings", step 4
+// for chunks of one token), with scores that are capped, biased by distance,
+// windowed or opened for a prefix (chunk_common.cuh).
+//
+// This file: the kernel for row tiles of up to 16 rows (a row is a new token
+// and a query head of one KV head), and the merge of split pieces.
+//
+// A CTA takes the up to 16 rows of one tile of one (sequence, KV head) over
+// one split of the tile's visible keys, in 64-key steps: warp w loads keys
+// 16w..16w+15 of every step by TMA into its own part of a ring (K and V, one
+// box of 16 tokens per lane and 128-byte column band), on barriers of its
+// own, and refills its slot as soon as it has read it, so that no warp waits
+// for another; the warps merge (m, l, O) through shared memory at the end.
+// S = Q K^T and O += P V are mma.sync m16n8k16 products with fp32 sums: bf16
+// for bf16 caches, f16 for E4M3 ones (every code is an f16).  P is rounded to
+// that type: at most 2^-8 (bf16) or 2^-11 (f16) of each weight, next to the
+// output's own 2^-8.  The bound is the HBM stream of 2 D bytes x type size
+// per visible key and KV head.
+
+#include "chunk_common.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kSmallTile = 64;        // keys per step
+
+template <int D, bool FP8>
+struct SmallShape {
+  using L = Layout<D, FP8>;
+  static constexpr int STAGE = 4 * L::STAGEB;             // 64 keys of K and V
+  static constexpr int NS = 65536 / STAGE > 8 ? 8 : 65536 / STAGE;  // 64 KB: three CTAs per SM
+  static constexpr int DP = D + 4;
+  static constexpr int BYTES = NS * STAGE + 4 * NS * 8 + kChunkMaxSplitBlocks * 4 + 1024;
+  static_assert(4 * 16 * DP * 4 + 4 * 16 * 2 * 4 <= NS * STAGE, "merge buffer fits the stages");
+};
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(128, 3)
+    chunk_small_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                       const ChunkParams p) {
+  using L = Layout<D, FP8>;
+  using C = SmallShape<D, FP8>;
+  constexpr int KS = D / 16, NS = C::NS, STAGE = C::STAGE, DP = C::DP;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = lane >> 2, j = lane & 3;
+  const int G = p.group, H_q = p.num_q_heads;
+  const int ntq = (p.max_q_len + p.tile_q - 1) / p.tile_q;
+  const int h = blockIdx.y / ntq;
+  const int i0 = (blockIdx.y - h * ntq) * p.tile_q;
+  const int b = blockIdx.z, split = blockIdx.x;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + NS * STAGE);  // [NS][4]: per stage and warp
+  int* s_blk = reinterpret_cast<int*>(full + 4 * NS);
+  const uint32_t stage0 = smem_u32(smem);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 4 * NS; ++s) mbar_init(smem_u32(full + s), 1);
+    fence_mbar_init();
+    prefetch_tmap(&tmap_k);
+    prefetch_tmap(&tmap_v);
+  }
+  wait_prior_grid();
+
+  const ChunkSeq sq = chunk_seq(p, b, split == 0 && blockIdx.y == 0 && threadIdx.x == 0);
+  if (i0 >= sq.n) return;
+  const int i1 = min(sq.n, i0 + p.tile_q) - 1;
+  const int rows = (i1 - i0 + 1) * G;
+  const ChunkRange rg = chunk_range<kSmallTile>(p, sq, i0, i1);
+  const int per_split = p.split_tokens / kSmallTile;
+  const int nsplit = max(1, (rg.n + per_split - 1) / per_split);
+  if (split >= nsplit) return;
+  const int k0 = split * per_split;
+  const int ntile = min(rg.n - k0, per_split);
+  const int64_t row_base = static_cast<int64_t>(sq.start + i0) * H_q + h * G;  // of row (0, g = 0)
+  auto out_row = [&](int row) { return row_base + static_cast<int64_t>(row / G) * H_q + row % G; };
+
+  // block ids of the split's keys; blocks that no row sees (behind the window,
+  // past the last query) are not looked up and read as zeros
+  const int bshift = p.block_size == 16 ? 4 : 5;
+  const int per_tile = kSmallTile >> bshift;
+  const int32_t* tbl = p.block_tables + static_cast<int64_t>(b) * p.max_blocks;
+  for (int i = threadIdx.x; i < ntile * per_tile; i += blockDim.x) {
+    const int t0 = rg.tile(k0 + i / per_tile) * kSmallTile + (i % per_tile) * p.block_size;
+    int phys = -1;  // outside the tensor map: the TMA unit fills zeros
+    if (rg.sees(t0, t0 + p.block_size)) {
+      phys = tbl[t0 >> bshift];
+      if (phys < 0 || phys >= p.num_blocks) {
+        record_error(p.err, kDevErrBlockId);
+        phys = -1;
+      }
+    }
+    s_blk[i] = phys;
+  }
+  __syncthreads();
+
+  auto issue = [&](int k) {
+    const int s = k % NS;
+    const uint32_t dst = stage0 + s * STAGE + warp * L::STAGEB;
+    const uint32_t bar = smem_u32(full + 4 * s + warp);
+    if (lane == 0) {
+      fence_proxy_async_smem();  // this warp's reads of the slot come before the copy
+      mbar_arrive_expect_tx(bar, L::STAGEB);
+    }
+    __syncwarp();
+    if (lane < 2 * L::NBOX) {
+      const int v = lane / L::NBOX, bx = lane % L::NBOX;
+      const int o = warp * kTileTokens;  // token within the 64-key step
+      tma_load_4d(dst + v * L::TILEB + bx * L::BOX_BYTES, v ? &tmap_v : &tmap_k, bar, bx * L::BOX_ELEMS,
+                  o & (p.block_size - 1), h, s_blk[k * per_tile + (o >> bshift)]);
+    }
+  };
+  int issued = 0;
+  for (; issued < ntile && issued < NS; ++issued) issue(issued);
+
+  // this lane's two rows: ra = r, rb = r + 8 of the tile
+  const int ra = r, rb = r + 8;
+  uint32_t qa[KS][4];
+  {
+    const uint16_t* q = static_cast<const uint16_t*>(p.q);
+    const uint16_t* qra = ra < rows ? q + out_row(ra) * D : nullptr;
+    const uint16_t* qrb = rb < rows ? q + out_row(rb) * D : nullptr;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      if constexpr (!FP8) {
+        const int d0 = 16 * ks + 2 * j;
+        qa[ks][0] = qra ? *reinterpret_cast<const uint32_t*>(qra + d0) : 0u;
+        qa[ks][1] = qrb ? *reinterpret_cast<const uint32_t*>(qrb + d0) : 0u;
+        qa[ks][2] = qra ? *reinterpret_cast<const uint32_t*>(qra + d0 + 8) : 0u;
+        qa[ks][3] = qrb ? *reinterpret_cast<const uint32_t*>(qrb + d0 + 8) : 0u;
+      } else {  // f16, in the d-order of the widened E4M3 fragments
+        const int d0 = 16 * ks + 4 * j;
+        const uint2 wa = qra ? *reinterpret_cast<const uint2*>(qra + d0) : make_uint2(0u, 0u);
+        const uint2 wb = qrb ? *reinterpret_cast<const uint2*>(qrb + d0) : make_uint2(0u, 0u);
+        qa[ks][0] = pack_f16x2(bf16lo_to_f32(wa.x), bf16hi_to_f32(wa.x));
+        qa[ks][1] = pack_f16x2(bf16lo_to_f32(wb.x), bf16hi_to_f32(wb.x));
+        qa[ks][2] = pack_f16x2(bf16lo_to_f32(wa.y), bf16hi_to_f32(wa.y));
+        qa[ks][3] = pack_f16x2(bf16lo_to_f32(wb.y), bf16hi_to_f32(wb.y));
+      }
+    }
+  }
+  // per row: position (-1 where it sees nothing), first key of the window
+  auto pos_of = [&](int row) { return row < rows ? sq.ctx - sq.n + i0 + row / G : -1; };
+  const int pos_a = pos_of(ra), pos_b = pos_of(rb);
+  auto lo_of = [&](int pos) { return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0; };
+  const int lo_a = lo_of(pos_a), lo_b = lo_of(pos_b);
+  const int pf_a = pos_a >= 0 ? sq.prefix : 0, pf_b = pos_b >= 0 ? sq.prefix : 0;
+  constexpr float kLog2e = 1.4426950408889634f;
+  float sl_a = 0.f, sl_b = 0.f;
+  if (p.slopes != nullptr) {
+    sl_a = ra < rows ? p.slopes[h * G + ra % G] * kLog2e : 0.f;
+    sl_b = rb < rows ? p.slopes[h * G + rb % G] * kLog2e : 0.f;
+  }
+  float qk_mult = p.qk_log2, v_mult = 1.f;
+  if constexpr (FP8) {
+    qk_mult *= p.k_scale[static_cast<int64_t>(b) * p.scale_stride + h];
+    v_mult = p.v_scale[static_cast<int64_t>(b) * p.scale_stride + h];
+  }
+
+  float m_a = -CUDART_INF_F, m_b = -CUDART_INF_F, l_a = 0.f, l_b = 0.f;
+  float o[D / 8][4];
+#pragma unroll
+  for (int nt = 0; nt < D / 8; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
+  // ldmatrix lanes: K (tok 0-7,c)(tok 0-7,c+1)(tok 8-15,c)(tok 8-15,c+1);
+  //                 V (tok 0-7,c)(tok 8-15,c)(tok 0-7,c+1)(tok 8-15,c+1)
+  const int mq = lane >> 3;
+  const int tok_k = (lane & 7) + (mq >> 1) * 8, ch_k = mq & 1;
+  const int tok_v = (lane & 7) + (mq & 1) * 8, ch_v = mq >> 1;
+
+  bool healthy = true;
+  for (int k = 0; k < ntile; ++k) {
+    const int s = k % NS;
+    const bool arrived = mbar_wait(smem_u32(full + 4 * s + warp), static_cast<uint32_t>((k / NS) & 1), p.err);
+    if (!__all_sync(kFull, arrived)) healthy = false;
+    const uint32_t base = stage0 + s * STAGE + warp * L::STAGEB;
+    const int t_warp = rg.tile(k0 + k) * kSmallTile + warp * kTileTokens;  // this warp's first key
+    if (healthy) {
+      // ---- S = Q K^T: two 8-key n-tiles
+      float sc[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+      if constexpr (!FP8) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t Rk[4];
+          ldsm_x4(base + L::off(tok_k, 2 * ks + ch_k), Rk);
+          mma_bf16_16816(sc[0], qa[ks], Rk[0], Rk[1]);
+          mma_bf16_16816(sc[1], qa[ks], Rk[2], Rk[3]);
+        }
+      } else {  // a 16-byte chunk holds the 16 d of one k-step
+#pragma unroll
+        for (int pk = 0; pk < KS / 2; ++pk) {
+          uint32_t Rk[4];
+          ldsm_x4(base + L::off(tok_k, 2 * pk + ch_k), Rk);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            mma_f16_16816(sc[0], qa[2 * pk + e], e4m3x2_to_f16x2(static_cast<uint16_t>(Rk[e] & 0xFFFFu)),
+                          e4m3x2_to_f16x2(static_cast<uint16_t>(Rk[e] >> 16)));
+            mma_f16_16816(sc[1], qa[2 * pk + e], e4m3x2_to_f16x2(static_cast<uint16_t>(Rk[2 + e] & 0xFFFFu)),
+                          e4m3x2_to_f16x2(static_cast<uint16_t>(Rk[2 + e] >> 16)));
+          }
+        }
+      }
+      // ---- scores (log2 units), masks, online softmax (rows a: e = 0, 1; b: e = 2, 3)
+      float mx_a = -CUDART_INF_F, mx_b = -CUDART_INF_F;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = t_warp + 8 * nt + 2 * j + (e & 1);
+          const int pos = e < 2 ? pos_a : pos_b, lo = e < 2 ? lo_a : lo_b, pf = e < 2 ? pf_a : pf_b;
+          float x = sc[nt][e] * qk_mult;
+          if (p.cap_log2 > 0.f) x = capped(x, p.cap_log2);
+          x = fmaf(e < 2 ? sl_a : sl_b, static_cast<float>(t - pos), x);
+          sc[nt][e] = (t <= pos && t >= lo) || t < pf ? x : -CUDART_INF_F;
+        }
+        mx_a = fmaxf(mx_a, fmaxf(sc[nt][0], sc[nt][1]));
+        mx_b = fmaxf(mx_b, fmaxf(sc[nt][2], sc[nt][3]));
+      }
+      mx_a = fmaxf(mx_a, __shfl_xor_sync(kFull, mx_a, 1));
+      mx_a = fmaxf(mx_a, __shfl_xor_sync(kFull, mx_a, 2));
+      mx_b = fmaxf(mx_b, __shfl_xor_sync(kFull, mx_b, 1));
+      mx_b = fmaxf(mx_b, __shfl_xor_sync(kFull, mx_b, 2));
+      const float mn_a = fmaxf(m_a, mx_a), mn_b = fmaxf(m_b, mx_b);
+      const float mu_a = (mn_a == -CUDART_INF_F) ? 0.f : mn_a;
+      const float mu_b = (mn_b == -CUDART_INF_F) ? 0.f : mn_b;
+      const float al_a = fast_exp2(m_a - mu_a), al_b = fast_exp2(m_b - mu_b);
+      m_a = mn_a;
+      m_b = mn_b;
+      float sum_a = 0.f, sum_b = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        sc[nt][0] = fast_exp2(sc[nt][0] - mu_a);
+        sc[nt][1] = fast_exp2(sc[nt][1] - mu_a);
+        sc[nt][2] = fast_exp2(sc[nt][2] - mu_b);
+        sc[nt][3] = fast_exp2(sc[nt][3] - mu_b);
+        sum_a += sc[nt][0] + sc[nt][1];
+        sum_b += sc[nt][2] + sc[nt][3];
+      }
+      l_a = l_a * al_a + sum_a;
+      l_b = l_b * al_b + sum_b;
+#pragma unroll
+      for (int nt = 0; nt < D / 8; ++nt) {
+        const float2 u = __fmul2_rn(make_float2(o[nt][0], o[nt][1]), make_float2(al_a, al_a));
+        const float2 w = __fmul2_rn(make_float2(o[nt][2], o[nt][3]), make_float2(al_b, al_b));
+        o[nt][0] = u.x;
+        o[nt][1] = u.y;
+        o[nt][2] = w.x;
+        o[nt][3] = w.y;
+      }
+      // ---- O += P V.  V rows at or past the end of the sequence may hold
+      // anything (NaN included): zeroed in the fragments, P is 0 there.
+      const int vvalid = sq.ctx - t_warp;
+      const uint32_t keep0 = ((2 * j < vvalid) ? 0x0000FFFFu : 0u) | ((2 * j + 1 < vvalid) ? 0xFFFF0000u : 0u);
+      const uint32_t keep1 = ((2 * j + 8 < vvalid) ? 0x0000FFFFu : 0u) | ((2 * j + 9 < vvalid) ? 0xFFFF0000u : 0u);
+      const uint32_t vt = base + L::TILEB;
+      uint32_t ph[4];
+      if constexpr (!FP8) {
+        ph[0] = pack_bf16x2(sc[0][0], sc[0][1]);
+        ph[1] = pack_bf16x2(sc[0][2], sc[0][3]);
+        ph[2] = pack_bf16x2(sc[1][0], sc[1][1]);
+        ph[3] = pack_bf16x2(sc[1][2], sc[1][3]);
+#pragma unroll
+        for (int dp = 0; dp < KS; ++dp) {
+          uint32_t Rv[4];
+          ldsm_x4_trans(vt + L::off(tok_v, 2 * dp + ch_v), Rv);
+          mma_bf16_16816(o[2 * dp], ph, Rv[0] & keep0, Rv[1] & keep1);
+          mma_bf16_16816(o[2 * dp + 1], ph, Rv[2] & keep0, Rv[3] & keep1);
+        }
+      } else {
+        ph[0] = pack_f16x2(sc[0][0], sc[0][1]);
+        ph[1] = pack_f16x2(sc[0][2], sc[0][3]);
+        ph[2] = pack_f16x2(sc[1][0], sc[1][1]);
+        ph[3] = pack_f16x2(sc[1][2], sc[1][3]);
+#pragma unroll
+        for (int pk = 0; pk < KS / 2; ++pk) {
+          uint32_t Rv[4];
+          ldsm_x4_trans(vt + L::off(tok_v, 2 * pk + ch_v), Rv);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // 16-d chunk 2 pk + e: n-tile 2c its even d, 2c + 1 its odd d
+            const uint32_t e0 = prmt(Rv[2 * e] & keep0, 0u, 0x3120u);       // keys 0-7
+            const uint32_t e1 = prmt(Rv[2 * e + 1] & keep1, 0u, 0x3120u);   // keys 8-15
+            const int c = 2 * pk + e;
+            mma_f16_16816(o[2 * c], ph, e4m3x2_to_f16x2(static_cast<uint16_t>(e0 & 0xFFFFu)),
+                          e4m3x2_to_f16x2(static_cast<uint16_t>(e1 & 0xFFFFu)));
+            mma_f16_16816(o[2 * c + 1], ph, e4m3x2_to_f16x2(static_cast<uint16_t>(e0 >> 16)),
+                          e4m3x2_to_f16x2(static_cast<uint16_t>(e1 >> 16)));
+          }
+        }
+      }
+    }
+    __syncwarp();  // this warp has read its part of the slot: refill it
+    if (healthy && k + NS < ntile) issue(issued++);
+  }
+  if (!healthy && lane == 0) {
+    // a copy of this warp's may still be landing: one more bounded wait each
+    for (int kk = issued > NS ? issued - NS : 0; kk < issued; ++kk)
+      mbar_wait(smem_u32(full + 4 * (kk % NS) + warp), static_cast<uint32_t>((kk / NS) & 1), nullptr);
+  }
+  allow_next_grid();
+
+  // ---- row sums over the quad; the warps' results merge through shared memory
+  l_a += __shfl_xor_sync(kFull, l_a, 1);
+  l_a += __shfl_xor_sync(kFull, l_a, 2);
+  l_b += __shfl_xor_sync(kFull, l_b, 1);
+  l_b += __shfl_xor_sync(kFull, l_b, 2);
+  __syncthreads();  // every warp is done with the stages
+  float* s_o = reinterpret_cast<float*>(smem);  // [4 warps][16][DP]
+  float* s_ml = s_o + 4 * 16 * DP;              // [4 warps][16][2]
+  {
+    float* wo = s_o + warp * 16 * DP;
+#pragma unroll
+    for (int nt = 0; nt < D / 8; ++nt) {
+      if constexpr (!FP8) {
+        *reinterpret_cast<float2*>(wo + r * DP + 8 * nt + 2 * j) = make_float2(o[nt][0], o[nt][1]);
+        *reinterpret_cast<float2*>(wo + (r + 8) * DP + 8 * nt + 2 * j) = make_float2(o[nt][2], o[nt][3]);
+      } else {  // columns 2j, 2j + 1 of n-tile 2c (2c + 1) are d = 16 c + 4 j, + 2 (+ 1, + 3)
+        const int d = 16 * (nt >> 1) + 4 * j + (nt & 1);
+        wo[r * DP + d] = o[nt][0];
+        wo[r * DP + d + 2] = o[nt][1];
+        wo[(r + 8) * DP + d] = o[nt][2];
+        wo[(r + 8) * DP + d + 2] = o[nt][3];
+      }
+    }
+    if (j == 0) {
+      float* ml = s_ml + warp * 32;
+      ml[2 * r] = m_a;
+      ml[2 * r + 1] = l_a;
+      ml[2 * (r + 8)] = m_b;
+      ml[2 * (r + 8) + 1] = l_b;
+    }
+  }
+  __syncthreads();
+
+  for (int idx = threadIdx.x; idx < rows * (D / 2); idx += blockDim.x) {
+    const int row = idx / (D / 2), d = 2 * (idx - row * (D / 2));
+    float M = -CUDART_INF_F;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) M = fmaxf(M, s_ml[w * 32 + 2 * row]);
+    float a0 = 0.f, a1 = 0.f, lsum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float mw = s_ml[w * 32 + 2 * row];
+      const float wt = (mw == -CUDART_INF_F) ? 0.f : fast_exp2(mw - M);
+      const float2 v = *reinterpret_cast<const float2*>(s_o + (w * 16 + row) * DP + d);
+      a0 += wt * v.x;
+      a1 += wt * v.y;
+      lsum += wt * s_ml[w * 32 + 2 * row + 1];
+    }
+    const int64_t orow = out_row(row);
+    if (nsplit == 1) {
+      const float inv = lsum > 0.f ? v_mult / lsum : 0.f;
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + orow * D + d) = pack_bf16x2(a0 * inv, a1 * inv);
+    } else {
+      const int64_t slot = orow * p.max_splits + split;
+      *reinterpret_cast<float2*>(p.ws_o + slot * D + d) = make_float2(a0 * v_mult, a1 * v_mult);
+      if (d == 0) {
+        p.ws_ml[slot * 2] = M;
+        p.ws_ml[slot * 2 + 1] = lsum;
+      }
+    }
+  }
+}
+
+// Merge of the split pieces: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
+// One CTA per token, a warp per query head in turn; rows of one piece were
+// written by the attention kernel itself.
+template <int D>
+__global__ void __launch_bounds__(256) chunk_combine_kernel(const ChunkParams p, int nk) {
+  constexpr int E = D / 32;  // elements per lane
+  wait_prior_grid();
+  allow_next_grid();
+  const int tok = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = warp_search(p.batch, tok, [&](int i) { return p.q_starts[i]; });
+  const ChunkSeq sq = chunk_seq(p, b, false);
+  const int i = tok - sq.start;
+  if (i < 0 || i >= sq.n) return;  // a row of no sequence
+  const int i0 = i / p.tile_q * p.tile_q, i1 = min(sq.n, i0 + p.tile_q) - 1;
+  const int n = nk == 64 ? chunk_range<64>(p, sq, i0, i1).n : chunk_range<128>(p, sq, i0, i1).n;
+  const int per_split = p.split_tokens / nk;
+  const int nsplit = (n + per_split - 1) / per_split;
+  if (nsplit <= 1) return;
+  for (int hq = warp; hq < p.num_q_heads; hq += 8) {
+    const int64_t row = static_cast<int64_t>(tok) * p.num_q_heads + hq;
+    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + row * p.max_splits;
+    const float* po = p.ws_o + row * p.max_splits * D + lane * E;
+    float M = -CUDART_INF_F;
+    for (int s = lane; s < nsplit; s += 32) M = fmaxf(M, ml[s].x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
+    float acc[E], l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < nsplit; ++s) {
+      const float2 v = ml[s];
+      const float wt = v.x == -CUDART_INF_F ? 0.f : fast_exp2(v.x - M);
+      l += wt * v.y;
+      const float* src = po + static_cast<int64_t>(s) * D;
+      if constexpr (E == 4) {
+        const float4 u = *reinterpret_cast<const float4*>(src);
+        acc[0] += wt * u.x;
+        acc[1] += wt * u.y;
+        acc[2] += wt * u.z;
+        acc[3] += wt * u.w;
+      } else {
+        const float2 u = *reinterpret_cast<const float2*>(src);
+        acc[0] += wt * u.x;
+        acc[1] += wt * u.y;
+      }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  }
+}
+
+template <int D, bool FP8>
+cudaError_t launch_small_t(const ChunkParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
+  auto kern = chunk_small_kernel<D, FP8>;
+  constexpr int smem = SmallShape<D, FP8>::BYTES;
+  static int configured[64] = {};
+  cudaError_t e = set_smem_once(kern, smem, configured);
+  if (e != cudaSuccess) return e;
+  const int ntq = (p.max_q_len + p.tile_q - 1) / p.tile_q;
+  return launch_pdl(kern, dim3(p.max_splits, p.num_kv_heads * ntq, p.batch), dim3(128), smem, stream, tk, tv, p);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_small(const ChunkParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                               cudaStream_t stream) {
+  const bool fp8 = p.cache_dtype == kE4M3;
+  if (p.head_dim == 128)
+    return fp8 ? launch_small_t<128, true>(p, tk, tv, stream) : launch_small_t<128, false>(p, tk, tv, stream);
+  return fp8 ? launch_small_t<64, true>(p, tk, tv, stream) : launch_small_t<64, false>(p, tk, tv, stream);
+}
+
+cudaError_t launch_chunk_combine(const ChunkParams& p, cudaStream_t stream) {
+  const int nk = kSmallTile;
+  if (p.head_dim == 128)
+    return launch_pdl(chunk_combine_kernel<128>, dim3(p.n_tokens), dim3(256), 0, stream, p, nk);
+  return launch_pdl(chunk_combine_kernel<64>, dim3(p.n_tokens), dim3(256), 0, stream, p, nk);
+}
+
+}  // namespace pkv

@@ -1,0 +1,106 @@
+// Pieces shared by the ragged-chunk attention kernels (chunk.cu, chunk_tc.cu):
+// which sequence a token or a row tile belongs to, which keys a row tile sees,
+// and the scores' definition.
+//
+// Query i of the n new tokens of a sequence with ctx tokens sits at position
+// pos = ctx - n + i and sees key t when t < ctx and
+//   t < prefix, or pos - window < t <= pos   (window 0: 0 <= t <= pos);
+// a query before position 0 sees nothing.  Its score against key t is
+//   z = scale q.k,   cap * tanh(z / cap) with a cap,   + slope (t - pos) with a bias.
+#pragma once
+
+#include "decode_common.cuh"
+
+namespace pkv {
+
+// One sequence of the call as the kernels see it.
+struct ChunkSeq {
+  int start, n, ctx, prefix;  // first query row, new tokens, tokens attended, tokens every query sees
+  bool ok;                    // its row range lies inside the call's bounds
+};
+
+__device__ __forceinline__ int chunk_clamp_ctx(const ChunkParams& p, int ctx) {
+  const int64_t cap = static_cast<int64_t>(p.max_blocks) * p.block_size;
+  const int lim = static_cast<int>(cap < p.max_ctx ? cap : p.max_ctx);
+  return ctx < 0 ? 0 : (ctx > lim ? lim : ctx);
+}
+
+// `note`: this thread records a range or length that had to be refused or clamped.
+__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int b, bool note) {
+  ChunkSeq s;
+  const int q0 = p.q_starts[b], q1 = p.q_starts[b + 1];
+  const int ctx_raw = p.context_lens[b];
+  const int pfx = p.prefix_lens != nullptr ? p.prefix_lens[b] : 0;
+  s.start = q0;
+  s.ok = q0 >= 0 && q1 >= q0 && q1 <= p.n_tokens && q1 - q0 <= p.max_q_len;
+  s.n = s.ok ? q1 - q0 : 0;
+  s.ctx = chunk_clamp_ctx(p, ctx_raw);
+  s.prefix = pfx < 0 ? 0 : (pfx < s.ctx ? pfx : s.ctx);
+  if (note && (!s.ok || s.ctx != ctx_raw)) record_error(p.err, kDevErrContextLen);
+  return s;
+}
+
+// Largest b in [0, n) with key(b) <= x, for keys that do not decrease and
+// key(0) <= x: a whole warp looks at 32 places of the range per round, so a
+// thousand sequences take two dependent loads.  (Keys that do decrease give
+// some b of the range.)
+template <class F>
+__device__ __forceinline__ int warp_search(int n, int x, F&& key) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = n;
+  while (len > 1) {
+    const int step = (len + 31) / 32;
+    const int at = lane * step;
+    const bool le = at < len && (lane == 0 || key(lo + at) <= x);
+    const unsigned m = __ballot_sync(kFull, le);
+    const int last = 31 - __clz(m);   // lane 0's bit is always set
+    const int off = last * step;
+    lo += off;
+    len = min(step, len - off);
+  }
+  return lo;
+}
+
+// Row tiles of the tcgen05 kernel: sequence b's tiles take numbers from
+// floor(q_starts[b] / tile_q) + b on, which leaves each one room for its
+// ceil(n / tile_q) tiles and needs no prefix sum; some numbers stay unused.
+__device__ __forceinline__ int chunk_tile_base(const ChunkParams& p, int b) {
+  const int q = p.q_starts[b];
+  return (q < 0 ? 0 : (q > p.n_tokens ? p.n_tokens : q)) / p.tile_q + b;
+}
+
+// The keys that queries [i0, i1] of a sequence see, in tiles of NK tokens:
+// tiles [0, na) for the prefix, then nb tiles from b0 on.
+struct ChunkRange {
+  int lo, hi, prefix;  // some query sees t iff lo <= t < hi or t < prefix
+  int na, b0, n;       // n = na + the tiles of [lo, hi) past them
+  __device__ __forceinline__ int tile(int k) const { return k < na ? k : b0 + (k - na); }
+  __device__ __forceinline__ bool sees(int t0, int t1) const {  // any of tokens [t0, t1)
+    return t0 < prefix || (t0 < hi && t1 > lo);
+  }
+};
+
+template <int NK>
+__device__ __forceinline__ ChunkRange chunk_range(const ChunkParams& p, const ChunkSeq& s, int i0, int i1) {
+  ChunkRange r;
+  const int pos0 = s.ctx - s.n + i0, pos1 = s.ctx - s.n + i1;
+  r.hi = pos1 < 0 ? 0 : pos1 + 1;
+  r.prefix = pos1 < 0 ? 0 : s.prefix;
+  r.lo = p.window > 0 && pos0 >= p.window ? pos0 - p.window + 1 : 0;
+  r.na = (r.prefix + NK - 1) / NK;
+  const int first = r.lo / NK, end = (r.hi + NK - 1) / NK;
+  r.b0 = first > r.na ? first : r.na;
+  r.n = r.na + (end > r.b0 ? end - r.b0 : 0);
+  return r;
+}
+
+// cap * tanh(z / cap) in log2 units from w = 2 z log2(e) / cap:
+// tanh(y) = 1 - 2 / (e^2y + 1), whose absolute error of about 2^-23 is what a
+// score's error has to be measured by (times cap).
+__device__ __forceinline__ float capped(float w, float cap_log2) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fast_exp2(w) + 1.f));
+  return fmaf(-2.f * cap_log2, r, cap_log2);
+}
+
+}  // namespace pkv

@@ -27,7 +27,10 @@ enum KernelKind {
   kKindBlockCopy = 4,
   kKindMultiQuery = 5,
   kKindSlotMapping = 6,
-  kNumKernelKinds = 8  // room for later kinds; the trace aggregates by kind
+  kKindChunk = 7,
+  kKindRotary = 8,
+  kKindCompact = 9,
+  kNumKernelKinds = 10  // the trace aggregates by kind
 };
 
 // Decode work split: balanced stream-K ranges over the flattened
@@ -142,6 +145,91 @@ struct CopyParams {
   int* err;
 };
 
+// Attention of ragged chunks of new tokens over the paged cache (chunk.cu,
+// chunk_tc.cu).  Sequence b owns query rows [q_starts[b], q_starts[b + 1]);
+// query i of its n sits at position context_lens[b] - n + i.
+struct ChunkParams {
+  const void* q;                 // bf16 [T, H_q, D]
+  void* out;                     // bf16 [T, H_q, D]
+  const int32_t* q_starts;       // [B + 1]
+  const int32_t* block_tables;   // [B, MB]
+  const int32_t* context_lens;   // [B]
+  const float* slopes;           // [H_q] or NULL: score bias per token of distance
+  const int32_t* prefix_lens;    // [B] or NULL: tokens every query of the sequence sees
+  const float* k_scale;
+  const float* v_scale;
+  int64_t scale_stride;
+  int64_t num_blocks;
+  float* ws_o;                   // [T, H_q, S, D] partial rows (S > 1)
+  float* ws_ml;                  // [T, H_q, S, 2]
+  int32_t n_tokens;              // T
+  int32_t batch;
+  int32_t max_q_len;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t group;
+  int32_t head_dim;
+  int32_t block_size;
+  int32_t max_blocks;
+  int32_t max_ctx;
+  int32_t window;                // tokens a query sees back, itself included (0: all)
+  int32_t split_tokens;          // visible tokens per split (a multiple of 128)
+  int32_t max_splits;
+  int32_t tile_q;                // query tokens of one row tile
+  float qk_log2;                 // scale * log2(e); with a cap: 2 * scale * log2(e) / cap
+  float cap_log2;                // cap * log2(e), 0 without a cap
+  int32_t cache_dtype;
+  int* err;
+};
+
+// Rotary positions and append of new tokens (rotary.cu).
+struct RotaryParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;                   // bf16
+  int64_t q_stride, k_stride, v_stride, out_stride;  // elements between tokens
+  const int64_t* positions;
+  const double* inv_freq;        // [rotary_dim / 2], radians per position
+  float magnitude;
+  const int64_t* slots;
+  void* k_cache;
+  void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  int64_t scale_stride;
+  int64_t n_tokens;
+  int64_t num_slots;
+  int32_t block_size;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  int32_t src_dtype;             // PKV_BF16 / PKV_F32
+  int32_t cache_dtype;           // PKV_BF16 / PKV_E4M3
+  int* err;
+};
+
+// In-place compaction of sequences' token rows (compact.cu).
+struct CompactParams {
+  void* k_cache;
+  void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* keep;           // [N] logical positions to keep
+  const int32_t* keep_starts;    // [B + 1]
+  const int32_t* dst_start;      // [B] or NULL: first destination (0)
+  int64_t num_blocks;
+  int32_t n_keep;                // N
+  int32_t batch;
+  int32_t max_keep;
+  int32_t max_blocks;
+  int32_t block_size;
+  int32_t num_kv_heads;
+  int32_t row_bytes;             // bytes of one token row of one head
+  int* err;
+};
+
 // Message returned by pkv_last_error() on this host thread.
 void set_last_error(const char* msg);
 
@@ -164,6 +252,13 @@ cudaError_t launch_multi_query(const DecodeParams& p, const CUtensorMap& tmap_k,
 // (the cascade kernel's pipeline, one 128-row group per CTA).
 cudaError_t launch_multi_query_tc(const DecodeParams& p, const CUtensorMap& tmap_k,
                                   const CUtensorMap& tmap_v, cudaStream_t stream);
+// Ragged chunks: the mma.sync kernel (row tiles of up to 16 rows), the tcgen05
+// kernel (row tiles of up to 256 rows) and the merge of their split pieces.
+cudaError_t launch_chunk_small(const ChunkParams& p, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
+                               cudaStream_t stream);
+cudaError_t launch_chunk_combine(const ChunkParams& p, cudaStream_t stream);
+cudaError_t launch_rotary(const RotaryParams& p, cudaStream_t stream);
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
 // Self-test of the bounded waits (0: mbarrier wait; 1: tensor-core CTA abort
 // path); records PKV_DEVERR_WAIT_TIMEOUT after about limit_ns.
 cudaError_t launch_wait_selftest(int which, uint64_t limit_ns, int* err, cudaStream_t stream);
@@ -179,6 +274,13 @@ constexpr int kMultiQueryTile = 64;
 constexpr int kMultiQueryMaxSplitBlocks = 1024;
 // Token lanes (warps sharing the same 16 rows) for R rows per (sequence, head).
 inline int multi_query_lanes(int rows) { return rows <= 16 ? 4 : (rows <= 32 ? 2 : 1); }
+
+// Ragged chunks: rows of one row tile of the mma.sync and of the tcgen05
+// kernel, and blocks of one split of the mma.sync kernel (their ids are staged
+// in shared memory).
+constexpr int kChunkSmallRows = 16;
+constexpr int kChunkTcRows = 256;
+constexpr int kChunkMaxSplitBlocks = 1024;
 
 // Rows of query heads one cascade prefix CTA covers: two groups of 128 TMEM
 // lanes.

@@ -1234,7 +1234,7 @@ bool chunk_small(int32_t max_q_len, int32_t group) {
 }
 
 int32_t chunk_tile_q(int32_t max_q_len, int32_t group) {
-  return pkv::kChunkSmallRows / group;
+  return (chunk_small(max_q_len, group) ? pkv::kChunkSmallRows : pkv::kChunkTcRows) / group;
 }
 
 pkv_status chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_t num_q_heads,
@@ -1257,8 +1257,8 @@ pkv_status chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_
     return fail(PKV_ERR_INVALID_ARG, "split_tokens %d (0, or a multiple of 128 up to %lld)", split_tokens,
                 static_cast<long long>(max_st));
   if (sms <= 0) sms = kDefaultSms;
-  const bool small = true;
-  const int64_t tile_q = chunk_tile_q(max_q_len, group), nk = 64;
+  const bool small = chunk_small(max_q_len, group);
+  const int64_t tile_q = chunk_tile_q(max_q_len, group), nk = small ? pkv::kChunkSmallTile : pkv::kChunkTcTile;
   // visible keys of one row tile, in tiles of nk
   int64_t tiles = ceil_div(max_ctx, nk);
   if (window > 0 && !has_prefix) {
@@ -1274,14 +1274,13 @@ pkv_status chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_
     // the longest split that still gives every SM work: three CTAs per SM and
     // about six waves of them on the mma.sync kernel (as for decode), two
     // units per SM on the tcgen05 kernel
-    const int64_t want = static_cast<int64_t>(sms) * (small ? 18 : 2);
-    st = small ? 4096 : max_st;
-    while (st > 256 && units * ceil_div(tiles * nk, st) < want) st /= 2;
-    if (units >= want && small) st = ceil_div(tiles * nk, 128) * 128;
-    if (st > max_st) st = max_st;
+    const int64_t want = static_cast<int64_t>(sms) * (small ? 18 : 2), all = ceil_div(tiles * nk, 128) * 128;
+    st = small && units < want ? 4096 : all;
+    while (st > 256 && units * ceil_div(tiles * nk, st) < want) st = ceil_div(st / 2, 128) * 128;
+    if (small && st > max_st) st = max_st;
   }
-  if (small && c->num_kv_heads * ceil_div(max_q_len, tile_q) > 65535)
-    return fail(PKV_ERR_UNSUPPORTED, "num_kv_heads x row tiles beyond the grid");
+  if ((ceil_div(n_tokens, tile_q) + batch) * c->num_kv_heads > 0x7FFFFFFFll)
+    return fail(PKV_ERR_UNSUPPORTED, "row tiles x num_kv_heads beyond the grid");
   const int64_t splits = ceil_div(tiles * nk, st);
   if (splits > 65535) return fail(PKV_ERR_UNSUPPORTED, "%lld splits", static_cast<long long>(splits));
   *out = pkv_decode_plan_t{};
@@ -1351,9 +1350,11 @@ extern "C" pkv_status pkv_chunk_attention(
   const pkv_cache_desc& c = *cache;
   const int32_t group = num_q_heads / c.num_kv_heads;
   CUtensorMap tk, tv;
-  s = make_cache_tmap(&tk, k_cache, c, pkv::kTileTokens);
+  const bool small = pl.workers == 1;
+  const int box = small ? pkv::kTileTokens : c.block_size;  // token rows per TMA box
+  s = make_cache_tmap(&tk, k_cache, c, box);
   if (s != PKV_OK) return s;
-  s = make_cache_tmap(&tv, v_cache, c, pkv::kTileTokens);
+  s = make_cache_tmap(&tv, v_cache, c, box);
   if (s != PKV_OK) return s;
   pkv::ChunkParams p = {};
   p.q = q;
@@ -1392,9 +1393,13 @@ extern "C" pkv_status pkv_chunk_attention(
   p.cache_dtype = c.dtype;
   p.err = st->err;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = traced(pkv::kKindChunk, cs, [&] { return pkv::launch_chunk_small(p, tk, tv, cs); });
+  cudaError_t e = traced(pkv::kKindChunk, cs, [&] {
+    return small ? pkv::launch_chunk_small(p, tk, tv, cs) : pkv::launch_chunk_tc(p, tk, tv, cs);
+  });
   if (e == cudaSuccess && pl.max_splits > 1)
-    e = traced(pkv::kKindCombine, cs, [&] { return pkv::launch_chunk_combine(p, cs); });
+    e = traced(pkv::kKindCombine, cs, [&] {
+      return pkv::launch_chunk_combine(p, small ? pkv::kChunkSmallTile : pkv::kChunkTcTile, cs);
+    });
   if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
   return PKV_OK;
 }

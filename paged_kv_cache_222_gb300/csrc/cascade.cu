@@ -53,35 +53,6 @@ namespace {
 // never waits for a P.V), S and P.V issued by two warps, and six stages.
 // ----------------------------------------------------------------------------
 
-// Wait for a barrier phase; false once the CTA aborts (or on time-out, which
-// records the error and raises the abort flag).
-// max(a, b, c) in one instruction (three-input max.f32).
-__device__ __forceinline__ float max3f(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, int* err, volatile int* abort,
-                                              uint64_t limit_ns = kWaitLimitNs) {
-  if (mbar_try_wait(bar, parity)) return true;
-  uint64_t t0 = 0;
-  for (uint32_t n = 1;; ++n) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (n % 16 == 0 && *abort) return false;
-    if (n % kWaitTriesPerClockRead == 0) {
-      const uint64_t t = global_timer_ns();
-      if (t0 == 0) {
-        t0 = t;
-      } else if (t - t0 > limit_ns) {
-        record_error(err, kDevErrWaitTimeout);
-        *abort = 1;
-        return false;
-      }
-    }
-  }
-}
-
 // Tile geometry of the tensor-core kernels: 128 query rows per group, 64-key
 // K and V tiles stored as 128-byte rows (one d-half after the other),
 // 128B-swizzled.

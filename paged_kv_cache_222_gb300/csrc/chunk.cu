@@ -24,7 +24,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kSmallTile = 64;        // keys per step
+constexpr int kSmallTile = kChunkSmallTile;  // keys per step
 
 template <int D, bool FP8>
 struct SmallShape {
@@ -442,8 +442,7 @@ cudaError_t launch_chunk_small(const ChunkParams& p, const CUtensorMap& tk, cons
   return fp8 ? launch_small_t<64, true>(p, tk, tv, stream) : launch_small_t<64, false>(p, tk, tv, stream);
 }
 
-cudaError_t launch_chunk_combine(const ChunkParams& p, cudaStream_t stream) {
-  const int nk = kSmallTile;
+cudaError_t launch_chunk_combine(const ChunkParams& p, int nk, cudaStream_t stream) {
   if (p.head_dim == 128)
     return launch_pdl(chunk_combine_kernel<128>, dim3(p.n_tokens), dim3(256), 0, stream, p, nk);
   return launch_pdl(chunk_combine_kernel<64>, dim3(p.n_tokens), dim3(256), 0, stream, p, nk);

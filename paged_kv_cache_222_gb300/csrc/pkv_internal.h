@@ -256,7 +256,10 @@ cudaError_t launch_multi_query_tc(const DecodeParams& p, const CUtensorMap& tmap
 // kernel (row tiles of up to 256 rows) and the merge of their split pieces.
 cudaError_t launch_chunk_small(const ChunkParams& p, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
                                cudaStream_t stream);
-cudaError_t launch_chunk_combine(const ChunkParams& p, cudaStream_t stream);
+cudaError_t launch_chunk_tc(const ChunkParams& p, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
+                            cudaStream_t stream);
+// `nk`: keys per tile of the kernel that wrote the pieces.
+cudaError_t launch_chunk_combine(const ChunkParams& p, int nk, cudaStream_t stream);
 cudaError_t launch_rotary(const RotaryParams& p, cudaStream_t stream);
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
 // Self-test of the bounded waits (0: mbarrier wait; 1: tensor-core CTA abort
@@ -281,6 +284,8 @@ inline int multi_query_lanes(int rows) { return rows <= 16 ? 4 : (rows <= 32 ? 2
 constexpr int kChunkSmallRows = 16;
 constexpr int kChunkTcRows = 256;
 constexpr int kChunkMaxSplitBlocks = 1024;
+// Keys per tile of the two kernels.
+constexpr int kChunkSmallTile = 64, kChunkTcTile = 128;
 
 // Rows of query heads one cascade prefix CTA covers: two groups of 128 TMEM
 // lanes.

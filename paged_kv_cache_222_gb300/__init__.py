@@ -322,20 +322,46 @@ def multi_query_attention(q, k_cache, v_cache, block_tables, context_lens, scale
     return out
 
 
-class _OnDevice:
-    """torch.cuda.device(dev) that costs nothing when dev is already current."""
-    __slots__ = ("_guard",)
+# The serving calls below run once per layer and step, many of them on a few
+# tokens, where the host's time is what counts: their checks are single
+# comparisons on the good path (the helper that names the fault runs on the bad
+# one), descriptors and plans are kept by their sizes, and the stream is read
+# without building a torch.cuda.Stream.
 
-    def __init__(self, dev):
-        self._guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+def _check(t, dtype, name, index, device):
+    if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        _contig(t, dtype, name, device)
 
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
 
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+@functools.lru_cache(maxsize=256)
+def _desc_of(shape, dtype):
+    if len(shape) != 4:
+        raise ValueError("cache must be [num_blocks, num_kv_heads, block_size, head_dim]")
+    if dtype == torch.bfloat16:
+        kind = PKV_BF16
+    elif dtype in (torch.uint8, torch.float8_e4m3fn):
+        kind = PKV_E4M3
+    else:
+        raise TypeError(f"cache dtype {dtype}: expected bfloat16 or uint8/float8_e4m3fn")
+    desc = CacheDesc(shape[0], shape[2], shape[1], shape[3], kind)
+    return desc, ctypes.byref(desc), (shape[0], shape[2], shape[1], shape[3], kind)
+
+
+def _caches(k_cache, v_cache):
+    """(device index, device, descriptor, pointer to it, its fields) of a pair of caches."""
+    shape, dtype, index = k_cache.shape, k_cache.dtype, k_cache.get_device()
+    if (v_cache.shape != shape or v_cache.dtype is not dtype or index < 0 or v_cache.get_device() != index
+            or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+        _check_pair(k_cache, v_cache)
+    return (index, k_cache.device) + _desc_of(shape, dtype)
+
+
+def _on_device(index, call, *args):
+    """call(*args, stream) with `index` the current device, on its current stream."""
+    if torch.cuda.current_device() == index:
+        return call(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        return call(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
 @functools.lru_cache(maxsize=None)
@@ -347,25 +373,21 @@ def _scale_stride(k_scale, v_scale, rows, heads, dev, stride):
     """Row stride of an E4M3 cache's scales, [rows, H_kv] or [H_kv] each."""
     if k_scale is None or v_scale is None:
         raise ValueError("E4M3 cache needs k_scale and v_scale")
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _contig(t, torch.float32, name, dev)
-        if stride is None and tuple(t.shape) not in ((rows, heads), (heads,)):
-            raise ValueError(f"{name} must be [{rows}, {heads}] or [{heads}]")
-    if k_scale.shape != v_scale.shape:
+    _check(k_scale, torch.float32, "k_scale", dev.index, dev)
+    _check(v_scale, torch.float32, "v_scale", dev.index, dev)
+    shape = k_scale.shape
+    if v_scale.shape != shape:
         raise ValueError("k_scale and v_scale differ in shape")
     if stride is None:
-        return heads if k_scale.dim() == 2 else 0
+        if shape == (rows, heads):
+            return heads
+        if shape == (heads,):
+            return 0
+        raise ValueError(f"k_scale and v_scale must be [{rows}, {heads}] or [{heads}]")
     stride = int(stride)
     if stride < 0 or (rows > 0 and k_scale.numel() < stride * (rows - 1) + heads):
         raise ValueError("scale_row_stride reaches past the scales")
     return stride
-
-
-def _check_tables(block_tables, context_lens, b, dev):
-    _contig(block_tables, torch.int32, "block_tables", dev)
-    _contig(context_lens, torch.int32, "context_lens", dev)
-    if block_tables.dim() != 2 or block_tables.shape[0] != b or context_lens.shape != (b,):
-        raise ValueError("block_tables must be [B, MB] and context_lens [B]")
 
 
 def chunk_plan(n_tokens, batch, max_q_len, num_q_heads, k_cache_or_desc, max_context_len, window=0,
@@ -406,59 +428,65 @@ def chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_starts, s
     pos (window 0: t <= pos).  E4M3 caches take k_scale / v_scale float32 [B,
     H_kv] or [H_kv].
     """
-    lib = library()
-    _check_pair(k_cache, v_cache)
-    dev = k_cache.device
-    desc = cache_desc(k_cache)
-    _contig(q, torch.bfloat16, "q", dev)
-    if q.dim() != 3 or q.shape[2] != desc.head_dim:
+    index, dev, desc, desc_ptr, fields = _caches(k_cache, v_cache)
+    _check(q, torch.bfloat16, "q", index, dev)
+    _check(q_starts, torch.int32, "q_starts", index, dev)
+    _check(block_tables, torch.int32, "block_tables", index, dev)
+    _check(context_lens, torch.int32, "context_lens", index, dev)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != fields[3]:
         raise ValueError("q must be [T, H_q, head_dim]")
-    t, hq, d = q.shape
-    _contig(q_starts, torch.int32, "q_starts", dev)
+    t, hq, _ = shape
     if q_starts.dim() != 1 or q_starts.shape[0] < 1:
         raise ValueError("q_starts must be [B + 1]")
     b = q_starts.shape[0] - 1
-    _check_tables(block_tables, context_lens, b, dev)
+    if block_tables.dim() != 2 or block_tables.shape[0] != b or context_lens.shape != (b,):
+        raise ValueError("block_tables must be [B, MB] and context_lens [B]")
     mb = block_tables.shape[1]
     max_q_len = max(t, 1) if max_q_len is None else int(max_q_len)
-    max_context_len = mb * desc.block_size if max_context_len is None else int(max_context_len)
+    max_context_len = mb * fields[1] if max_context_len is None else int(max_context_len)
     split_tokens, window = int(split_tokens), int(window)
     if out is None:
-        out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=dev)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     else:
-        _contig(out, torch.bfloat16, "out", dev)
-        if out.shape != q.shape:
+        _check(out, torch.bfloat16, "out", index, dev)
+        if out.shape != shape:
             raise ValueError("out must be [T, H_q, D]")
+    ks = vs = None
     stride = 0
-    if desc.dtype == PKV_E4M3:
-        stride = _scale_stride(k_scale, v_scale, b, desc.num_kv_heads, dev, scale_row_stride)
+    if fields[4] == PKV_E4M3:
+        stride = _scale_stride(k_scale, v_scale, b, fields[2], dev, scale_row_stride)
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("scales given for a bf16 cache")
+    sl = pf = None
     if slopes is not None:
-        _contig(slopes, torch.float32, "slopes", dev)
+        _check(slopes, torch.float32, "slopes", index, dev)
         if slopes.shape != (hq,):
             raise ValueError("slopes must be [H_q]")
+        sl = slopes.data_ptr()
     if prefix_lens is not None:
-        _contig(prefix_lens, torch.int32, "prefix_lens", dev)
+        _check(prefix_lens, torch.int32, "prefix_lens", index, dev)
         if prefix_lens.shape != (b,):
             raise ValueError("prefix_lens must be [B]")
-    mods = ScoreMods(softcap, window, None if slopes is None else slopes.data_ptr(),
-                     None if prefix_lens is None else prefix_lens.data_ptr())
-    with _OnDevice(dev):
-        # planned for this device's SMs, as the library plans the call itself
-        need = _chunk_workspace(t, b, max_q_len, hq, (desc.num_blocks, desc.block_size, desc.num_kv_heads,
-                                                      desc.head_dim, desc.dtype), max_context_len, window,
-                                prefix_lens is not None, split_tokens, _num_sms(dev.index))
-        have = 0
-        if need > 0:
-            if workspace is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            _contig(workspace, torch.uint8, "workspace", dev)
-            have = workspace.numel()
-        st = lib.pkv_chunk_attention(
-            q.data_ptr(), t, q_starts.data_ptr(), b, max_q_len, hq, k_cache.data_ptr(), v_cache.data_ptr(),
-            ctypes.byref(desc), block_tables.data_ptr(), mb, context_lens.data_ptr(), max_context_len, float(scale),
-            ctypes.byref(mods), out.data_ptr(), _ptr(k_scale), _ptr(v_scale), stride,
-            workspace.data_ptr() if have else None, have, split_tokens, _stream(dev))
-    _lib.check(st, "pkv_chunk_attention")
+        pf = prefix_lens.data_ptr()
+    # planned for this device's SMs, as the library plans the call itself
+    need = _chunk_workspace(t, b, max_q_len, hq, fields, max_context_len, window, pf is not None, split_tokens,
+                            _num_sms(index))
+    ws, have = None, 0
+    if need > 0:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            _check(workspace, torch.uint8, "workspace", index, dev)
+        ws, have = workspace.data_ptr(), workspace.numel()
+    st = _on_device(index, library().pkv_chunk_attention,
+                    q.data_ptr(), t, q_starts.data_ptr(), b, max_q_len, hq, k_cache.data_ptr(), v_cache.data_ptr(),
+                    desc_ptr, block_tables.data_ptr(), mb, context_lens.data_ptr(), max_context_len, scale,
+                    ctypes.byref(ScoreMods(softcap, window, sl, pf)), out.data_ptr(), ks, vs, stride, ws, have,
+                    split_tokens)
+    if st:
+        _lib.check(st, "pkv_chunk_attention")
     return out
 
 
@@ -497,18 +525,20 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, origi
     return f.to(device) if device is not None else f
 
 
-def _token_rows(t, name, dtype, heads, d, n, dev):
+def _token_rows(t, name, dtype, shape, index, dev):
     """[N, heads, D] tensor whose tokens may lie further apart than their rows
     (a slice of a fused projection); returns the elements between tokens."""
-    if t.dtype != dtype:
+    n, heads, d = shape
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
+    if t.get_device() != index:
         raise ValueError(f"{name} must be on {dev}")
-    if tuple(t.shape) != (n, heads, d):
+    if t.shape != shape:
         raise ValueError(f"{name} must be [{n}, {heads}, {d}]")
-    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
+    between, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.stride(0) if n > 1 else heads * d
+    return between if n > 1 else heads * d
 
 
 def rotary_append(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=None,
@@ -523,45 +553,48 @@ def rotary_append(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, 
     rotary_dim pass through.  slot_mapping and scales as `append` (a negative
     slot stores nothing; its query is still returned).  `out` may be q itself.
     """
-    lib = library()
-    _check_pair(k_cache, v_cache)
-    dev = k_cache.device
-    desc = cache_desc(k_cache)
-    if q.dim() != 3:
+    index, dev, desc, desc_ptr, fields = _caches(k_cache, v_cache)
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3:
         raise ValueError("q must be [N, H_q, D]")
-    n, hq, d = q.shape
-    hkv = desc.num_kv_heads
-    if d != desc.head_dim:
+    n, hq, d = shape
+    if d != fields[3]:
         raise ValueError("q's head_dim does not match the cache")
-    if q.dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         src = PKV_BF16
-    elif q.dtype == torch.float32:
+    elif dtype is torch.float32:
         src = PKV_F32
     else:
-        raise TypeError(f"q dtype {q.dtype}: expected bfloat16 or float32")
-    qs = _token_rows(q, "q", q.dtype, hq, d, n, dev)
-    ks = _token_rows(k, "k", q.dtype, hkv, d, n, dev)
-    vs = _token_rows(v, "v", q.dtype, hkv, d, n, dev)
-    _contig(positions, torch.int64, "positions", dev)
-    _contig(slot_mapping, torch.int64, "slot_mapping", dev)
+        raise TypeError(f"q dtype {dtype}: expected bfloat16 or float32")
+    kv_shape = (n, fields[2], d)
+    q_st = _token_rows(q, "q", dtype, shape, index, dev)
+    k_st = _token_rows(k, "k", dtype, kv_shape, index, dev)
+    v_st = _token_rows(v, "v", dtype, kv_shape, index, dev)
+    _check(positions, torch.int64, "positions", index, dev)
+    _check(slot_mapping, torch.int64, "slot_mapping", index, dev)
+    _check(inv_freq, torch.float64, "inv_freq", index, dev)
     if positions.shape != (n,) or slot_mapping.shape != (n,):
         raise ValueError("positions and slot_mapping must have one entry per token")
-    _contig(inv_freq, torch.float64, "inv_freq", dev)
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be [rotary_dim / 2]")
     if out is None:
-        out = torch.empty((n, hq, d), dtype=torch.bfloat16, device=dev)
-    os_ = _token_rows(out, "out", torch.bfloat16, hq, d, n, dev)
+        out, o_st = torch.empty(shape, dtype=torch.bfloat16, device=dev), hq * d
+    else:
+        o_st = _token_rows(out, "out", torch.bfloat16, shape, index, dev)
+    ks = vs = None
     stride = 0
-    if desc.dtype == PKV_E4M3:
-        stride = _scale_stride(k_scale, v_scale, n, hkv, dev, scale_row_stride)
-    with _OnDevice(dev):
-        st = lib.pkv_rotary_append(
-            q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, src, n, hq, positions.data_ptr(),
-            inv_freq.data_ptr(), 2 * inv_freq.shape[0], int(bool(interleaved)), float(magnitude),
-            slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ctypes.byref(desc), _ptr(k_scale),
-            _ptr(v_scale), stride, out.data_ptr(), os_, _stream(dev))
-    _lib.check(st, "pkv_rotary_append")
+    if fields[4] == PKV_E4M3:
+        stride = _scale_stride(k_scale, v_scale, n, fields[2], dev, scale_row_stride)
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("scales given for a bf16 cache")
+    st = _on_device(index, library().pkv_rotary_append,
+                    q.data_ptr(), q_st, k.data_ptr(), k_st, v.data_ptr(), v_st, src, n, hq, positions.data_ptr(),
+                    inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0, magnitude,
+                    slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), desc_ptr, ks, vs, stride,
+                    out.data_ptr(), o_st)
+    if st:
+        _lib.check(st, "pkv_rotary_append")
     return out
 
 
@@ -574,29 +607,27 @@ def compact_tokens(k_cache, v_cache, block_tables, keep, keep_starts, dst_start=
     must not lie before it.  `max_keep` is a host bound on a sequence's entries
     (default N).  Shorten the sequences afterwards (BlockManager.truncate).
     """
-    lib = library()
-    _check_pair(k_cache, v_cache)
-    dev = k_cache.device
-    desc = cache_desc(k_cache)
-    _contig(block_tables, torch.int32, "block_tables", dev)
-    _contig(keep, torch.int32, "keep", dev)
-    _contig(keep_starts, torch.int32, "keep_starts", dev)
+    index, dev, desc, desc_ptr, fields = _caches(k_cache, v_cache)
+    _check(block_tables, torch.int32, "block_tables", index, dev)
+    _check(keep, torch.int32, "keep", index, dev)
+    _check(keep_starts, torch.int32, "keep_starts", index, dev)
     if block_tables.dim() != 2 or keep.dim() != 1:
         raise ValueError("block_tables must be [B, MB] and keep 1-D")
-    b = block_tables.shape[0]
+    b, mb = block_tables.shape
     if keep_starts.shape != (b + 1,):
         raise ValueError("keep_starts must be [B + 1]")
+    ds = None
     if dst_start is not None:
-        _contig(dst_start, torch.int32, "dst_start", dev)
+        _check(dst_start, torch.int32, "dst_start", index, dev)
         if dst_start.shape != (b,):
             raise ValueError("dst_start must be [B]")
-    n = keep.numel()
-    with _OnDevice(dev):
-        st = lib.pkv_compact_tokens(
-            k_cache.data_ptr(), v_cache.data_ptr(), ctypes.byref(desc), block_tables.data_ptr(),
-            max(1, block_tables.shape[1]), b, keep.data_ptr(), n, keep_starts.data_ptr(), _ptr(dst_start),
-            n if max_keep is None else int(max_keep), _stream(dev))
-    _lib.check(st, "pkv_compact_tokens")
+        ds = dst_start.data_ptr()
+    n = keep.shape[0]
+    st = _on_device(index, library().pkv_compact_tokens,
+                    k_cache.data_ptr(), v_cache.data_ptr(), desc_ptr, block_tables.data_ptr(), max(1, mb), b,
+                    keep.data_ptr(), n, keep_starts.data_ptr(), ds, n if max_keep is None else int(max_keep))
+    if st:
+        _lib.check(st, "pkv_compact_tokens")
 
 
 def slot_mapping(block_tables, positions, k_cache, seq_index=None, out=None):

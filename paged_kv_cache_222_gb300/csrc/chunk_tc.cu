@@ -44,7 +44,7 @@ struct TcShape {
   static constexpr int RAW = NK * D;               // an E4M3 K or V tile
   static constexpr int NS = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
   static constexpr int NR = FP8 ? (D == 128 ? 4 : 8) : 0;
-  static constexpr int NBARS = 2 * NS + 2 * NR + 3 * GROUPS + 2;
+  static constexpr int NBARS = 2 * NS + 2 * NR + 3 * GROUPS + 3;
   static constexpr int BYTES = QBYTES + NS * TILE + NR * RAW + NBARS * 8 + 16 + 1024;
   static_assert(BYTES <= 232448, "shared memory per CTA");
   static constexpr int THREADS = FP8 ? 512 : 384;
@@ -66,7 +66,8 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
   constexpr int kMma = 8, kProd = 9, kConv = 12;
   static_assert(COL_O + GROUPS * D <= 512, "TMEM columns");
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the warp number as a broadcast: roles branch uniformly
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
   const int G = p.group, H_q = p.num_q_heads;
   wait_prior_grid();
 
@@ -89,6 +90,9 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
   const int k0 = split * per_split;
   const int ntile = min(rg.n - k0, per_split);
   const int ng = rows > M ? 2 : 1;
+  // the sequence ends inside a block of the last tile (later tiles hold later keys)
+  const int t_last = ntile > 0 ? rg.tile(k0 + ntile - 1) * NK : 0;
+  const bool v_tail = ntile > 0 && sq.ctx - t_last < NK && (sq.ctx - t_last) % p.block_size != 0;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -104,7 +108,8 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
   uint64_t* pfull = sfull + GROUPS;  // [GROUPS]: P_g(k) is in TMEM
   uint64_t* odone = pfull + GROUPS;  // [GROUPS]: O_g is complete
   uint64_t* qfull = odone + GROUPS;
-  uint64_t* done = qfull + 1;
+  uint64_t* vfix = qfull + 1;       // the last V tile's rows past the end are zeros
+  uint64_t* done = vfix + 1;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
 
@@ -123,6 +128,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
       mbar_init(smem_u32(odone + g), 1);
     }
     mbar_init(smem_u32(qfull), 4 * ng);
+    mbar_init(smem_u32(vfix), 1);
     mbar_init(smem_u32(done), 1);
     *s_abort = 0;
     fence_mbar_init();
@@ -136,91 +142,83 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = *s_tmem;
+  const uint32_t tbase = __shfl_sync(kFull, *s_tmem, 0);
 
   if (warp >= kMma) {
     regs_dec<C::REGS_OTHER>();
     if (warp == kMma) {
       // ------------------------------------------------------------ products
-      bool ok = wait_or_abort(smem_u32(qfull), 0u, p.err, s_abort);
-      auto wait_item = [&](int item) {
-        ok = ok && wait_or_abort(smem_u32(full + item % NS), static_cast<uint32_t>((item / NS) & 1), p.err, s_abort);
-        ok = __all_sync(kFull, ok);
+      // the whole warp walks this role, one lane's products are issued: see
+      // tc_mma_ss_if
+      const uint32_t leader = elect_one();
+      const int nt = __shfl_sync(kFull, ntile, 0), groups = __shfl_sync(kFull, ng, 0);
+      const uint32_t ring0 = __shfl_sync(kFull, smem_u32(ring), 0), q0 = __shfl_sync(kFull, smem_u32(q_sm), 0);
+      auto wait = [&](uint64_t* bar, int phase) {
+        return __all_sync(kFull, wait_or_abort(smem_u32(bar), static_cast<uint32_t>(phase & 1), p.err, s_abort)) != 0;
       };
-      auto issue_s = [&](int g, int k) {
-        const uint32_t qa = smem_u32(q_sm) + g * M * 128;
-        const uint32_t kst = smem_u32(ring) + ((2 * k) % NS) * C::TILE;
+      auto issue_s = [&](int g, int slot) {
+        const uint64_t a0 = smem_desc_sw128(q0 + g * M * 128, 0, 1024);
+        const uint64_t b0 = smem_desc_sw128(ring0 + slot * C::TILE, 0, 1024);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t ad = smem_desc_sw128(qa + (kk / 4) * C::QHALF + (kk % 4) * 32, 0, 1024);
-          const uint64_t bd = smem_desc_sw128(kst + (kk / 4) * C::HALFB + (kk % 4) * 32, 0, 1024);
-          tc_mma_ss(tbase + COL_S + g * NK, ad, bd, IDESC_S, kk > 0 ? 1u : 0u);
-        }
-        tc_commit(smem_u32(sfull + g));
+        for (int kk = 0; kk < D / 16; ++kk)  // descriptor addresses are in 16-byte units
+          tc_mma_ss_if(leader, tbase + COL_S + g * NK, a0 + ((kk / 4) * C::QHALF + (kk % 4) * 32) / 16,
+                       b0 + ((kk / 4) * C::HALFB + (kk % 4) * 32) / 16, IDESC_S, kk > 0 ? 1u : 0u);
+        tc_commit_if(leader, smem_u32(sfull + g));
       };
-      if (ntile > 0) {
-        wait_item(0);
-        if (ok && lane == 0) {
+      bool ok = wait(qfull, 0);
+      int slot = 0, use = 0;  // ring slot of the next item, and its use number
+      auto next_slot = [&]() {
+        if (++slot == NS) {
+          slot = 0;
+          ++use;
+        }
+      };
+      if (nt > 0 && ok) {
+        ok = wait(full, 0);
+        if (ok) {
           tc_fence_after();
-          for (int g = 0; g < ng; ++g) issue_s(g, 0);
-          tc_commit(smem_u32(empty));  // item 0's slot
+          for (int g = 0; g < groups; ++g) issue_s(g, 0);
+          tc_commit_if(leader, smem_u32(empty));
         }
+        next_slot();
       }
-      for (int k = 0; k < ntile && ok; ++k) {
-        const int vi = 2 * k + 1;
-        wait_item(vi);
+      for (int k = 0; k < nt && ok; ++k) {
+        const int vslot = slot;
+        ok = wait(full + vslot, use);
         if (!ok) break;
-        uint8_t* vt = ring + (vi % NS) * C::TILE;
-        if constexpr (!FP8) {
-          // rows of the last block past the sequence's end may hold anything
-          // (NaN included): zero them, P is 0 there.  Whole blocks past it were
-          // loaded as zeros.
-          const int first = sq.ctx - rg.tile(k0 + k) * NK;
-          const int last = min(NK, (first + p.block_size - 1) / p.block_size * p.block_size);
-          if (first < last) {
-            const int chunks = (last - first) * 8;
-            for (int c = lane; c < C::HALVES * chunks; c += 32) {
-              const int hf = c / chunks, cc = c - hf * chunks;
-              *reinterpret_cast<uint4*>(vt + hf * C::HALFB + first * 128 + cc * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-        }
-        const bool more = k + 1 < ntile;
-#pragma unroll 1
-        for (int g = 0; g < ng; ++g) {
-          ok = wait_or_abort(smem_u32(pfull + g), static_cast<uint32_t>(k & 1), p.err, s_abort);
-          ok = __all_sync(kFull, ok);
+        if (!FP8 && k == nt - 1 && v_tail) {  // its loader has zeroed the rows past the sequence's end
+          ok = wait(vfix, 0);
           if (!ok) break;
-          if (lane == 0) {
-            tc_fence_after();
-            const uint32_t vst = smem_u32(vt);
+        }
+        next_slot();
+        const bool more = k + 1 < nt;
+        const uint64_t v0 = smem_desc_sw128(ring0 + vslot * C::TILE, C::HALVES > 1 ? C::HALFB : 0, 1024);
+        for (int g = 0; g < groups && ok; ++g) {
+          ok = wait(pfull + g, k);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < NK / 16; ++kk) {
-              // MN-major V: 8-key groups 1024 B apart, column halves HALFB apart
-              const uint64_t vd = smem_desc_sw128(vst + kk * 2048, C::HALVES > 1 ? C::HALFB : 0, 1024);
-              tc_mma_ts(tbase + COL_O + g * D, tbase + COL_S + g * NK + kk * 8, vd, IDESC_PV,
-                        (k > 0 || kk > 0) ? 1u : 0u);
-            }
-            if (g == ng - 1) tc_commit(smem_u32(empty + vi % NS));
-            if (!more) tc_commit(smem_u32(odone + g));
-          }
+          for (int kk = 0; kk < NK / 16; ++kk)  // MN-major V: 8-key groups 1024 B apart, column halves HALFB apart
+            tc_mma_ts_if(leader, tbase + COL_O + g * D, tbase + COL_S + g * NK + kk * 8, v0 + kk * (2048 / 16),
+                         IDESC_PV, (k > 0 || kk > 0) ? 1u : 0u);
+          if (g == groups - 1) tc_commit_if(leader, smem_u32(empty + vslot));
           if (more) {
-            if (g == 0) wait_item(vi + 1);
-            if (!ok) break;
-            if (lane == 0) {
+            if (g == 0) {
+              ok = wait(full + slot, use);
+              if (!ok) break;
               tc_fence_after();
-              issue_s(g, k + 1);
-              if (g == ng - 1) tc_commit(smem_u32(empty + (vi + 1) % NS));
             }
+            issue_s(g, slot);
+            if (g == groups - 1) tc_commit_if(leader, smem_u32(empty + slot));
+          } else {
+            tc_commit_if(leader, smem_u32(odone + g));
           }
         }
+        if (more) next_slot();
       }
-      if (lane == 0) {  // nothing of this thread's may still be running when TMEM is freed
-        tc_commit(smem_u32(done));
-        mbar_wait(smem_u32(done), 0u, nullptr);
-      }
+      // nothing of this warp's may still be running when TMEM is freed
+      tc_commit_if(leader, smem_u32(done));
+      mbar_wait(smem_u32(done), 0u, nullptr);
     } else if (warp == kProd || warp == kProd + 1) {
       // ------------------------------------------------------------ loads
       const int v = warp - kProd;
@@ -270,6 +268,25 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
         if (lane < nbox) tma_load_4d(base + s * BYTES + off, tmap, bar, hf * 64, 0, h, phys);
         phys = next;
         issued = k + 1;
+      }
+      if (!FP8 && v == 1 && v_tail && issued == ntile) {
+        // Rows of the last block past the sequence's end may hold anything
+        // (NaN included): zero them once they have landed, P is 0 there.  Whole
+        // blocks past it were loaded as zeros.
+        const int item = 2 * (ntile - 1) + 1, s = item % nring;
+        bool ok = wait_or_abort(smem_u32(bfull + s), static_cast<uint32_t>((item / nring) & 1), p.err, s_abort);
+        if (__all_sync(kFull, ok)) {
+          const int first = sq.ctx - rg.tile(k0 + ntile - 1) * NK;
+          const int chunks = ((first + p.block_size - 1) / p.block_size * p.block_size - first) * 8;
+          for (int c = lane; c < C::HALVES * chunks; c += 32) {
+            const int hh = c / chunks, cc = c - hh * chunks;
+            *reinterpret_cast<uint4*>(ring + s * C::TILE + hh * C::HALFB + first * 128 + cc * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(vfix));
+        }
       }
       if (lane == 0 && *s_abort) {  // the copies in flight land before the CTA leaves
         for (int k = 0; k < issued; ++k) {

@@ -42,19 +42,91 @@ struct TcShape {
   static constexpr int HALFB = NK * 128;
   static constexpr int TILE = HALVES * HALFB;      // a 16-bit K or V tile
   static constexpr int RAW = NK * D;               // an E4M3 K or V tile
-  static constexpr int NS = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+  static constexpr int NS = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
   static constexpr int NR = FP8 ? (D == 128 ? 4 : 8) : 0;
-  static constexpr int NBARS = 2 * NS + 2 * NR + 3 * GROUPS + 3;
+  static constexpr int NBARS = 2 * NS + 2 * NR + 4 * GROUPS + 2;
   static constexpr int BYTES = QBYTES + NS * TILE + NR * RAW + NBARS * 8 + 16 + 1024;
   static_assert(BYTES <= 232448, "shared memory per CTA");
   static constexpr int THREADS = FP8 ? 512 : 384;
   // registers: 384 x 168 or 512 x 128 at launch
-  static constexpr int REGS_SOFTMAX = FP8 ? 176 : 208;
-  static constexpr int REGS_OTHER = FP8 ? 80 : 88;
+  static constexpr int REGS_SOFTMAX = FP8 ? 176 : 200;
+  static constexpr int REGS_OTHER = FP8 ? 80 : 104;
   static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * (FP8 ? 128 : 168), "register file");
 };
 
-template <int D, bool FP8, bool MODS>
+// What a score is besides scale * q.k: nothing; capped; biased (capped or not).
+constexpr int kPlain = 0, kCapped = 1, kBiased = 2;
+
+__device__ __forceinline__ float min_nan(float a, float b) {  // NaN if one is
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// x := cap * tanh(x * y_mult) in log2 units, for the 128 scores of a row.
+//
+// Small arguments, |y| <= 1/2 in the whole warp (scores up to half the cap):
+// tanh(y) = y (c0 + c1 y^2 + c2 y^4 + c3 y^6) with the coefficients of the
+// least largest relative error on that range (5.4e-7: below 2^-15 of a
+// weight's exponent for scores up to 25), powers of y_mult folded in: five
+// packed FMA-pipe operations per two scores and nothing on the
+// special-function unit, which the exponentials need.
+// Others: 1 - 2 / (e^2y + 1), one reciprocal shared by four scores,
+// 1 / a = b c d / (a b c d); 2y is held below 28 log2 units, where tanh is 1 to
+// binary32 and the product of four cannot overflow.
+template <int N>
+__device__ __forceinline__ void cap_scores(float (&x)[N], float w_mult, float cap_log2, bool masked,
+                                           const uint32_t (&see)[N / 32]) {
+  constexpr float kY = 0.34657359027997264f;  // ln 2 / 2: y = kY * w
+  const float y_mult = w_mult * kY;
+  float am = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) am = max3f(am, fabsf(x[i]), fabsf(x[i + 1]));
+  if (__all_sync(kFull, am * y_mult <= 0.5f) && y_mult > 1e-5f) {
+    const float y2 = y_mult * y_mult, f0 = cap_log2 * y_mult;
+    const float f1 = f0 * y2, f2 = f1 * y2, f3 = f2 * y2;
+    const float2 c0 = make_float2(0.99999946f * f0, 0.99999946f * f0);
+    const float2 c1 = make_float2(-0.33326318f * f1, -0.33326318f * f1);
+    const float2 c2 = make_float2(0.13190297f * f2, 0.13190297f * f2);
+    const float2 c3 = make_float2(-0.04440223f * f3, -0.04440223f * f3);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 v = make_float2(x[i], x[i + 1]);
+      const float2 t = __fmul2_rn(v, v);
+      float2 h = __ffma2_rn(c3, t, c2);
+      h = __ffma2_rn(h, t, c1);
+      h = __ffma2_rn(h, t, c0);
+      h = __fmul2_rn(h, v);
+      x[i] = h.x;
+      x[i + 1] = h.y;
+    }
+    return;
+  }
+  if (masked) {  // what lies past the sequence's end may be NaN: it must not reach its neighbours
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (!((see[i / 32] >> (i % 32)) & 1u)) x[i] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    float q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = fast_exp2(min_nan(x[i + j] * w_mult, 28.f)) + 1.f;
+    const float2 pr = __fmul2_rn(make_float2(q[0], q[2]), make_float2(q[1], q[3]));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(pr.x * pr.y));
+    const float2 rp = __fmul2_rn(make_float2(r, r), make_float2(pr.y, pr.x));  // 1 / (q0 q1), 1 / (q2 q3)
+    const float2 m2c = make_float2(-2.f * cap_log2, -2.f * cap_log2), c = make_float2(cap_log2, cap_log2);
+    const float2 a = __ffma2_rn(__fmul2_rn(make_float2(rp.x, rp.x), make_float2(q[1], q[0])), m2c, c);
+    const float2 b = __ffma2_rn(__fmul2_rn(make_float2(rp.y, rp.y), make_float2(q[3], q[2])), m2c, c);
+    x[i] = a.x;
+    x[i + 1] = a.y;
+    x[i + 2] = b.x;
+    x[i + 3] = b.y;
+  }
+}
+
+template <int D, bool FP8, int MODE>
 __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
     chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                     const ChunkParams p) {
@@ -110,13 +182,13 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
   uint64_t* qfull = odone + GROUPS;
   uint64_t* vfix = qfull + 1;       // the last V tile's rows past the end are zeros
   uint64_t* done = vfix + 1;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + 1);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + GROUPS);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(smem_u32(full + s), FP8 ? 4 : 1);
-      mbar_init(smem_u32(empty + s), 1);
+      mbar_init(smem_u32(empty + s), ng);
     }
     for (int s = 0; s < NR; ++s) {
       mbar_init(smem_u32(rfull + s), 1);
@@ -126,10 +198,10 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
       mbar_init(smem_u32(sfull + g), 1);
       mbar_init(smem_u32(pfull + g), 4);
       mbar_init(smem_u32(odone + g), 1);
+      mbar_init(smem_u32(done + g), 1);
     }
     mbar_init(smem_u32(qfull), 4 * ng);
     mbar_init(smem_u32(vfix), 1);
-    mbar_init(smem_u32(done), 1);
     *s_abort = 0;
     fence_mbar_init();
     prefetch_tmap(&tmap_k);
@@ -146,24 +218,27 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
 
   if (warp >= kMma) {
     regs_dec<C::REGS_OTHER>();
-    if (warp == kMma) {
+    if (warp == kMma || warp == kMma + 3) {
       // ------------------------------------------------------------ products
-      // the whole warp walks this role, one lane's products are issued: see
-      // tc_mma_ss_if
+      // The whole warp walks this role, one lane's products are issued: see
+      // tc_mma_ss_if.
+      const int g = warp == kMma ? 0 : 1;
       const uint32_t leader = elect_one();
-      const int nt = __shfl_sync(kFull, ntile, 0), groups = __shfl_sync(kFull, ng, 0);
+      const int nt = __shfl_sync(kFull, g < ng ? ntile : 0, 0);
       const uint32_t ring0 = __shfl_sync(kFull, smem_u32(ring), 0), q0 = __shfl_sync(kFull, smem_u32(q_sm), 0);
+      const uint32_t c_s = tbase + COL_S + g * NK, c_o = tbase + COL_O + g * D;
       auto wait = [&](uint64_t* bar, int phase) {
         return __all_sync(kFull, wait_or_abort(smem_u32(bar), static_cast<uint32_t>(phase & 1), p.err, s_abort)) != 0;
       };
-      auto issue_s = [&](int g, int slot) {
-        const uint64_t a0 = smem_desc_sw128(q0 + g * M * 128, 0, 1024);
+      const uint64_t a0 = smem_desc_sw128(q0 + g * M * 128, 0, 1024);
+      auto issue_s = [&](int slot) {
         const uint64_t b0 = smem_desc_sw128(ring0 + slot * C::TILE, 0, 1024);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)  // descriptor addresses are in 16-byte units
-          tc_mma_ss_if(leader, tbase + COL_S + g * NK, a0 + ((kk / 4) * C::QHALF + (kk % 4) * 32) / 16,
+          tc_mma_ss_if(leader, c_s, a0 + ((kk / 4) * C::QHALF + (kk % 4) * 32) / 16,
                        b0 + ((kk / 4) * C::HALFB + (kk % 4) * 32) / 16, IDESC_S, kk > 0 ? 1u : 0u);
         tc_commit_if(leader, smem_u32(sfull + g));
+        tc_commit_if(leader, smem_u32(empty + slot));
       };
       bool ok = wait(qfull, 0);
       int slot = 0, use = 0;  // ring slot of the next item, and its use number
@@ -177,8 +252,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
         ok = wait(full, 0);
         if (ok) {
           tc_fence_after();
-          for (int g = 0; g < groups; ++g) issue_s(g, 0);
-          tc_commit_if(leader, smem_u32(empty));
+          issue_s(0);
         }
         next_slot();
       }
@@ -192,33 +266,25 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
         }
         next_slot();
         const bool more = k + 1 < nt;
+        if (more) ok = wait(full + slot, use);  // K(k+1), ahead of the wait for P
         const uint64_t v0 = smem_desc_sw128(ring0 + vslot * C::TILE, C::HALVES > 1 ? C::HALFB : 0, 1024);
-        for (int g = 0; g < groups && ok; ++g) {
-          ok = wait(pfull + g, k);
-          if (!ok) break;
-          tc_fence_after();
+        ok = ok && wait(pfull + g, k);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < NK / 16; ++kk)  // MN-major V: 8-key groups 1024 B apart, column halves HALFB apart
-            tc_mma_ts_if(leader, tbase + COL_O + g * D, tbase + COL_S + g * NK + kk * 8, v0 + kk * (2048 / 16),
-                         IDESC_PV, (k > 0 || kk > 0) ? 1u : 0u);
-          if (g == groups - 1) tc_commit_if(leader, smem_u32(empty + vslot));
-          if (more) {
-            if (g == 0) {
-              ok = wait(full + slot, use);
-              if (!ok) break;
-              tc_fence_after();
-            }
-            issue_s(g, slot);
-            if (g == groups - 1) tc_commit_if(leader, smem_u32(empty + slot));
-          } else {
-            tc_commit_if(leader, smem_u32(odone + g));
-          }
+        for (int kk = 0; kk < NK / 16; ++kk)  // MN-major V: 8-key groups 1024 B apart, column halves HALFB apart
+          tc_mma_ts_if(leader, c_o, c_s + kk * 8, v0 + kk * (2048 / 16), IDESC_PV, (k > 0 || kk > 0) ? 1u : 0u);
+        tc_commit_if(leader, smem_u32(empty + vslot));
+        if (more) {
+          issue_s(slot);
+          next_slot();
+        } else {
+          tc_commit_if(leader, smem_u32(odone + g));
         }
-        if (more) next_slot();
       }
       // nothing of this warp's may still be running when TMEM is freed
-      tc_commit_if(leader, smem_u32(done));
-      mbar_wait(smem_u32(done), 0u, nullptr);
+      tc_commit_if(leader, smem_u32(done + g));
+      mbar_wait(smem_u32(done + g), 0u, nullptr);
     } else if (warp == kProd || warp == kProd + 1) {
       // ------------------------------------------------------------ loads
       const int v = warp - kProd;
@@ -380,10 +446,9 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
         qk *= p.k_scale[static_cast<int64_t>(b) * p.scale_stride + h];
         v_mult = p.v_scale[static_cast<int64_t>(b) * p.scale_stride + h];
       }
-      const float slope = MODS && p.slopes != nullptr && row_ok ? p.slopes[h * G + r_in % G] * kLog2e : 0.f;
-      const bool cap = MODS && p.cap_log2 > 0.f, bias = MODS && p.slopes != nullptr;
+      const float slope = MODE == kBiased && row_ok ? p.slopes[h * G + r_in % G] * kLog2e : 0.f;
       // scores times ex_mult are log2 weights
-      const float ex_mult = MODS ? 1.f : qk;
+      const float ex_mult = MODE != kPlain ? 1.f : qk;
 
       const uint32_t lanes = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
       const uint32_t t_s = lanes + COL_S + grp * NK, t_o = lanes + COL_O + grp * D;
@@ -400,34 +465,35 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
           for (int c = 0; c < NK / 32; ++c) tmem_ld32(t_s + 32 * c, x + 32 * c);
           tmem_wait_ld();
           const int t0 = rg.tile(k0 + k) * NK;
-          if constexpr (MODS) {
-            if (cap) {
-#pragma unroll
-              for (int i = 0; i < NK; ++i) x[i] = capped(x[i] * qk, p.cap_log2);
-            } else {
-#pragma unroll
-              for (int i = 0; i < NK; ++i) x[i] *= qk;
-            }
-            if (bias) {
-              const float base = slope * static_cast<float>(t0 - pos);
-#pragma unroll
-              for (int i = 0; i < NK; ++i) x[i] += fmaf(slope, static_cast<float>(i), base);
-            }
-          }
           const bool whole = (t0 + NK - 1 <= pos && t0 >= lo) || t0 + NK <= pf;
-          if (!__all_sync(kFull, whole)) {
-            // bit i of word w: key t0 + 32 w + i is seen
+          const bool masked = !__all_sync(kFull, whole);
+          uint32_t see[NK / 32];  // bit i of word w: key t0 + 32 w + i is seen
+          if (masked) {
             auto below = [&](int n, int w) {  // the first n keys of the tile
               n -= 32 * w;
               return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
             };
 #pragma unroll
-            for (int w = 0; w < NK / 32; ++w) {
-              const uint32_t see = (below(pos - t0 + 1, w) & ~below(lo - t0, w)) | below(pf - t0, w);
+            for (int w = 0; w < NK / 32; ++w)
+              see[w] = (below(pos - t0 + 1, w) & ~below(lo - t0, w)) | below(pf - t0, w);
+          }
+          if (MODE == kCapped || (MODE == kBiased && p.cap_log2 > 0.f)) cap_scores(x, qk, p.cap_log2, masked, see);
+          if constexpr (MODE == kBiased) {
+            const float mult = p.cap_log2 > 0.f ? 1.f : qk, base = slope * static_cast<float>(t0 - pos);
+            const float2 mult2 = make_float2(mult, mult), slope2 = make_float2(slope, slope);
+            const float2 base2 = make_float2(base, base);
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((see >> i) & 1u)) x[32 * w + i] = -CUDART_INF_F;
+            for (int i = 0; i < NK; i += 2) {
+              const float2 at = make_float2(static_cast<float>(i), static_cast<float>(i + 1));
+              const float2 z = __ffma2_rn(make_float2(x[i], x[i + 1]), mult2, __ffma2_rn(slope2, at, base2));
+              x[i] = z.x;
+              x[i + 1] = z.y;
             }
+          }
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < NK; ++i)
+              if (!((see[i / 32] >> (i % 32)) & 1u)) x[i] = -CUDART_INF_F;
           }
           float mt;
           {
@@ -475,7 +541,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float2 xx = make_float2(x[32 * c + 2 * i], x[32 * c + 2 * i + 1]);
-              const float2 e = MODS ? __fadd2_rn(xx, neg_mu) : __ffma2_rn(xx, mult2, neg_mu);
+              const float2 e = MODE != kPlain ? __fadd2_rn(xx, neg_mu) : __ffma2_rn(xx, mult2, neg_mu);
               const float2 pp = make_float2(fast_exp2(e.x), fast_exp2(e.y));
               ls[i & 1] = __fadd2_rn(ls[i & 1], pp);
               hi[i] = FP8 ? pack_f16x2(pp.x, pp.y) : pack_bf16x2(pp.x, pp.y);
@@ -571,9 +637,9 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
   }
 }
 
-template <int D, bool FP8, bool MODS>
+template <int D, bool FP8, int MODE>
 cudaError_t launch_tc_t(const ChunkParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
-  auto kern = chunk_tc_kernel<D, FP8, MODS>;
+  auto kern = chunk_tc_kernel<D, FP8, MODE>;
   // at least 120 KB: one CTA per SM (it holds all 512 TMEM columns)
   constexpr int smem = TcShape<D, FP8>::BYTES > 120 * 1024 ? TcShape<D, FP8>::BYTES : 120 * 1024;
   static int configured[64] = {};
@@ -586,8 +652,9 @@ cudaError_t launch_tc_t(const ChunkParams& p, const CUtensorMap& tk, const CUten
 
 template <int D, bool FP8>
 cudaError_t launch_tc_m(const ChunkParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
-  return p.cap_log2 > 0.f || p.slopes != nullptr ? launch_tc_t<D, FP8, true>(p, tk, tv, stream)
-                                                 : launch_tc_t<D, FP8, false>(p, tk, tv, stream);
+  if (p.slopes != nullptr) return launch_tc_t<D, FP8, kBiased>(p, tk, tv, stream);
+  if (p.cap_log2 > 0.f) return launch_tc_t<D, FP8, kCapped>(p, tk, tv, stream);
+  return launch_tc_t<D, FP8, kPlain>(p, tk, tv, stream);
 }
 
 }  // namespace

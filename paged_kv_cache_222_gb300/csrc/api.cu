@@ -155,6 +155,26 @@ pkv_status make_cache_tmap(CUtensorMap* tm, const void* base, const pkv_cache_de
   return PKV_OK;
 }
 
+// 4-D view (d, head of the group, KV head, token) of the queries [T, H_q, D]: a
+// box is the rows (token, head) of `box_tokens` tokens and one KV head, 128
+// bytes (64 columns) of each, 128B-swizzled; tokens past T read as zeros.
+pkv_status make_query_tmap(CUtensorMap* tm, const void* q, const pkv_cache_desc& c, int64_t n_tokens, int group,
+                           int box_tokens) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  const cuuint64_t row = static_cast<cuuint64_t>(c.head_dim) * 2;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(group),
+                        static_cast<cuuint64_t>(c.num_kv_heads), static_cast<cuuint64_t>(n_tokens)};
+  cuuint64_t strides[3] = {row, row * group, row * group * c.num_kv_heads};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(group), 1, static_cast<cuuint32_t>(box_tokens)};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled(q) failed (%d)", int(r));
+  return PKV_OK;
+}
+
 // ------------------------------------------------------------ trace
 
 struct TraceRec {
@@ -1351,6 +1371,11 @@ extern "C" pkv_status pkv_chunk_attention(
   const int32_t group = num_q_heads / c.num_kv_heads;
   CUtensorMap tk, tv;
   const bool small = pl.workers == 1;
+  CUtensorMap tq = {};
+  if (!small) {
+    s = make_query_tmap(&tq, q, c, n_tokens, group, chunk_tile_q(max_q_len, group));
+    if (s != PKV_OK) return s;
+  }
   const int box = small ? pkv::kTileTokens : c.block_size;  // token rows per TMA box
   s = make_cache_tmap(&tk, k_cache, c, box);
   if (s != PKV_OK) return s;
@@ -1394,7 +1419,7 @@ extern "C" pkv_status pkv_chunk_attention(
   p.err = st->err;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = traced(pkv::kKindChunk, cs, [&] {
-    return small ? pkv::launch_chunk_small(p, tk, tv, cs) : pkv::launch_chunk_tc(p, tk, tv, cs);
+    return small ? pkv::launch_chunk_small(p, tk, tv, cs) : pkv::launch_chunk_tc(p, tq, tk, tv, cs);
   });
   if (e == cudaSuccess && pl.max_splits > 1)
     e = traced(pkv::kKindCombine, cs, [&] {

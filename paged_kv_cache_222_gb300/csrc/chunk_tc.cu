@@ -43,15 +43,38 @@ struct TcShape {
   static constexpr int TILE = HALVES * HALFB;      // a 16-bit K or V tile
   static constexpr int RAW = NK * D;               // an E4M3 K or V tile
   static constexpr int NS = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
-  static constexpr int NR = FP8 ? (D == 128 ? 4 : 8) : 0;
-  static constexpr int NBARS = 2 * NS + 2 * NR + 4 * GROUPS + 2;
-  static constexpr int BYTES = QBYTES + NS * TILE + NR * RAW + NBARS * 8 + 16 + 1024;
+  static constexpr int NR = FP8 ? (D == 128 ? 3 : 6) : 0;
+  static constexpr int STAGE = 32 * 64;            // output staging of a softmax warp: 64 bytes of its rows
+  static constexpr int RU = 4;                     // units in flight between the roles
+  static constexpr int UNIT = 20;                  // words of one
+  static constexpr int NBARS = 2 * NS + 2 * NR + 3 * GROUPS + 5 + 2 * RU + GROUPS;
+  static constexpr int BYTES = QBYTES + NS * TILE + NR * RAW + 8 * STAGE + 16 + NBARS * 8 + RU * UNIT * 4 + 16 + 1024;
   static_assert(BYTES <= 232448, "shared memory per CTA");
   static constexpr int THREADS = FP8 ? 512 : 384;
   // registers: 384 x 168 or 512 x 128 at launch
   static constexpr int REGS_SOFTMAX = FP8 ? 176 : 200;
   static constexpr int REGS_OTHER = FP8 ? 80 : 104;
   static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * (FP8 ? 128 : 168), "register file");
+};
+
+// One work unit as the roles read it from shared memory.
+struct TcUnit {
+  int b;            // sequence, -1: no unit is left
+  int h;            // KV head
+  int row0;         // first query token (row of q and out)
+  int rows;         // rows of the tile: tokens x group
+  int pos0;         // position of the first token
+  int ctx, prefix, lo, hi, na, b0;
+  int k0, ntile;    // tiles [k0, k0 + ntile) of the row tile's visible ones
+  int split, nsplit;
+  int k_bits, v_bits;  // scales of the sequence's head (binary32 words)
+  __device__ __forceinline__ int tile(int k) const { return k0 + k < na ? k0 + k : b0 + (k0 + k - na); }
+  __device__ __forceinline__ bool sees(int t0, int t1) const { return t0 < prefix || (t0 < hi && t1 > lo); }
+  // rows of V's last tile past the sequence's end that share a block with its last token
+  __device__ __forceinline__ int tail_first(int nk) const { return ctx - tile(ntile - 1) * nk; }
+  __device__ __forceinline__ bool v_tail(int nk, int block_size) const {
+    return ntile > 0 && tail_first(nk) < nk && tail_first(nk) % block_size != 0;
+  }
 };
 
 // What a score is besides scale * q.k: nothing; capped; biased (capped or not).
@@ -126,69 +149,92 @@ __device__ __forceinline__ void cap_scores(float (&x)[N], float w_mult, float ca
   }
 }
 
+// The unit that block index (x, y) stands for; false if it stands for none (a
+// tile number no sequence uses, a split past the tile's keys).  A whole warp.
+template <int NK, bool FP8>
+__device__ __forceinline__ bool tc_unit(const ChunkParams& p, int x, int y, TcUnit& u) {
+  u.h = x % p.num_kv_heads;
+  const int t = x / p.num_kv_heads;
+  u.b = warp_search(p.batch, t, [&](int i) { return chunk_tile_base(p, i); });
+  const ChunkSeq sq = chunk_seq(p, u.b, (threadIdx.x & 31) == 0 && y == 0 && u.h == 0);
+  // longest first within a sequence: its last tokens see the most keys
+  const int ntq = (sq.n + p.tile_q - 1) / p.tile_q;
+  const int tile = ntq - 1 - (t - chunk_tile_base(p, u.b));
+  if (tile < 0 || tile >= ntq) return false;
+  const int i0 = tile * p.tile_q, i1 = min(sq.n, i0 + p.tile_q) - 1;
+  const ChunkRange rg = chunk_range<NK>(p, sq, i0, i1);
+  const int per_split = p.split_tokens / NK;
+  u.nsplit = max(1, (rg.n + per_split - 1) / per_split);
+  u.split = y;
+  if (u.split >= u.nsplit) return false;
+  u.row0 = sq.start + i0;
+  u.rows = (i1 - i0 + 1) * p.group;
+  u.pos0 = sq.ctx - sq.n + i0;
+  u.ctx = sq.ctx;
+  u.prefix = rg.prefix;
+  u.lo = rg.lo;
+  u.hi = rg.hi;
+  u.na = rg.na;
+  u.b0 = rg.b0;
+  u.k0 = u.split * per_split;
+  u.ntile = min(rg.n - u.k0, per_split);
+  u.k_bits = u.v_bits = 0;
+  if constexpr (FP8) {
+    u.k_bits = __float_as_int(p.k_scale[static_cast<int64_t>(u.b) * p.scale_stride + u.h]);
+    u.v_bits = __float_as_int(p.v_scale[static_cast<int64_t>(u.b) * p.scale_stride + u.h]);
+  }
+  return true;
+}
+
 template <int D, bool FP8, int MODE>
 __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
-    chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                    const ChunkParams p) {
+    chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                    const __grid_constant__ CUtensorMap tmap_v, const ChunkParams p) {
   using C = TcShape<D, FP8>;
-  constexpr int M = C::M, NK = C::NK, NS = C::NS, NR = C::NR, GROUPS = C::GROUPS;
+  constexpr int M = C::M, NK = C::NK, NS = C::NS, NR = C::NR, GROUPS = C::GROUPS, RU = C::RU;
   constexpr uint32_t COL_S = 0, COL_O = GROUPS * NK;  // + g * NK, + g * D
   constexpr uint32_t IDESC_S = FP8 ? idesc_f16(M, NK, false) : idesc_bf16(M, NK, false);
   constexpr uint32_t IDESC_PV = FP8 ? idesc_f16(M, D, true) : idesc_bf16(M, D, true);
-  constexpr int kMma = 8, kProd = 9, kConv = 12;
+  constexpr int kMma = 8, kLoadK = 9, kLoadV = 10, kMma1 = 11, kConv = 12;
+  constexpr int READERS = 8 + 2 + 1 + (FP8 ? 4 : 0);  // warps that read a unit
   static_assert(COL_O + GROUPS * D <= 512, "TMEM columns");
+  static_assert(sizeof(TcUnit) <= C::UNIT * 4, "unit slot");
 
   // the warp number as a broadcast: roles branch uniformly
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
   const int G = p.group, H_q = p.num_q_heads;
-  wait_prior_grid();
-
-  // ---- the CTA's row tile: number t of the sequences' tiles, longest first
-  // within a sequence (its last tokens see the most keys)
-  const int h = blockIdx.x % p.num_kv_heads;
-  const int t = blockIdx.x / p.num_kv_heads;
-  const int b = warp_search(p.batch, t, [&](int i) { return chunk_tile_base(p, i); });
-  const ChunkSeq sq = chunk_seq(p, b, tid == 0 && blockIdx.y == 0 && h == 0);
-  const int ntq = (sq.n + p.tile_q - 1) / p.tile_q;
-  const int tile = ntq - 1 - (t - chunk_tile_base(p, b));
-  if (tile < 0 || tile >= ntq) return;
-  const int i0 = tile * p.tile_q, i1 = min(sq.n, i0 + p.tile_q) - 1;
-  const int rows = (i1 - i0 + 1) * G;
-  const ChunkRange rg = chunk_range<NK>(p, sq, i0, i1);
-  const int per_split = p.split_tokens / NK;
-  const int nsplit = max(1, (rg.n + per_split - 1) / per_split);
-  const int split = blockIdx.y;
-  if (split >= nsplit) return;
-  const int k0 = split * per_split;
-  const int ntile = min(rg.n - k0, per_split);
-  const int ng = rows > M ? 2 : 1;
-  // the sequence ends inside a block of the last tile (later tiles hold later keys)
-  const int t_last = ntile > 0 ? rg.tile(k0 + ntile - 1) * NK : 0;
-  const bool v_tail = ntile > 0 && sq.ctx - t_last < NK && (sq.ctx - t_last) % p.block_size != 0;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* q_sm = smem;                              // half hf, row r at hf * QHALF + r * 128
-  uint8_t* ring = smem + C::QBYTES;                  // K(k) is item 2k, V(k) item 2k + 1
-  uint8_t* raw = ring + NS * C::TILE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(raw + NR * C::RAW);
+  uint8_t* ring = smem + C::QBYTES;                  // 16-bit K and V tiles, alternately
+  uint8_t* raw = ring + NS * C::TILE;                // E4M3 K and V tiles, alternately
+  uint8_t* s_stage = raw + NR * C::RAW;
+  uint8_t* s_clc = s_stage + 8 * C::STAGE;           // 16 bytes
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_clc + 16);
   uint64_t* empty = full + NS;
   uint64_t* rfull = empty + NS;
   uint64_t* rempty = rfull + NR;
-  uint64_t* sfull = rempty + NR;    // [GROUPS]: S_g(k) is in TMEM
-  uint64_t* pfull = sfull + GROUPS;  // [GROUPS]: P_g(k) is in TMEM
-  uint64_t* odone = pfull + GROUPS;  // [GROUPS]: O_g is complete
-  uint64_t* qfull = odone + GROUPS;
-  uint64_t* vfix = qfull + 1;       // the last V tile's rows past the end are zeros
-  uint64_t* done = vfix + 1;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + GROUPS);
+  uint64_t* sfull = rempty + NR;     // [GROUPS]: S_g of the next tile is in TMEM
+  uint64_t* pfull = sfull + GROUPS;  // [GROUPS]: P_g is in TMEM
+  uint64_t* odone = pfull + GROUPS;  // [GROUPS]: O_g of the unit is complete
+  uint64_t* qfull = odone + GROUPS;  // Q of the unit is in shared memory
+  uint64_t* qready = qfull + 1;      // ... as f16 (E4M3 caches)
+  uint64_t* qempty = qready + 1;     // every S of the unit has read it
+  uint64_t* vfix = qempty + 1;       // the last V tile's rows past the end are zeros
+  uint64_t* clc = vfix + 1;          // the next unit's block index has arrived
+  uint64_t* ufull = clc + 1;         // [RU]
+  uint64_t* uempty = ufull + RU;     // [RU]
+  uint64_t* done = uempty + RU;      // [GROUPS]
+  uint32_t* s_unit = reinterpret_cast<uint32_t*>(done + GROUPS);
+  uint32_t* s_tmem = s_unit + RU * C::UNIT;
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(smem_u32(full + s), FP8 ? 4 : 1);
-      mbar_init(smem_u32(empty + s), ng);
+      mbar_init(smem_u32(empty + s), GROUPS);
     }
     for (int s = 0; s < NR; ++s) {
       mbar_init(smem_u32(rfull + s), 1);
@@ -200,10 +246,18 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
       mbar_init(smem_u32(odone + g), 1);
       mbar_init(smem_u32(done + g), 1);
     }
-    mbar_init(smem_u32(qfull), 4 * ng);
+    mbar_init(smem_u32(qfull), 1);
+    mbar_init(smem_u32(qready), 4);
+    mbar_init(smem_u32(qempty), GROUPS);
     mbar_init(smem_u32(vfix), 1);
+    mbar_init(smem_u32(clc), 1);
+    for (int i = 0; i < RU; ++i) {
+      mbar_init(smem_u32(ufull + i), 1);
+      mbar_init(smem_u32(uempty + i), READERS);
+    }
     *s_abort = 0;
     fence_mbar_init();
+    prefetch_tmap(&tmap_q);
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
   }
@@ -215,23 +269,47 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = __shfl_sync(kFull, *s_tmem, 0);
+  wait_prior_grid();
+
+  auto wait = [&](uint64_t* bar, int phase) {  // a whole warp
+    return __all_sync(kFull, wait_or_abort(smem_u32(bar), static_cast<uint32_t>(phase & 1), p.err, s_abort)) != 0;
+  };
+  // Unit number n of this CTA; false when none is left (or the CTA aborts).  A
+  // whole warp; every value is the same in all its lanes.
+  auto read_unit = [&](int n, TcUnit& u) {
+    const int slot = n % RU;
+    if (!wait(ufull + slot, n / RU)) return false;
+    constexpr int W = sizeof(TcUnit) / 4;
+    const uint32_t w = lane < W ? s_unit[slot * C::UNIT + lane] : 0u;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(uempty + slot));
+    uint32_t* to = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+    for (int i = 0; i < W; ++i) to[i] = __shfl_sync(kFull, w, i);
+    return u.b >= 0;
+  };
 
   if (warp >= kMma) {
     regs_dec<C::REGS_OTHER>();
-    if (warp == kMma || warp == kMma + 3) {
+    if (warp == kMma || warp == kMma1) {
       // ------------------------------------------------------------ products
       // The whole warp walks this role, one lane's products are issued: see
       // tc_mma_ss_if.
       const int g = warp == kMma ? 0 : 1;
       const uint32_t leader = elect_one();
-      const int nt = __shfl_sync(kFull, g < ng ? ntile : 0, 0);
       const uint32_t ring0 = __shfl_sync(kFull, smem_u32(ring), 0), q0 = __shfl_sync(kFull, smem_u32(q_sm), 0);
       const uint32_t c_s = tbase + COL_S + g * NK, c_o = tbase + COL_O + g * D;
-      auto wait = [&](uint64_t* bar, int phase) {
-        return __all_sync(kFull, wait_or_abort(smem_u32(bar), static_cast<uint32_t>(phase & 1), p.err, s_abort)) != 0;
-      };
       const uint64_t a0 = smem_desc_sw128(q0 + g * M * 128, 0, 1024);
-      auto issue_s = [&](int slot) {
+      int slot = 0, use = 0;  // ring slot of the next item, and its use number
+      int pk = 0, tails = 0;  // this group's tiles so far; units with a zeroed tail so far
+      bool ok = true;
+      auto next_slot = [&]() {
+        if (++slot == NS) {
+          slot = 0;
+          ++use;
+        }
+      };
+      auto issue_s = [&]() {  // S of the K tile in `slot`, which then goes back to its loader
         const uint64_t b0 = smem_desc_sw128(ring0 + slot * C::TILE, 0, 1024);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)  // descriptor addresses are in 16-byte units
@@ -239,59 +317,70 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
                        b0 + ((kk / 4) * C::HALFB + (kk % 4) * 32) / 16, IDESC_S, kk > 0 ? 1u : 0u);
         tc_commit_if(leader, smem_u32(sfull + g));
         tc_commit_if(leader, smem_u32(empty + slot));
-      };
-      bool ok = wait(qfull, 0);
-      int slot = 0, use = 0;  // ring slot of the next item, and its use number
-      auto next_slot = [&]() {
-        if (++slot == NS) {
-          slot = 0;
-          ++use;
-        }
-      };
-      if (nt > 0 && ok) {
-        ok = wait(full, 0);
-        if (ok) {
-          tc_fence_after();
-          issue_s(0);
-        }
         next_slot();
-      }
-      for (int k = 0; k < nt && ok; ++k) {
-        const int vslot = slot;
-        ok = wait(full + vslot, use);
-        if (!ok) break;
-        if (!FP8 && k == nt - 1 && v_tail) {  // its loader has zeroed the rows past the sequence's end
-          ok = wait(vfix, 0);
+      };
+      TcUnit u;
+      for (int n = 0; ok && read_unit(n, u); ++n) {
+        const bool tail = !FP8 && u.v_tail(NK, p.block_size);
+        if (g * M >= u.rows) {
+          // no rows of this group: its arrivals keep the ring's phases
+          ok = wait(FP8 ? qready : qfull, n);
+          tc_commit_if(leader, smem_u32(qempty));
+          for (int i = 0; i < 2 * u.ntile && ok; ++i) {
+            ok = wait(full + slot, use);
+            tc_commit_if(leader, smem_u32(empty + slot));
+            next_slot();
+          }
+          if (tail && ok) ok = wait(vfix, tails++);
+          continue;
+        }
+        ok = wait(FP8 ? qready : qfull, n);
+        if (ok && u.ntile > 0) {
+          ok = wait(full + slot, use);
           if (!ok) break;
+          tc_fence_after();
+          issue_s();
         }
-        next_slot();
-        const bool more = k + 1 < nt;
-        if (more) ok = wait(full + slot, use);  // K(k+1), ahead of the wait for P
-        const uint64_t v0 = smem_desc_sw128(ring0 + vslot * C::TILE, C::HALVES > 1 ? C::HALFB : 0, 1024);
-        ok = ok && wait(pfull + g, k);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < NK / 16; ++kk)  // MN-major V: 8-key groups 1024 B apart, column halves HALFB apart
-          tc_mma_ts_if(leader, c_o, c_s + kk * 8, v0 + kk * (2048 / 16), IDESC_PV, (k > 0 || kk > 0) ? 1u : 0u);
-        tc_commit_if(leader, smem_u32(empty + vslot));
-        if (more) {
-          issue_s(slot);
+        if (u.ntile <= 1) tc_commit_if(leader, smem_u32(qempty));
+        for (int k = 0; k < u.ntile && ok; ++k, ++pk) {
+          const int vslot = slot;
+          ok = wait(full + vslot, use);
+          if (!ok) break;
+          if (tail && k == u.ntile - 1) {  // its loader has zeroed the rows past the sequence's end
+            ok = wait(vfix, tails++);
+            if (!ok) break;
+          }
           next_slot();
-        } else {
-          tc_commit_if(leader, smem_u32(odone + g));
+          const bool more = k + 1 < u.ntile;
+          if (more) ok = wait(full + slot, use);  // K(k+1), ahead of the wait for P
+          const uint64_t v0 = smem_desc_sw128(ring0 + vslot * C::TILE, C::HALVES > 1 ? C::HALFB : 0, 1024);
+          ok = ok && wait(pfull + g, pk);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < NK / 16; ++kk)  // MN-major V: 8-key groups 1024 B apart, column halves HALFB apart
+            tc_mma_ts_if(leader, c_o, c_s + kk * 8, v0 + kk * (2048 / 16), IDESC_PV, (k > 0 || kk > 0) ? 1u : 0u);
+          tc_commit_if(leader, smem_u32(empty + vslot));
+          if (more) {
+            issue_s();
+            if (k + 2 == u.ntile) tc_commit_if(leader, smem_u32(qempty));  // the unit's last S
+          } else {
+            tc_commit_if(leader, smem_u32(odone + g));
+          }
         }
       }
       // nothing of this warp's may still be running when TMEM is freed
       tc_commit_if(leader, smem_u32(done + g));
       mbar_wait(smem_u32(done + g), 0u, nullptr);
-    } else if (warp == kProd || warp == kProd + 1) {
+    } else if (warp == kLoadK || warp == kLoadV) {
       // ------------------------------------------------------------ loads
-      const int v = warp - kProd;
+      // The K loader also hands out the units: its own block index first, then
+      // those of CTAs that it keeps from starting.
+      const int v = warp == kLoadV ? 1 : 0;
       const CUtensorMap* tmap = v ? &tmap_v : &tmap_k;
       constexpr int ROWB = FP8 ? D : 128;              // bytes of a box row
       constexpr int BYTES = FP8 ? C::RAW : C::TILE;
-      const int nring = FP8 ? NR : NS;
+      constexpr int NRING = FP8 ? NR : NS;
       const uint32_t base = smem_u32(FP8 ? raw : ring);
       uint64_t* bfull = FP8 ? rfull : full;
       uint64_t* bempty = FP8 ? rempty : empty;
@@ -299,50 +388,103 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
       const int nbox = per_half * (FP8 ? 1 : C::HALVES);
       const int hf = lane / per_half, bi = lane % per_half;
       const uint32_t off = hf * C::HALFB + bi * p.block_size * ROWB;
-      const int32_t* tbl = p.block_tables + static_cast<int64_t>(b) * p.max_blocks;
-      // the block this lane's box of tile k holds; blocks that no row sees are
-      // not looked up and read as zeros (outside the tensor map)
-      auto block_of = [&](int k) {
-        int phys = -1;
-        if (lane < nbox && k < ntile) {
-          const int t0 = rg.tile(k0 + k) * NK + bi * p.block_size;
-          if (rg.sees(t0, t0 + p.block_size)) {
-            phys = tbl[t0 / p.block_size];
-            if (phys < 0 || phys >= p.num_blocks) {
-              if (v == 0 && hf == 0) record_error(p.err, kDevErrBlockId);
-              phys = -1;
+      int item = v;  // K of tile j is item 2 j of the ring, V item 2 j + 1
+      int asked = 0;
+      bool ok = true;
+      uint32_t bx = blockIdx.x, by = blockIdx.y;
+      TcUnit u;
+      for (int n = 0; ok; ++n) {
+        if (v == 0) {
+          // the next unit there is, published to the other warps
+          bool have = n == 0;
+          u.b = -1;
+          while (ok) {
+            if (!have) {
+              ok = wait(clc, asked - 1);
+              if (!ok) break;
+              have = clc_answer(smem_u32(s_clc), bx, by);
+              if (!have) break;  // none is left, and none is asked for again
+            }
+            // one answer ahead, so that it has arrived when it is wanted
+            __syncwarp();
+            if (lane == 0) {
+              fence_proxy_async_smem();  // the last answer has been read
+              mbar_arrive_expect_tx(smem_u32(clc), 16);
+              clc_ask(smem_u32(s_clc), smem_u32(clc));
+            }
+            __syncwarp();
+            ++asked;
+            if (tc_unit<NK, FP8>(p, static_cast<int>(bx), static_cast<int>(by), u)) break;
+            u.b = -1;
+            have = false;
+          }
+          if (!ok) u.b = -1;
+          const int slot = n % RU;
+          if (n >= RU) ok = wait(uempty + slot, n / RU - 1) && ok;
+          constexpr int W = sizeof(TcUnit) / 4;
+          const uint32_t* from = reinterpret_cast<const uint32_t*>(&u);
+          if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) s_unit[slot * C::UNIT + i] = from[i];
+            mbar_arrive(smem_u32(ufull + slot));  // releases the slot's values to the readers
+          }
+          __syncwarp();
+          if (u.b < 0) break;
+        } else {
+          if (!read_unit(n, u)) break;
+          // Q of the unit, once every S of the last one has read its own
+          if (n > 0) ok = wait(qempty, n - 1);
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t bytes = static_cast<uint32_t>(p.tile_q * G * 128);
+            fence_proxy_async_smem();
+            mbar_arrive_expect_tx(smem_u32(qfull), C::HALVES * bytes);
+#pragma unroll
+            for (int hh = 0; hh < C::HALVES; ++hh)  // rows (token, head), 128 bytes each
+              tma_load_4d(smem_u32(q_sm) + hh * C::QHALF, &tmap_q, smem_u32(qfull), hh * 64, 0, u.h, u.row0);
+          }
+          __syncwarp();
+        }
+        const int32_t* tbl = p.block_tables + static_cast<int64_t>(u.b) * p.max_blocks;
+        // the block this lane's box of tile k holds; blocks that no row sees are
+        // not looked up and read as zeros (outside the tensor map)
+        auto block_of = [&](int k) {
+          int phys = -1;
+          if (lane < nbox && k < u.ntile) {
+            const int t0 = u.tile(k) * NK + bi * p.block_size;
+            if (u.sees(t0, t0 + p.block_size)) {
+              phys = tbl[t0 / p.block_size];
+              if (phys < 0 || phys >= p.num_blocks) {
+                if (v == 0 && hf == 0) record_error(p.err, kDevErrBlockId);
+                phys = -1;
+              }
             }
           }
+          return phys;
+        };
+        int phys = block_of(0);
+        for (int k = 0; k < u.ntile; ++k, item += 2) {
+          const int s = item % NRING;
+          const int next = block_of(k + 1);
+          if (item >= NRING) ok = wait(bempty + s, item / NRING - 1);
+          if (!ok) break;
+          const uint32_t bar = smem_u32(bfull + s);
+          if (lane == 0) {
+            fence_proxy_async_smem();
+            mbar_arrive_expect_tx(bar, BYTES);
+          }
+          __syncwarp();
+          if (lane < nbox) tma_load_4d(base + s * BYTES + off, tmap, bar, hf * 64, 0, u.h, phys);
+          phys = next;
         }
-        return phys;
-      };
-      int phys = block_of(0);
-      int issued = 0;
-      for (int k = 0; k < ntile; ++k) {
-        const int item = 2 * k + v, s = item % nring;
-        const int next = block_of(k + 1);
-        bool go = true;
-        if (lane == 0 && item >= nring)
-          go = wait_or_abort(smem_u32(bempty + s), static_cast<uint32_t>((item / nring - 1) & 1), p.err, s_abort);
-        if (!__shfl_sync(kFull, go ? 1 : 0, 0)) break;
-        const uint32_t bar = smem_u32(bfull + s);
-        if (lane == 0) {
-          fence_proxy_async_smem();
-          mbar_arrive_expect_tx(bar, BYTES);
-        }
-        __syncwarp();
-        if (lane < nbox) tma_load_4d(base + s * BYTES + off, tmap, bar, hf * 64, 0, h, phys);
-        phys = next;
-        issued = k + 1;
-      }
-      if (!FP8 && v == 1 && v_tail && issued == ntile) {
-        // Rows of the last block past the sequence's end may hold anything
-        // (NaN included): zero them once they have landed, P is 0 there.  Whole
-        // blocks past it were loaded as zeros.
-        const int item = 2 * (ntile - 1) + 1, s = item % nring;
-        bool ok = wait_or_abort(smem_u32(bfull + s), static_cast<uint32_t>((item / nring) & 1), p.err, s_abort);
-        if (__all_sync(kFull, ok)) {
-          const int first = sq.ctx - rg.tile(k0 + ntile - 1) * NK;
+        if (!FP8 && v == 1 && ok && u.v_tail(NK, p.block_size)) {
+          // Rows of the last block past the sequence's end may hold anything
+          // (NaN included): zero them once they have landed, P is 0 there.  Whole
+          // blocks past it were loaded as zeros.
+          const int last = item - 2, s = last % NRING;
+          ok = wait(bfull + s, last / NRING);
+          if (!ok) break;
+          const int first = u.tail_first(NK);
           const int chunks = ((first + p.block_size - 1) / p.block_size * p.block_size - first) * 8;
           for (int c = lane; c < C::HALVES * chunks; c += 32) {
             const int hh = c / chunks, cc = c - hh * chunks;
@@ -355,108 +497,104 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
         }
       }
       if (lane == 0 && *s_abort) {  // the copies in flight land before the CTA leaves
-        for (int k = 0; k < issued; ++k) {
-          const int item = 2 * k + v;
-          if (item + nring < 2 * issued) continue;
-          mbar_wait(smem_u32(bfull + item % nring), static_cast<uint32_t>((item / nring) & 1), nullptr);
-        }
+        for (int i = item - 2; i >= 0 && i > item - 2 - NRING; i -= 2)
+          mbar_wait(smem_u32(bfull + i % NRING), static_cast<uint32_t>((i / NRING) & 1), nullptr);
+        if (v == 0 && asked > 0) mbar_wait(smem_u32(clc), static_cast<uint32_t>((asked - 1) & 1), nullptr);
       }
     } else if (FP8 && warp >= kConv) {
       // ------------------------------------------------------------ widening
-      // thread t: key t of the tile, 16 codes -> 32 bytes at a time
+      // of the unit's Q (bf16 -> f16, in place) and its K and V tiles (thread t:
+      // key t of the tile, 16 codes -> 32 bytes at a time)
       if constexpr (FP8) {
-        const int key = (warp - kConv) * 32 + lane;
+        const int t = (warp - kConv) * 32 + lane;
         constexpr int CH = D / 16;                     // 16-byte chunks of a raw row
-        const uint32_t rsw = D == 128 ? (key & 7) : ((key >> 1) & 3);
+        const uint32_t rsw = D == 128 ? (t & 7) : ((t >> 1) & 3);
+        int item = 0;
         bool ok = true;
-        for (int item = 0; item < 2 * ntile; ++item) {
-          const int rs = item % NR, s = item % NS;
-          ok = wait_or_abort(smem_u32(rfull + rs), static_cast<uint32_t>((item / NR) & 1), p.err, s_abort);
-          if (ok && item >= NS)
-            ok = wait_or_abort(smem_u32(empty + s), static_cast<uint32_t>((item / NS - 1) & 1), p.err, s_abort);
-          if (!__all_sync(kFull, ok)) break;
-          const uint8_t* src = raw + rs * C::RAW + key * D;
-          uint8_t* dst = ring + s * C::TILE + key * 128;
-          // rows past the sequence's end may hold anything: zeros instead
-          const bool live = rg.tile(k0 + (item >> 1)) * NK + key < sq.ctx;
-#pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            uint4 w = *reinterpret_cast<const uint4*>(src + ((c ^ rsw) << 4));
-            if (!live) w = make_uint4(0u, 0u, 0u, 0u);
-            uint4 a, e;
-            a.x = e4m3x2_to_f16x2(static_cast<uint16_t>(w.x & 0xFFFFu));
-            a.y = e4m3x2_to_f16x2(static_cast<uint16_t>(w.x >> 16));
-            a.z = e4m3x2_to_f16x2(static_cast<uint16_t>(w.y & 0xFFFFu));
-            a.w = e4m3x2_to_f16x2(static_cast<uint16_t>(w.y >> 16));
-            e.x = e4m3x2_to_f16x2(static_cast<uint16_t>(w.z & 0xFFFFu));
-            e.y = e4m3x2_to_f16x2(static_cast<uint16_t>(w.z >> 16));
-            e.z = e4m3x2_to_f16x2(static_cast<uint16_t>(w.w & 0xFFFFu));
-            e.w = e4m3x2_to_f16x2(static_cast<uint16_t>(w.w >> 16));
-            uint8_t* to = dst + (c / 4) * C::HALFB;
-            *reinterpret_cast<uint4*>(to + (((2 * (c % 4)) ^ (key & 7)) << 4)) = a;
-            *reinterpret_cast<uint4*>(to + (((2 * (c % 4) + 1) ^ (key & 7)) << 4)) = e;
+        TcUnit u;
+        for (int n = 0; ok && read_unit(n, u); ++n) {
+          ok = wait(qfull, n);
+          if (!ok) break;
+          for (int i = t; i < C::HALVES * u.rows * 8; i += 128) {
+            const int hh = i / (u.rows * 8);
+            uint4* at = reinterpret_cast<uint4*>(q_sm + hh * C::QHALF + (i - hh * u.rows * 8) * 16);
+            uint4 w = *at;
+            w.x = pack_f16x2(bf16lo_to_f32(w.x), bf16hi_to_f32(w.x));
+            w.y = pack_f16x2(bf16lo_to_f32(w.y), bf16hi_to_f32(w.y));
+            w.z = pack_f16x2(bf16lo_to_f32(w.z), bf16hi_to_f32(w.z));
+            w.w = pack_f16x2(bf16lo_to_f32(w.w), bf16hi_to_f32(w.w));
+            *at = w;
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(smem_u32(full + s));
-            mbar_arrive(smem_u32(rempty + rs));
+          if (lane == 0) mbar_arrive(smem_u32(qready));
+          for (int i = 0; i < 2 * u.ntile; ++i, ++item) {
+            const int rs = item % NR, s = item % NS;
+            ok = wait(rfull + rs, item / NR);
+            if (ok && item >= NS) ok = wait(empty + s, item / NS - 1);
+            if (!ok) break;
+            const uint8_t* src = raw + rs * C::RAW + t * D;
+            uint8_t* dst = ring + s * C::TILE + t * 128;
+            // rows past the sequence's end may hold anything: zeros instead
+            const bool live = u.tile(i >> 1) * NK + t < u.ctx;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+              uint4 w = *reinterpret_cast<const uint4*>(src + ((c ^ rsw) << 4));
+              if (!live) w = make_uint4(0u, 0u, 0u, 0u);
+              uint4 a, e;
+              a.x = e4m3x2_to_f16x2(static_cast<uint16_t>(w.x & 0xFFFFu));
+              a.y = e4m3x2_to_f16x2(static_cast<uint16_t>(w.x >> 16));
+              a.z = e4m3x2_to_f16x2(static_cast<uint16_t>(w.y & 0xFFFFu));
+              a.w = e4m3x2_to_f16x2(static_cast<uint16_t>(w.y >> 16));
+              e.x = e4m3x2_to_f16x2(static_cast<uint16_t>(w.z & 0xFFFFu));
+              e.y = e4m3x2_to_f16x2(static_cast<uint16_t>(w.z >> 16));
+              e.z = e4m3x2_to_f16x2(static_cast<uint16_t>(w.w & 0xFFFFu));
+              e.w = e4m3x2_to_f16x2(static_cast<uint16_t>(w.w >> 16));
+              uint8_t* to = dst + (c / 4) * C::HALFB;
+              *reinterpret_cast<uint4*>(to + (((2 * (c % 4)) ^ (t & 7)) << 4)) = a;
+              *reinterpret_cast<uint4*>(to + (((2 * (c % 4) + 1) ^ (t & 7)) << 4)) = e;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(smem_u32(full + s));
+              mbar_arrive(smem_u32(rempty + rs));
+            }
           }
         }
       }
     }
   } else {
     regs_inc<C::REGS_SOFTMAX>();
+    // -------------------------------------------------------------- softmax
     const int grp = warp >> 2;
-    if (grp < ng) {
-      // ------------------------------------------------------------ softmax
+    const uint32_t lanes = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t t_s = lanes + COL_S + grp * NK, t_o = lanes + COL_O + grp * D;
+    uint8_t* stage = s_stage + warp * C::STAGE;
+    int sk = 0, outs = 0;  // this group's tiles and its units with tiles so far
+    bool ok = true;
+    TcUnit u;
+    for (int n = 0; ok && read_unit(n, u); ++n) {
+      if (grp * M >= u.rows) continue;
       const int r_in = tid;                              // row of the tile
-      const bool row_ok = r_in < rows;
-      const bool warp_ok = warp * 32 < rows;             // some lane has a row
-      const int64_t orow = (static_cast<int64_t>(sq.start) + i0 + r_in / G) * H_q + h * G + r_in % G;
-      {  // this row of Q into shared memory, 128B-swizzled; f16 for E4M3 caches
-        const uint16_t* qr = row_ok ? static_cast<const uint16_t*>(p.q) + orow * D : nullptr;
-        uint4 w[D / 8];
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          w[c] = qr ? *reinterpret_cast<const uint4*>(qr + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          if constexpr (FP8) {
-            w[c].x = pack_f16x2(bf16lo_to_f32(w[c].x), bf16hi_to_f32(w[c].x));
-            w[c].y = pack_f16x2(bf16lo_to_f32(w[c].y), bf16hi_to_f32(w[c].y));
-            w[c].z = pack_f16x2(bf16lo_to_f32(w[c].z), bf16hi_to_f32(w[c].z));
-            w[c].w = pack_f16x2(bf16lo_to_f32(w[c].w), bf16hi_to_f32(w[c].w));
-          }
-          *reinterpret_cast<uint4*>(q_sm + (c >> 3) * C::QHALF + r_in * 128 + (((c & 7) ^ (r_in & 7)) << 4)) = w[c];
-        }
-        fence_proxy_async_smem();  // the tensor core reads Q through the async proxy
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(qfull));
-      }
+      const bool row_ok = r_in < u.rows;
+      const bool warp_ok = warp * 32 < u.rows;           // some lane has a row
+      const int tok = r_in / G, gh = r_in - tok * G;
       // what the row sees; a row past the tile's takes no mask (nothing of it
       // is ever written)
       constexpr int kFar = 0x3FFFFFFF;
-      const int pos = row_ok ? sq.ctx - sq.n + i0 + r_in / G : kFar;
+      const int pos = row_ok ? u.pos0 + tok : kFar;
       const int lo = row_ok && p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
-      const int pf = row_ok && pos >= 0 ? sq.prefix : 0;
+      const int pf = row_ok && pos >= 0 ? u.prefix : 0;
       constexpr float kLog2e = 1.4426950408889634f;
-      float qk = p.qk_log2, v_mult = 1.f;
-      if constexpr (FP8) {
-        qk *= p.k_scale[static_cast<int64_t>(b) * p.scale_stride + h];
-        v_mult = p.v_scale[static_cast<int64_t>(b) * p.scale_stride + h];
-      }
-      const float slope = MODE == kBiased && row_ok ? p.slopes[h * G + r_in % G] * kLog2e : 0.f;
+      const float qk = FP8 ? p.qk_log2 * __int_as_float(u.k_bits) : p.qk_log2;
+      const float slope = MODE == kBiased && row_ok ? p.slopes[u.h * G + gh] * kLog2e : 0.f;
       // scores times ex_mult are log2 weights
       const float ex_mult = MODE != kPlain ? 1.f : qk;
 
-      const uint32_t lanes = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-      const uint32_t t_s = lanes + COL_S + grp * NK, t_o = lanes + COL_O + grp * D;
-      const uint32_t b_sfull = smem_u32(sfull + grp), b_pfull = smem_u32(pfull + grp);
       float m_used = -CUDART_INF_F, lsum = 0.f;
-      bool ok = true;
-      for (int k = 0; k < ntile; ++k) {
-        ok = __all_sync(kFull, wait_or_abort(b_sfull, static_cast<uint32_t>(k & 1), p.err, s_abort));
+      for (int k = 0; k < u.ntile; ++k, ++sk) {
+        ok = wait(sfull + grp, sk);
         if (!ok) break;
         tc_fence_after();
         if (warp_ok) {
@@ -464,7 +602,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
 #pragma unroll
           for (int c = 0; c < NK / 32; ++c) tmem_ld32(t_s + 32 * c, x + 32 * c);
           tmem_wait_ld();
-          const int t0 = rg.tile(k0 + k) * NK;
+          const int t0 = u.tile(k) * NK;
           const bool whole = (t0 + NK - 1 <= pos && t0 >= lo) || t0 + NK <= pf;
           const bool masked = !__all_sync(kFull, whole);
           uint32_t see[NK / 32];  // bit i of word w: key t0 + 32 w + i is seen
@@ -553,32 +691,42 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(b_pfull);  // P(k) is in TMEM
+        if (lane == 0) mbar_arrive(smem_u32(pfull + grp));  // P is in TMEM
       }
-      if (ok && ntile > 0) ok = __all_sync(kFull, wait_or_abort(smem_u32(odone + grp), 0u, p.err, s_abort));
+      if (ok && u.ntile > 0) ok = wait(odone + grp, outs++);
       if (ok && warp_ok) {
-        // ---- O leaves through this warp's part of the Q region (every S of
-        // the group has completed), so that a store instruction writes whole
-        // rows: direct outputs as bf16 rows, pieces as binary32 in 64-column
-        // passes, both 128 bytes of a row per half
+        // ---- O leaves through the warp's staging, 64 bytes of its rows per
+        // pass, so that a store instruction writes whole 64-byte pieces: bf16
+        // outputs 32 columns at a time, binary32 pieces of split rows 16
         tc_fence_after();
-        const float inv = lsum > 0.f ? v_mult / lsum : 0.f;
-        const float mult = nsplit == 1 ? inv : v_mult;
-        auto stage = [&](int hf, int c) { return q_sm + hf * C::QHALF + r_in * 128 + ((c ^ (r_in & 7)) << 4); };
-        auto row_of = [&](int r) {                       // output row of tile row r
-          return (static_cast<int64_t>(sq.start) + i0 + r / G) * H_q + h * G + r % G;
+        const float inv = lsum > 0.f ? (FP8 ? __int_as_float(u.v_bits) / lsum : 1.f / lsum) : 0.f;
+        const bool direct = u.nsplit == 1;
+        const float mult = direct ? inv : (FP8 ? __int_as_float(u.v_bits) : 1.f);
+        // chunk c (16 bytes) of row r at r * 64 + ((c ^ (r / 2 % 4)) * 16): eight
+        // consecutive rows' chunks c lie in distinct banks
+        auto at = [&](int r, int c) { return stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4); };
+        // this lane stores chunk lane % 4 of rows lane / 4 + 8 i
+        auto row_of = [&](int r) {
+          const int rr = warp * 32 + r;
+          return (static_cast<int64_t>(u.row0) + rr / G) * H_q + u.h * G + rr % G;
         };
-        if (nsplit == 1) {
+        int64_t to[4];
 #pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            float o[32];
-            if (ntile > 0) {
-              tmem_ld32(t_o + c0, o);
-              tmem_wait_ld();
-            } else {
+        for (int i = 0; i < 4; ++i) {
+          const int r = (lane >> 2) + 8 * i;
+          to[i] = warp * 32 + r < u.rows ? (direct ? row_of(r) : row_of(r) * p.max_splits + u.split) : -1;
+        }
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = 0.f;
-            }
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          float o[32];
+          if (u.ntile > 0) {
+            tmem_ld32(t_o + c0, o);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+          }
+          if (direct) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint4 w;
@@ -586,45 +734,39 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
               w.y = pack_bf16x2(o[8 * i + 2] * mult, o[8 * i + 3] * mult);
               w.z = pack_bf16x2(o[8 * i + 4] * mult, o[8 * i + 5] * mult);
               w.w = pack_bf16x2(o[8 * i + 6] * mult, o[8 * i + 7] * mult);
-              *reinterpret_cast<uint4*>(stage(c0 / 64, (c0 % 64) / 8 + i)) = w;
-            }
-          }
-          __syncwarp();
-          constexpr int CPR = D / 8;                     // 16-byte chunks of an output row
-#pragma unroll
-          for (int i = 0; i < CPR; ++i) {
-            const int r = warp * 32 + (i * 32 + lane) / CPR, c = lane % CPR;
-            if (r < rows)
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row_of(r) * D + c * 8) =
-                  *reinterpret_cast<const uint4*>(q_sm + (c >> 3) * C::QHALF + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-          }
-        } else {
-          // 32 columns (128 bytes) of a row per pass, in the first half's rows
-#pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            float o[32];
-            tmem_ld32(t_o + c0, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float4*>(stage(0, i)) = make_float4(o[4 * i] * mult, o[4 * i + 1] * mult,
-                                                                    o[4 * i + 2] * mult, o[4 * i + 3] * mult);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = warp * 32 + i * 4 + (lane >> 3), c = lane & 7;
-              const float4 u = *reinterpret_cast<const float4*>(q_sm + r * 128 + ((c ^ (r & 7)) << 4));
-              if (r < rows)
-                *reinterpret_cast<float4*>(p.ws_o + (row_of(r) * p.max_splits + split) * D + c0 + c * 4) = u;
+              *reinterpret_cast<uint4*>(at(lane, i)) = w;
             }
             __syncwarp();
-          }
-          if (row_ok) {
-            float* ml = p.ws_ml + (orow * p.max_splits + split) * 2;
-            ml[0] = m_used;
-            ml[1] = lsum;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (to[i] >= 0)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + to[i] * D + c0 + (lane & 3) * 8) =
+                    *reinterpret_cast<const uint4*>(at((lane >> 2) + 8 * i, lane & 3));
+            __syncwarp();
+          } else {
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4*>(at(lane, i)) =
+                    make_float4(o[16 * hh + 4 * i] * mult, o[16 * hh + 4 * i + 1] * mult,
+                                o[16 * hh + 4 * i + 2] * mult, o[16 * hh + 4 * i + 3] * mult);
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (to[i] >= 0)
+                  *reinterpret_cast<float4*>(p.ws_o + to[i] * D + c0 + 16 * hh + (lane & 3) * 4) =
+                      *reinterpret_cast<const float4*>(at((lane >> 2) + 8 * i, lane & 3));
+              __syncwarp();
+            }
           }
         }
+        if (!direct && row_ok) {
+          float* ml = p.ws_ml + (row_of(lane) * p.max_splits + u.split) * 2;
+          ml[0] = m_used;
+          ml[1] = lsum;
+        }
+        tc_fence_before();  // O has been read: the next unit's products may overwrite it after P's hand-over
       }
     }
   }
@@ -638,7 +780,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
 }
 
 template <int D, bool FP8, int MODE>
-cudaError_t launch_tc_t(const ChunkParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
+cudaError_t launch_tc_t(const ChunkParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
   auto kern = chunk_tc_kernel<D, FP8, MODE>;
   // at least 120 KB: one CTA per SM (it holds all 512 TMEM columns)
   constexpr int smem = TcShape<D, FP8>::BYTES > 120 * 1024 ? TcShape<D, FP8>::BYTES : 120 * 1024;
@@ -647,23 +789,23 @@ cudaError_t launch_tc_t(const ChunkParams& p, const CUtensorMap& tk, const CUten
   if (e != cudaSuccess) return e;
   const int tiles = p.n_tokens / p.tile_q + p.batch;
   return launch_pdl(kern, dim3(tiles * p.num_kv_heads, p.max_splits), dim3(TcShape<D, FP8>::THREADS), smem, stream,
-                    tk, tv, p);
+                    tq, tk, tv, p);
 }
 
 template <int D, bool FP8>
-cudaError_t launch_tc_m(const ChunkParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
-  if (p.slopes != nullptr) return launch_tc_t<D, FP8, kBiased>(p, tk, tv, stream);
-  if (p.cap_log2 > 0.f) return launch_tc_t<D, FP8, kCapped>(p, tk, tv, stream);
-  return launch_tc_t<D, FP8, kPlain>(p, tk, tv, stream);
+cudaError_t launch_tc_m(const ChunkParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
+  if (p.slopes != nullptr) return launch_tc_t<D, FP8, kBiased>(p, tq, tk, tv, stream);
+  if (p.cap_log2 > 0.f) return launch_tc_t<D, FP8, kCapped>(p, tq, tk, tv, stream);
+  return launch_tc_t<D, FP8, kPlain>(p, tq, tk, tv, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_tc(const ChunkParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
+cudaError_t launch_chunk_tc(const ChunkParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
   const bool fp8 = p.cache_dtype == kE4M3;
   if (p.head_dim == 128)
-    return fp8 ? launch_tc_m<128, true>(p, tk, tv, stream) : launch_tc_m<128, false>(p, tk, tv, stream);
-  return fp8 ? launch_tc_m<64, true>(p, tk, tv, stream) : launch_tc_m<64, false>(p, tk, tv, stream);
+    return fp8 ? launch_tc_m<128, true>(p, tq, tk, tv, stream) : launch_tc_m<128, false>(p, tq, tk, tv, stream);
+  return fp8 ? launch_tc_m<64, true>(p, tq, tk, tv, stream) : launch_tc_m<64, false>(p, tq, tk, tv, stream);
 }
 
 }  // namespace pkv

@@ -256,8 +256,8 @@ cudaError_t launch_multi_query_tc(const DecodeParams& p, const CUtensorMap& tmap
 // kernel (row tiles of up to 256 rows) and the merge of their split pieces.
 cudaError_t launch_chunk_small(const ChunkParams& p, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
                                cudaStream_t stream);
-cudaError_t launch_chunk_tc(const ChunkParams& p, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
-                            cudaStream_t stream);
+cudaError_t launch_chunk_tc(const ChunkParams& p, const CUtensorMap& tmap_q, const CUtensorMap& tmap_k,
+                            const CUtensorMap& tmap_v, cudaStream_t stream);
 // `nk`: keys per tile of the kernel that wrote the pieces.
 cudaError_t launch_chunk_combine(const ChunkParams& p, int nk, cudaStream_t stream);
 cudaError_t launch_rotary(const RotaryParams& p, cudaStream_t stream);

@@ -126,6 +126,31 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) 
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// Ask the hardware for a CTA of this grid that has not started (it will then
+// not start, and this CTA does its work): the answer lands in 16 bytes of
+// shared memory at `dst`, completing 16 transaction bytes on `bar`.
+__device__ __forceinline__ void clc_ask(uint32_t dst, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+               "r"(bar)
+               : "memory");
+}
+// The answer: whether there was one, and its block index.
+__device__ __forceinline__ bool clc_answer(uint32_t src, uint32_t& x, uint32_t& y) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%3];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %2, 1, 0, p;\n\t"
+      "mov.u32 %0, 0;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, %1, _, _}, h;\n\t}"
+      : "=r"(x), "=r"(y), "=r"(ok)
+      : "r"(src)
+      : "memory");
+  return ok != 0;
+}
+
 // Registers per thread of this warpgroup (every warp of it executes this).
 template <int N>
 __device__ __forceinline__ void regs_inc() {

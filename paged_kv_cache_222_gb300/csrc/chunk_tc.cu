@@ -52,8 +52,8 @@ struct TcShape {
   static_assert(BYTES <= 232448, "shared memory per CTA");
   static constexpr int THREADS = FP8 ? 512 : 384;
   // registers: 384 x 168 or 512 x 128 at launch
-  static constexpr int REGS_SOFTMAX = FP8 ? 176 : 200;
-  static constexpr int REGS_OTHER = FP8 ? 80 : 104;
+  static constexpr int REGS_SOFTMAX = FP8 ? 192 : 224;
+  static constexpr int REGS_OTHER = FP8 ? 64 : 56;
   static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * (FP8 ? 128 : 168), "register file");
 };
 
@@ -537,19 +537,24 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
             uint8_t* dst = ring + s * C::TILE + t * 128;
             // rows past the sequence's end may hold anything: zeros instead
             const bool live = u.tile(i >> 1) * NK + t < u.ctx;
+            uint4 w[CH];                               // every load before the first store
+#pragma unroll
+            for (int c = 0; c < CH; ++c) w[c] = *reinterpret_cast<const uint4*>(src + ((c ^ rsw) << 4));
+            if (!live) {
+#pragma unroll
+              for (int c = 0; c < CH; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
+            }
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-              uint4 w = *reinterpret_cast<const uint4*>(src + ((c ^ rsw) << 4));
-              if (!live) w = make_uint4(0u, 0u, 0u, 0u);
               uint4 a, e;
-              a.x = e4m3x2_to_f16x2(static_cast<uint16_t>(w.x & 0xFFFFu));
-              a.y = e4m3x2_to_f16x2(static_cast<uint16_t>(w.x >> 16));
-              a.z = e4m3x2_to_f16x2(static_cast<uint16_t>(w.y & 0xFFFFu));
-              a.w = e4m3x2_to_f16x2(static_cast<uint16_t>(w.y >> 16));
-              e.x = e4m3x2_to_f16x2(static_cast<uint16_t>(w.z & 0xFFFFu));
-              e.y = e4m3x2_to_f16x2(static_cast<uint16_t>(w.z >> 16));
-              e.z = e4m3x2_to_f16x2(static_cast<uint16_t>(w.w & 0xFFFFu));
-              e.w = e4m3x2_to_f16x2(static_cast<uint16_t>(w.w >> 16));
+              a.x = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].x & 0xFFFFu));
+              a.y = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].x >> 16));
+              a.z = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].y & 0xFFFFu));
+              a.w = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].y >> 16));
+              e.x = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].z & 0xFFFFu));
+              e.y = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].z >> 16));
+              e.z = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].w & 0xFFFFu));
+              e.w = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].w >> 16));
               uint8_t* to = dst + (c / 4) * C::HALFB;
               *reinterpret_cast<uint4*>(to + (((2 * (c % 4)) ^ (t & 7)) << 4)) = a;
               *reinterpret_cast<uint4*>(to + (((2 * (c % 4) + 1) ^ (t & 7)) << 4)) = e;

@@ -27,6 +27,8 @@
 // flag, which ends every role's loop, and the CTA drains its copies and
 // products before it frees TMEM.
 
+#include <type_traits>
+
 #include "chunk_common.cuh"
 #include "pkv_tc.cuh"
 
@@ -77,8 +79,8 @@ struct TcUnit {
   }
 };
 
-// What a score is besides scale * q.k: nothing; capped; biased (capped or not).
-constexpr int kPlain = 0, kCapped = 1, kBiased = 2;
+// What a score is besides scale * q.k: nothing; capped; biased; both.
+constexpr int kPlain = 0, kCapped = 1, kBiased = 2, kCappedBiased = 3;
 
 __device__ __forceinline__ float min_nan(float a, float b) {  // NaN if one is
   float d;
@@ -86,55 +88,45 @@ __device__ __forceinline__ float min_nan(float a, float b) {  // NaN if one is
   return d;
 }
 
-// x := cap * tanh(x * y_mult) in log2 units, for the 128 scores of a row.
-//
-// Small arguments, |y| <= 1/2 in the whole warp (scores up to half the cap):
-// tanh(y) = y (c0 + c1 y^2 + c2 y^4 + c3 y^6) with the coefficients of the
-// least largest relative error on that range (5.4e-7: below 2^-15 of a
-// weight's exponent for scores up to 25), powers of y_mult folded in: five
-// packed FMA-pipe operations per two scores and nothing on the
-// special-function unit, which the exponentials need.
-// Others: 1 - 2 / (e^2y + 1), one reciprocal shared by four scores,
-// 1 / a = b c d / (a b c d); 2y is held below 28 log2 units, where tanh is 1 to
-// binary32 and the product of four cannot overflow.
+// Scores up to 0.35 of the cap: with y = score / cap,
+// tanh(y) = y (c0 + c1 y^2 + c2 y^4) with the coefficients of the least largest
+// relative error on |y| <= 0.35, 2.9e-6: a weight is off by less than 2^-13 at
+// a cap of 50, next to its own rounding.  Powers of the multipliers folded in,
+// that is x * ((k2 x^2 + k1) x^2 + k0) for a raw product x: four packed
+// FMA-pipe operations for two weights' exponents instead of one, and nothing
+// on the special-function unit, which the exponentials need.
+struct CapPoly {
+  float2 k0, k1, k2;
+  float y_mult;  // y = x * y_mult
+  __device__ __forceinline__ CapPoly(float w_mult, float cap_log2) {
+    y_mult = w_mult * 0.34657359027997264f;  // ln 2 / 2: w = 2 y log2(e)
+    const float y2 = y_mult * y_mult, f0 = cap_log2 * y_mult, f1 = f0 * y2, f2 = f1 * y2;
+    k0 = make_float2(0.99999713f * f0, 0.99999713f * f0);
+    k1 = make_float2(-0.33290954f * f1, -0.33290954f * f1);
+    k2 = make_float2(0.12395031f * f2, 0.12395031f * f2);
+  }
+  __device__ __forceinline__ bool holds(float abs_max) const { return abs_max * y_mult <= 0.35f && y_mult > 1e-5f; }
+  __device__ __forceinline__ float2 minus(float2 x, float2 neg_mu) const {  // the capped scores - mu
+    const float2 t = __fmul2_rn(x, x);
+    return __ffma2_rn(__ffma2_rn(__ffma2_rn(k2, t, k1), t, k0), x, neg_mu);
+  }
+};
+
+// x := cap * tanh(x / cap) in log2 units for any x: 1 - 2 / (e^2y + 1), one
+// reciprocal shared by four scores, 1 / a = b c d / (a b c d); 2y is held below
+// 28 log2 units, where tanh is 1 to binary32 and the product of four cannot
+// overflow.  What lies past the sequence's end may be NaN and must not reach
+// its neighbours: scores that are not seen enter as 0.
 template <int N>
-__device__ __forceinline__ void cap_scores(float (&x)[N], float w_mult, float cap_log2, bool masked,
-                                           const uint32_t (&see)[N / 32]) {
-  constexpr float kY = 0.34657359027997264f;  // ln 2 / 2: y = kY * w
-  const float y_mult = w_mult * kY;
-  float am = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; i += 2) am = max3f(am, fabsf(x[i]), fabsf(x[i + 1]));
-  if (__all_sync(kFull, am * y_mult <= 0.5f) && y_mult > 1e-5f) {
-    const float y2 = y_mult * y_mult, f0 = cap_log2 * y_mult;
-    const float f1 = f0 * y2, f2 = f1 * y2, f3 = f2 * y2;
-    const float2 c0 = make_float2(0.99999946f * f0, 0.99999946f * f0);
-    const float2 c1 = make_float2(-0.33326318f * f1, -0.33326318f * f1);
-    const float2 c2 = make_float2(0.13190297f * f2, 0.13190297f * f2);
-    const float2 c3 = make_float2(-0.04440223f * f3, -0.04440223f * f3);
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const float2 v = make_float2(x[i], x[i + 1]);
-      const float2 t = __fmul2_rn(v, v);
-      float2 h = __ffma2_rn(c3, t, c2);
-      h = __ffma2_rn(h, t, c1);
-      h = __ffma2_rn(h, t, c0);
-      h = __fmul2_rn(h, v);
-      x[i] = h.x;
-      x[i + 1] = h.y;
-    }
-    return;
-  }
-  if (masked) {  // what lies past the sequence's end may be NaN: it must not reach its neighbours
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (!((see[i / 32] >> (i % 32)) & 1u)) x[i] = 0.f;
-  }
+__device__ __forceinline__ void cap_scores(float* x, float w_mult, float cap_log2, bool masked, const uint32_t* see) {
 #pragma unroll
   for (int i = 0; i < N; i += 4) {
     float q[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) q[j] = fast_exp2(min_nan(x[i + j] * w_mult, 28.f)) + 1.f;
+    for (int j = 0; j < 4; ++j) {
+      const float v = masked && !((see[(i + j) / 32] >> ((i + j) % 32)) & 1u) ? 0.f : x[i + j];
+      q[j] = fast_exp2(min_nan(v * w_mult, 28.f)) + 1.f;
+    }
     const float2 pr = __fmul2_rn(make_float2(q[0], q[2]), make_float2(q[1], q[3]));
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(pr.x * pr.y));
@@ -147,6 +139,19 @@ __device__ __forceinline__ void cap_scores(float (&x)[N], float w_mult, float ca
     x[i + 2] = b.x;
     x[i + 3] = b.y;
   }
+}
+
+// x := -inf where the key is not seen; words that every lane sees whole are
+// passed over.
+template <int N>
+__device__ __forceinline__ void mask_scores(float* x, const uint32_t* see) {
+#pragma unroll
+  for (int w = 0; w < N / 32; ++w)
+    if (!__all_sync(kFull, see[w] == 0xFFFFFFFFu)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (!((see[w] >> i) & 1u)) x[32 * w + i] = -CUDART_INF_F;
+    }
 }
 
 // The unit that block index (x, y) stands for; false if it stands for none (a
@@ -576,6 +581,10 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
     const uint32_t lanes = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t t_s = lanes + COL_S + grp * NK, t_o = lanes + COL_O + grp * D;
     uint8_t* stage = s_stage + warp * C::STAGE;
+    // r / G for a row r < 256 of the tile: exact, since r times the rounding of
+    // the reciprocal (less than G / 65536) stays below 1 / G
+    const uint32_t inv_g = (65536u + G - 1) / G;
+    auto token_of = [&](int r) { return static_cast<int>(static_cast<uint32_t>(r) * inv_g >> 16); };
     int sk = 0, outs = 0;  // this group's tiles and its units with tiles so far
     bool ok = true;
     TcUnit u;
@@ -584,7 +593,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
       const int r_in = tid;                              // row of the tile
       const bool row_ok = r_in < u.rows;
       const bool warp_ok = warp * 32 < u.rows;           // some lane has a row
-      const int tok = r_in / G, gh = r_in - tok * G;
+      const int tok = token_of(r_in), gh = r_in - tok * G;
       // what the row sees; a row past the tile's takes no mask (nothing of it
       // is ever written)
       constexpr int kFar = 0x3FFFFFFF;
@@ -593,9 +602,8 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
       const int pf = row_ok && pos >= 0 ? u.prefix : 0;
       constexpr float kLog2e = 1.4426950408889634f;
       const float qk = FP8 ? p.qk_log2 * __int_as_float(u.k_bits) : p.qk_log2;
-      const float slope = MODE == kBiased && row_ok ? p.slopes[u.h * G + gh] * kLog2e : 0.f;
-      // scores times ex_mult are log2 weights
-      const float ex_mult = MODE != kPlain ? 1.f : qk;
+      const float slope = (MODE == kBiased || MODE == kCappedBiased) && row_ok ? p.slopes[u.h * G + gh] * kLog2e : 0.f;
+      const CapPoly poly(qk, p.cap_log2);
 
       float m_used = -CUDART_INF_F, lsum = 0.f;
       for (int k = 0; k < u.ntile; ++k, ++sk) {
@@ -620,9 +628,20 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
             for (int w = 0; w < NK / 32; ++w)
               see[w] = (below(pos - t0 + 1, w) & ~below(lo - t0, w)) | below(pf - t0, w);
           }
-          if (MODE == kCapped || (MODE == kBiased && p.cap_log2 > 0.f)) cap_scores(x, qk, p.cap_log2, masked, see);
-          if constexpr (MODE == kBiased) {
-            const float mult = p.cap_log2 > 0.f ? 1.f : qk, base = slope * static_cast<float>(t0 - pos);
+          // Capped: the row maximum is taken of the raw products (a cap does not
+          // change which is the largest), the cap enters with the exponent.
+          bool small = false;
+          if constexpr (MODE == kCapped) {
+            float am[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < NK; i += 8)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) am[j] = max3f(am[j], fabsf(x[i + 2 * j]), fabsf(x[i + 2 * j + 1]));
+            small = __all_sync(kFull, poly.holds(fmaxf(max3f(am[0], am[1], am[2]), am[3])));
+          }
+          if constexpr (MODE == kCappedBiased) cap_scores<NK>(x, qk, p.cap_log2, masked, see);
+          if constexpr (MODE == kBiased || MODE == kCappedBiased) {
+            const float mult = MODE == kBiased ? qk : 1.f, base = slope * static_cast<float>(t0 - pos);
             const float2 mult2 = make_float2(mult, mult), slope2 = make_float2(slope, slope);
             const float2 base2 = make_float2(base, base);
 #pragma unroll
@@ -633,11 +652,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
               x[i + 1] = z.y;
             }
           }
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < NK; ++i)
-              if (!((see[i / 32] >> (i % 32)) & 1u)) x[i] = -CUDART_INF_F;
-          }
+          if (masked) mask_scores<NK>(x, see);
           float mt;
           {
             float mp[8];
@@ -648,7 +663,9 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
               for (int i = 24; i + 8 < NK; i += 16) mp[j] = max3f(mp[j], x[i + j], x[i + 8 + j]);
               mp[j] = fmaxf(mp[j], x[NK - 8 + j]);
             }
-            mt = max3f(max3f(mp[0], mp[1], mp[2]), max3f(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7])) * ex_mult;
+            mt = max3f(max3f(mp[0], mp[1], mp[2]), max3f(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
+            if constexpr (MODE == kPlain) mt *= qk;
+            if constexpr (MODE == kCapped) mt = mt == -CUDART_INF_F ? mt : capped(mt * qk, p.cap_log2);
           }
           float alpha = 1.f;
           bool resc = false;
@@ -676,20 +693,40 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
             lsum *= alpha;
           }
           const float mu = m_used == -CUDART_INF_F ? 0.f : m_used;
-          const float2 neg_mu = make_float2(-mu, -mu), mult2 = make_float2(ex_mult, ex_mult);
+          const float2 neg_mu = make_float2(-mu, -mu), mult2 = make_float2(qk, qk);
           float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          // weights of the row, 2^(score - m), into S's columns; WAY: the scores
+          // are raw products, raw products to be capped, or done
+          auto weights = [&](auto way) {
+            constexpr int WAY = decltype(way)::value;
 #pragma unroll
-          for (int c = 0; c < NK / 32; ++c) {
-            uint32_t hi[16];
+            for (int c = 0; c < NK / 32; ++c) {
+              uint32_t hi[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 xx = make_float2(x[32 * c + 2 * i], x[32 * c + 2 * i + 1]);
-              const float2 e = MODE != kPlain ? __fadd2_rn(xx, neg_mu) : __ffma2_rn(xx, mult2, neg_mu);
-              const float2 pp = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-              ls[i & 1] = __fadd2_rn(ls[i & 1], pp);
-              hi[i] = FP8 ? pack_f16x2(pp.x, pp.y) : pack_bf16x2(pp.x, pp.y);
+              for (int i = 0; i < 16; ++i) {
+                const float2 xx = make_float2(x[32 * c + 2 * i], x[32 * c + 2 * i + 1]);
+                const float2 e = WAY == 0   ? __ffma2_rn(xx, mult2, neg_mu)
+                                 : WAY == 1 ? poly.minus(xx, neg_mu)
+                                            : __fadd2_rn(xx, neg_mu);
+                const float2 pp = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+                ls[i & 1] = __fadd2_rn(ls[i & 1], pp);
+                hi[i] = FP8 ? pack_f16x2(pp.x, pp.y) : pack_bf16x2(pp.x, pp.y);
+              }
+              tmem_st16(t_s + 16 * c, hi);
             }
-            tmem_st16(t_s + 16 * c, hi);
+          };
+          if constexpr (MODE == kPlain) {
+            weights(std::integral_constant<int, 0>{});
+          } else if constexpr (MODE == kCapped) {
+            if (small) {
+              weights(std::integral_constant<int, 1>{});
+            } else {
+              cap_scores<NK>(x, qk, p.cap_log2, masked, see);
+              if (masked) mask_scores<NK>(x, see);
+              weights(std::integral_constant<int, 2>{});
+            }
+          } else {
+            weights(std::integral_constant<int, 2>{});
           }
           lsum += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
           tmem_wait_st();
@@ -710,60 +747,68 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
         // chunk c (16 bytes) of row r at r * 64 + ((c ^ (r / 2 % 4)) * 16): eight
         // consecutive rows' chunks c lie in distinct banks
         auto at = [&](int r, int c) { return stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4); };
-        // this lane stores chunk lane % 4 of rows lane / 4 + 8 i
-        auto row_of = [&](int r) {
-          const int rr = warp * 32 + r;
-          return (static_cast<int64_t>(u.row0) + rr / G) * H_q + u.h * G + rr % G;
+        auto row_of = [&](int r) {                       // output row of the warp's row r
+          const int rr = warp * 32 + r, tk = token_of(rr);
+          return static_cast<int64_t>(u.row0 + tk) * H_q + u.h * G + (rr - tk * G);
         };
+        // this lane stores chunk lane % 4 of rows lane / 4 + 8 i
         int64_t to[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = (lane >> 2) + 8 * i;
-          to[i] = warp * 32 + r < u.rows ? (direct ? row_of(r) : row_of(r) * p.max_splits + u.split) : -1;
+          to[i] = warp * 32 + r < u.rows ? (direct ? row_of(r) * D + (lane & 3) * 8
+                                                    : (row_of(r) * p.max_splits + u.split) * D + (lane & 3) * 4)
+                                         : -1;
         }
+        float o[D];
+        if (u.ntile > 0) {
 #pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          float o[32];
-          if (u.ntile > 0) {
-            tmem_ld32(t_o + c0, o);
-            tmem_wait_ld();
-          } else {
+          for (int c = 0; c < D / 32; ++c) tmem_ld32(t_o + 32 * c, o + 32 * c);
+          tmem_wait_ld();
+        } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0.f;
-          }
-          if (direct) {
+          for (int i = 0; i < D; ++i) o[i] = 0.f;
+        }
+        tc_fence_before();  // O has been read: the next unit's products may overwrite it after P's hand-over
+        if (direct) {
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 32) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+              const float* v = o + c0 + 8 * i;
               uint4 w;
-              w.x = pack_bf16x2(o[8 * i] * mult, o[8 * i + 1] * mult);
-              w.y = pack_bf16x2(o[8 * i + 2] * mult, o[8 * i + 3] * mult);
-              w.z = pack_bf16x2(o[8 * i + 4] * mult, o[8 * i + 5] * mult);
-              w.w = pack_bf16x2(o[8 * i + 6] * mult, o[8 * i + 7] * mult);
+              w.x = pack_bf16x2(v[0] * mult, v[1] * mult);
+              w.y = pack_bf16x2(v[2] * mult, v[3] * mult);
+              w.z = pack_bf16x2(v[4] * mult, v[5] * mult);
+              w.w = pack_bf16x2(v[6] * mult, v[7] * mult);
               *reinterpret_cast<uint4*>(at(lane, i)) = w;
             }
             __syncwarp();
+            uint4 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(at((lane >> 2) + 8 * i, lane & 3));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               if (to[i] >= 0)
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + to[i] * D + c0 + (lane & 3) * 8) =
-                    *reinterpret_cast<const uint4*>(at((lane >> 2) + 8 * i, lane & 3));
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + to[i] + c0) = w[i];
             __syncwarp();
-          } else {
+          }
+        } else {
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
+          for (int c0 = 0; c0 < D; c0 += 16) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4*>(at(lane, i)) =
-                    make_float4(o[16 * hh + 4 * i] * mult, o[16 * hh + 4 * i + 1] * mult,
-                                o[16 * hh + 4 * i + 2] * mult, o[16 * hh + 4 * i + 3] * mult);
-              __syncwarp();
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (to[i] >= 0)
-                  *reinterpret_cast<float4*>(p.ws_o + to[i] * D + c0 + 16 * hh + (lane & 3) * 4) =
-                      *reinterpret_cast<const float4*>(at((lane >> 2) + 8 * i, lane & 3));
-              __syncwarp();
+            for (int i = 0; i < 4; ++i) {
+              const float* v = o + c0 + 4 * i;
+              *reinterpret_cast<float4*>(at(lane, i)) = make_float4(v[0] * mult, v[1] * mult, v[2] * mult, v[3] * mult);
             }
+            __syncwarp();
+            float4 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(at((lane >> 2) + 8 * i, lane & 3));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (to[i] >= 0) *reinterpret_cast<float4*>(p.ws_o + to[i] + c0) = w[i];
+            __syncwarp();
           }
         }
         if (!direct && row_ok) {
@@ -771,7 +816,6 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
           ml[0] = m_used;
           ml[1] = lsum;
         }
-        tc_fence_before();  // O has been read: the next unit's products may overwrite it after P's hand-over
       }
     }
   }
@@ -799,7 +843,9 @@ cudaError_t launch_tc_t(const ChunkParams& p, const CUtensorMap& tq, const CUten
 
 template <int D, bool FP8>
 cudaError_t launch_tc_m(const ChunkParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
-  if (p.slopes != nullptr) return launch_tc_t<D, FP8, kBiased>(p, tq, tk, tv, stream);
+  if (p.slopes != nullptr)
+    return p.cap_log2 > 0.f ? launch_tc_t<D, FP8, kCappedBiased>(p, tq, tk, tv, stream)
+                            : launch_tc_t<D, FP8, kBiased>(p, tq, tk, tv, stream);
   if (p.cap_log2 > 0.f) return launch_tc_t<D, FP8, kCapped>(p, tq, tk, tv, stream);
   return launch_tc_t<D, FP8, kPlain>(p, tq, tk, tv, stream);
 }

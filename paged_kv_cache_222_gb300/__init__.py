@@ -447,7 +447,7 @@ def chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_starts, s
     max_context_len = mb * fields[1] if max_context_len is None else int(max_context_len)
     split_tokens, window = int(split_tokens), int(window)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(q)
     else:
         _check(out, torch.bfloat16, "out", index, dev)
         if out.shape != shape:

@@ -1291,13 +1291,21 @@ pkv_status chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_
   const int64_t units = row_tiles * c->num_kv_heads;
   int64_t st = split_tokens;
   if (st == 0) {
-    // the longest split that still gives every SM work: three CTAs per SM and
-    // about six waves of them on the mma.sync kernel (as for decode), two
-    // units per SM on the tcgen05 kernel
-    const int64_t want = static_cast<int64_t>(sms) * (small ? 18 : 2), all = ceil_div(tiles * nk, 128) * 128;
-    st = small && units < want ? 4096 : all;
-    while (st > 256 && units * ceil_div(tiles * nk, st) < want) st = ceil_div(st / 2, 128) * 128;
-    if (small && st > max_st) st = max_st;
+    // mma.sync kernel: as for decode, three CTAs per SM streaming one split
+    // each, but below 1024 tokens, where a split's fixed cost weighs, no more
+    // CTAs than SMs (16 sequences of 1000-4000 tokens: 42.5 us at 256 tokens, 36
+    // at 1024; one of 60k 56.6 and 55; 8 of 31k take 1280: 159 us).  tcgen05
+    // kernel: the longest split that still gives two units per SM.
+    const int64_t all = ceil_div(tiles * nk, 128) * 128;
+    if (small) {
+      st = decode_split_tokens(static_cast<int32_t>(row_tiles < 0x7FFFFFFF ? row_tiles : 0x7FFFFFFF), c->num_kv_heads,
+                               static_cast<int32_t>(all < 0x7FFFFFC0 ? all : 0x7FFFFFC0), sms);
+      while (st < 1024 && st < all && units * ceil_div(all, st) > sms) st += 64;
+      if (st > max_st) st = max_st;
+    } else {
+      st = all;
+      while (st > 256 && units * ceil_div(tiles * nk, st) < static_cast<int64_t>(sms) * 2) st = ceil_div(st / 2, 128) * 128;
+    }
   }
   if ((ceil_div(n_tokens, tile_q) + batch) * c->num_kv_heads > 0x7FFFFFFFll)
     return fail(PKV_ERR_UNSUPPORTED, "row tiles x num_kv_heads beyond the grid");

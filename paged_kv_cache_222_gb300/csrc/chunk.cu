@@ -19,6 +19,8 @@
 // output's own 2^-8.  The bound is the HBM stream of 2 D bytes x type size
 // per visible key and KV head.
 
+#include <type_traits>
+
 #include "chunk_common.cuh"
 
 namespace pkv {
@@ -36,7 +38,9 @@ struct SmallShape {
   static_assert(4 * 16 * DP * 4 + 4 * 16 * 2 * 4 <= NS * STAGE, "merge buffer fits the stages");
 };
 
-template <int D, bool FP8>
+// TWO: tiles of more than 8 rows (a lane holds rows r and r + 8 of the product;
+// without it the second one is empty and its softmax left out).
+template <int D, bool FP8, bool TWO>
 __global__ void __launch_bounds__(128, 3)
     chunk_small_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                        const ChunkParams p) {
@@ -72,11 +76,9 @@ __global__ void __launch_bounds__(128, 3)
   const int i1 = min(sq.n, i0 + p.tile_q) - 1;
   const int rows = (i1 - i0 + 1) * G;
   const ChunkRange rg = chunk_range<kSmallTile>(p, sq, i0, i1);
-  const int per_split = p.split_tokens / kSmallTile;
-  const int nsplit = max(1, (rg.n + per_split - 1) / per_split);
+  const ChunkSplit sp(rg.n, p.split_tokens / kSmallTile, split);
+  const int nsplit = sp.nsplit, k0 = sp.k0, ntile = sp.ntile;
   if (split >= nsplit) return;
-  const int k0 = split * per_split;
-  const int ntile = min(rg.n - k0, per_split);
   const int64_t row_base = static_cast<int64_t>(sq.start + i0) * H_q + h * G;  // of row (0, g = 0)
   auto out_row = [&](int row) { return row_base + static_cast<int64_t>(row / G) * H_q + row % G; };
 
@@ -162,6 +164,8 @@ __global__ void __launch_bounds__(128, 3)
     v_mult = p.v_scale[static_cast<int64_t>(b) * p.scale_stride + h];
   }
 
+  const float ex_mult = p.cap_log2 > 0.f || p.slopes != nullptr ? 1.f : qk_mult;  // scores to log2 weights
+
   float m_a = -CUDART_INF_F, m_b = -CUDART_INF_F, l_a = 0.f, l_b = 0.f;
   float o[D / 8][4];
 #pragma unroll
@@ -206,93 +210,129 @@ __global__ void __launch_bounds__(128, 3)
           }
         }
       }
-      // ---- scores (log2 units), masks, online softmax (rows a: e = 0, 1; b: e = 2, 3)
-      float mx_a = -CUDART_INF_F, mx_b = -CUDART_INF_F;
+      // ---- scores, masks, online softmax (rows a: e = 0, 1; b: e = 2, 3).
+      // Without cap and bias the multiplier waits for the exponent's FMA.  The
+      // maximum is lazy: it moves when it grows by more than 2^8, so weights
+      // stay within 2^8 and most steps rescale nothing.
+      constexpr int NE = TWO ? 4 : 2;
+      if (p.cap_log2 > 0.f) {
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
+        for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int t = t_warp + 8 * nt + 2 * j + (e & 1);
-          const int pos = e < 2 ? pos_a : pos_b, lo = e < 2 ? lo_a : lo_b, pf = e < 2 ? pf_a : pf_b;
-          float x = sc[nt][e] * qk_mult;
-          if (p.cap_log2 > 0.f) x = capped(x, p.cap_log2);
-          x = fmaf(e < 2 ? sl_a : sl_b, static_cast<float>(t - pos), x);
-          sc[nt][e] = (t <= pos && t >= lo) || t < pf ? x : -CUDART_INF_F;
-        }
-        mx_a = fmaxf(mx_a, fmaxf(sc[nt][0], sc[nt][1]));
-        mx_b = fmaxf(mx_b, fmaxf(sc[nt][2], sc[nt][3]));
+          for (int e = 0; e < NE; ++e) sc[nt][e] = capped(sc[nt][e] * qk_mult, p.cap_log2);
       }
+      if (p.slopes != nullptr) {
+        const float m = p.cap_log2 > 0.f ? 1.f : qk_mult;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < NE; ++e) {
+            const int t = t_warp + 8 * nt + 2 * j + (e & 1);
+            sc[nt][e] = fmaf(sc[nt][e], m, (e < 2 ? sl_a : sl_b) * static_cast<float>(t - (e < 2 ? pos_a : pos_b)));
+          }
+      }
+      const auto whole = [&](int pos, int lo, int pf) {
+        return (t_warp + kTileTokens - 1 <= pos && t_warp >= lo) || t_warp + kTileTokens <= pf;
+      };
+      if (!__all_sync(kFull, whole(pos_a, lo_a, pf_a) && (!TWO || whole(pos_b, lo_b, pf_b)))) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < NE; ++e) {
+            const int t = t_warp + 8 * nt + 2 * j + (e & 1);
+            const int pos = e < 2 ? pos_a : pos_b, lo = e < 2 ? lo_a : lo_b, pf = e < 2 ? pf_a : pf_b;
+            if (!((t <= pos && t >= lo) || t < pf)) sc[nt][e] = -CUDART_INF_F;
+          }
+      }
+      float mx_a = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+      float mx_b = TWO ? fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3])) : -CUDART_INF_F;
       mx_a = fmaxf(mx_a, __shfl_xor_sync(kFull, mx_a, 1));
-      mx_a = fmaxf(mx_a, __shfl_xor_sync(kFull, mx_a, 2));
-      mx_b = fmaxf(mx_b, __shfl_xor_sync(kFull, mx_b, 1));
-      mx_b = fmaxf(mx_b, __shfl_xor_sync(kFull, mx_b, 2));
-      const float mn_a = fmaxf(m_a, mx_a), mn_b = fmaxf(m_b, mx_b);
-      const float mu_a = (mn_a == -CUDART_INF_F) ? 0.f : mn_a;
-      const float mu_b = (mn_b == -CUDART_INF_F) ? 0.f : mn_b;
-      const float al_a = fast_exp2(m_a - mu_a), al_b = fast_exp2(m_b - mu_b);
-      m_a = mn_a;
-      m_b = mn_b;
-      float sum_a = 0.f, sum_b = 0.f;
+      mx_a = fmaxf(mx_a, __shfl_xor_sync(kFull, mx_a, 2)) * ex_mult;
+      if constexpr (TWO) {
+        mx_b = fmaxf(mx_b, __shfl_xor_sync(kFull, mx_b, 1));
+        mx_b = fmaxf(mx_b, __shfl_xor_sync(kFull, mx_b, 2)) * ex_mult;
+      }
+      // (-inf: nothing seen yet, any seen key moves it and there is nothing to rescale)
+      const bool up_a = mx_a > m_a + 8.f, up_b = TWO && mx_b > m_b + 8.f;
+      if (__any_sync(kFull, up_a || up_b)) {
+        const float al_a = up_a ? fast_exp2(m_a - mx_a) : 1.f, al_b = up_b ? fast_exp2(m_b - mx_b) : 1.f;
+        if (up_a) m_a = mx_a;
+        if (up_b) m_b = mx_b;
+        l_a *= al_a;
+        l_b *= al_b;
+#pragma unroll
+        for (int nt = 0; nt < D / 8; ++nt) {
+          o[nt][0] *= al_a;
+          o[nt][1] *= al_a;
+          o[nt][2] *= al_b;
+          o[nt][3] *= al_b;
+        }
+      }
+      const float mu_a = m_a == -CUDART_INF_F ? 0.f : m_a, mu_b = m_b == -CUDART_INF_F ? 0.f : m_b;
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
-        sc[nt][0] = fast_exp2(sc[nt][0] - mu_a);
-        sc[nt][1] = fast_exp2(sc[nt][1] - mu_a);
-        sc[nt][2] = fast_exp2(sc[nt][2] - mu_b);
-        sc[nt][3] = fast_exp2(sc[nt][3] - mu_b);
-        sum_a += sc[nt][0] + sc[nt][1];
-        sum_b += sc[nt][2] + sc[nt][3];
-      }
-      l_a = l_a * al_a + sum_a;
-      l_b = l_b * al_b + sum_b;
-#pragma unroll
-      for (int nt = 0; nt < D / 8; ++nt) {
-        const float2 u = __fmul2_rn(make_float2(o[nt][0], o[nt][1]), make_float2(al_a, al_a));
-        const float2 w = __fmul2_rn(make_float2(o[nt][2], o[nt][3]), make_float2(al_b, al_b));
-        o[nt][0] = u.x;
-        o[nt][1] = u.y;
-        o[nt][2] = w.x;
-        o[nt][3] = w.y;
+        sc[nt][0] = fast_exp2(fmaf(sc[nt][0], ex_mult, -mu_a));
+        sc[nt][1] = fast_exp2(fmaf(sc[nt][1], ex_mult, -mu_a));
+        l_a += sc[nt][0] + sc[nt][1];
+        if constexpr (TWO) {
+          sc[nt][2] = fast_exp2(fmaf(sc[nt][2], ex_mult, -mu_b));
+          sc[nt][3] = fast_exp2(fmaf(sc[nt][3], ex_mult, -mu_b));
+          l_b += sc[nt][2] + sc[nt][3];
+        } else {
+          sc[nt][2] = sc[nt][3] = 0.f;
+        }
       }
       // ---- O += P V.  V rows at or past the end of the sequence may hold
       // anything (NaN included): zeroed in the fragments, P is 0 there.
       const int vvalid = sq.ctx - t_warp;
-      const uint32_t keep0 = ((2 * j < vvalid) ? 0x0000FFFFu : 0u) | ((2 * j + 1 < vvalid) ? 0xFFFF0000u : 0u);
-      const uint32_t keep1 = ((2 * j + 8 < vvalid) ? 0x0000FFFFu : 0u) | ((2 * j + 9 < vvalid) ? 0xFFFF0000u : 0u);
       const uint32_t vt = base + L::TILEB;
       uint32_t ph[4];
-      if constexpr (!FP8) {
-        ph[0] = pack_bf16x2(sc[0][0], sc[0][1]);
-        ph[1] = pack_bf16x2(sc[0][2], sc[0][3]);
-        ph[2] = pack_bf16x2(sc[1][0], sc[1][1]);
-        ph[3] = pack_bf16x2(sc[1][2], sc[1][3]);
-#pragma unroll
-        for (int dp = 0; dp < KS; ++dp) {
-          uint32_t Rv[4];
-          ldsm_x4_trans(vt + L::off(tok_v, 2 * dp + ch_v), Rv);
-          mma_bf16_16816(o[2 * dp], ph, Rv[0] & keep0, Rv[1] & keep1);
-          mma_bf16_16816(o[2 * dp + 1], ph, Rv[2] & keep0, Rv[3] & keep1);
-        }
-      } else {
+      if constexpr (FP8) {
         ph[0] = pack_f16x2(sc[0][0], sc[0][1]);
         ph[1] = pack_f16x2(sc[0][2], sc[0][3]);
         ph[2] = pack_f16x2(sc[1][0], sc[1][1]);
         ph[3] = pack_f16x2(sc[1][2], sc[1][3]);
+      } else {
+        ph[0] = pack_bf16x2(sc[0][0], sc[0][1]);
+        ph[1] = pack_bf16x2(sc[0][2], sc[0][3]);
+        ph[2] = pack_bf16x2(sc[1][0], sc[1][1]);
+        ph[3] = pack_bf16x2(sc[1][2], sc[1][3]);
+      }
+      const auto add_pv = [&](auto tail) {
+        constexpr bool TAIL = decltype(tail)::value;
+        const uint32_t keep0 = ((2 * j < vvalid) ? 0x0000FFFFu : 0u) | ((2 * j + 1 < vvalid) ? 0xFFFF0000u : 0u);
+        const uint32_t keep1 = ((2 * j + 8 < vvalid) ? 0x0000FFFFu : 0u) | ((2 * j + 9 < vvalid) ? 0xFFFF0000u : 0u);
 #pragma unroll
-        for (int pk = 0; pk < KS / 2; ++pk) {
+        for (int q = 0; q < (FP8 ? KS / 2 : KS); ++q) {
           uint32_t Rv[4];
-          ldsm_x4_trans(vt + L::off(tok_v, 2 * pk + ch_v), Rv);
+          ldsm_x4_trans(vt + L::off(tok_v, 2 * q + ch_v), Rv);
+          if constexpr (TAIL) {
+            Rv[0] &= keep0;
+            Rv[1] &= keep1;
+            Rv[2] &= keep0;
+            Rv[3] &= keep1;
+          }
+          if constexpr (!FP8) {
+            mma_bf16_16816(o[2 * q], ph, Rv[0], Rv[1]);
+            mma_bf16_16816(o[2 * q + 1], ph, Rv[2], Rv[3]);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {  // 16-d chunk 2 pk + e: n-tile 2c its even d, 2c + 1 its odd d
-            const uint32_t e0 = prmt(Rv[2 * e] & keep0, 0u, 0x3120u);       // keys 0-7
-            const uint32_t e1 = prmt(Rv[2 * e + 1] & keep1, 0u, 0x3120u);   // keys 8-15
-            const int c = 2 * pk + e;
-            mma_f16_16816(o[2 * c], ph, e4m3x2_to_f16x2(static_cast<uint16_t>(e0 & 0xFFFFu)),
-                          e4m3x2_to_f16x2(static_cast<uint16_t>(e1 & 0xFFFFu)));
-            mma_f16_16816(o[2 * c + 1], ph, e4m3x2_to_f16x2(static_cast<uint16_t>(e0 >> 16)),
-                          e4m3x2_to_f16x2(static_cast<uint16_t>(e1 >> 16)));
+            for (int e = 0; e < 2; ++e) {  // 16-d chunk 2 q + e: n-tile 2c its even d, 2c + 1 its odd d
+              const uint32_t e0 = prmt(Rv[2 * e], 0u, 0x3120u);       // keys 0-7
+              const uint32_t e1 = prmt(Rv[2 * e + 1], 0u, 0x3120u);   // keys 8-15
+              const int c = 2 * q + e;
+              mma_f16_16816(o[2 * c], ph, e4m3x2_to_f16x2(static_cast<uint16_t>(e0 & 0xFFFFu)),
+                            e4m3x2_to_f16x2(static_cast<uint16_t>(e1 & 0xFFFFu)));
+              mma_f16_16816(o[2 * c + 1], ph, e4m3x2_to_f16x2(static_cast<uint16_t>(e0 >> 16)),
+                            e4m3x2_to_f16x2(static_cast<uint16_t>(e1 >> 16)));
+            }
           }
         }
-      }
+      };
+      if (vvalid < kTileTokens)
+        add_pv(std::true_type{});
+      else
+        add_pv(std::false_type{});
     }
     __syncwarp();  // this warp has read its part of the slot: refill it
     if (healthy && k + NS < ntile) issue(issued++);
@@ -368,62 +408,110 @@ __global__ void __launch_bounds__(128, 3)
 }
 
 // Merge of the split pieces: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
-// One CTA per token, a warp per query head in turn; rows of one piece were
-// written by the attention kernel itself.
-template <int D>
+// A row (token, query head) is merged by W warps that share its pieces, eight
+// pieces' rows in flight per warp; rows of one piece were written by the
+// attention kernel itself.  Latency counts: one CTA per token with its heads in
+// turn took 45 us for one token of 64 heads and 32 pieces.
+template <int D, int W>
 __global__ void __launch_bounds__(256) chunk_combine_kernel(const ChunkParams p, int nk) {
   constexpr int E = D / 32;  // elements per lane
+  constexpr int BATCH = 8;
+  __shared__ float s_acc[W > 1 ? 8 : 1][D];
+  __shared__ float2 s_ml[8];
   wait_prior_grid();
   allow_next_grid();
-  const int tok = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = warp_search(p.batch, tok, [&](int i) { return p.q_starts[i]; });
-  const ChunkSeq sq = chunk_seq(p, b, false);
-  const int i = tok - sq.start;
-  if (i < 0 || i >= sq.n) return;  // a row of no sequence
-  const int i0 = i / p.tile_q * p.tile_q, i1 = min(sq.n, i0 + p.tile_q) - 1;
-  const int n = nk == 64 ? chunk_range<64>(p, sq, i0, i1).n : chunk_range<128>(p, sq, i0, i1).n;
-  const int per_split = p.split_tokens / nk;
-  const int nsplit = (n + per_split - 1) / per_split;
-  if (nsplit <= 1) return;
-  for (int hq = warp; hq < p.num_q_heads; hq += 8) {
-    const int64_t row = static_cast<int64_t>(tok) * p.num_q_heads + hq;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = warp % W, tok = blockIdx.x, hq = blockIdx.y * (8 / W) + warp / W;
+  int nsplit = 0;  // 0: this warp has no row to merge
+  if (hq < p.num_q_heads) {
+    const int b = warp_search(p.batch, tok, [&](int i) { return p.q_starts[i]; });
+    const ChunkSeq sq = chunk_seq(p, b, false);
+    const int i = tok - sq.start;
+    if (i >= 0 && i < sq.n) {  // else a row of no sequence
+      const int i0 = i / p.tile_q * p.tile_q, i1 = min(sq.n, i0 + p.tile_q) - 1;
+      const int n = nk == 64 ? chunk_range<64>(p, sq, i0, i1).n : chunk_range<128>(p, sq, i0, i1).n;
+      nsplit = ChunkSplit(n, p.split_tokens / nk, 0).nsplit;
+      if (nsplit == 1) nsplit = 0;
+    }
+  }
+  const int64_t row = static_cast<int64_t>(tok) * p.num_q_heads + hq;
+  float acc[E], l = 0.f, M = -CUDART_INF_F;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  // this warp's pieces: part, part + W, ...
+  const int mine = nsplit > part ? (nsplit - part + W - 1) / W : 0;
+  if (mine > 0) {
     const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + row * p.max_splits;
     const float* po = p.ws_o + row * p.max_splits * D + lane * E;
-    float M = -CUDART_INF_F;
-    for (int s = lane; s < nsplit; s += 32) M = fmaxf(M, ml[s].x);
+    for (int s = lane; s < mine; s += 32) M = fmaxf(M, ml[part + s * W].x);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
-    float acc[E], l = 0.f;
+    for (int s0 = 0; s0 < mine; s0 += 32) {
+      const float2 v = s0 + lane < mine ? ml[part + (s0 + lane) * W] : make_float2(-CUDART_INF_F, 0.f);
+      const float wl = v.x == -CUDART_INF_F ? 0.f : fast_exp2(v.x - M);  // weight of piece s0 + lane
+      l += wl * v.y;
+      for (int s = s0; s < mine && s < s0 + 32; s += BATCH) {
+        float u[BATCH][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < nsplit; ++s) {
-      const float2 v = ml[s];
-      const float wt = v.x == -CUDART_INF_F ? 0.f : fast_exp2(v.x - M);
-      l += wt * v.y;
-      const float* src = po + static_cast<int64_t>(s) * D;
-      if constexpr (E == 4) {
-        const float4 u = *reinterpret_cast<const float4*>(src);
-        acc[0] += wt * u.x;
-        acc[1] += wt * u.y;
-        acc[2] += wt * u.z;
-        acc[3] += wt * u.w;
-      } else {
-        const float2 u = *reinterpret_cast<const float2*>(src);
-        acc[0] += wt * u.x;
-        acc[1] += wt * u.y;
+        for (int q = 0; q < BATCH; ++q) {
+          const float* src = po + static_cast<int64_t>(part + (s + q < mine ? s + q : s) * W) * D;
+          if constexpr (E == 4) {
+            const float4 w = *reinterpret_cast<const float4*>(src);
+            u[q][0] = w.x;
+            u[q][1] = w.y;
+            u[q][2] = w.z;
+            u[q][3] = w.w;
+          } else {
+            const float2 w = *reinterpret_cast<const float2*>(src);
+            u[q][0] = w.x;
+            u[q][1] = w.y;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < BATCH; ++q) {
+          const float wt = __shfl_sync(kFull, wl, (s - s0 + q) & 31);
+          if (s + q < mine) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += wt * u[q][e];
+          }
+        }
       }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + lane * E);
 #pragma unroll
-    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(kFull, l, x);
   }
+  if constexpr (W > 1) {  // the warps' parts, by the row's first warp
+    if (lane == 0) s_ml[warp] = make_float2(M, l);
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+    __syncthreads();
+    if (part != 0) return;
+    const float own = M;
+#pragma unroll
+    for (int w = 1; w < W; ++w) M = fmaxf(M, s_ml[warp + w].x);
+    const float w0 = own == -CUDART_INF_F ? 0.f : fast_exp2(own - M);
+    l *= w0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= w0;
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      const float2 v = s_ml[warp + w];
+      const float wt = v.x == -CUDART_INF_F ? 0.f : fast_exp2(v.x - M);
+      l += wt * v.y;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += wt * s_acc[warp + w][lane * E + e];
+    }
+  }
+  if (nsplit == 0) return;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool TWO>
 cudaError_t launch_small_t(const ChunkParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
-  auto kern = chunk_small_kernel<D, FP8>;
+  auto kern = chunk_small_kernel<D, FP8, TWO>;
   constexpr int smem = SmallShape<D, FP8>::BYTES;
   static int configured[64] = {};
   cudaError_t e = set_smem_once(kern, smem, configured);
@@ -432,20 +520,31 @@ cudaError_t launch_small_t(const ChunkParams& p, const CUtensorMap& tk, const CU
   return launch_pdl(kern, dim3(p.max_splits, p.num_kv_heads * ntq, p.batch), dim3(128), smem, stream, tk, tv, p);
 }
 
+template <int D, bool FP8>
+cudaError_t launch_small_r(const ChunkParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
+  return p.max_q_len * p.group > 8 ? launch_small_t<D, FP8, true>(p, tk, tv, stream)
+                                   : launch_small_t<D, FP8, false>(p, tk, tv, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_chunk_small(const ChunkParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                cudaStream_t stream) {
   const bool fp8 = p.cache_dtype == kE4M3;
   if (p.head_dim == 128)
-    return fp8 ? launch_small_t<128, true>(p, tk, tv, stream) : launch_small_t<128, false>(p, tk, tv, stream);
-  return fp8 ? launch_small_t<64, true>(p, tk, tv, stream) : launch_small_t<64, false>(p, tk, tv, stream);
+    return fp8 ? launch_small_r<128, true>(p, tk, tv, stream) : launch_small_r<128, false>(p, tk, tv, stream);
+  return fp8 ? launch_small_r<64, true>(p, tk, tv, stream) : launch_small_r<64, false>(p, tk, tv, stream);
 }
 
 cudaError_t launch_chunk_combine(const ChunkParams& p, int nk, cudaStream_t stream) {
+  // a whole CTA per row while the rows alone leave SMs idle
+  const bool few = static_cast<int64_t>(p.n_tokens) * p.num_q_heads <= 2048 && p.max_splits > 8;
+  const dim3 grid(p.n_tokens, few ? p.num_q_heads : (p.num_q_heads + 7) / 8);
   if (p.head_dim == 128)
-    return launch_pdl(chunk_combine_kernel<128>, dim3(p.n_tokens), dim3(256), 0, stream, p, nk);
-  return launch_pdl(chunk_combine_kernel<64>, dim3(p.n_tokens), dim3(256), 0, stream, p, nk);
+    return few ? launch_pdl(chunk_combine_kernel<128, 8>, grid, dim3(256), 0, stream, p, nk)
+               : launch_pdl(chunk_combine_kernel<128, 1>, grid, dim3(256), 0, stream, p, nk);
+  return few ? launch_pdl(chunk_combine_kernel<64, 8>, grid, dim3(256), 0, stream, p, nk)
+             : launch_pdl(chunk_combine_kernel<64, 1>, grid, dim3(256), 0, stream, p, nk);
 }
 
 }  // namespace pkv

@@ -94,6 +94,19 @@ __device__ __forceinline__ ChunkRange chunk_range(const ChunkParams& p, const Ch
   return r;
 }
 
+// Split `split` of a row tile's n visible key tiles: as many splits as pieces of
+// at most `most` tiles take, of even length.
+struct ChunkSplit {
+  int nsplit, k0, ntile;
+  __device__ __forceinline__ ChunkSplit(int n, int most, int split) {
+    nsplit = n > most ? (n + most - 1) / most : 1;
+    const int each = (n + nsplit - 1) / nsplit;
+    k0 = split * each;
+    ntile = n - k0 < each ? n - k0 : each;
+    if (ntile < 0) ntile = 0;
+  }
+};
+
 // cap * tanh(z / cap) in log2 units from w = 2 z log2(e) / cap:
 // tanh(y) = 1 - 2 / (e^2y + 1), whose absolute error of about 2^-23 is what a
 // score's error has to be measured by (times cap).

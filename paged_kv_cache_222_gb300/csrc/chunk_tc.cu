@@ -168,8 +168,8 @@ __device__ __forceinline__ bool tc_unit(const ChunkParams& p, int x, int y, TcUn
   if (tile < 0 || tile >= ntq) return false;
   const int i0 = tile * p.tile_q, i1 = min(sq.n, i0 + p.tile_q) - 1;
   const ChunkRange rg = chunk_range<NK>(p, sq, i0, i1);
-  const int per_split = p.split_tokens / NK;
-  u.nsplit = max(1, (rg.n + per_split - 1) / per_split);
+  const ChunkSplit sp(rg.n, p.split_tokens / NK, y);
+  u.nsplit = sp.nsplit;
   u.split = y;
   if (u.split >= u.nsplit) return false;
   u.row0 = sq.start + i0;
@@ -181,8 +181,8 @@ __device__ __forceinline__ bool tc_unit(const ChunkParams& p, int x, int y, TcUn
   u.hi = rg.hi;
   u.na = rg.na;
   u.b0 = rg.b0;
-  u.k0 = u.split * per_split;
-  u.ntile = min(rg.n - u.k0, per_split);
+  u.k0 = sp.k0;
+  u.ntile = sp.ntile;
   u.k_bits = u.v_bits = 0;
   if constexpr (FP8) {
     u.k_bits = __float_as_int(p.k_scale[static_cast<int64_t>(u.b) * p.scale_stride + u.h]);

@@ -1431,7 +1431,9 @@ extern "C" pkv_status pkv_chunk_attention(
   });
   if (e == cudaSuccess && pl.max_splits > 1)
     e = traced(pkv::kKindCombine, cs, [&] {
-      return pkv::launch_chunk_combine(p, small ? pkv::kChunkSmallTile : pkv::kChunkTcTile, cs);
+      const int nk = small ? pkv::kChunkSmallTile
+                           : pkv::chunk_tc_tile(c.head_dim, c.dtype == PKV_E4M3, m.softcap > 0.f || m.slopes != nullptr);
+      return pkv::launch_chunk_combine(p, nk, cs);
     });
   if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
   return PKV_OK;

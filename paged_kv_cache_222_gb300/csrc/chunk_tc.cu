@@ -35,21 +35,30 @@
 namespace pkv {
 namespace {
 
-template <int D, bool FP8>
+// What a score is besides scale * q.k: nothing; capped; biased; both.
+constexpr int kPlain = 0, kCapped = 1, kBiased = 2, kCappedBiased = 3;
+
+template <int D, bool FP8, int MODE>
 struct TcShape {
-  static constexpr int M = 128, GROUPS = 2, ROWS = M * GROUPS, NK = 128;
+  static constexpr int M = 128, GROUPS = 2, ROWS = M * GROUPS;
+  // EARLY: P has TMEM columns of its own, so that S(k+1) is issued as soon as the
+  // softmax has read S(k).  They are there for 64-wide heads; 128-wide ones need
+  // 64-key tiles for it.
+  static constexpr bool EARLY = chunk_tc_early(FP8, MODE != kPlain);
+  static constexpr int NK = chunk_tc_tile(D, FP8, MODE != kPlain);
   static constexpr int HALVES = D / 64;            // 128-byte column halves of a 16-bit row
   static constexpr int QHALF = ROWS * 128;
   static constexpr int QBYTES = HALVES * QHALF;
   static constexpr int HALFB = NK * 128;
   static constexpr int TILE = HALVES * HALFB;      // a 16-bit K or V tile
   static constexpr int RAW = NK * D;               // an E4M3 K or V tile
-  static constexpr int NS = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
+  static constexpr int NS = FP8 ? (D == 128 ? 3 : 6) : 131072 / TILE;
   static constexpr int NR = FP8 ? (D == 128 ? 3 : 6) : 0;
-  static constexpr int STAGE = 32 * 64;            // output staging of a softmax warp: 64 bytes of its rows
+  static constexpr int SB = 64;                    // output staging of a softmax warp: SB bytes of its 32 rows
+  static constexpr int STAGE = 32 * SB;
   static constexpr int RU = 4;                     // units in flight between the roles
   static constexpr int UNIT = 20;                  // words of one
-  static constexpr int NBARS = 2 * NS + 2 * NR + 3 * GROUPS + 5 + 2 * RU + GROUPS;
+  static constexpr int NBARS = 2 * NS + 2 * NR + 5 * GROUPS + 5 + 2 * RU + GROUPS;
   static constexpr int BYTES = QBYTES + NS * TILE + NR * RAW + 8 * STAGE + 16 + NBARS * 8 + RU * UNIT * 4 + 16 + 1024;
   static_assert(BYTES <= 232448, "shared memory per CTA");
   static constexpr int THREADS = FP8 ? 512 : 384;
@@ -78,9 +87,6 @@ struct TcUnit {
     return ntile > 0 && tail_first(nk) < nk && tail_first(nk) % block_size != 0;
   }
 };
-
-// What a score is besides scale * q.k: nothing; capped; biased; both.
-constexpr int kPlain = 0, kCapped = 1, kBiased = 2, kCappedBiased = 3;
 
 __device__ __forceinline__ float min_nan(float a, float b) {  // NaN if one is
   float d;
@@ -192,12 +198,15 @@ __device__ __forceinline__ bool tc_unit(const ChunkParams& p, int x, int y, TcUn
 }
 
 template <int D, bool FP8, int MODE>
-__global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
+__global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
     chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v, const ChunkParams p) {
-  using C = TcShape<D, FP8>;
+  using C = TcShape<D, FP8, MODE>;
   constexpr int M = C::M, NK = C::NK, NS = C::NS, NR = C::NR, GROUPS = C::GROUPS, RU = C::RU;
-  constexpr uint32_t COL_S = 0, COL_O = GROUPS * NK;  // + g * NK, + g * D
+  constexpr bool EARLY = C::EARLY;
+  // + g * NK, + g * (EARLY ? NK / 2 : NK), + g * D
+  constexpr uint32_t COL_S = 0, COL_P = EARLY ? GROUPS * NK : COL_S, COL_O = COL_P + GROUPS * (EARLY ? NK / 2 : NK);
+  constexpr uint32_t P_STEP = EARLY ? NK / 2 : NK;
   constexpr uint32_t IDESC_S = FP8 ? idesc_f16(M, NK, false) : idesc_bf16(M, NK, false);
   constexpr uint32_t IDESC_PV = FP8 ? idesc_f16(M, D, true) : idesc_bf16(M, D, true);
   constexpr int kMma = 8, kLoadK = 9, kLoadV = 10, kMma1 = 11, kConv = 12;
@@ -223,7 +232,9 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
   uint64_t* rempty = rfull + NR;
   uint64_t* sfull = rempty + NR;     // [GROUPS]: S_g of the next tile is in TMEM
   uint64_t* pfull = sfull + GROUPS;  // [GROUPS]: P_g is in TMEM
-  uint64_t* odone = pfull + GROUPS;  // [GROUPS]: O_g of the unit is complete
+  uint64_t* sfree = pfull + GROUPS;  // [GROUPS]: the softmax has read S_g (EARLY)
+  uint64_t* pfree = sfree + GROUPS;  // [GROUPS]: P_g's product has completed (EARLY)
+  uint64_t* odone = pfree + GROUPS;  // [GROUPS]: O_g of the unit is complete
   uint64_t* qfull = odone + GROUPS;  // Q of the unit is in shared memory
   uint64_t* qready = qfull + 1;      // ... as f16 (E4M3 caches)
   uint64_t* qempty = qready + 1;     // every S of the unit has read it
@@ -248,6 +259,8 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
     for (int g = 0; g < GROUPS; ++g) {
       mbar_init(smem_u32(sfull + g), 1);
       mbar_init(smem_u32(pfull + g), 4);
+      mbar_init(smem_u32(sfree + g), 4);
+      mbar_init(smem_u32(pfree + g), 1);
       mbar_init(smem_u32(odone + g), 1);
       mbar_init(smem_u32(done + g), 1);
     }
@@ -303,7 +316,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
       const int g = warp == kMma ? 0 : 1;
       const uint32_t leader = elect_one();
       const uint32_t ring0 = __shfl_sync(kFull, smem_u32(ring), 0), q0 = __shfl_sync(kFull, smem_u32(q_sm), 0);
-      const uint32_t c_s = tbase + COL_S + g * NK, c_o = tbase + COL_O + g * D;
+      const uint32_t c_s = tbase + COL_S + g * NK, c_p = tbase + COL_P + g * P_STEP, c_o = tbase + COL_O + g * D;
       const uint64_t a0 = smem_desc_sw128(q0 + g * M * 128, 0, 1024);
       int slot = 0, use = 0;  // ring slot of the next item, and its use number
       int pk = 0, tails = 0;  // this group's tiles so far; units with a zeroed tail so far
@@ -342,36 +355,44 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
         ok = wait(FP8 ? qready : qfull, n);
         if (ok && u.ntile > 0) {
           ok = wait(full + slot, use);
+          if (EARLY && ok && pk > 0) ok = wait(sfree + g, pk - 1);
           if (!ok) break;
           tc_fence_after();
           issue_s();
         }
         if (u.ntile <= 1) tc_commit_if(leader, smem_u32(qempty));
         for (int k = 0; k < u.ntile && ok; ++k, ++pk) {
-          const int vslot = slot;
-          ok = wait(full + vslot, use);
+          const int vslot = slot, vuse = use;
+          next_slot();
+          const bool more = k + 1 < u.ntile;
+          if (EARLY && more) {  // S(k+1), once the softmax has read S(k)
+            ok = wait(full + slot, use) && wait(sfree + g, pk);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s();
+            if (k + 2 == u.ntile) tc_commit_if(leader, smem_u32(qempty));  // the unit's last S
+          }
+          ok = wait(full + vslot, vuse);
           if (!ok) break;
           if (tail && k == u.ntile - 1) {  // its loader has zeroed the rows past the sequence's end
             ok = wait(vfix, tails++);
             if (!ok) break;
           }
-          next_slot();
-          const bool more = k + 1 < u.ntile;
-          if (more) ok = wait(full + slot, use);  // K(k+1), ahead of the wait for P
+          if (!EARLY && more) ok = wait(full + slot, use);  // K(k+1), ahead of the wait for P
           const uint64_t v0 = smem_desc_sw128(ring0 + vslot * C::TILE, C::HALVES > 1 ? C::HALFB : 0, 1024);
           ok = ok && wait(pfull + g, pk);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < NK / 16; ++kk)  // MN-major V: 8-key groups 1024 B apart, column halves HALFB apart
-            tc_mma_ts_if(leader, c_o, c_s + kk * 8, v0 + kk * (2048 / 16), IDESC_PV, (k > 0 || kk > 0) ? 1u : 0u);
+            tc_mma_ts_if(leader, c_o, c_p + kk * 8, v0 + kk * (2048 / 16), IDESC_PV, (k > 0 || kk > 0) ? 1u : 0u);
+          if (EARLY) tc_commit_if(leader, smem_u32(pfree + g));
           tc_commit_if(leader, smem_u32(empty + vslot));
-          if (more) {
+          if (!EARLY && more) {
             issue_s();
             if (k + 2 == u.ntile) tc_commit_if(leader, smem_u32(qempty));  // the unit's last S
-          } else {
-            tc_commit_if(leader, smem_u32(odone + g));
           }
+          if (!more) tc_commit_if(leader, smem_u32(odone + g));
         }
       }
       // nothing of this warp's may still be running when TMEM is freed
@@ -511,6 +532,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
       // of the unit's Q (bf16 -> f16, in place) and its K and V tiles (thread t:
       // key t of the tile, 16 codes -> 32 bytes at a time)
       if constexpr (FP8) {
+        static_assert(NK == 128, "a widening thread per key");
         const int t = (warp - kConv) * 32 + lane;
         constexpr int CH = D / 16;                     // 16-byte chunks of a raw row
         const uint32_t rsw = D == 128 ? (t & 7) : ((t >> 1) & 3);
@@ -579,7 +601,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
     // -------------------------------------------------------------- softmax
     const int grp = warp >> 2;
     const uint32_t lanes = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t t_s = lanes + COL_S + grp * NK, t_o = lanes + COL_O + grp * D;
+    const uint32_t t_s = lanes + COL_S + grp * NK, t_p = lanes + COL_P + grp * P_STEP, t_o = lanes + COL_O + grp * D;
     uint8_t* stage = s_stage + warp * C::STAGE;
     // r / G for a row r < 256 of the tile: exact, since r times the rounding of
     // the reciprocal (less than G / 65536) stays below 1 / G
@@ -615,6 +637,11 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
 #pragma unroll
           for (int c = 0; c < NK / 32; ++c) tmem_ld32(t_s + 32 * c, x + 32 * c);
           tmem_wait_ld();
+          if constexpr (EARLY) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(sfree + grp));  // S may be overwritten
+          }
           const int t0 = u.tile(k) * NK;
           const bool whole = (t0 + NK - 1 <= pos && t0 >= lo) || t0 + NK <= pf;
           const bool masked = !__all_sync(kFull, whole);
@@ -676,7 +703,12 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
             m_used = mt;
             resc = true;
           }
-          if (__any_sync(kFull, resc)) {  // O holds tiles 0..k-1 (PV(k-1) came before S(k))
+          if (EARLY && sk > 0) {  // P(k-1)'s product has read it (and O holds tiles 0..k-1)
+            ok = wait(pfree + grp, sk - 1);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          if (__any_sync(kFull, resc)) {  // O holds tiles 0..k-1 (else PV(k-1) came before S(k))
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += 32) {
               uint32_t u[2][16];
@@ -712,7 +744,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
                 ls[i & 1] = __fadd2_rn(ls[i & 1], pp);
                 hi[i] = FP8 ? pack_f16x2(pp.x, pp.y) : pack_bf16x2(pp.x, pp.y);
               }
-              tmem_st16(t_s + 16 * c, hi);
+              tmem_st16(t_p + 16 * c, hi);
             }
           };
           if constexpr (MODE == kPlain) {
@@ -730,6 +762,10 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
           }
           lsum += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
           tmem_wait_st();
+        } else if constexpr (EARLY) {
+          if (lane == 0) mbar_arrive(smem_u32(sfree + grp));
+          if (sk > 0) ok = wait(pfree + grp, sk - 1);
+          if (!ok) break;
         }
         tc_fence_before();
         __syncwarp();
@@ -737,29 +773,12 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
       }
       if (ok && u.ntile > 0) ok = wait(odone + grp, outs++);
       if (ok && warp_ok) {
-        // ---- O leaves through the warp's staging, 64 bytes of its rows per
-        // pass, so that a store instruction writes whole 64-byte pieces: bf16
-        // outputs 32 columns at a time, binary32 pieces of split rows 16
+        // ---- O leaves through the warp's staging, SB bytes of its rows per
+        // pass, so that a store instruction writes whole pieces of that size
         tc_fence_after();
         const float inv = lsum > 0.f ? (FP8 ? __int_as_float(u.v_bits) / lsum : 1.f / lsum) : 0.f;
         const bool direct = u.nsplit == 1;
         const float mult = direct ? inv : (FP8 ? __int_as_float(u.v_bits) : 1.f);
-        // chunk c (16 bytes) of row r at r * 64 + ((c ^ (r / 2 % 4)) * 16): eight
-        // consecutive rows' chunks c lie in distinct banks
-        auto at = [&](int r, int c) { return stage + r * 64 + ((c ^ ((r >> 1) & 3)) << 4); };
-        auto row_of = [&](int r) {                       // output row of the warp's row r
-          const int rr = warp * 32 + r, tk = token_of(rr);
-          return static_cast<int64_t>(u.row0 + tk) * H_q + u.h * G + (rr - tk * G);
-        };
-        // this lane stores chunk lane % 4 of rows lane / 4 + 8 i
-        int64_t to[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = (lane >> 2) + 8 * i;
-          to[i] = warp * 32 + r < u.rows ? (direct ? row_of(r) * D + (lane & 3) * 8
-                                                    : (row_of(r) * p.max_splits + u.split) * D + (lane & 3) * 4)
-                                         : -1;
-        }
         float o[D];
         if (u.ntile > 0) {
 #pragma unroll
@@ -770,12 +789,40 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
           for (int i = 0; i < D; ++i) o[i] = 0.f;
         }
         tc_fence_before();  // O has been read: the next unit's products may overwrite it after P's hand-over
+        constexpr int CR = C::SB / 16;                   // 16-byte chunks of a row and pass
+        // chunk c of row r, placed so that eight consecutive rows' chunks c lie
+        // in distinct banks
+        auto at = [&](int r, int c) { return stage + r * C::SB + ((c ^ (r * C::SB / 128 % CR)) << 4); };
+        auto row_of = [&](int r) {                       // output row of the warp's row r
+          const int rr = warp * 32 + r, tk = token_of(rr);
+          return static_cast<int64_t>(u.row0 + tk) * H_q + u.h * G + (rr - tk * G);
+        };
+        // this lane stores chunk lane % CR of rows lane / CR + (32 / CR) i: byte
+        // offsets in the output or the workspace, -1 past the tile's rows
+        int64_t to[CR];
+#pragma unroll
+        for (int i = 0; i < CR; ++i) {
+          const int r = lane / CR + (32 / CR) * i;
+          const int64_t at_row = direct ? row_of(r) * (D * 2) : (row_of(r) * p.max_splits + u.split) * (D * 4);
+          to[i] = warp * 32 + r < u.rows ? at_row + (lane % CR) * 16 : -1;
+        }
+        char* dst = direct ? static_cast<char*>(p.out) : reinterpret_cast<char*>(p.ws_o);
+        auto leave = [&](int pass) {                     // SB bytes of every row
+          __syncwarp();
+          uint4 w[CR];
+#pragma unroll
+          for (int i = 0; i < CR; ++i) w[i] = *reinterpret_cast<const uint4*>(at(lane / CR + (32 / CR) * i, lane % CR));
+#pragma unroll
+          for (int i = 0; i < CR; ++i)
+            if (to[i] >= 0) *reinterpret_cast<uint4*>(dst + to[i] + pass * C::SB) = w[i];
+          __syncwarp();
+        };
         if (direct) {
 #pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 32) {
+          for (int pass = 0; pass < D * 2 / C::SB; ++pass) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float* v = o + c0 + 8 * i;
+            for (int i = 0; i < CR; ++i) {
+              const float* v = o + pass * (C::SB / 2) + 8 * i;
               uint4 w;
               w.x = pack_bf16x2(v[0] * mult, v[1] * mult);
               w.y = pack_bf16x2(v[2] * mult, v[3] * mult);
@@ -783,32 +830,17 @@ __global__ void __launch_bounds__(TcShape<D, FP8>::THREADS, 1)
               w.w = pack_bf16x2(v[6] * mult, v[7] * mult);
               *reinterpret_cast<uint4*>(at(lane, i)) = w;
             }
-            __syncwarp();
-            uint4 w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(at((lane >> 2) + 8 * i, lane & 3));
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (to[i] >= 0)
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + to[i] + c0) = w[i];
-            __syncwarp();
+            leave(pass);
           }
         } else {
 #pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 16) {
+          for (int pass = 0; pass < D * 4 / C::SB; ++pass) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float* v = o + c0 + 4 * i;
+            for (int i = 0; i < CR; ++i) {
+              const float* v = o + pass * (C::SB / 4) + 4 * i;
               *reinterpret_cast<float4*>(at(lane, i)) = make_float4(v[0] * mult, v[1] * mult, v[2] * mult, v[3] * mult);
             }
-            __syncwarp();
-            float4 w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(at((lane >> 2) + 8 * i, lane & 3));
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (to[i] >= 0) *reinterpret_cast<float4*>(p.ws_o + to[i] + c0) = w[i];
-            __syncwarp();
+            leave(pass);
           }
         }
         if (!direct && row_ok) {
@@ -832,12 +864,12 @@ template <int D, bool FP8, int MODE>
 cudaError_t launch_tc_t(const ChunkParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
   auto kern = chunk_tc_kernel<D, FP8, MODE>;
   // at least 120 KB: one CTA per SM (it holds all 512 TMEM columns)
-  constexpr int smem = TcShape<D, FP8>::BYTES > 120 * 1024 ? TcShape<D, FP8>::BYTES : 120 * 1024;
+  constexpr int smem = TcShape<D, FP8, MODE>::BYTES > 120 * 1024 ? TcShape<D, FP8, MODE>::BYTES : 120 * 1024;
   static int configured[64] = {};
   cudaError_t e = set_smem_once(kern, smem, configured);
   if (e != cudaSuccess) return e;
   const int tiles = p.n_tokens / p.tile_q + p.batch;
-  return launch_pdl(kern, dim3(tiles * p.num_kv_heads, p.max_splits), dim3(TcShape<D, FP8>::THREADS), smem, stream,
+  return launch_pdl(kern, dim3(tiles * p.num_kv_heads, p.max_splits), dim3(TcShape<D, FP8, MODE>::THREADS), smem, stream,
                     tq, tk, tv, p);
 }
 

@@ -284,8 +284,13 @@ inline int multi_query_lanes(int rows) { return rows <= 16 ? 4 : (rows <= 32 ? 2
 constexpr int kChunkSmallRows = 16;
 constexpr int kChunkTcRows = 256;
 constexpr int kChunkMaxSplitBlocks = 1024;
-// Keys per tile of the two kernels.
+// Keys per tile: of the mma.sync kernel; of the tcgen05 kernel at most, and by
+// its variant (chunk_tc.cu: whether S(k+1) is issued ahead of P(k)'s product).
 constexpr int kChunkSmallTile = 64, kChunkTcTile = 128;
+constexpr bool chunk_tc_early(bool fp8, bool mods) { return !fp8 && mods; }
+constexpr int chunk_tc_tile(int head_dim, bool fp8, bool mods) {
+  return head_dim == 128 && chunk_tc_early(fp8, mods) ? 64 : kChunkTcTile;
+}
 
 // Rows of query heads one cascade prefix CTA covers: two groups of 128 TMEM
 // lanes.

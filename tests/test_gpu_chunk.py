@@ -117,6 +117,112 @@ def test_large_and_peaked_scores(lens, kv):
     C.check(run(case), case, ref, 2 * tol)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("softcap,q_mult,bias", [(5.0, 30.0, False), (50.0, 12.0, False), (50.0, 40.0, False),
+                                                 (30.0, 12.0, True)])
+@pytest.mark.parametrize("lens", [SINGLE, RAGGED], ids=["single", "ragged"])
+def test_caps_that_bite(lens, softcap, q_mult, bias, D, kv):
+    # scores from far below the cap to many times it.  A product is off by at
+    # most D 2^-23 sum |q k| scale (about 2^-16 x 8 x q_mult), which the cap's slope, at
+    # most 1, does not enlarge; the cap's own error is below 3e-6 of a score up to
+    # 0.35 softcap and cap x 2^-22 above: 2^-8 of a weight in all
+    case = C.make_case(*lens, 8, 2, D, 16, kv, softcap=softcap, bias=bias, seed=41, q_mult=q_mult)
+    ref, tol = C.want(case)
+    C.check(run(case), case, ref, 2 * tol)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("mods", [{}, dict(softcap=30.0)], ids=["plain", "capped"])
+def test_many_short_sequences(mods, kv):
+    # more sequences than one round of the search over their starts looks at,
+    # many of them without new tokens, more row tiles than SMs
+    rng = np.random.default_rng(3)
+    q = rng.integers(0, 30, 1500)
+    q[rng.random(1500) < 0.3] = 0
+    ctx = q + rng.integers(0, 40, 1500)
+    case = C.make_case(q.tolist(), ctx.tolist(), 4, 2, 64, 16, kv, seed=14, **mods)
+    C.check(run(case), case)
+
+
+@pytest.mark.parametrize("n", [40, 300])
+def test_many_pieces_per_row(n):
+    # 47 and more pieces of 128 tokens: the merges by whole CTAs and by warps
+    case = C.make_case([n, 1], [6000 + n, 7001], 8, 1, 128, 16, seed=15)
+    C.check(run(case, split_tokens=128), case)
+    case = C.make_case([1, 1], [6000, 7001], 16, 1, 64, 32, "e4m3", seed=16)
+    C.check(run(case, split_tokens=128), case)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_a_sequence_of_a_hundred_thousand_tokens(n):
+    case = C.make_case([n], [150_001], 1, 1, 64, 16, bias=True, seed=17)
+    C.check(run(case), case)
+    case = C.make_case([n], [150_001], 1, 1, 64, 16, window=3000, prefix=[5], seed=17)
+    C.check(run(case), case)
+
+
+def test_two_calls_at_once_on_two_streams():
+    cases = [C.make_case(*RAGGED, 8, 2, 128, 16, seed=51), C.make_case(*RAGGED, 8, 2, 128, 16, softcap=20.0, seed=52)]
+    args = [C.device_args(c, DEV) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(pkv.chunk_attention(*args[i][0], **dict(args[i][1], split_tokens=128 if i else 0)))
+    torch.cuda.synchronize()
+    assert pkv.device_error(DEV) == 0
+    for i, c in enumerate(cases):
+        ref, tol = C.want(c)
+        for o in outs[i]:
+            C.check(o, c, ref, tol)
+
+
+def test_default_bounds_are_the_tensors_own():
+    case = C.make_case(*RAGGED, 8, 2, 128, 16, seed=53)
+    args, kw = C.device_args(case, DEV)
+    out = pkv.chunk_attention(*args)
+    assert pkv.device_error(DEV) == 0
+    C.check(out, case)
+
+
+def test_refusals():
+    case = C.make_case([4, 1], [40, 20], 8, 2, 128, 16, seed=2)
+    args, kw = C.device_args(case, DEV)
+    q, k, v, t, c, s, scale = args
+    call = pkv.chunk_attention
+    for bad, err in [
+        ((q.float(), k, v, t, c, s, scale), TypeError), ((q[:, :, :64].contiguous(), k, v, t, c, s, scale), ValueError),
+        ((q.transpose(0, 1), k, v, t, c, s, scale), ValueError), ((q, k, v[:-1], t, c, s, scale), ValueError),
+        ((q, k, v, t.long(), c, s, scale), TypeError), ((q, k, v, t[:1], c, s, scale), ValueError),
+        ((q, k, v, t, c[:1], s, scale), ValueError), ((q, k, v, t, c, s[:-1], scale), ValueError),
+        ((q, k, v, t, c, s.cpu(), scale), ValueError), ((q, k, v, t, c, s, 0.0), pkv.PkvError),
+        ((q[:, :7].contiguous(), k, v, t, c, s, scale), pkv.PkvError),
+    ]:
+        with pytest.raises(err):
+            call(*bad, **kw)
+    for bad, err in [(dict(out=torch.empty_like(q).float()), TypeError), (dict(out=q[:1]), ValueError),
+                     (dict(slopes=torch.zeros(7, device=DEV)), ValueError),
+                     (dict(prefix_lens=torch.zeros(3, dtype=torch.int32, device=DEV)), ValueError),
+                     (dict(softcap=-1.0), pkv.PkvError), (dict(window=-1), pkv.PkvError),
+                     (dict(max_context_len=10 ** 6), pkv.PkvError), (dict(split_tokens=100), pkv.PkvError),
+                     (dict(k_scale=torch.ones(2, device=DEV)), ValueError),
+                     (dict(split_tokens=128, max_context_len=48, workspace=torch.empty(0, dtype=torch.uint8, device=DEV)),
+                      None)]:
+        if err is None:
+            call(*args, **dict(kw, **bad))  # one piece: no workspace needed
+            continue
+        with pytest.raises(err):
+            call(*args, **dict(kw, **bad))
+    with pytest.raises(pkv.PkvError):  # two pieces, too little workspace
+        big = C.make_case([1], [400], 8, 2, 128, 16)
+        a, kk = C.device_args(big, DEV)
+        call(*a, **dict(kk, split_tokens=128, workspace=torch.empty(256, dtype=torch.uint8, device=DEV)))
+    assert pkv.device_error(DEV) == 0
+
+
 def test_a_long_sequence_and_far_blocks():
     # block ids past 2^17 at 8 KV heads: byte offsets beyond 2^32
     nb, bs, hkv, d = 140_000, 16, 8, 128
@@ -157,20 +263,20 @@ def test_captured_graphs_with_workspaces_of_their_own(lens):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             pkv.chunk_attention(*args, **kw)
-        runs.append((g, out, args))
+        runs.append((g, out, args, kw))  # a graph's inputs and workspace live as long as it is replayed
     streams = [torch.cuda.Stream() for _ in runs]
-    for _, out, _ in runs:
+    for _, out, _, _ in runs:
         out.zero_()
     torch.cuda.synchronize()
     for _ in range(3):
-        for (g, _, _), s in zip(runs, streams):
+        for (g, _, _, _), s in zip(runs, streams):
             with torch.cuda.stream(s):
                 g.replay()
     torch.cuda.synchronize()
-    for (_, out, _), c, (ref, tol) in zip(runs, cases, refs):
+    for (_, out, _, _), c, (ref, tol) in zip(runs, cases, refs):
         C.check(out, c, ref, tol)
     # new inputs through the captured pointers
-    g, out, args = runs[0]
+    g, out, args, _ = runs[0]
     args[0].copy_(cases[1]["q"])
     cases[0]["q"] = cases[1]["q"]
     g.replay()

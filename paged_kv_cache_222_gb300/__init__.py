@@ -3,7 +3,9 @@
 Every function here only checks tensor shapes / dtypes and hands raw device
 pointers plus the current CUDA stream to the C ABI (include/pkv.h); all of the
 computation runs in the library's sm_103a kernels.  PyTorch supplies device
-memory and streams.
+memory and streams.  The calls made once per layer and step on a few tokens
+(chunk_attention, rotary_append, compact_tokens) do this in a compiled module
+(csrc/binding.cpp), the others through ctypes.
 
     append(k_new, v_new, slot_mapping, k_cache, v_cache[, k_scale, v_scale])
     decode_attention(q, k_cache, v_cache, block_tables, context_lens, scale
@@ -18,7 +20,6 @@ Cache tensors are [num_blocks, H_kv, block_size, head_dim], bf16 or E4M3
 """
 
 import ctypes
-import functools
 import math
 
 import numpy as np
@@ -26,7 +27,7 @@ import torch
 
 from . import _lib
 from ._lib import (PKV_BF16, PKV_E4M3, PKV_F32, CacheDesc, DecodePlan, PkvError,  # noqa: F401
-                   ScoreMods, TraceEntry)
+                   TraceEntry)
 
 __all__ = ["append", "decode_attention", "decode_plan", "cache_desc", "slot_mapping",
            "cascade_plan", "cascade_decode_attention", "multi_query_plan", "multi_query_attention",
@@ -322,74 +323,6 @@ def multi_query_attention(q, k_cache, v_cache, block_tables, context_lens, scale
     return out
 
 
-# The serving calls below run once per layer and step, many of them on a few
-# tokens, where the host's time is what counts: their checks are single
-# comparisons on the good path (the helper that names the fault runs on the bad
-# one), descriptors and plans are kept by their sizes, and the stream is read
-# without building a torch.cuda.Stream.
-
-def _check(t, dtype, name, index, device):
-    if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
-        _contig(t, dtype, name, device)
-
-
-@functools.lru_cache(maxsize=256)
-def _desc_of(shape, dtype):
-    if len(shape) != 4:
-        raise ValueError("cache must be [num_blocks, num_kv_heads, block_size, head_dim]")
-    if dtype == torch.bfloat16:
-        kind = PKV_BF16
-    elif dtype in (torch.uint8, torch.float8_e4m3fn):
-        kind = PKV_E4M3
-    else:
-        raise TypeError(f"cache dtype {dtype}: expected bfloat16 or uint8/float8_e4m3fn")
-    desc = CacheDesc(shape[0], shape[2], shape[1], shape[3], kind)
-    return desc, ctypes.byref(desc), (shape[0], shape[2], shape[1], shape[3], kind)
-
-
-def _caches(k_cache, v_cache):
-    """(device index, device, descriptor, pointer to it, its fields) of a pair of caches."""
-    shape, dtype, index = k_cache.shape, k_cache.dtype, k_cache.get_device()
-    if (v_cache.shape != shape or v_cache.dtype is not dtype or index < 0 or v_cache.get_device() != index
-            or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
-        _check_pair(k_cache, v_cache)
-    return (index, k_cache.device) + _desc_of(shape, dtype)
-
-
-def _on_device(index, call, *args):
-    """call(*args, stream) with `index` the current device, on its current stream."""
-    if torch.cuda.current_device() == index:
-        return call(*args, torch._C._cuda_getCurrentRawStream(index))
-    with torch.cuda.device(index):
-        return call(*args, torch._C._cuda_getCurrentRawStream(index))
-
-
-@functools.lru_cache(maxsize=None)
-def _num_sms(index):
-    return torch.cuda.get_device_properties(index).multi_processor_count
-
-
-def _scale_stride(k_scale, v_scale, rows, heads, dev, stride):
-    """Row stride of an E4M3 cache's scales, [rows, H_kv] or [H_kv] each."""
-    if k_scale is None or v_scale is None:
-        raise ValueError("E4M3 cache needs k_scale and v_scale")
-    _check(k_scale, torch.float32, "k_scale", dev.index, dev)
-    _check(v_scale, torch.float32, "v_scale", dev.index, dev)
-    shape = k_scale.shape
-    if v_scale.shape != shape:
-        raise ValueError("k_scale and v_scale differ in shape")
-    if stride is None:
-        if shape == (rows, heads):
-            return heads
-        if shape == (heads,):
-            return 0
-        raise ValueError(f"k_scale and v_scale must be [{rows}, {heads}] or [{heads}]")
-    stride = int(stride)
-    if stride < 0 or (rows > 0 and k_scale.numel() < stride * (rows - 1) + heads):
-        raise ValueError("scale_row_stride reaches past the scales")
-    return stride
-
-
 def chunk_plan(n_tokens, batch, max_q_len, num_q_heads, k_cache_or_desc, max_context_len, window=0,
                has_prefix=False, split_tokens=0, num_sms=0):
     """Plan of a chunk_attention call (host only): visible tokens per split,
@@ -400,14 +333,6 @@ def chunk_plan(n_tokens, batch, max_q_len, num_q_heads, k_cache_or_desc, max_con
                                         ctypes.byref(desc), int(max_context_len), int(window), int(bool(has_prefix)),
                                         int(split_tokens), int(num_sms), ctypes.byref(plan)), "pkv_chunk_plan")
     return plan
-
-
-@functools.lru_cache(maxsize=4096)
-def _chunk_workspace(n_tokens, batch, max_q_len, num_q_heads, desc, max_context_len, window, has_prefix,
-                     split_tokens, num_sms):
-    """Workspace bytes of a chunk_plan (a function of these numbers alone)."""
-    return int(chunk_plan(n_tokens, batch, max_q_len, num_q_heads, CacheDesc(*desc), max_context_len, window,
-                          has_prefix, split_tokens, num_sms).workspace_bytes)
 
 
 def chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_starts, scale, max_q_len=None,
@@ -428,66 +353,12 @@ def chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_starts, s
     pos (window 0: t <= pos).  E4M3 caches take k_scale / v_scale float32 [B,
     H_kv] or [H_kv].
     """
-    index, dev, desc, desc_ptr, fields = _caches(k_cache, v_cache)
-    _check(q, torch.bfloat16, "q", index, dev)
-    _check(q_starts, torch.int32, "q_starts", index, dev)
-    _check(block_tables, torch.int32, "block_tables", index, dev)
-    _check(context_lens, torch.int32, "context_lens", index, dev)
-    shape = q.shape
-    if len(shape) != 3 or shape[2] != fields[3]:
-        raise ValueError("q must be [T, H_q, head_dim]")
-    t, hq, _ = shape
-    if q_starts.dim() != 1 or q_starts.shape[0] < 1:
-        raise ValueError("q_starts must be [B + 1]")
-    b = q_starts.shape[0] - 1
-    if block_tables.dim() != 2 or block_tables.shape[0] != b or context_lens.shape != (b,):
-        raise ValueError("block_tables must be [B, MB] and context_lens [B]")
-    mb = block_tables.shape[1]
-    max_q_len = max(t, 1) if max_q_len is None else int(max_q_len)
-    max_context_len = mb * fields[1] if max_context_len is None else int(max_context_len)
-    split_tokens, window = int(split_tokens), int(window)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _check(out, torch.bfloat16, "out", index, dev)
-        if out.shape != shape:
-            raise ValueError("out must be [T, H_q, D]")
-    ks = vs = None
-    stride = 0
-    if fields[4] == PKV_E4M3:
-        stride = _scale_stride(k_scale, v_scale, b, fields[2], dev, scale_row_stride)
-        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
-    elif k_scale is not None or v_scale is not None:
-        raise ValueError("scales given for a bf16 cache")
-    sl = pf = None
-    if slopes is not None:
-        _check(slopes, torch.float32, "slopes", index, dev)
-        if slopes.shape != (hq,):
-            raise ValueError("slopes must be [H_q]")
-        sl = slopes.data_ptr()
-    if prefix_lens is not None:
-        _check(prefix_lens, torch.int32, "prefix_lens", index, dev)
-        if prefix_lens.shape != (b,):
-            raise ValueError("prefix_lens must be [B]")
-        pf = prefix_lens.data_ptr()
-    # planned for this device's SMs, as the library plans the call itself
-    need = _chunk_workspace(t, b, max_q_len, hq, fields, max_context_len, window, pf is not None, split_tokens,
-                            _num_sms(index))
-    ws, have = None, 0
-    if need > 0:
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        else:
-            _check(workspace, torch.uint8, "workspace", index, dev)
-        ws, have = workspace.data_ptr(), workspace.numel()
-    st = _on_device(index, library().pkv_chunk_attention,
-                    q.data_ptr(), t, q_starts.data_ptr(), b, max_q_len, hq, k_cache.data_ptr(), v_cache.data_ptr(),
-                    desc_ptr, block_tables.data_ptr(), mb, context_lens.data_ptr(), max_context_len, scale,
-                    ctypes.byref(ScoreMods(softcap, window, sl, pf)), out.data_ptr(), ks, vs, stride, ws, have,
-                    split_tokens)
-    if st:
-        _lib.check(st, "pkv_chunk_attention")
-    return out
+    r = _lib.binding().chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_starts, scale, max_q_len,
+                                       max_context_len, k_scale, v_scale, softcap, window, slopes, prefix_lens, out,
+                                       workspace, split_tokens, scale_row_stride)
+    if type(r) is int:
+        _lib.check(r, "pkv_chunk_attention")
+    return r
 
 
 def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_len=None, beta_fast=32.0,
@@ -525,22 +396,6 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, origi
     return f.to(device) if device is not None else f
 
 
-def _token_rows(t, name, dtype, shape, index, dev):
-    """[N, heads, D] tensor whose tokens may lie further apart than their rows
-    (a slice of a fused projection); returns the elements between tokens."""
-    n, heads, d = shape
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on {dev}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be [{n}, {heads}, {d}]")
-    between, head, one = t.stride()
-    if one != 1 or (heads > 1 and head != d):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return between if n > 1 else heads * d
-
-
 def rotary_append(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=None,
                   magnitude=1.0, interleaved=False, out=None, scale_row_stride=None):
     """Turn new tokens' queries and keys by their rotary angles, append keys
@@ -553,49 +408,11 @@ def rotary_append(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, 
     rotary_dim pass through.  slot_mapping and scales as `append` (a negative
     slot stores nothing; its query is still returned).  `out` may be q itself.
     """
-    index, dev, desc, desc_ptr, fields = _caches(k_cache, v_cache)
-    shape, dtype = q.shape, q.dtype
-    if len(shape) != 3:
-        raise ValueError("q must be [N, H_q, D]")
-    n, hq, d = shape
-    if d != fields[3]:
-        raise ValueError("q's head_dim does not match the cache")
-    if dtype is torch.bfloat16:
-        src = PKV_BF16
-    elif dtype is torch.float32:
-        src = PKV_F32
-    else:
-        raise TypeError(f"q dtype {dtype}: expected bfloat16 or float32")
-    kv_shape = (n, fields[2], d)
-    q_st = _token_rows(q, "q", dtype, shape, index, dev)
-    k_st = _token_rows(k, "k", dtype, kv_shape, index, dev)
-    v_st = _token_rows(v, "v", dtype, kv_shape, index, dev)
-    _check(positions, torch.int64, "positions", index, dev)
-    _check(slot_mapping, torch.int64, "slot_mapping", index, dev)
-    _check(inv_freq, torch.float64, "inv_freq", index, dev)
-    if positions.shape != (n,) or slot_mapping.shape != (n,):
-        raise ValueError("positions and slot_mapping must have one entry per token")
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be [rotary_dim / 2]")
-    if out is None:
-        out, o_st = torch.empty(shape, dtype=torch.bfloat16, device=dev), hq * d
-    else:
-        o_st = _token_rows(out, "out", torch.bfloat16, shape, index, dev)
-    ks = vs = None
-    stride = 0
-    if fields[4] == PKV_E4M3:
-        stride = _scale_stride(k_scale, v_scale, n, fields[2], dev, scale_row_stride)
-        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
-    elif k_scale is not None or v_scale is not None:
-        raise ValueError("scales given for a bf16 cache")
-    st = _on_device(index, library().pkv_rotary_append,
-                    q.data_ptr(), q_st, k.data_ptr(), k_st, v.data_ptr(), v_st, src, n, hq, positions.data_ptr(),
-                    inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0, magnitude,
-                    slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), desc_ptr, ks, vs, stride,
-                    out.data_ptr(), o_st)
-    if st:
-        _lib.check(st, "pkv_rotary_append")
-    return out
+    r = _lib.binding().rotary_append(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, k_scale, v_scale,
+                                     magnitude, interleaved, out, scale_row_stride)
+    if type(r) is int:
+        _lib.check(r, "pkv_rotary_append")
+    return r
 
 
 def compact_tokens(k_cache, v_cache, block_tables, keep, keep_starts, dst_start=None, max_keep=None):
@@ -607,27 +424,8 @@ def compact_tokens(k_cache, v_cache, block_tables, keep, keep_starts, dst_start=
     must not lie before it.  `max_keep` is a host bound on a sequence's entries
     (default N).  Shorten the sequences afterwards (BlockManager.truncate).
     """
-    index, dev, desc, desc_ptr, fields = _caches(k_cache, v_cache)
-    _check(block_tables, torch.int32, "block_tables", index, dev)
-    _check(keep, torch.int32, "keep", index, dev)
-    _check(keep_starts, torch.int32, "keep_starts", index, dev)
-    if block_tables.dim() != 2 or keep.dim() != 1:
-        raise ValueError("block_tables must be [B, MB] and keep 1-D")
-    b, mb = block_tables.shape
-    if keep_starts.shape != (b + 1,):
-        raise ValueError("keep_starts must be [B + 1]")
-    ds = None
-    if dst_start is not None:
-        _check(dst_start, torch.int32, "dst_start", index, dev)
-        if dst_start.shape != (b,):
-            raise ValueError("dst_start must be [B]")
-        ds = dst_start.data_ptr()
-    n = keep.shape[0]
-    st = _on_device(index, library().pkv_compact_tokens,
-                    k_cache.data_ptr(), v_cache.data_ptr(), desc_ptr, block_tables.data_ptr(), max(1, mb), b,
-                    keep.data_ptr(), n, keep_starts.data_ptr(), ds, n if max_keep is None else int(max_keep))
-    if st:
-        _lib.check(st, "pkv_compact_tokens")
+    _lib.check(_lib.binding().compact_tokens(k_cache, v_cache, block_tables, keep, keep_starts, dst_start, max_keep),
+               "pkv_compact_tokens")
 
 
 def slot_mapping(block_tables, positions, k_cache, seq_index=None, out=None):

@@ -140,6 +140,28 @@ def load(path=LIB_PATH):
         return lib
 
 
+_binding = None
+
+
+def binding():
+    """The compiled calls (csrc/binding.cpp), bound to the loaded library."""
+    global _binding
+    if _binding is not None:
+        return _binding
+    lib = load()
+    with _lock:
+        if _binding is None:
+            try:
+                from . import _binding as mod
+            except ImportError as e:
+                raise RuntimeError("the compiled binding is not built or does not fit this PyTorch; run "
+                                   "`python -m paged_kv_cache_222_gb300.build`") from e
+            mod.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+                       for f in ("pkv_chunk_plan", "pkv_chunk_attention", "pkv_rotary_append", "pkv_compact_tokens")))
+            _binding = mod
+    return _binding
+
+
 class PkvError(RuntimeError):
     def __init__(self, status, where):
         lib = load()

@@ -1,4 +1,5 @@
-"""Build libpkv.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Build libpkv.so (the C-ABI library) in-tree with nvcc for sm_103a, and
+_binding.so, the compiled Python entry of its most frequent calls.
 
 Each CUDA translation unit is compiled in parallel, then linked into a shared
 library next to this file.  CUDA's runtime is linked statically and the driver
@@ -20,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libpkv.so")
+BINDING_PATH = os.path.join(PKG, "_binding.so")
 
 SOURCES = ["api.cu", "append.cu", "decode.cu", "cascade.cu", "multi_query.cu", "blocks.cu", "chunk.cu", "chunk_tc.cu", "rotary.cu",
            "compact.cu", "block_manager.cpp"]
@@ -43,10 +45,25 @@ def _inputs():
 
 
 def up_to_date():
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def _binding_command(out):
+    """g++ command of the Python extension module against the installed PyTorch."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return ([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [f"-I{i}" for i in inc]
+            + [os.path.join(CSRC, "binding.cpp"), "-o", out, "-L" + os.path.join(root, "lib"), "-ltorch_python",
+               "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"])
 
 
 def build(force=False, verbose=False, ptxas_verbose=False):
@@ -68,6 +85,11 @@ def build(force=False, verbose=False, ptxas_verbose=False):
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    binding_tmp = BINDING_PATH + ".tmp"
+    cmd = _binding_command(binding_tmp)
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    procs.append(("binding.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -78,7 +100,7 @@ def build(force=False, verbose=False, ptxas_verbose=False):
             sys.stdout.write(text)
     if failed:
         msg = "\n".join(f"--- {s}\n{t}" for s, t in failed)
-        raise RuntimeError(f"nvcc failed:\n{msg}")
+        raise RuntimeError(f"compilation failed:\n{msg}")
     tmp = LIB_PATH + ".tmp"
     cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static"]
     if verbose:
@@ -87,6 +109,7 @@ def build(force=False, verbose=False, ptxas_verbose=False):
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
     os.replace(tmp, LIB_PATH)
+    os.replace(binding_tmp, BINDING_PATH)
     return LIB_PATH
 
 

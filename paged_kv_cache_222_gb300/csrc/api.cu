@@ -3,6 +3,7 @@
 // timing trace.  Every check that can be made on the host is made before any
 // CUDA runtime call, so a rejected call touches no GPU state.
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -1257,6 +1258,30 @@ int32_t chunk_tile_q(int32_t max_q_len, int32_t group) {
   return (chunk_small(max_q_len, group) ? pkv::kChunkSmallRows : pkv::kChunkTcRows) / group;
 }
 
+// Key tiles per split of the tcgen05 kernel: the number of splits that
+// minimises waves of units over the SMs x (a unit's fixed cost and its tiles),
+// plus the merge, all in units of one tile's time (about 1.5 us for 128 keys of
+// 256 rows).  A unit's fixed cost is about three tiles; a merge costs two and
+// the pieces' traffic, 10 MB per tile.  Sequences fill part of their last row
+// tile, half of it on average.
+int64_t tc_split_tiles(int64_t n_tokens, int64_t batch, int64_t tile_q, int64_t num_q_heads,
+                       const pkv_cache_desc& c, int64_t tiles, int64_t sms) {
+  const int64_t row_tiles = std::max(batch, n_tokens / tile_q + (batch + 1) / 2);
+  const int64_t units = row_tiles * c.num_kv_heads;
+  const double piece = static_cast<double>(n_tokens) * num_q_heads * c.head_dim * 8.0 / 10e6;
+  int64_t best_each = tiles;
+  double best = -1.0;
+  for (int64_t s = 1; s <= tiles && (s == 1 || units * (s - 1) < 4 * sms); ++s) {
+    const int64_t each = ceil_div(tiles, s), n = ceil_div(tiles, each);
+    const double cost = static_cast<double>(ceil_div(units * n, sms) * (3 + each)) + (n > 1 ? 2.0 + piece * n : 0.0);
+    if (best < 0.0 || cost < best) {
+      best = cost;
+      best_each = each;
+    }
+  }
+  return best_each;
+}
+
 pkv_status chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_t num_q_heads,
                       const pkv_cache_desc* c, int32_t max_ctx, int32_t window, bool has_prefix,
                       int32_t split_tokens, int32_t sms, pkv_decode_plan_t* out) {
@@ -1294,8 +1319,7 @@ pkv_status chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_
     // mma.sync kernel: as for decode, three CTAs per SM streaming one split
     // each, but below 1024 tokens, where a split's fixed cost weighs, no more
     // CTAs than SMs (16 sequences of 1000-4000 tokens: 42.5 us at 256 tokens, 36
-    // at 1024; one of 60k 56.6 and 55; 8 of 31k take 1280: 159 us).  tcgen05
-    // kernel: the longest split that still gives two units per SM.
+    // at 1024; one of 60k 56.6 and 55; 8 of 31k take 1280: 159 us).
     const int64_t all = ceil_div(tiles * nk, 128) * 128;
     if (small) {
       st = decode_split_tokens(static_cast<int32_t>(row_tiles < 0x7FFFFFFF ? row_tiles : 0x7FFFFFFF), c->num_kv_heads,
@@ -1303,8 +1327,8 @@ pkv_status chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_
       while (st < 1024 && st < all && units * ceil_div(all, st) > sms) st += 64;
       if (st > max_st) st = max_st;
     } else {
-      st = all;
-      while (st > 256 && units * ceil_div(tiles * nk, st) < static_cast<int64_t>(sms) * 2) st = ceil_div(st / 2, 128) * 128;
+      const int64_t each = tc_split_tiles(n_tokens, batch, tile_q, num_q_heads, *c, tiles, sms);
+      st = each * nk;
     }
   }
   if ((ceil_div(n_tokens, tile_q) + batch) * c->num_kv_heads > 0x7FFFFFFFll)

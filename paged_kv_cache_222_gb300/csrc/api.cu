@@ -1378,6 +1378,10 @@ extern "C" pkv_status pkv_chunk_attention(
   if (!std::isfinite(m.softcap) || m.softcap < 0.f) return fail(PKV_ERR_INVALID_ARG, "softcap must be finite and >= 0");
   if (!aligned(m.slopes, 4) || !aligned(m.prefix_lens, 4) || !aligned(q_starts, 4))
     return fail(PKV_ERR_INVALID_ARG, "slopes, prefix_lens and q_starts must be 4-byte aligned");
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float qk_log2 = m.softcap > 0.f ? 2.f * kLog2e * (scale / m.softcap) : scale * kLog2e;
+  if (!std::isfinite(qk_log2) || !std::isfinite(m.softcap * kLog2e))
+    return fail(PKV_ERR_INVALID_ARG, "scale / softcap is beyond binary32");
   pkv_decode_plan_t pl;
   s = chunk_plan(n_tokens, batch, max_q_len, num_q_heads, cache, max_context_len, m.window,
                  m.prefix_lens != nullptr, split_tokens, kDefaultSms, &pl);
@@ -1444,8 +1448,7 @@ extern "C" pkv_status pkv_chunk_attention(
   p.split_tokens = pl.split_tokens;
   p.max_splits = pl.max_splits;
   p.tile_q = chunk_tile_q(max_q_len, group);
-  constexpr float kLog2e = 1.4426950408889634f;
-  p.qk_log2 = m.softcap > 0.f ? 2.f * kLog2e * (scale / m.softcap) : scale * kLog2e;
+  p.qk_log2 = qk_log2;
   p.cap_log2 = m.softcap * kLog2e;
   p.cache_dtype = c.dtype;
   p.err = st->err;

@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(128, 3)
     v_mult = p.v_scale[static_cast<int64_t>(b) * p.scale_stride + h];
   }
 
+  const CapPoly poly(qk_mult, p.cap_log2);
   const float ex_mult = p.cap_log2 > 0.f || p.slopes != nullptr ? 1.f : qk_mult;  // scores to log2 weights
 
   float m_a = -CUDART_INF_F, m_b = -CUDART_INF_F, l_a = 0.f, l_b = 0.f;
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(128, 3)
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-          for (int e = 0; e < NE; ++e) sc[nt][e] = capped(sc[nt][e] * qk_mult, p.cap_log2);
+          for (int e = 0; e < NE; ++e) sc[nt][e] = capped(sc[nt][e], qk_mult, p.cap_log2, poly);
       }
       if (p.slopes != nullptr) {
         const float m = p.cap_log2 > 0.f ? 1.f : qk_mult;

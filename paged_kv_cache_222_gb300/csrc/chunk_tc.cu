@@ -94,37 +94,15 @@ __device__ __forceinline__ float min_nan(float a, float b) {  // NaN if one is
   return d;
 }
 
-// Scores up to 0.35 of the cap: with y = score / cap,
-// tanh(y) = y (c0 + c1 y^2 + c2 y^4) with the coefficients of the least largest
-// relative error on |y| <= 0.35, 2.9e-6: a weight is off by less than 2^-13 at
-// a cap of 50, next to its own rounding.  Powers of the multipliers folded in,
-// that is x * ((k2 x^2 + k1) x^2 + k0) for a raw product x: four packed
-// FMA-pipe operations for two weights' exponents instead of one, and nothing
-// on the special-function unit, which the exponentials need.
-struct CapPoly {
-  float2 k0, k1, k2;
-  float y_mult;  // y = x * y_mult
-  __device__ __forceinline__ CapPoly(float w_mult, float cap_log2) {
-    y_mult = w_mult * 0.34657359027997264f;  // ln 2 / 2: w = 2 y log2(e)
-    const float y2 = y_mult * y_mult, f0 = cap_log2 * y_mult, f1 = f0 * y2, f2 = f1 * y2;
-    k0 = make_float2(0.99999713f * f0, 0.99999713f * f0);
-    k1 = make_float2(-0.33290954f * f1, -0.33290954f * f1);
-    k2 = make_float2(0.12395031f * f2, 0.12395031f * f2);
-  }
-  __device__ __forceinline__ bool holds(float abs_max) const { return abs_max * y_mult <= 0.35f && y_mult > 1e-5f; }
-  __device__ __forceinline__ float2 minus(float2 x, float2 neg_mu) const {  // the capped scores - mu
-    const float2 t = __fmul2_rn(x, x);
-    return __ffma2_rn(__ffma2_rn(__ffma2_rn(k2, t, k1), t, k0), x, neg_mu);
-  }
-};
-
-// x := cap * tanh(x / cap) in log2 units for any x: 1 - 2 / (e^2y + 1), one
-// reciprocal shared by four scores, 1 / a = b c d / (a b c d); 2y is held below
-// 28 log2 units, where tanh is 1 to binary32 and the product of four cannot
-// overflow.  What lies past the sequence's end may be NaN and must not reach
-// its neighbours: scores that are not seen enter as 0.
+// x := cap * tanh(x / cap) in log2 units for any x: the polynomial up to 0.35 of
+// the cap, else 1 - 2 / (e^2y + 1), one reciprocal shared by four scores,
+// 1 / a = b c d / (a b c d); 2y is held below 28 log2 units, where tanh is 1 to
+// binary32 and the product of four cannot overflow.  What lies past the
+// sequence's end may be NaN and must not reach its neighbours: scores that are
+// not seen enter as 0.
 template <int N>
-__device__ __forceinline__ void cap_scores(float* x, float w_mult, float cap_log2, bool masked, const uint32_t* see) {
+__device__ __forceinline__ void cap_scores(float* x, float w_mult, float cap_log2, const CapPoly& poly, bool masked,
+                                           const uint32_t* see) {
 #pragma unroll
   for (int i = 0; i < N; i += 4) {
     float q[4];
@@ -140,10 +118,10 @@ __device__ __forceinline__ void cap_scores(float* x, float w_mult, float cap_log
     const float2 m2c = make_float2(-2.f * cap_log2, -2.f * cap_log2), c = make_float2(cap_log2, cap_log2);
     const float2 a = __ffma2_rn(__fmul2_rn(make_float2(rp.x, rp.x), make_float2(q[1], q[0])), m2c, c);
     const float2 b = __ffma2_rn(__fmul2_rn(make_float2(rp.y, rp.y), make_float2(q[3], q[2])), m2c, c);
-    x[i] = a.x;
-    x[i + 1] = a.y;
-    x[i + 2] = b.x;
-    x[i + 3] = b.y;
+    x[i] = poly.holds(fabsf(x[i])) ? poly.of(x[i]) : a.x;
+    x[i + 1] = poly.holds(fabsf(x[i + 1])) ? poly.of(x[i + 1]) : a.y;
+    x[i + 2] = poly.holds(fabsf(x[i + 2])) ? poly.of(x[i + 2]) : b.x;
+    x[i + 3] = poly.holds(fabsf(x[i + 3])) ? poly.of(x[i + 3]) : b.y;
   }
 }
 
@@ -666,7 +644,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
               for (int j = 0; j < 4; ++j) am[j] = max3f(am[j], fabsf(x[i + 2 * j]), fabsf(x[i + 2 * j + 1]));
             small = __all_sync(kFull, poly.holds(fmaxf(max3f(am[0], am[1], am[2]), am[3])));
           }
-          if constexpr (MODE == kCappedBiased) cap_scores<NK>(x, qk, p.cap_log2, masked, see);
+          if constexpr (MODE == kCappedBiased) cap_scores<NK>(x, qk, p.cap_log2, poly, masked, see);
           if constexpr (MODE == kBiased || MODE == kCappedBiased) {
             const float mult = MODE == kBiased ? qk : 1.f, base = slope * static_cast<float>(t0 - pos);
             const float2 mult2 = make_float2(mult, mult), slope2 = make_float2(slope, slope);
@@ -692,7 +670,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
             }
             mt = max3f(max3f(mp[0], mp[1], mp[2]), max3f(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
             if constexpr (MODE == kPlain) mt *= qk;
-            if constexpr (MODE == kCapped) mt = mt == -CUDART_INF_F ? mt : capped(mt * qk, p.cap_log2);
+            if constexpr (MODE == kCapped) mt = mt == -CUDART_INF_F ? mt : capped(mt, qk, p.cap_log2, poly);
           }
           float alpha = 1.f;
           bool resc = false;
@@ -753,7 +731,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
             if (small) {
               weights(std::integral_constant<int, 1>{});
             } else {
-              cap_scores<NK>(x, qk, p.cap_log2, masked, see);
+              cap_scores<NK>(x, qk, p.cap_log2, poly, masked, see);
               if (masked) mask_scores<NK>(x, see);
               weights(std::integral_constant<int, 2>{});
             }

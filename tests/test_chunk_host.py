@@ -45,7 +45,7 @@ def chunk(lib, c, **kw):
     (dict(hq=60), {}, 1), (dict(hq=8 * 17), {}, 2), (dict(max_ctx=-1), {}, 1), (dict(max_ctx=129), {}, 1),
     (dict(mb=0), {}, 1), (dict(scale=0.0), {}, 1), (dict(scale=-1.0), {}, 1), (dict(scale=math.nan), {}, 1),
     (dict(scale=math.inf), {}, 1), (dict(softcap=-1.0), {}, 1), (dict(softcap=math.inf), {}, 1),
-    (dict(softcap=math.nan), {}, 1), (dict(window=-1), {}, 1), (dict(q=None), {}, 1), (dict(qs=None), {}, 1),
+    (dict(softcap=math.nan), {}, 1), (dict(softcap=1e-45), {}, 1), (dict(softcap=3e38), {}, 1), (dict(window=-1), {}, 1), (dict(q=None), {}, 1), (dict(qs=None), {}, 1),
     (dict(out=FAKE + 4), {}, 1), (dict(q=FAKE + 2), {}, 1), (dict(kc=FAKE + 8), {}, 1), (dict(qs=FAKE + 2), {}, 1),
     (dict(slopes=FAKE + 1), {}, 1), (dict(prefix=FAKE + 1), {}, 1), (dict(ks=FAKE, vs=FAKE), {}, 1),
     ({}, dict(dtype=L.PKV_E4M3), 1), ({}, dict(dtype=L.PKV_F32), 1), ({}, dict(head_dim=96), 2),

@@ -51,9 +51,19 @@ def _with_prefix(mods, n):
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("mods", MODS, ids=[",".join(f"{k}={v}" for k, v in m.items()) for m in MODS])
 @pytest.mark.parametrize("lens", [SINGLE, RAGGED], ids=["single", "ragged"])
-@pytest.mark.parametrize("D", [64, 128])
-def test_modified_scores(lens, mods, kv, D):
-    case = C.make_case(*lens, 8, 2, D, 16, kv, seed=77, **_with_prefix(mods, len(lens[0])))
+@pytest.mark.parametrize("D,bs", [(64, 16), (128, 16), (128, 32)])
+def test_modified_scores(lens, mods, kv, D, bs):
+    case = C.make_case(*lens, 8, 2, D, bs, kv, seed=77, **_with_prefix(mods, len(lens[0])))
+    C.check(run(case), case)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("softcap", [1e-3, 0.5, 1e4, 1e7, 1e30])
+@pytest.mark.parametrize("lens", [SINGLE, RAGGED], ids=["single", "ragged"])
+def test_tiny_and_enormous_caps(lens, softcap, bias, kv):
+    # a cap far above every score changes nothing, one far below levels them
+    case = C.make_case(*lens, 8, 2, 128, 16, kv, softcap=softcap, bias=bias, seed=78)
     C.check(run(case), case)
 
 

@@ -58,7 +58,7 @@ struct TcShape {
   static constexpr int STAGE = 32 * SB;
   static constexpr int RU = 4;                     // units in flight between the roles
   static constexpr int UNIT = 20;                  // words of one
-  static constexpr int NBARS = 2 * NS + 2 * NR + 5 * GROUPS + 5 + 2 * RU + GROUPS;
+  static constexpr int NBARS = 2 * NS + 2 * NR + 5 * GROUPS + 6 + 2 * RU + GROUPS;
   static constexpr int BYTES = QBYTES + NS * TILE + NR * RAW + 8 * STAGE + 16 + NBARS * 8 + RU * UNIT * 4 + 16 + 1024;
   static_assert(BYTES <= 232448, "shared memory per CTA");
   static constexpr int THREADS = FP8 ? 512 : 384;
@@ -216,8 +216,11 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
   uint64_t* qfull = odone + GROUPS;  // Q of the unit is in shared memory
   uint64_t* qready = qfull + 1;      // ... as f16 (E4M3 caches)
   uint64_t* qempty = qready + 1;     // every S of the unit has read it
-  uint64_t* vfix = qempty + 1;       // the last V tile's rows past the end are zeros
-  uint64_t* clc = vfix + 1;          // the next unit's block index has arrived
+  // [2]: the last V tile's rows past the end are zeros, of alternate units: the
+  // loader may be one unit ahead of a product issuer that has yet to ask, and
+  // two phases of one barrier cannot be told apart
+  uint64_t* vfix = qempty + 1;
+  uint64_t* clc = vfix + 2;          // the next unit's block index has arrived
   uint64_t* ufull = clc + 1;         // [RU]
   uint64_t* uempty = ufull + RU;     // [RU]
   uint64_t* done = uempty + RU;      // [GROUPS]
@@ -246,6 +249,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
     mbar_init(smem_u32(qready), 4);
     mbar_init(smem_u32(qempty), GROUPS);
     mbar_init(smem_u32(vfix), 1);
+    mbar_init(smem_u32(vfix + 1), 1);
     mbar_init(smem_u32(clc), 1);
     for (int i = 0; i < RU; ++i) {
       mbar_init(smem_u32(ufull + i), 1);
@@ -315,6 +319,10 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
         tc_commit_if(leader, smem_u32(empty + slot));
         next_slot();
       };
+      auto fixed = [&]() {
+        const int i = tails++;
+        return wait(vfix + (i & 1), i >> 1);
+      };
       TcUnit u;
       for (int n = 0; ok && read_unit(n, u); ++n) {
         const bool tail = !FP8 && u.v_tail(NK, p.block_size);
@@ -327,7 +335,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
             tc_commit_if(leader, smem_u32(empty + slot));
             next_slot();
           }
-          if (tail && ok) ok = wait(vfix, tails++);
+          if (tail && ok) ok = fixed();
           continue;
         }
         ok = wait(FP8 ? qready : qfull, n);
@@ -353,7 +361,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
           ok = wait(full + vslot, vuse);
           if (!ok) break;
           if (tail && k == u.ntile - 1) {  // its loader has zeroed the rows past the sequence's end
-            ok = wait(vfix, tails++);
+            ok = fixed();
             if (!ok) break;
           }
           if (!EARLY && more) ok = wait(full + slot, use);  // K(k+1), ahead of the wait for P
@@ -393,7 +401,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
       const int hf = lane / per_half, bi = lane % per_half;
       const uint32_t off = hf * C::HALFB + bi * p.block_size * ROWB;
       int item = v;  // K of tile j is item 2 j of the ring, V item 2 j + 1
-      int asked = 0;
+      int asked = 0, fixes = 0;  // units asked for; units with a zeroed tail so far
       bool ok = true;
       uint32_t bx = blockIdx.x, by = blockIdx.y;
       TcUnit u;
@@ -497,7 +505,8 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(vfix));
+          if (lane == 0) mbar_arrive(smem_u32(vfix + (fixes & 1)));
+          ++fixes;
         }
       }
       if (lane == 0 && *s_abort) {  // the copies in flight land before the CTA leaves

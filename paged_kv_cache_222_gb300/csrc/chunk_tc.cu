@@ -1,27 +1,53 @@
 // Attention of ragged chunks of new tokens over the paged cache on the
 // 5th-generation tensor cores (what it computes: chunk_common.cuh).
 //
-// A CTA takes a row tile of one (sequence, KV head): up to 256 rows, a row
-// being a new token and one of the KV head's query heads, as two groups of 128
-// TMEM lanes, over one split of the tile's visible keys in 128-key tiles.
-// Its warps have fixed roles:
-//   0-7   softmax: thread t of group g is row 128 g + t
-//   8     issues the products: S_g(k) = Q_g K(k)^T and O_g += P_g(k) V(k)
-//   9, 10 load the K and the V tiles by TMA (one box per lane: a block's rows
-//         of one 128-byte column half), alternately into one ring
-//   12-15 (E4M3 caches) widen the loaded codes to f16 tiles of the ring
-// TMEM: S of both groups (128 columns each) and O of both; P_g(k), 16-bit
-// pairs, takes the first half of S_g's columns once the softmax has read them.
-// The products are issued in the order
-//   PV_0(k), S_0(k+1), PV_1(k), S_1(k+1), PV_0(k+1), ...
-// so that one group's softmax runs under the other group's two products.  They
-// execute in issue order: S_g(k+1) cannot overtake the PV_g(k) that reads P
-// from its columns, and S_g(k) having completed (sfull) means that PV_g(k-1)
-// has, so the softmax may then rescale O_g without a barrier of its own.
+// One CTA per SM stays and works through units: a row tile of one (sequence, KV
+// head), up to 256 rows, a row being a new token and one of the KV head's query
+// heads, over one split of the tile's visible keys, in key tiles of 128 (64
+// where EARLY needs the columns).  A CTA starts with the unit of its own block
+// index and then takes those of blocks that have not started (cluster launch
+// control), so that unequal units even out, and loads and products of a unit
+// begin under the softmax and the output of the one before.  The rows are two
+// groups of 128 TMEM lanes, which share every K and V tile.  Roles:
+//   0-7   softmax and output: thread t of group g is row 128 g + t
+//   8, 11 issue the products of group 0 and of group 1:
+//         S_g(k) = Q_g K(k)^T and O_g += P_g(k) V(k)
+//   9     takes the units and loads K, 10 loads V and Q: TMA, a lane per box (a
+//         block's rows of one 128-byte column half), K and V alternately in one
+//         ring of 128 KB (E4M3 caches: 96 KB, and 48 KB for the codes)
+//   12-15 (E4M3 caches) widen the codes to f16 tiles of the ring, and Q to f16
+// TMEM: S of both groups and O of both, 512 columns for 128-wide heads, so that
+// P_g(k), 16-bit pairs, takes the first half of S_g's columns once the softmax
+// has read them, and S_g(k+1) is issued behind PV_g(k), which reads P from its
+// columns: one group's softmax runs under the other group's products, and
+// S_g(k) having completed (sfull) means that PV_g(k-1) has, so the softmax may
+// rescale O_g without a barrier of its own.  EARLY (capped or biased scores of
+// bf16 caches, whose softmax is the longer part): P has columns of its own and
+// S(k+1) is issued as soon as the softmax has read S(k); for plain scores it
+// costs (128-wide heads 1175 us where the other takes 1015, 64-wide 175 / 164).
+//
+// A whole warp walks an issuing role and an elected lane's predicate issues the
+// products: a branch on the lane costs 115 cycles per product.
+//
 // The running maximum is lazy: O is rescaled only when the maximum grows by
 // more than 2^8, so P stays within 2^8 (f16 holds that) and most tiles rescale
 // nothing.  Sums, maxima and O are binary32; P is rounded to 16 bits (bf16
 // 2^-8, f16 2^-11 of a weight), next to the output's own 2^-8.
+//
+// Bound: 4 D flops per row and visible key on the tensor pipe, with the
+// softmax's exponentials (8 a cycle and sub-partition) at half its time.  Two
+// chunks of 4096 tokens over 4096, 64 + 8 heads of 128, bf16: 1010-1080 us
+// with the clock (1.93 GHz under the power cap), 1530-1630 Tflop/s, 78-83 % of
+// the measured library product; the tensor pipe is active 70 % of the time,
+// the rest is the first and last tile of a unit and the softmax's two warps per
+// sub-partition waiting for each other's issue slots.  Steps that did not pay:
+// 16 softmax warps, half a row each (1410-1540 us: they spill); P handed over
+// in halves (12 % slower) and S as two products of 64 keys (24 %); three ring
+// slots instead of four (1290); 128 bytes of a row per output pass (1045).
+// E4M3 caches: chunks of 512 tokens over 3584 take 614 us where bf16 takes 521:
+// the softmax has 200 registers a thread instead of 224 (570 us for bf16 with
+// 192) and the widening warps take issue slots; S from the codes themselves,
+// with Q as two E4M3 planes, has half the widening but was no faster (633 us).
 //
 // Every wait is bounded; a time-out records the error, raises the CTA's abort
 // flag, which ends every role's loop, and the CTA drains its copies and

@@ -19,7 +19,7 @@
 // least 64 bytes.  The rows' addresses (keep list, then block table) are
 // looked up 256 at a time, a batch ahead.  Bound: the moved bytes, each read
 // and written once: half of 32 x 4096 tokens of 8 heads of 128 (536 MB) takes
-// 88 us, 6.1 TB/s, 91 % of the measured copy (without the next step's loads
+// 86.5 us, 6.2 TB/s, 93 % of the measured copy (without the next step's loads
 // ahead 90 us; twice the rows per step 100, half of them 104; 128-byte bands
 // for twice the CTAs 98: each then reads half a row's line).
 

@@ -13,15 +13,16 @@
 // box of 16 tokens per lane and 128-byte column band), on barriers of its
 // own, and refills its slot as soon as it has read it, so that no warp waits
 // for another; the warps merge (m, l, O) through shared memory at the end.
-// S = Q K^T and O += P V are mma.sync m16n8k16 products with fp32 sums: bf16
+// The products are mma.sync m16n8k16 products with fp32 sums: bf16
 // for bf16 caches, f16 for E4M3 ones (every code is an f16).  P is rounded to
 // that type: at most 2^-8 (bf16) or 2^-11 (f16) of each weight, next to the
 // output's own 2^-8.  Bound: the HBM stream of 2 D bytes x type size per visible
 // key and KV head.  64 sequences of 512-8192 tokens, 64 + 8 heads of 128, bf16,
-// capped scores: 188-190 us with the merge, 6.5 TB/s, 97 % of the measured copy;
-// 256 sequences of 1040 visible tokens in E4M3: 110 us, 5.0 TB/s, 75 %: a CTA
-// streams 266 KB, and its first loads' latency and the merge of its four warps
-// weigh a quarter.
+// capped scores: 188-191 us with the merge, 6.5 TB/s, 96-97 % of the measured
+// copy; 256 sequences of 1040 visible tokens in E4M3: 104 us, 5.3 TB/s, 79 %.
+// There a call costs 20 us besides its stream, whatever the window: a CTA's
+// first loads and the merge of its four warps, which CTAs that stream E4M3 are
+// too busy to make up for (in bf16 it is 5 us).
 
 #include <type_traits>
 
@@ -42,8 +43,8 @@ struct SmallShape {
   static_assert(4 * 16 * DP * 4 + 4 * 16 * 2 * 4 <= NS * STAGE, "merge buffer fits the stages");
 };
 
-// TWO: tiles of more than 8 rows (a lane holds rows r and r + 8 of the product;
-// without it the second one is empty and its softmax left out).
+// TWO: tiles of more than 8 rows, S = Q K^T and O += P V with a lane's rows r
+// and r + 8.  Up to 8 rows: the products transposed.
 template <int D, bool FP8, bool TWO>
 __global__ void __launch_bounds__(128, 3)
     chunk_small_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -51,6 +52,11 @@ __global__ void __launch_bounds__(128, 3)
   using L = Layout<D, FP8>;
   using C = SmallShape<D, FP8>;
   constexpr int KS = D / 16, NS = C::NS, STAGE = C::STAGE, DP = C::DP;
+  // Up to 8 rows: S^T = K Q^T and O^T += V^T P^T, keys as the products' 16 rows
+  // and tile rows as their 8 columns: half as many products as the other form,
+  // which leaves half of its 16 rows empty, and half the registers of O (256
+  // sequences of 1040 visible tokens: E4M3 112 -> 104 us; 1024 in bf16 165 -> 164).
+  constexpr bool TR = !TWO;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, j = lane & 3;
@@ -124,13 +130,14 @@ __global__ void __launch_bounds__(128, 3)
   int issued = 0;
   for (; issued < ntile && issued < NS; ++issued) issue(issued);
 
-  // this lane's two rows: ra = r, rb = r + 8 of the tile
-  const int ra = r, rb = r + 8;
+  // this lane's two rows of the tile: r, r + 8 (transposed: 2 j, 2 j + 1; its
+  // fragments of Q still hold row r)
+  const int ra = TR ? 2 * j : r, rb = TR ? 2 * j + 1 : r + 8;
   uint32_t qa[KS][4];
   {
     const uint16_t* q = static_cast<const uint16_t*>(p.q);
-    const uint16_t* qra = ra < rows ? q + out_row(ra) * D : nullptr;
-    const uint16_t* qrb = rb < rows ? q + out_row(rb) * D : nullptr;
+    const uint16_t* qra = r < rows ? q + out_row(r) * D : nullptr;
+    const uint16_t* qrb = TWO && r + 8 < rows ? q + out_row(r + 8) * D : nullptr;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       if constexpr (!FP8) {
@@ -172,9 +179,10 @@ __global__ void __launch_bounds__(128, 3)
   const float ex_mult = p.cap_log2 > 0.f || p.slopes != nullptr ? 1.f : qk_mult;  // scores to log2 weights
 
   float m_a = -CUDART_INF_F, m_b = -CUDART_INF_F, l_a = 0.f, l_b = 0.f;
-  float o[D / 8][4];
+  constexpr int NO = TR ? D / 16 : D / 8;  // products' accumulators of O
+  float o[NO][4];
 #pragma unroll
-  for (int nt = 0; nt < D / 8; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
+  for (int nt = 0; nt < NO; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
   // ldmatrix lanes: K (tok 0-7,c)(tok 0-7,c+1)(tok 8-15,c)(tok 8-15,c+1);
   //                 V (tok 0-7,c)(tok 8-15,c)(tok 0-7,c+1)(tok 8-15,c+1)
   const int mq = lane >> 3;
@@ -188,7 +196,124 @@ __global__ void __launch_bounds__(128, 3)
     if (!__all_sync(kFull, arrived)) healthy = false;
     const uint32_t base = stage0 + s * STAGE + warp * L::STAGEB;
     const int t_warp = rg.tile(k0 + k) * kSmallTile + warp * kTileTokens;  // this warp's first key
-    if (healthy) {
+    if constexpr (TR) {
+      if (healthy) {
+        // ---- S^T: keys r, r + 8 (e >= 2) of rows 2 j, 2 j + 1 (odd e), in two
+        // accumulators to halve the chain
+        float sc[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int pk = 0; pk < (FP8 ? KS / 2 : KS); ++pk) {
+          uint32_t Rk[4];
+          ldsm_x4(base + L::off(tok_k, 2 * pk + ch_k), Rk);
+          if constexpr (!FP8) {
+            const uint32_t a[4] = {Rk[0], Rk[2], Rk[1], Rk[3]};
+            mma_bf16_16816(pk & 1 ? s2 : sc, a, qa[pk][0], qa[pk][2]);
+            continue;
+          }
+#pragma unroll
+          for (int e = 0; FP8 && e < 2; ++e) {  // a 16-byte chunk holds the 16 d of one k-step
+            const uint32_t lo = Rk[e], hi = Rk[2 + e];
+            const uint32_t a[4] = {e4m3x2_to_f16x2(static_cast<uint16_t>(lo & 0xFFFFu)),
+                                   e4m3x2_to_f16x2(static_cast<uint16_t>(hi & 0xFFFFu)),
+                                   e4m3x2_to_f16x2(static_cast<uint16_t>(lo >> 16)),
+                                   e4m3x2_to_f16x2(static_cast<uint16_t>(hi >> 16))};
+            mma_f16_16816(e ? s2 : sc, a, qa[(2 * pk + e) % KS][0], qa[(2 * pk + e) % KS][2]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[e] += s2[e];
+        const int ta = t_warp + r, tb = ta + 8;
+        if (p.cap_log2 > 0.f) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[e] = capped(sc[e], qk_mult, p.cap_log2, poly);
+        }
+        if (p.slopes != nullptr) {
+          const float m = p.cap_log2 > 0.f ? 1.f : qk_mult;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sc[e] = fmaf(sc[e], m, (e & 1 ? sl_b : sl_a) * static_cast<float>((e < 2 ? ta : tb) - (e & 1 ? pos_b : pos_a)));
+        }
+        const auto whole = [&](int pos, int lo, int pf) {
+          return (t_warp + kTileTokens - 1 <= pos && t_warp >= lo) || t_warp + kTileTokens <= pf;
+        };
+        if (!__all_sync(kFull, whole(pos_a, lo_a, pf_a) && whole(pos_b, lo_b, pf_b))) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int t = e < 2 ? ta : tb, pos = e & 1 ? pos_b : pos_a, lo = e & 1 ? lo_b : lo_a, pf = e & 1 ? pf_b : pf_a;
+            if (!((t <= pos && t >= lo) || t < pf)) sc[e] = -CUDART_INF_F;
+          }
+        }
+        float mx_a = fmaxf(sc[0], sc[2]), mx_b = fmaxf(sc[1], sc[3]);
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) {
+          mx_a = fmaxf(mx_a, __shfl_xor_sync(kFull, mx_a, sh));
+          mx_b = fmaxf(mx_b, __shfl_xor_sync(kFull, mx_b, sh));
+        }
+        mx_a *= ex_mult;
+        mx_b *= ex_mult;
+        const bool up_a = mx_a > m_a + 8.f, up_b = mx_b > m_b + 8.f;  // lazy maximum, as below
+        if (__any_sync(kFull, up_a || up_b)) {
+          const float al_a = up_a ? fast_exp2(m_a - mx_a) : 1.f, al_b = up_b ? fast_exp2(m_b - mx_b) : 1.f;
+          if (up_a) m_a = mx_a;
+          if (up_b) m_b = mx_b;
+          l_a *= al_a;
+          l_b *= al_b;
+#pragma unroll
+          for (int mt = 0; mt < NO; ++mt) {
+            o[mt][0] *= al_a;
+            o[mt][1] *= al_b;
+            o[mt][2] *= al_a;
+            o[mt][3] *= al_b;
+          }
+        }
+        const float mu_a = m_a == -CUDART_INF_F ? 0.f : m_a, mu_b = m_b == -CUDART_INF_F ? 0.f : m_b;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[e] = fast_exp2(fmaf(sc[e], ex_mult, e & 1 ? -mu_b : -mu_a));
+        l_a += sc[0] + sc[2];
+        l_b += sc[1] + sc[3];
+        // ---- O^T += V^T P^T; rows of the first operand: 16 d, E4M3 the even ones
+        // of a 16-d chunk and then the odd ones
+        const uint32_t p0 = movmatrix_trans(FP8 ? pack_f16x2(sc[0], sc[1]) : pack_bf16x2(sc[0], sc[1])),
+                       p1 = movmatrix_trans(FP8 ? pack_f16x2(sc[2], sc[3]) : pack_bf16x2(sc[2], sc[3]));
+        const int vvalid = sq.ctx - t_warp;
+        const uint32_t vt = base + L::TILEB;
+        const auto add_pv = [&](auto tail) {
+          constexpr bool TAIL = decltype(tail)::value;
+          const uint32_t keep0 = ((2 * j < vvalid) ? 0x0000FFFFu : 0u) | ((2 * j + 1 < vvalid) ? 0xFFFF0000u : 0u);
+          const uint32_t keep1 = ((2 * j + 8 < vvalid) ? 0x0000FFFFu : 0u) | ((2 * j + 9 < vvalid) ? 0xFFFF0000u : 0u);
+#pragma unroll
+          for (int q = 0; q < (FP8 ? KS / 2 : KS); ++q) {
+            uint32_t Rv[4];
+            ldsm_x4_trans(vt + L::off(tok_v, 2 * q + ch_v), Rv);
+            if constexpr (TAIL) {
+              Rv[0] &= keep0;
+              Rv[1] &= keep1;
+              Rv[2] &= keep0;
+              Rv[3] &= keep1;
+            }
+            if constexpr (!FP8) {
+              const uint32_t a[4] = {Rv[0], Rv[2], Rv[1], Rv[3]};
+              mma_bf16_16816(o[q], a, p0, p1);
+              continue;
+            }
+#pragma unroll
+            for (int e = 0; FP8 && e < 2; ++e) {
+              const uint32_t e0 = prmt(Rv[2 * e], 0u, 0x3120u);       // keys 0-7
+              const uint32_t e1 = prmt(Rv[2 * e + 1], 0u, 0x3120u);   // keys 8-15
+              const uint32_t a[4] = {e4m3x2_to_f16x2(static_cast<uint16_t>(e0 & 0xFFFFu)),
+                                     e4m3x2_to_f16x2(static_cast<uint16_t>(e0 >> 16)),
+                                     e4m3x2_to_f16x2(static_cast<uint16_t>(e1 & 0xFFFFu)),
+                                     e4m3x2_to_f16x2(static_cast<uint16_t>(e1 >> 16))};
+              mma_f16_16816(o[(2 * q + e) % NO], a, p0, p1);
+            }
+          }
+        };
+        if (vvalid < kTileTokens)
+          add_pv(std::true_type{});
+        else
+          add_pv(std::false_type{});
+      }
+    } else if (healthy) {
       // ---- S = Q K^T: two 8-key n-tiles
       float sc[2][4];
 #pragma unroll
@@ -219,19 +344,18 @@ __global__ void __launch_bounds__(128, 3)
       // Without cap and bias the multiplier waits for the exponent's FMA.  The
       // maximum is lazy: it moves when it grows by more than 2^8, so weights
       // stay within 2^8 and most steps rescale nothing.
-      constexpr int NE = TWO ? 4 : 2;
       if (p.cap_log2 > 0.f) {
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-          for (int e = 0; e < NE; ++e) sc[nt][e] = capped(sc[nt][e], qk_mult, p.cap_log2, poly);
+          for (int e = 0; e < 4; ++e) sc[nt][e] = capped(sc[nt][e], qk_mult, p.cap_log2, poly);
       }
       if (p.slopes != nullptr) {
         const float m = p.cap_log2 > 0.f ? 1.f : qk_mult;
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-          for (int e = 0; e < NE; ++e) {
+          for (int e = 0; e < 4; ++e) {
             const int t = t_warp + 8 * nt + 2 * j + (e & 1);
             sc[nt][e] = fmaf(sc[nt][e], m, (e < 2 ? sl_a : sl_b) * static_cast<float>(t - (e < 2 ? pos_a : pos_b)));
           }
@@ -239,26 +363,24 @@ __global__ void __launch_bounds__(128, 3)
       const auto whole = [&](int pos, int lo, int pf) {
         return (t_warp + kTileTokens - 1 <= pos && t_warp >= lo) || t_warp + kTileTokens <= pf;
       };
-      if (!__all_sync(kFull, whole(pos_a, lo_a, pf_a) && (!TWO || whole(pos_b, lo_b, pf_b)))) {
+      if (!__all_sync(kFull, whole(pos_a, lo_a, pf_a) && whole(pos_b, lo_b, pf_b))) {
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-          for (int e = 0; e < NE; ++e) {
+          for (int e = 0; e < 4; ++e) {
             const int t = t_warp + 8 * nt + 2 * j + (e & 1);
             const int pos = e < 2 ? pos_a : pos_b, lo = e < 2 ? lo_a : lo_b, pf = e < 2 ? pf_a : pf_b;
             if (!((t <= pos && t >= lo) || t < pf)) sc[nt][e] = -CUDART_INF_F;
           }
       }
       float mx_a = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-      float mx_b = TWO ? fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3])) : -CUDART_INF_F;
+      float mx_b = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
       mx_a = fmaxf(mx_a, __shfl_xor_sync(kFull, mx_a, 1));
       mx_a = fmaxf(mx_a, __shfl_xor_sync(kFull, mx_a, 2)) * ex_mult;
-      if constexpr (TWO) {
-        mx_b = fmaxf(mx_b, __shfl_xor_sync(kFull, mx_b, 1));
-        mx_b = fmaxf(mx_b, __shfl_xor_sync(kFull, mx_b, 2)) * ex_mult;
-      }
+      mx_b = fmaxf(mx_b, __shfl_xor_sync(kFull, mx_b, 1));
+      mx_b = fmaxf(mx_b, __shfl_xor_sync(kFull, mx_b, 2)) * ex_mult;
       // (-inf: nothing seen yet, any seen key moves it and there is nothing to rescale)
-      const bool up_a = mx_a > m_a + 8.f, up_b = TWO && mx_b > m_b + 8.f;
+      const bool up_a = mx_a > m_a + 8.f, up_b = mx_b > m_b + 8.f;
       if (__any_sync(kFull, up_a || up_b)) {
         const float al_a = up_a ? fast_exp2(m_a - mx_a) : 1.f, al_b = up_b ? fast_exp2(m_b - mx_b) : 1.f;
         if (up_a) m_a = mx_a;
@@ -279,13 +401,9 @@ __global__ void __launch_bounds__(128, 3)
         sc[nt][0] = fast_exp2(fmaf(sc[nt][0], ex_mult, -mu_a));
         sc[nt][1] = fast_exp2(fmaf(sc[nt][1], ex_mult, -mu_a));
         l_a += sc[nt][0] + sc[nt][1];
-        if constexpr (TWO) {
-          sc[nt][2] = fast_exp2(fmaf(sc[nt][2], ex_mult, -mu_b));
-          sc[nt][3] = fast_exp2(fmaf(sc[nt][3], ex_mult, -mu_b));
-          l_b += sc[nt][2] + sc[nt][3];
-        } else {
-          sc[nt][2] = sc[nt][3] = 0.f;
-        }
+        sc[nt][2] = fast_exp2(fmaf(sc[nt][2], ex_mult, -mu_b));
+        sc[nt][3] = fast_exp2(fmaf(sc[nt][3], ex_mult, -mu_b));
+        l_b += sc[nt][2] + sc[nt][3];
       }
       // ---- O += P V.  V rows at or past the end of the sequence may hold
       // anything (NaN included): zeroed in the fragments, P is 0 there.
@@ -349,19 +467,28 @@ __global__ void __launch_bounds__(128, 3)
   }
   allow_next_grid();
 
-  // ---- row sums over the quad; the warps' results merge through shared memory
-  l_a += __shfl_xor_sync(kFull, l_a, 1);
-  l_a += __shfl_xor_sync(kFull, l_a, 2);
-  l_b += __shfl_xor_sync(kFull, l_b, 1);
-  l_b += __shfl_xor_sync(kFull, l_b, 2);
+  // ---- row sums over the lanes that share a row; the warps' results merge through shared memory
+#pragma unroll
+  for (int sh = TR ? 4 : 1; sh < (TR ? 32 : 4); sh <<= 1) {
+    l_a += __shfl_xor_sync(kFull, l_a, sh);
+    l_b += __shfl_xor_sync(kFull, l_b, sh);
+  }
   __syncthreads();  // every warp is done with the stages
   float* s_o = reinterpret_cast<float*>(smem);  // [4 warps][16][DP]
   float* s_ml = s_o + 4 * 16 * DP;              // [4 warps][16][2]
   {
     float* wo = s_o + warp * 16 * DP;
 #pragma unroll
-    for (int nt = 0; nt < D / 8; ++nt) {
-      if constexpr (!FP8) {
+    for (int nt = 0; nt < NO; ++nt) {
+      if constexpr (TR && !FP8) {  // d = 16 nt + r, + 8 of both rows
+        wo[ra * DP + 16 * nt + r] = o[nt][0];
+        wo[rb * DP + 16 * nt + r] = o[nt][1];
+        wo[ra * DP + 16 * nt + 8 + r] = o[nt][2];
+        wo[rb * DP + 16 * nt + 8 + r] = o[nt][3];
+      } else if constexpr (TR) {   // d = 16 nt + 2 r, + 1
+        *reinterpret_cast<float2*>(wo + ra * DP + 16 * nt + 2 * r) = make_float2(o[nt][0], o[nt][2]);
+        *reinterpret_cast<float2*>(wo + rb * DP + 16 * nt + 2 * r) = make_float2(o[nt][1], o[nt][3]);
+      } else if constexpr (!FP8) {
         *reinterpret_cast<float2*>(wo + r * DP + 8 * nt + 2 * j) = make_float2(o[nt][0], o[nt][1]);
         *reinterpret_cast<float2*>(wo + (r + 8) * DP + 8 * nt + 2 * j) = make_float2(o[nt][2], o[nt][3]);
       } else {  // columns 2j, 2j + 1 of n-tile 2c (2c + 1) are d = 16 c + 4 j, + 2 (+ 1, + 3)
@@ -372,12 +499,12 @@ __global__ void __launch_bounds__(128, 3)
         wo[(r + 8) * DP + d + 2] = o[nt][3];
       }
     }
-    if (j == 0) {
+    if ((TR ? r : j) == 0) {
       float* ml = s_ml + warp * 32;
-      ml[2 * r] = m_a;
-      ml[2 * r + 1] = l_a;
-      ml[2 * (r + 8)] = m_b;
-      ml[2 * (r + 8) + 1] = l_b;
+      ml[2 * ra] = m_a;
+      ml[2 * ra + 1] = l_a;
+      ml[2 * rb] = m_b;
+      ml[2 * rb + 1] = l_b;
     }
   }
   __syncthreads();

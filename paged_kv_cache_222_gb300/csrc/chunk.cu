@@ -19,8 +19,8 @@
 // output's own 2^-8.  Bound: the HBM stream of 2 D bytes x type size per visible
 // key and KV head.  64 sequences of 512-8192 tokens, 64 + 8 heads of 128, bf16,
 // capped scores: 188-191 us with the merge, 6.5 TB/s, 96-97 % of the measured
-// copy; 256 sequences of 1040 visible tokens in E4M3: 104 us, 5.3 TB/s, 79 %.
-// There a call costs 20 us besides its stream, whatever the window: a CTA's
+// copy; 256 sequences of 1040 visible tokens in E4M3: 100 us, 5.5 TB/s, 82 %.
+// There a call costs 18 us besides its stream, whatever the window: a CTA's
 // first loads and the merge of its four warps, which CTAs that stream E4M3 are
 // too busy to make up for (in bf16 it is 5 us).
 
@@ -33,11 +33,17 @@ namespace {
 
 constexpr int kSmallTile = kChunkSmallTile;  // keys per step
 
-template <int D, bool FP8>
+// CTAs per SM, and a ring that lets them fit: the smaller a row, the more of a
+// CTA's life is its start and its merge, which others have to stream under.
+// Up to 8 rows leave registers for four (E4M3 of 128 or bf16 of 64 wide: 256
+// sequences of 1024 visible keys 102 -> 100 us and 90.8 -> 88, of 512 64 -> 59) or five
+// (E4M3 of 64 wide: 78 -> 61, four 66), with two stages of bf16 rows of 128 three.
+template <int D, bool FP8, bool TWO>
 struct SmallShape {
   using L = Layout<D, FP8>;
   static constexpr int STAGE = 4 * L::STAGEB;             // 64 keys of K and V
-  static constexpr int NS = 65536 / STAGE > 8 ? 8 : 65536 / STAGE;  // 64 KB: three CTAs per SM
+  static constexpr int CTAS = TWO || STAGE >= 32768 ? 3 : (STAGE == 16384 ? 4 : 5);
+  static constexpr int NS = (CTAS == 3 ? 65536 : (CTAS == 4 ? 49152 : 32768)) / STAGE;
   static constexpr int DP = D + 4;
   static constexpr int BYTES = NS * STAGE + 4 * NS * 8 + kChunkMaxSplitBlocks * 4 + 1024;
   static_assert(4 * 16 * DP * 4 + 4 * 16 * 2 * 4 <= NS * STAGE, "merge buffer fits the stages");
@@ -46,16 +52,16 @@ struct SmallShape {
 // TWO: tiles of more than 8 rows, S = Q K^T and O += P V with a lane's rows r
 // and r + 8.  Up to 8 rows: the products transposed.
 template <int D, bool FP8, bool TWO>
-__global__ void __launch_bounds__(128, 3)
+__global__ void __launch_bounds__(128, SmallShape<D, FP8, TWO>::CTAS)
     chunk_small_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                        const ChunkParams p) {
   using L = Layout<D, FP8>;
-  using C = SmallShape<D, FP8>;
+  using C = SmallShape<D, FP8, TWO>;
   constexpr int KS = D / 16, NS = C::NS, STAGE = C::STAGE, DP = C::DP;
   // Up to 8 rows: S^T = K Q^T and O^T += V^T P^T, keys as the products' 16 rows
   // and tile rows as their 8 columns: half as many products as the other form,
   // which leaves half of its 16 rows empty, and half the registers of O (256
-  // sequences of 1040 visible tokens: E4M3 112 -> 104 us; 1024 in bf16 165 -> 164).
+  // sequences of 1040 visible tokens: E4M3 112 -> 104 us; 1024 in bf16 165 -> 164, three CTAs per SM each).
   constexpr bool TR = !TWO;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -644,7 +650,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const ChunkParams p,
 template <int D, bool FP8, bool TWO>
 cudaError_t launch_small_t(const ChunkParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
   auto kern = chunk_small_kernel<D, FP8, TWO>;
-  constexpr int smem = SmallShape<D, FP8>::BYTES;
+  constexpr int smem = SmallShape<D, FP8, TWO>::BYTES;
   static int configured[64] = {};
   cudaError_t e = set_smem_once(kern, smem, configured);
   if (e != cudaSuccess) return e;

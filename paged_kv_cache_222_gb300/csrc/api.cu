@@ -1316,15 +1316,29 @@ pkv_status chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_
   const int64_t units = row_tiles * c->num_kv_heads;
   int64_t st = split_tokens;
   if (st == 0) {
-    // mma.sync kernel: as for decode, three CTAs per SM streaming one split
-    // each, but below 1024 tokens, where a split's fixed cost weighs, no more
-    // CTAs than SMs (16 sequences of 1000-4000 tokens: 42.5 us at 256 tokens, 36
-    // at 1024; one of 60k 56.6 and 55; 8 of 31k take 1280: 159 us).
     const int64_t all = ceil_div(tiles * nk, 128) * 128;
     if (small) {
-      st = decode_split_tokens(static_cast<int32_t>(row_tiles < 0x7FFFFFFF ? row_tiles : 0x7FFFFFFF), c->num_kv_heads,
-                               static_cast<int32_t>(all < 0x7FFFFFC0 ? all : 0x7FFFFFC0), sms);
-      while (st < 1024 && st < all && units * ceil_div(all, st) > sms) st += 64;
+      // mma.sync kernel: what counts is one round of the CTAs that fit at once, a
+      // few beyond it cost a second one (4 sequences of 16k-30k E4M3 tokens: 44 us
+      // at 0.97 rounds, 54 at 1.07): as many splits as fit if every sequence is
+      // as long as the bound (16 of 1k-2k 18.7 us with 512 tokens, 25.6 with 1024;
+      // 2 of 8k 15 with 256, 18 with 1024; below 256 the merge costs more), but
+      // none of up to 1024 tokens where every SM has a unit (32 of 500-1000: 16
+      // us, two splits 18).  With
+      // splits above 1024 tokens, where sequences shorter than the bound leave
+      // much of the round empty and the longest is waited for, only where there
+      // are eight and more (16 of 511-8191: 45 us with 2048, 32 with 1024), or one
+      // each of up to 2048 tokens that nearly fill the round (64 of 1k-2k: 43 us,
+      // two splits 49).  Else as for decode, from 1024 tokens.
+      const int64_t slots = sms * pkv::chunk_small_ctas(c->head_dim, c->dtype == PKV_E4M3, max_q_len * group <= 8);
+      const int64_t n = units > 0 ? slots / units : slots;
+      st = n > 0 && !(all <= 1024 && units >= sms) ? ceil_div(ceil_div(all, n), 128) * 128 : all;
+      if (st < 256) st = 256;
+      if (n == 0 || (st > 1024 && n < 8 && !(n == 1 && units * 5 >= slots * 3 && all <= 2048))) {
+        st = decode_split_tokens(static_cast<int32_t>(row_tiles < 0x7FFFFFFF ? row_tiles : 0x7FFFFFFF), c->num_kv_heads,
+                                 static_cast<int32_t>(all < 0x7FFFFFC0 ? all : 0x7FFFFFC0), sms);
+        while (st < 1024 && st < all) st += 64;
+      }
       if (st > max_st) st = max_st;
     } else {
       const int64_t each = tc_split_tiles(n_tokens, batch, tile_q, num_q_heads, *c, tiles, sms);

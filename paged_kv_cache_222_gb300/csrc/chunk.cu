@@ -42,7 +42,7 @@ template <int D, bool FP8, bool TWO>
 struct SmallShape {
   using L = Layout<D, FP8>;
   static constexpr int STAGE = 4 * L::STAGEB;             // 64 keys of K and V
-  static constexpr int CTAS = TWO || STAGE >= 32768 ? 3 : (STAGE == 16384 ? 4 : 5);
+  static constexpr int CTAS = chunk_small_ctas(D, FP8, !TWO);
   static constexpr int NS = (CTAS == 3 ? 65536 : (CTAS == 4 ? 49152 : 32768)) / STAGE;
   static constexpr int DP = D + 4;
   static constexpr int BYTES = NS * STAGE + 4 * NS * 8 + kChunkMaxSplitBlocks * 4 + 1024;
@@ -675,8 +675,9 @@ cudaError_t launch_chunk_small(const ChunkParams& p, const CUtensorMap& tk, cons
 }
 
 cudaError_t launch_chunk_combine(const ChunkParams& p, int nk, cudaStream_t stream) {
-  // a whole CTA per row while the rows alone leave SMs idle
-  const bool few = static_cast<int64_t>(p.n_tokens) * p.num_q_heads <= 2048 && p.max_splits > 8;
+  // a whole CTA per row while the rows alone leave SMs idle and a warp would
+  // have many pieces (9 pieces of 128 rows: 5 us slower than by warps)
+  const bool few = static_cast<int64_t>(p.n_tokens) * p.num_q_heads <= 2048 && p.max_splits > 16;
   const dim3 grid(p.n_tokens, few ? p.num_q_heads : (p.num_q_heads + 7) / 8);
   if (p.head_dim == 128)
     return few ? launch_pdl(chunk_combine_kernel<128, 8>, grid, dim3(256), 0, stream, p, nk)

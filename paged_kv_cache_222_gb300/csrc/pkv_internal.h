@@ -287,6 +287,11 @@ constexpr int kChunkMaxSplitBlocks = 1024;
 // Keys per tile: of the mma.sync kernel; of the tcgen05 kernel at most, and by
 // its variant (chunk_tc.cu: whether S(k+1) is issued ahead of P(k)'s product).
 constexpr int kChunkSmallTile = 64, kChunkTcTile = 128;
+// CTAs per SM of the mma.sync kernel, by the bytes of a 64-key step (chunk.cu).
+constexpr int chunk_small_ctas(int head_dim, bool fp8, bool eight_rows) {
+  const int stage = 2 * kChunkSmallTile * head_dim * (fp8 ? 1 : 2);
+  return !eight_rows || stage >= 32768 ? 3 : (stage == 16384 ? 4 : 5);
+}
 constexpr bool chunk_tc_early(bool fp8, bool mods) { return !fp8 && mods; }
 constexpr int chunk_tc_tile(int head_dim, bool fp8, bool mods) {
   return head_dim == 128 && chunk_tc_early(fp8, mods) ? 64 : kChunkTcTile;

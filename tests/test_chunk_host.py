@@ -126,6 +126,23 @@ def test_chunk_plans(lib):
         pkv.chunk_plan(1, 1, 1, 60, c, 100)
 
 
+@pytest.mark.parametrize("dkw", [{}, dict(head_dim=64), dict(dtype=pkv.PKV_E4M3), dict(head_dim=64, dtype=pkv.PKV_E4M3)])
+@pytest.mark.parametrize("group", [1, 8, 16])
+def test_plans_of_single_tokens(lib, dkw, group):
+    # every size: the pieces hold the context, fit the block list and are whole
+    # steps; nothing to do is a plan too
+    c = desc(num_blocks=1 << 20, **dkw)
+    h = c.num_kv_heads
+    assert pkv.chunk_plan(0, 0, 1, group * h, c, 0).workspace_bytes == 0
+    for batch in (1, 2, 3, 8, 17, 64, 300, 4000):
+        for ctx in (1, 64, 100, 1000, 1025, 2048, 2049, 8192, 30000, 200001, 1 << 21):
+            p = pkv.chunk_plan(batch, batch, 1, group * h, c, ctx)
+            assert p.workers == 1 and p.split_tokens % 64 == 0
+            assert 64 <= p.split_tokens <= 1024 * c.block_size
+            steps = -(-ctx // 64) * 64
+            assert (p.max_splits - 1) * p.split_tokens < steps <= p.max_splits * p.split_tokens
+
+
 def test_python_checks_come_before_the_library():
     q = torch.zeros((2, 8, 128), dtype=torch.bfloat16)
     kc = torch.zeros((4, 2, 16, 128), dtype=torch.bfloat16)

@@ -823,6 +823,8 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
       if (ok && warp_ok) {
         // ---- O leaves through the warp's staging, SB bytes of its rows per
         // pass, so that a store instruction writes whole pieces of that size
+        // (four prompts of 1000 tokens: 88 us; 32 bytes of its row per lane and
+        // store 90.5, 16 bytes 97; without any output 72)
         tc_fence_after();
         const float inv = lsum > 0.f ? (FP8 ? __int_as_float(u.v_bits) / lsum : 1.f / lsum) : 0.f;
         const bool direct = u.nsplit == 1;

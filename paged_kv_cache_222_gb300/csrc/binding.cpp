@@ -148,16 +148,23 @@ Scales scales(PyObject* ko, PyObject* vo, PyObject* so, const Caches& c, int64_t
   return s;
 }
 
-// Runs the ABI call on the device's current stream without the interpreter's lock.
+// The interpreter's lock, given up while this lives and taken back on every way out.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// Runs the ABI call on the device's current stream without the interpreter's
+// lock: `call` neither touches Python objects nor refuses arguments.
 template <class F>
 pkv_status on_stream(at::Device dev, F&& call) {
   const c10::cuda::CUDAGuard guard(dev);
   pkv_stream_t stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-  pkv_status st;
-  Py_BEGIN_ALLOW_THREADS;
-  st = call(stream);
-  Py_END_ALLOW_THREADS;
-  return st;
+  const Unlocked unlocked;
+  return call(stream);
 }
 
 void expect(Py_ssize_t got, Py_ssize_t want) {
@@ -262,6 +269,7 @@ PyObject* rotary_append(PyObject* const* a, Py_ssize_t n_args) {
   if (pos.dim() != 1 || pos.size(0) != n || slots.dim() != 1 || slots.size(0) != n)
     raise(PyExc_ValueError, "positions and slot_mapping must have one entry per token");
   if (freq.dim() != 1) raise(PyExc_ValueError, "inv_freq must be [rotary_dim / 2]");
+  const int32_t heads = size32(hq, "H_q"), rotary_dim = size32(2 * freq.size(0), "rotary_dim");
   const Scales sc = scales(a[8], a[9], a[13], c, n);
   const float magnitude = real(a[10]);
   const int interleaved = PyObject_IsTrue(a[11]);
@@ -276,9 +284,8 @@ PyObject* rotary_append(PyObject* const* a, Py_ssize_t n_args) {
   }
   const pkv_status st = on_stream(c.dev, [&](pkv_stream_t stream) {
     return g_rotary_append(q.data_ptr(), q_st, k.data_ptr(), k_st, v.data_ptr(), v_st,
-                           type == at::kBFloat16 ? PKV_BF16 : PKV_F32, n, size32(hq, "H_q"),
-                           pos.const_data_ptr<int64_t>(), freq.const_data_ptr<double>(),
-                           size32(2 * freq.size(0), "rotary_dim"), interleaved, magnitude,
+                           type == at::kBFloat16 ? PKV_BF16 : PKV_F32, n, heads, pos.const_data_ptr<int64_t>(),
+                           freq.const_data_ptr<double>(), rotary_dim, interleaved, magnitude,
                            slots.const_data_ptr<int64_t>(), c.k.data_ptr(), c.v.data_ptr(), &c.desc, sc.k, sc.v,
                            sc.stride, out.data_ptr(), o_st, stream);
   });

@@ -49,9 +49,11 @@
 // 192) and the widening warps take issue slots; S from the codes themselves,
 // with Q as two E4M3 planes, has half the widening but was no faster (633 us).
 //
-// Every wait is bounded; a time-out records the error, raises the CTA's abort
-// flag, which ends every role's loop, and the CTA drains its copies and
-// products before it frees TMEM.
+// Every wait is bounded; a time-out records the error and raises the CTA's abort
+// flag, which ends every role's loop.  Each product issuer leaves after its
+// products.  Once every role has left, so that nothing is issued any more, an
+// aborted CTA waits (bounded again) for the last copy on every barrier, K, V, Q
+// and the launch control's answer, before its shared memory goes to another CTA.
 
 #include <type_traits>
 
@@ -85,7 +87,7 @@ struct TcShape {
   static constexpr int RU = 4;                     // units in flight between the roles
   static constexpr int UNIT = 20;                  // words of one
   static constexpr int NBARS = 2 * NS + 2 * NR + 5 * GROUPS + 6 + 2 * RU + GROUPS;
-  static constexpr int BYTES = QBYTES + NS * TILE + NR * RAW + 8 * STAGE + 16 + NBARS * 8 + RU * UNIT * 4 + 16 + 1024;
+  static constexpr int BYTES = QBYTES + NS * TILE + NR * RAW + 8 * STAGE + 16 + NBARS * 8 + RU * UNIT * 4 + 32 + 1024;
   static_assert(BYTES <= 232448, "shared memory per CTA");
   static constexpr int THREADS = FP8 ? 512 : 384;
   // registers: 384 x 168 or 512 x 128 at launch.  The softmax wants all it can
@@ -285,6 +287,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
   uint32_t* s_unit = reinterpret_cast<uint32_t*>(done + GROUPS);
   uint32_t* s_tmem = s_unit + RU * C::UNIT;
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  int* s_issued = reinterpret_cast<int*>(s_tmem + 2);  // [4]: next K item, next V item, answers asked for, Qs loaded
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -459,7 +462,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
       const int hf = lane / per_half, bi = lane % per_half;
       const uint32_t off = hf * C::HALFB + bi * p.block_size * ROWB;
       int item = v;  // K of tile j is item 2 j of the ring, V item 2 j + 1
-      int asked = 0, fixes = 0;  // units asked for; units with a zeroed tail so far
+      int asked = 0, loads = 0, fixes = 0;  // units asked for; Qs loaded; units with a zeroed tail so far
       bool ok = true;
       uint32_t bx = blockIdx.x, by = blockIdx.y;
       TcUnit u;
@@ -514,6 +517,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
               tma_load_4d(smem_u32(q_sm) + hh * C::QHALF, &tmap_q, smem_u32(qfull), hh * 64, 0, u.h, u.row0);
           }
           __syncwarp();
+          ++loads;
         }
         const int32_t* tbl = p.block_tables + static_cast<int64_t>(u.b) * p.max_blocks;
         // the block this lane's box of tile k holds; blocks that no row sees are
@@ -567,10 +571,9 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
           ++fixes;
         }
       }
-      if (lane == 0 && *s_abort) {  // the copies in flight land before the CTA leaves
-        for (int i = item - 2; i >= 0 && i > item - 2 - NRING; i -= 2)
-          mbar_wait(smem_u32(bfull + i % NRING), static_cast<uint32_t>((i / NRING) & 1), nullptr);
-        if (v == 0 && asked > 0) mbar_wait(smem_u32(clc), static_cast<uint32_t>((asked - 1) & 1), nullptr);
+      if (lane == 0) {
+        s_issued[v] = item;
+        s_issued[2 + v] = v == 0 ? asked : loads;
       }
     } else if (FP8 && warp >= kConv) {
       // ------------------------------------------------------------ widening
@@ -904,6 +907,15 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
   allow_next_grid();
   tc_fence_before();
   __syncthreads();
+  if (warp == kLoadK && *s_abort) {  // what is still in flight lands before the CTA leaves
+    constexpr int NRING = FP8 ? NR : NS;
+    uint64_t* bfull = FP8 ? rfull : full;
+    const int next_k = s_issued[0], next_v = s_issued[1], asked = s_issued[2], loads = s_issued[3];
+    const int last = lane < NRING ? ring_last_item(lane, NRING, next_k, next_v) : -1;
+    if (last >= 0) mbar_wait(smem_u32(bfull + lane), static_cast<uint32_t>((last / NRING) & 1), nullptr);
+    if (lane == 0 && asked > 0) mbar_wait(smem_u32(clc), static_cast<uint32_t>((asked - 1) & 1), nullptr);
+    if (lane == 0 && loads > 0) mbar_wait(smem_u32(qfull), static_cast<uint32_t>((loads - 1) & 1), nullptr);
+  }
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);

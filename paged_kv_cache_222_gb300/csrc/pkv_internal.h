@@ -297,6 +297,16 @@ constexpr int chunk_tc_tile(int head_dim, bool fp8, bool mods) {
   return head_dim == 128 && chunk_tc_early(fp8, mods) ? 64 : kChunkTcTile;
 }
 
+// Of a ring whose item i goes to slot i % slots, even items (K) issued by one
+// loader up to next_k - 2 and odd ones (V) by another up to next_v - 2: the last
+// item issued into `slot`, -1 if there was none.
+constexpr int ring_last_item(int slot, int slots, int next_k, int next_v) {
+  const int k = next_k - 2, v = next_v - 2;
+  for (int i = k > v ? k : v; i >= 0; --i)
+    if (i % slots == slot && i <= (i % 2 ? v : k)) return i;
+  return -1;
+}
+
 // Rows of query heads one cascade prefix CTA covers: two groups of 128 TMEM
 // lanes.
 constexpr int kCascadeRowsTc = 256;

@@ -458,8 +458,9 @@ pkv_status pkv_multi_query_attention(const void* q, int32_t batch, int32_t q_len
  *   context_lens[b] may hold anything; those before it that a query does not
  *   see must be finite.
  * A sequence whose row range leaves [0, n_tokens] or exceeds max_q_len is
- * recorded (PKV_DEVERR_CONTEXT_LEN) and skipped.  batch == 0 or n_tokens == 0
- * is a no-op.
+ * recorded (PKV_DEVERR_CONTEXT_LEN) and skipped; a context longer than
+ * max_context_len, the table or 2^31 - 256 tokens is recorded and cut to that.
+ * batch == 0 or n_tokens == 0 is a no-op.
  *
  * pkv_chunk_plan (host only): mode 4; split_tokens / max_splits as for decode;
  * workers = 1 when row tiles of up to 16 rows run (max_q_len x G <= 16), 0

@@ -1296,6 +1296,7 @@ pkv_status chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_
   const int32_t group = num_q_heads / c->num_kv_heads;
   if (group > 16) return fail(PKV_ERR_UNSUPPORTED, "group size %d > 16", group);
   if (max_ctx < 0) return fail(PKV_ERR_INVALID_ARG, "max_context_len %d", max_ctx);
+  max_ctx = std::min(max_ctx, pkv::kChunkMaxContext);
   if (window < 0) return fail(PKV_ERR_INVALID_ARG, "window %d", window);
   const int64_t max_st = static_cast<int64_t>(pkv::kChunkMaxSplitBlocks) * c->block_size;
   if (split_tokens < 0 || (split_tokens > 0 && (split_tokens % 128 != 0 || split_tokens > max_st)))
@@ -1457,7 +1458,7 @@ extern "C" pkv_status pkv_chunk_attention(
   p.head_dim = c.head_dim;
   p.block_size = c.block_size;
   p.max_blocks = max_blocks_per_seq;
-  p.max_ctx = max_context_len;
+  p.max_ctx = std::min(max_context_len, pkv::kChunkMaxContext);
   p.window = m.window;
   p.split_tokens = pl.split_tokens;
   p.max_splits = pl.max_splits;

@@ -284,6 +284,9 @@ inline int multi_query_lanes(int rows) { return rows <= 16 ? 4 : (rows <= 32 ? 2
 constexpr int kChunkSmallRows = 16;
 constexpr int kChunkTcRows = 256;
 constexpr int kChunkMaxSplitBlocks = 1024;
+// Longest context: the end of its last key tile, and of the tile after it, are
+// still 32-bit numbers.
+constexpr int kChunkMaxContext = 0x7FFFFF00;
 // Keys per tile: of the mma.sync kernel; of the tcgen05 kernel at most, and by
 // its variant (chunk_tc.cu: whether S(k+1) is issued ahead of P(k)'s product).
 constexpr int kChunkSmallTile = 64, kChunkTcTile = 128;

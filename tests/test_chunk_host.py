@@ -143,6 +143,21 @@ def test_plans_of_single_tokens(lib, dkw, group):
             assert (p.max_splits - 1) * p.split_tokens < steps <= p.max_splits * p.split_tokens
 
 
+@pytest.mark.parametrize("dkw", [{}, dict(head_dim=64), dict(dtype=pkv.PKV_E4M3), dict(block_size=32)])
+@pytest.mark.parametrize("T,B,mq", [(200_000, 2, 100_000), (8192, 2, 4096), (1 << 20, 64, 1 << 20), (40, 1, 40)])
+def test_plans_at_the_longest_contexts(lib, T, B, mq, dkw):
+    # sizes of the tcgen05 kernel's splits stay 32-bit numbers up to the last
+    # bound there is; contexts count up to 2^31 - 256
+    c = desc(num_blocks=1 << 27, **dkw)
+    for ctx in (2 ** 31 - 1, 2 ** 31 - 64, 2 ** 31 - 127, 2 ** 31 - 128, 2 ** 31 - 256, 2 ** 31 - 257, 2 ** 30 + 1):
+        for window in (0, 1000, 2 ** 31 - 1):
+            p = pkv.chunk_plan(T, B, mq, 64, c, ctx, window=window, has_prefix=window == 1000)
+            assert p.workers == 0 and p.split_tokens > 0 and p.split_tokens % 128 == 0 and p.max_splits >= 1
+            assert p.split_tokens * p.max_splits >= min(ctx, 2 ** 31 - 256)
+            if p.max_splits > 1:
+                assert p.workspace_bytes >= T * 64 * p.max_splits * (c.head_dim + 2) * 4
+
+
 def test_python_checks_come_before_the_library():
     q = torch.zeros((2, 8, 128), dtype=torch.bfloat16)
     kc = torch.zeros((4, 2, 16, 128), dtype=torch.bfloat16)

@@ -115,9 +115,12 @@ struct ChunkSplit {
 // x * ((k2 x^2 + k1) x^2 + k0) for a raw product x: four packed FMA-pipe
 // operations for two weights' exponents instead of one, and nothing on the
 // special-function unit, which the exponentials need.
+// Where the powers pass binary32 (caps below about 1e-10 of the products) it
+// holds for no score, since infinity times a product of 0 is NaN.
 struct CapPoly {
   float2 k0, k1, k2;
   float y_mult;  // y = x * y_mult
+  float y_max;   // |y| up to which the polynomial is used
   __device__ __forceinline__ CapPoly(float w_mult, float cap_log2) {
     y_mult = w_mult * 0.34657359027997264f;  // ln 2 / 2: w = 2 y log2(e)
     const float y2 = y_mult * y_mult, f0 = cap_log2 * y_mult, f1 = f0 * y2, f2 = f1 * y2;
@@ -127,8 +130,9 @@ struct CapPoly {
     // score, -inf, then stays -inf (0 times its square would be NaN)
     const float c2 = fmaxf(0.12395031f * f2, 1.17549435e-38f);
     k2 = make_float2(c2, c2);
+    y_max = f2 <= 3.4028235e38f ? 0.35f : -1.f;
   }
-  __device__ __forceinline__ bool holds(float abs_max) const { return abs_max * y_mult <= 0.35f; }
+  __device__ __forceinline__ bool holds(float abs_max) const { return abs_max * y_mult <= y_max; }
   __device__ __forceinline__ float2 minus(float2 x, float2 neg_mu) const {  // the capped scores - mu
     const float2 t = __fmul2_rn(x, x);
     return __ffma2_rn(__ffma2_rn(__ffma2_rn(k2, t, k1), t, k0), x, neg_mu);

@@ -1465,6 +1465,8 @@ extern "C" pkv_status pkv_chunk_attention(
   p.tile_q = chunk_tile_q(max_q_len, group);
   p.qk_log2 = qk_log2;
   p.cap_log2 = m.softcap * kLog2e;
+  pkv::cap_coefficients(m.softcap, p.cap_c, p.cap_y_max);
+  p.cap_far = m.softcap > pkv::kCapNear;
   p.cache_dtype = c.dtype;
   p.err = st->err;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);

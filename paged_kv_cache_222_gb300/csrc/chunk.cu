@@ -50,8 +50,8 @@ struct SmallShape {
 };
 
 // TWO: tiles of more than 8 rows, S = Q K^T and O += P V with a lane's rows r
-// and r + 8.  Up to 8 rows: the products transposed.
-template <int D, bool FP8, bool TWO>
+// and r + 8.  Up to 8 rows: the products transposed.  FAR: a cap above kCapNear.
+template <int D, bool FP8, bool TWO, bool FAR>
 __global__ void __launch_bounds__(128, SmallShape<D, FP8, TWO>::CTAS)
     chunk_small_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                        const ChunkParams p) {
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(128, SmallShape<D, FP8, TWO>::CTAS)
     v_mult = p.v_scale[static_cast<int64_t>(b) * p.scale_stride + h];
   }
 
-  const CapPoly poly(qk_mult, p.cap_log2);
+  const CapPoly<FAR> poly(qk_mult, p);
   const float ex_mult = p.cap_log2 > 0.f || p.slopes != nullptr ? 1.f : qk_mult;  // scores to log2 weights
 
   float m_a = -CUDART_INF_F, m_b = -CUDART_INF_F, l_a = 0.f, l_b = 0.f;
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(128, SmallShape<D, FP8, TWO>::CTAS)
         const int ta = t_warp + r, tb = ta + 8;
         if (p.cap_log2 > 0.f) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[e] = capped(sc[e], qk_mult, p.cap_log2, poly);
+          for (int e = 0; e < 4; ++e) sc[e] = capped<FAR>(sc[e], qk_mult, p.cap_log2, poly);
         }
         if (p.slopes != nullptr) {
           const float m = p.cap_log2 > 0.f ? 1.f : qk_mult;
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(128, SmallShape<D, FP8, TWO>::CTAS)
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[nt][e] = capped(sc[nt][e], qk_mult, p.cap_log2, poly);
+          for (int e = 0; e < 4; ++e) sc[nt][e] = capped<FAR>(sc[nt][e], qk_mult, p.cap_log2, poly);
       }
       if (p.slopes != nullptr) {
         const float m = p.cap_log2 > 0.f ? 1.f : qk_mult;
@@ -647,9 +647,9 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const ChunkParams p,
   for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
 }
 
-template <int D, bool FP8, bool TWO>
+template <int D, bool FP8, bool TWO, bool FAR>
 cudaError_t launch_small_t(const ChunkParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
-  auto kern = chunk_small_kernel<D, FP8, TWO>;
+  auto kern = chunk_small_kernel<D, FP8, TWO, FAR>;
   constexpr int smem = SmallShape<D, FP8, TWO>::BYTES;
   static int configured[64] = {};
   cudaError_t e = set_smem_once(kern, smem, configured);
@@ -660,8 +660,11 @@ cudaError_t launch_small_t(const ChunkParams& p, const CUtensorMap& tk, const CU
 
 template <int D, bool FP8>
 cudaError_t launch_small_r(const ChunkParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
-  return p.max_q_len * p.group > 8 ? launch_small_t<D, FP8, true>(p, tk, tv, stream)
-                                   : launch_small_t<D, FP8, false>(p, tk, tv, stream);
+  if (p.max_q_len * p.group > 8)
+    return p.cap_far ? launch_small_t<D, FP8, true, true>(p, tk, tv, stream)
+                     : launch_small_t<D, FP8, true, false>(p, tk, tv, stream);
+  return p.cap_far ? launch_small_t<D, FP8, false, true>(p, tk, tv, stream)
+                   : launch_small_t<D, FP8, false, false>(p, tk, tv, stream);
 }
 
 }  // namespace

@@ -107,30 +107,38 @@ struct ChunkSplit {
   }
 };
 
-// Scores up to 0.35 of the cap: with y = score / cap,
-// tanh(y) = y (c0 + c1 y^2 + c2 y^4) with the coefficients of the least largest
-// relative error on |y| <= 0.35, 2.9e-6: a weight is off by less than 2^-13 at
-// a cap of 50, next to its own rounding, and a cap far above every score
-// changes nothing.  Powers of the multipliers folded in, that is
+// cap * tanh(score / cap), in two ways besides the exponential form; y = score / cap.
+//
+// Small scores: tanh(y) = y (c0 + c1 y^2 + c2 y^4) up to |y| = y_max, both from
+// cap_coefficients: the capped score is off by less than 2^-13, next to the
+// weight's own rounding.  Powers of the multipliers folded in, that is
 // x * ((k2 x^2 + k1) x^2 + k0) for a raw product x: four packed FMA-pipe
 // operations for two weights' exponents instead of one, and nothing on the
-// special-function unit, which the exponentials need.
-// Where the powers pass binary32 (caps below about 1e-10 of the products) it
-// holds for no score, since infinity times a product of 0 is NaN.
+// special-function unit, which the exponentials need.  Where the powers pass
+// binary32 (caps below about 1e-10 of the products) it holds for no score,
+// since infinity times a product of 0 is NaN.
+//
+// Caps above 100 (kernels of their own), scores up to 0.35 of the cap: the error
+// of so few coefficients would be more than the weight's rounding, so `far` has
+// one more and binary32's own rounding.  Below it would only cost: biased prompts
+// 6-18 %; chosen between at run time, all prompts 2-6 %.
+template <bool FAR>
 struct CapPoly {
   float2 k0, k1, k2;
-  float y_mult;  // y = x * y_mult
-  float y_max;   // |y| up to which the polynomial is used
-  __device__ __forceinline__ CapPoly(float w_mult, float cap_log2) {
+  float y_mult;    // y = x * y_mult
+  float y_max;     // |y| up to which the small scores' polynomial holds
+  __device__ __forceinline__ CapPoly(float w_mult, const ChunkParams& p) {
     y_mult = w_mult * 0.34657359027997264f;  // ln 2 / 2: w = 2 y log2(e)
-    const float y2 = y_mult * y_mult, f0 = cap_log2 * y_mult, f1 = f0 * y2, f2 = f1 * y2;
-    k0 = make_float2(0.99999713f * f0, 0.99999713f * f0);
-    k1 = make_float2(-0.33290954f * f1, -0.33290954f * f1);
+    const float y2 = y_mult * y_mult, f0 = p.cap_log2 * y_mult, f1 = f0 * y2, f2 = f1 * y2;
+    // (up to kCapNear constants: they cost no registers)
+    const float c0 = FAR ? p.cap_c[0] : kCapC[0], c1 = FAR ? p.cap_c[1] : kCapC[1];
+    k0 = make_float2(c0 * f0, c0 * f0);
+    k1 = make_float2(c1 * f1, c1 * f1);
     // positive also where the cap is so large that it underflows: a hidden
     // score, -inf, then stays -inf (0 times its square would be NaN)
-    const float c2 = fmaxf(0.12395031f * f2, 1.17549435e-38f);
+    const float c2 = fmaxf((FAR ? p.cap_c[2] : kCapC[2]) * f2, 1.17549435e-38f);
     k2 = make_float2(c2, c2);
-    y_max = f2 <= 3.4028235e38f ? 0.35f : -1.f;
+    y_max = f2 <= 3.4028235e38f ? (FAR ? p.cap_y_max : kCapLimit) : -1.f;
   }
   __device__ __forceinline__ bool holds(float abs_max) const { return abs_max * y_mult <= y_max; }
   __device__ __forceinline__ float2 minus(float2 x, float2 neg_mu) const {  // the capped scores - mu
@@ -141,15 +149,27 @@ struct CapPoly {
     const float t = x * x;
     return fmaf(fmaf(k2.x, t, k1.x), t, k0.x) * x;
   }
+  __device__ __forceinline__ bool far_holds(float x) const { return fabsf(x) * y_mult <= kCapLimit; }
+  __device__ __forceinline__ float far(float x, float cap_log2) const {
+    const float y = x * y_mult, t = y * y;
+    return y * cap_log2 * fmaf(fmaf(fmaf(kCapC3, t, kCapC2), t, kCapC1), t, 1.f);
+  }
 };
 
-// cap * tanh(score / cap) in log2 units of one raw product: the polynomial, or
-// 1 - 2 / (e^2y + 1) from w = 2 y log2(e), whose absolute error of about 2^-23
-// (times the cap) is small next to scores above 0.35 of the cap.
-__device__ __forceinline__ float capped(float x, float w_mult, float cap_log2, const CapPoly& poly) {
+// cap * tanh(score / cap) in log2 units of one raw product: a polynomial, or
+// 1 - 2 / (e^2y + 1) from w = 2 y log2(e), above 0.35 of the cap off by less than
+// 2^-22 of the cap, 2^-20 of the score.
+template <bool FAR>
+__device__ __forceinline__ float capped(float x, float w_mult, float cap_log2, const CapPoly<FAR>& poly) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fast_exp2(x * w_mult) + 1.f));
-  return poly.holds(fabsf(x)) ? poly.of(x) : fmaf(-2.f * cap_log2, r, cap_log2);
+  // (which of the two is written first: 10 % of two-token decode in either case)
+  if constexpr (FAR) {
+    const float e = fmaf(-2.f * cap_log2, r, cap_log2);
+    return poly.far_holds(x) ? poly.far(x, cap_log2) : e;
+  } else {
+    return poly.holds(fabsf(x)) ? poly.of(x) : fmaf(-2.f * cap_log2, r, cap_log2);
+  }
 }
 
 }  // namespace pkv

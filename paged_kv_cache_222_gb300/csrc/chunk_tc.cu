@@ -65,6 +65,7 @@ namespace {
 
 // What a score is besides scale * q.k: nothing; capped; biased; both.
 constexpr int kPlain = 0, kCapped = 1, kBiased = 2, kCappedBiased = 3;
+constexpr int kFar = 4;  // added to the capped ones: a cap above kCapNear
 
 template <int D, bool FP8, int MODE>
 struct TcShape {
@@ -126,14 +127,14 @@ __device__ __forceinline__ float min_nan(float a, float b) {  // NaN if one is
   return d;
 }
 
-// x := cap * tanh(x / cap) in log2 units for any x: the polynomial up to 0.35 of
+// x := cap * tanh(x / cap) in log2 units for any x: a polynomial up to 0.35 of
 // the cap, else 1 - 2 / (e^2y + 1), one reciprocal shared by four scores,
 // 1 / a = b c d / (a b c d); 2y is held below 28 log2 units, where tanh is 1 to
 // binary32 and the product of four cannot overflow.  What lies past the
 // sequence's end may be NaN and must not reach its neighbours: scores that are
 // not seen enter as 0.
-template <int N>
-__device__ __forceinline__ void cap_scores(float* x, float w_mult, float cap_log2, const CapPoly& poly, bool masked,
+template <int N, bool FAR>
+__device__ __forceinline__ void cap_scores(float* x, float w_mult, float cap_log2, const CapPoly<FAR>& poly, bool masked,
                                            const uint32_t* see) {
 #pragma unroll
   for (int i = 0; i < N; i += 4) {
@@ -150,10 +151,14 @@ __device__ __forceinline__ void cap_scores(float* x, float w_mult, float cap_log
     const float2 m2c = make_float2(-2.f * cap_log2, -2.f * cap_log2), c = make_float2(cap_log2, cap_log2);
     const float2 a = __ffma2_rn(__fmul2_rn(make_float2(rp.x, rp.x), make_float2(q[1], q[0])), m2c, c);
     const float2 b = __ffma2_rn(__fmul2_rn(make_float2(rp.y, rp.y), make_float2(q[3], q[2])), m2c, c);
-    x[i] = poly.holds(fabsf(x[i])) ? poly.of(x[i]) : a.x;
-    x[i + 1] = poly.holds(fabsf(x[i + 1])) ? poly.of(x[i + 1]) : a.y;
-    x[i + 2] = poly.holds(fabsf(x[i + 2])) ? poly.of(x[i + 2]) : b.x;
-    x[i + 3] = poly.holds(fabsf(x[i + 3])) ? poly.of(x[i + 3]) : b.y;
+    const float z[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (FAR)
+        x[i + j] = poly.far_holds(x[i + j]) ? poly.far(x[i + j], cap_log2) : z[j];
+      else
+        x[i + j] = poly.holds(fabsf(x[i + j])) ? poly.of(x[i + j]) : z[j];
+    }
   }
 }
 
@@ -241,7 +246,8 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
                     const __grid_constant__ CUtensorMap tmap_v, const ChunkParams p) {
   using C = TcShape<D, FP8, MODE>;
   constexpr int M = C::M, NK = C::NK, NS = C::NS, NR = C::NR, GROUPS = C::GROUPS, RU = C::RU;
-  constexpr bool EARLY = C::EARLY;
+  constexpr bool EARLY = C::EARLY, FAR = (MODE & kFar) != 0;
+  constexpr int SCORE = MODE & ~kFar;
   // + g * NK, + g * (EARLY ? NK / 2 : NK), + g * D
   constexpr uint32_t COL_S = 0, COL_P = EARLY ? GROUPS * NK : COL_S, COL_O = COL_P + GROUPS * (EARLY ? NK / 2 : NK);
   constexpr uint32_t P_STEP = EARLY ? NK / 2 : NK;
@@ -669,14 +675,14 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
       const int tok = token_of(r_in), gh = r_in - tok * G;
       // what the row sees; a row past the tile's takes no mask (nothing of it
       // is ever written)
-      constexpr int kFar = 0x3FFFFFFF;
-      const int pos = row_ok ? u.pos0 + tok : kFar;
+      constexpr int kFarPos = 0x3FFFFFFF;
+      const int pos = row_ok ? u.pos0 + tok : kFarPos;
       const int lo = row_ok && p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
       const int pf = row_ok && pos >= 0 ? u.prefix : 0;
       constexpr float kLog2e = 1.4426950408889634f;
       const float qk = FP8 ? p.qk_log2 * __int_as_float(u.k_bits) : p.qk_log2;
-      const float slope = (MODE == kBiased || MODE == kCappedBiased) && row_ok ? p.slopes[u.h * G + gh] * kLog2e : 0.f;
-      const CapPoly poly(qk, p.cap_log2);
+      const float slope = (SCORE == kBiased || SCORE == kCappedBiased) && row_ok ? p.slopes[u.h * G + gh] * kLog2e : 0.f;
+      const CapPoly<FAR> poly(qk, p);
 
       float m_used = -CUDART_INF_F, lsum = 0.f;
       for (int k = 0; k < u.ntile; ++k, ++sk) {
@@ -709,7 +715,7 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
           // Capped: the row maximum is taken of the raw products (a cap does not
           // change which is the largest), the cap enters with the exponent.
           bool small = false;
-          if constexpr (MODE == kCapped) {
+          if constexpr (SCORE == kCapped) {
             float am[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < NK; i += 8)
@@ -717,9 +723,9 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
               for (int j = 0; j < 4; ++j) am[j] = max3f(am[j], fabsf(x[i + 2 * j]), fabsf(x[i + 2 * j + 1]));
             small = __all_sync(kFull, poly.holds(fmaxf(max3f(am[0], am[1], am[2]), am[3])));
           }
-          if constexpr (MODE == kCappedBiased) cap_scores<NK>(x, qk, p.cap_log2, poly, masked, see);
-          if constexpr (MODE == kBiased || MODE == kCappedBiased) {
-            const float mult = MODE == kBiased ? qk : 1.f, base = slope * static_cast<float>(t0 - pos);
+          if constexpr (SCORE == kCappedBiased) cap_scores<NK, FAR>(x, qk, p.cap_log2, poly, masked, see);
+          if constexpr (SCORE == kBiased || SCORE == kCappedBiased) {
+            const float mult = SCORE == kBiased ? qk : 1.f, base = slope * static_cast<float>(t0 - pos);
             const float2 mult2 = make_float2(mult, mult), slope2 = make_float2(slope, slope);
             const float2 base2 = make_float2(base, base);
 #pragma unroll
@@ -742,8 +748,8 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
               mp[j] = fmaxf(mp[j], x[NK - 8 + j]);
             }
             mt = max3f(max3f(mp[0], mp[1], mp[2]), max3f(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
-            if constexpr (MODE == kPlain) mt *= qk;
-            if constexpr (MODE == kCapped) mt = mt == -CUDART_INF_F ? mt : capped(mt, qk, p.cap_log2, poly);
+            if constexpr (SCORE == kPlain) mt *= qk;
+            if constexpr (SCORE == kCapped) mt = mt == -CUDART_INF_F ? mt : capped<FAR>(mt, qk, p.cap_log2, poly);
           }
           float alpha = 1.f;
           bool resc = false;
@@ -798,13 +804,13 @@ __global__ void __launch_bounds__(TcShape<D, FP8, MODE>::THREADS, 1)
               tmem_st16(t_p + 16 * c, hi);
             }
           };
-          if constexpr (MODE == kPlain) {
+          if constexpr (SCORE == kPlain) {
             weights(std::integral_constant<int, 0>{});
-          } else if constexpr (MODE == kCapped) {
+          } else if constexpr (SCORE == kCapped) {
             if (small) {
               weights(std::integral_constant<int, 1>{});
             } else {
-              cap_scores<NK>(x, qk, p.cap_log2, poly, masked, see);
+              cap_scores<NK, FAR>(x, qk, p.cap_log2, poly, masked, see);
               if (masked) mask_scores<NK>(x, see);
               weights(std::integral_constant<int, 2>{});
             }
@@ -937,6 +943,9 @@ cudaError_t launch_tc_t(const ChunkParams& p, const CUtensorMap& tq, const CUten
 
 template <int D, bool FP8>
 cudaError_t launch_tc_m(const ChunkParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
+  if (p.cap_far)
+    return p.slopes != nullptr ? launch_tc_t<D, FP8, kCappedBiased | kFar>(p, tq, tk, tv, stream)
+                               : launch_tc_t<D, FP8, kCapped | kFar>(p, tq, tk, tv, stream);
   if (p.slopes != nullptr)
     return p.cap_log2 > 0.f ? launch_tc_t<D, FP8, kCappedBiased>(p, tq, tk, tv, stream)
                             : launch_tc_t<D, FP8, kBiased>(p, tq, tk, tv, stream);

@@ -2,6 +2,7 @@
 // units (append.cu, decode.cu).  Not installed; no stability promise.
 #pragma once
 
+#include <cmath>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -178,6 +179,9 @@ struct ChunkParams {
   int32_t tile_q;                // query tokens of one row tile
   float qk_log2;                 // scale * log2(e); with a cap: 2 * scale * log2(e) / cap
   float cap_log2;                // cap * log2(e), 0 without a cap
+  float cap_c[3];                // small scores' tanh(y) / y: coefficients of 1, y^2, y^4 ...
+  float cap_y_max;               // ... and the |y| = score / cap up to which they hold
+  bool cap_far;                  // caps above kCapNear
   int32_t cache_dtype;
   int* err;
 };
@@ -309,6 +313,33 @@ constexpr int ring_last_item(int slot, int slots, int next_k, int next_v) {
     if (i % slots == slot && i <= (i % 2 ? v : k)) return i;
   return -1;
 }
+
+// tanh(y) = y (c[0] + c[1] y^2 + c[2] y^4) for |y| <= y_max with cap times the
+// error below 2^-13.  Caps up to 100: the coefficients of the least largest
+// relative error on |y| <= 0.35, 2.9e-6.  Above, 1 exactly, so that the error
+// falls with the score, and the other two such that what is left of the next
+// term of the series, -17/315 y^6, is y^2 times a polynomial in y^2 with its two
+// zeros placed for the least largest value up to y_max (a Chebyshev polynomial
+// moved until its first zero is at 0: the others at 0.4641 and 0.9282 of y_max^2):
+// 2.1e-3 y_max^7 of the cap.
+constexpr double kCapNear = 100.0;
+constexpr float kCapLimit = 0.35f, kCapC[3] = {0.99999713f, -0.33290954f, 0.12395031f};
+inline void cap_coefficients(double cap, float (&c)[3], float& y_max) {
+  if (cap <= kCapNear) {
+    for (int i = 0; i < 3; ++i) c[i] = kCapC[i];
+    y_max = kCapLimit;
+    return;
+  }
+  const double a = std::pow(0.045 / cap, 1.0 / 7.0), next = -17.0 / 315.0;
+  c[0] = 1.f;
+  c[1] = static_cast<float>(-1.0 / 3.0 - next * 0.4641 * 0.9282 * a * a * a * a);
+  c[2] = static_cast<float>(2.0 / 15.0 + next * (0.4641 + 0.9282) * a * a);
+  y_max = static_cast<float>(a);
+}
+
+// tanh(y) = y (1 + kCapC1 y^2 + kCapC2 y^4 + kCapC3 y^6) for |y| <= kCapLimit, off
+// by less than 4.1e-8 of itself: the least largest relative error with 1 exactly.
+constexpr float kCapC1 = -0.33332663f, kCapC2 = 0.13299825f, kCapC3 = -0.0491485f;
 
 // Rows of query heads one cascade prefix CTA covers: two groups of 128 TMEM
 // lanes.

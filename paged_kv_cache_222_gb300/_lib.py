@@ -155,7 +155,8 @@ def binding():
                 from . import _binding as mod
             except ImportError as e:
                 raise RuntimeError("the compiled binding is not built or does not fit this PyTorch; run "
-                                   "`python -m paged_kv_cache_222_gb300.build`") from e
+                                   "`python -m paged_kv_cache_222_gb300.build`, which prints why where it does not "
+                                   "compile") from e
             mod.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                        for f in ("pkv_chunk_plan", "pkv_chunk_attention", "pkv_rotary_append", "pkv_compact_tokens")))
             _binding = mod

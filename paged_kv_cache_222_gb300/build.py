@@ -5,7 +5,12 @@ Each CUDA translation unit is compiled in parallel, then linked into a shared
 library next to this file.  CUDA's runtime is linked statically and the driver
 entry point for tensor-map encoding is looked up at run time, so the library
 loads on a machine without a GPU driver (only calls that reach the GPU need
-one).  Rebuilds only when a source or header is newer than the library.
+one).  Rebuilds only when a source or header is newer than the library, or the
+Python or PyTorch that the binding was built against is another.
+
+The library needs neither Python's nor PyTorch's headers: where the binding
+does not compile, the library is built all the same and the compiler's message
+printed; the calls that need the binding then raise.
 
     python -m paged_kv_cache_222_gb300.build [--force] [--verbose]
 """
@@ -44,11 +49,30 @@ def _inputs():
     return files
 
 
-def up_to_date():
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
+def _newest(path):
+    """No source is newer than the built file."""
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in _inputs())
+
+
+def _binding_against():
+    """What the binding is built against: another Python or PyTorch needs another."""
+    import torch
+    return f"{sys.version}\n{torch.__version__}\n{os.path.dirname(torch.__file__)}\n"
+
+
+def _stamp_path():
+    return BINDING_PATH + ".against"
+
+
+def _binding_up_to_date():
+    if not _newest(BINDING_PATH) or not os.path.exists(_stamp_path()):
         return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    with open(_stamp_path()) as f:
+        return f.read() == _binding_against()
+
+
+def up_to_date():
+    return _newest(LIB_PATH) and _binding_up_to_date()
 
 
 def _binding_command(out):
@@ -66,11 +90,56 @@ def _binding_command(out):
                "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"])
 
 
+def _start(cmd, verbose):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _start_binding(out, verbose):
+    """The running compiler, or the reason there is none."""
+    try:
+        return _start(_binding_command(out), verbose), ""
+    except (ImportError, OSError) as e:
+        return None, f"{type(e).__name__}: {e}"
+
+
+def _finish_binding(started, tmp, verbose):
+    proc, text = started
+    if proc is not None:
+        text = proc.communicate()[0].decode(errors="replace")
+        if proc.returncode == 0:
+            if verbose:
+                sys.stdout.write(text)
+            os.replace(tmp, BINDING_PATH)
+            with open(_stamp_path(), "w") as f:
+                f.write(_binding_against())
+            return
+    for stale in (BINDING_PATH, _stamp_path()):  # of other sources or another PyTorch
+        if os.path.exists(stale):
+            os.remove(stale)
+    print(f"the compiled binding was not built (libpkv.so does not need it):\n{text}", file=sys.stderr, flush=True)
+
+
 def build(force=False, verbose=False, ptxas_verbose=False):
-    """Compile and link libpkv.so; returns its path."""
-    if not force and up_to_date():
+    """Compile and link libpkv.so, and the binding where it compiles; returns the
+    library's path."""
+    lib, binding = force or not _newest(LIB_PATH), force or not _binding_up_to_date()
+    if not lib and not binding:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
+    binding_tmp = BINDING_PATH + ".tmp"
+    started = _start_binding(binding_tmp, verbose) if binding else None
+    try:
+        if lib:
+            _build_library(verbose, ptxas_verbose)
+    finally:
+        if binding:
+            _finish_binding(started, binding_tmp, verbose or ptxas_verbose)
+    return LIB_PATH
+
+
+def _build_library(verbose, ptxas_verbose):
     cc = nvcc()
     common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-I", INCLUDE, "-I", CSRC, "--expt-relaxed-constexpr"]
@@ -81,15 +150,7 @@ def build(force=False, verbose=False, ptxas_verbose=False):
     for src in SOURCES:
         obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
         objs.append(obj)
-        cmd = [cc] + common + ["-c", os.path.join(CSRC, src), "-o", obj]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    binding_tmp = BINDING_PATH + ".tmp"
-    cmd = _binding_command(binding_tmp)
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    procs.append(("binding.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+        procs.append((src, _start([cc] + common + ["-c", os.path.join(CSRC, src), "-o", obj], verbose)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -102,15 +163,11 @@ def build(force=False, verbose=False, ptxas_verbose=False):
         msg = "\n".join(f"--- {s}\n{t}" for s, t in failed)
         raise RuntimeError(f"compilation failed:\n{msg}")
     tmp = LIB_PATH + ".tmp"
-    cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static"]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
+    p = _start([cc] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static"], verbose)
+    out, _ = p.communicate()
+    if p.returncode != 0:
+        raise RuntimeError("link failed:\n" + out.decode(errors="replace"))
     os.replace(tmp, LIB_PATH)
-    os.replace(binding_tmp, BINDING_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":

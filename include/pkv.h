@@ -497,7 +497,7 @@ pkv_status pkv_chunk_attention(const void* q, int32_t n_tokens, const int32_t* q
  *                  PKV_F32), num_q_heads / num_kv_heads / num_kv_heads heads;
  *                  tokens q_stride / k_stride / v_stride elements apart (so
  *                  slices of one fused projection do), 16-byte aligned.
- *   positions      int64 [n_tokens], any value.
+ *   positions      int64 [n_tokens], negative ones too (see the angles' bound).
  *   inv_freq       float64 [rotary_dim / 2] (device), finite: radians per
  *                  position of each pair.
  *   magnitude      finite: factor on sine and cosine (1: a rotation).
@@ -508,9 +508,12 @@ pkv_status pkv_chunk_attention(const void* q, int32_t n_tokens, const int32_t* q
  *                  token's K/V rows; its query is still turned).
  *   q_out          bf16 [n_tokens, num_q_heads, head_dim], tokens out_stride
  *                  elements apart; may be q itself (same strides, bf16).
- * Sines and cosines are binary32 of the angle pos * inv_freq taken modulo one
- * turn without rounding; a turned element is rounded once, to bf16 or to the
- * code of x / scale.  n_tokens == 0 is a no-op.
+ * The angle pos * inv_freq is taken modulo one turn in 64-bit fixed point: off by
+ * at most |pos * inv_freq| 2^-52 + |pos| 2^-62 radians, and 2^-22 for binary32.
+ * With frequencies up to 1 that is below 2^-20 at positions up to 2^31 and below
+ * bf16's own rounding up to 2^42; far beyond, angles lose their meaning.  A
+ * turned element is rounded once, to bf16 or to the code of x / scale.
+ * n_tokens == 0 is a no-op.
  */
 pkv_status pkv_rotary_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                              int64_t v_stride, int32_t src_dtype, int64_t n_tokens, int32_t num_q_heads,

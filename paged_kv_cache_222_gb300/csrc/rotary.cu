@@ -12,9 +12,11 @@
 //
 // Angles of far positions: f_i / 2 pi is taken as a 64-bit fixed-point
 // fraction of a turn, so that pos * f_i modulo one turn is one wrapping 64-bit
-// integer product, exact up to f_i's own rounding (2^-53 of pos * f_i turns),
-// with no reduction and no 64-bit floating point per position.  The top 32
-// bits of it are the angle.
+// integer product, with no reduction and no 64-bit floating point per position.
+// 1 / 2 pi and its product with f_i are each rounded to 53 bits and the fraction
+// to 2^-64, which the product multiplies: at most |pos f_i| 2^-52 radians + |pos|
+// 2^-65 turns, 2^-21 + 2^-31 radians at |pos f_i| = 2^31.  The top 32 bits of the
+// product are the angle, rounded to binary32 (2^-25 of a turn).
 //
 // A CTA of 128 threads takes one token: its threads compute the token's (c, s)
 // once for all heads into shared memory, under the first item's loads, then

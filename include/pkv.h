@@ -445,7 +445,9 @@ pkv_status pkv_multi_query_attention(const void* q, int32_t batch, int32_t q_len
  *   out            bf16 [n_tokens, num_q_heads, head_dim], 16-byte aligned.
  *                  The weights are rounded to the cache's 16-bit type (bf16, or
  *                  f16 for E4M3 caches, whose q is taken as f16 too: finite
- *                  below 65520) and sums are binary32.
+ *                  below 65520, and held to 2^-25 below 2^-14) and sums are
+ *                  binary32; pkv_decode_attention holds weights over bf16 caches
+ *                  to 16 bits.
  *   k_scale, v_scale  as pkv_decode_attention; positive.
  *   split_tokens   0 = automatic, else visible tokens per split (a multiple of
  *                  128, at most 1024 * block_size).

@@ -44,10 +44,11 @@
 // 16 softmax warps, half a row each (1410-1540 us: they spill); P handed over
 // in halves (12 % slower) and S as two products of 64 keys (24 %); three ring
 // slots instead of four (1290); 128 bytes of a row per output pass (1045).
-// E4M3 caches: chunks of 512 tokens over 3584 take 614 us where bf16 takes 521:
-// the softmax has 200 registers a thread instead of 224 (570 us for bf16 with
-// 192) and the widening warps take issue slots; S from the codes themselves,
-// with Q as two E4M3 planes, has half the widening but was no faster (633 us).
+// E4M3 caches: chunks of 512 tokens over 3584 take 616 us where bf16 takes 513:
+// the softmax has 200 registers a thread instead of 224 (bf16 with 192: 570 us
+// where it then took 521), and the widening is worth 30 us (586 with none); S from
+// the codes themselves, with Q as two E4M3 planes, has half the widening but was
+// no faster (633 us).
 //
 // Every wait is bounded; a time-out records the error and raises the CTA's abort
 // flag, which ends every role's loop.  Each product issuer leaves after its
@@ -187,8 +188,10 @@ __device__ __forceinline__ bool tc_unit(const ChunkParams& p, int x, int y, TcUn
     // a lane per sequence: the sequences whose last tokens see most keys first
     // (equal ones in order), so that no long unit is left for the end (12 chunks
     // of 1-512 tokens over 0-3584: 250 us, in the order given 272); the tiles
-    // before a sequence's are those of the sequences ahead of it.  More
-    // sequences have so many units that the last ones weigh little.
+    // before a sequence's are those of the sequences ahead of it.  More than a
+    // warp's lanes come in the order they are given: 33 of 1-128 tokens 129 us
+    // if that is longest first and 152-158 if not, 64 246 and 257-270; of 1-512
+    // tokens less than 1 %.
     const int lane = threadIdx.x & 31;
     const ChunkSeq mine = chunk_seq(p, lane < p.batch ? lane : 0, lane < p.batch && y == 0 && u.h == 0);
     const int nt = lane < p.batch ? (mine.n + p.tile_q - 1) / p.tile_q : 0;

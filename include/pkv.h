@@ -61,7 +61,8 @@ typedef enum {
 typedef enum {
   PKV_BF16 = 0,  /* bfloat16 (2 bytes)                                   */
   PKV_F32 = 1,   /* IEEE binary32 (4 bytes); append sources only         */
-  PKV_E4M3 = 2   /* OCP FP8 E4M3 (1 byte), no infinities, max 448        */
+  PKV_E4M3 = 2,  /* OCP FP8 E4M3 (1 byte), no infinities, max 448        */
+  PKV_E2M1 = 3   /* 4-bit E2M1 codes with an E4M3 scale per 16 of them   */
 } pkv_dtype;
 
 /*
@@ -75,8 +76,18 @@ typedef enum {
  *                 Prefix Cache": fixed blocks of typically 16 or 32 tokens)
  *   head_dim      64 or 128
  *   num_kv_heads  >= 1
- *   dtype         PKV_BF16 or PKV_E4M3
+ *   dtype         PKV_BF16, PKV_E4M3 or PKV_E2M1
  * Both cache pointers must be 16-byte aligned.
+ *
+ * PKV_E2M1: every 16 elements of a row share a scale, an E4M3 number; each of
+ * them is a code of one sign bit (bit 3) and the magnitudes 0, 1/2, 1, 3/2, 2,
+ * 3, 4, 6 (bits 2..0), times that scale (and the head's scale, see k_scale).
+ * 4.5 bits per element.  The head_dim / 2 + head_dim / 16 bytes per row are
+ * laid out per (block, head): block_size rows of head_dim / 2 code bytes
+ * (element 2 i in the low half of byte i), then block_size rows of head_dim / 16
+ * scale bytes.  Taken by pkv_append, pkv_rotary_append, pkv_read_tokens,
+ * pkv_compact_tokens, pkv_slot_mapping and the block copies; the others return
+ * PKV_ERR_UNSUPPORTED.
  */
 typedef struct {
   int64_t num_blocks;
@@ -106,6 +117,12 @@ typedef struct {
  *                  RNE-satfinite(x / scale) with x / scale an IEEE binary32
  *                  division.  bf16 caches: bf16 sources are copied bit for bit,
  *                  f32 sources are rounded to nearest even.
+ *                  E2M1 caches: both or neither (neither: 1).  With y = x / scale
+ *                  (IEEE binary32), the group's scale is RNE-satfinite E4M3 of
+ *                  max |y| / 6 and the code RNE-satfinite E2M1 of y over it, both
+ *                  binary32 quotients.  A group whose scale rounds to zero (max
+ *                  |y| up to 6 x 2^-10) is stored as zeros; a group that holds a
+ *                  NaN reads as NaN; infinities saturate.
  *   n_tokens == 0 is a no-op.
  */
 pkv_status pkv_append(const void* k_new, const void* v_new, int32_t src_dtype,
@@ -113,6 +130,29 @@ pkv_status pkv_append(const void* k_new, const void* v_new, int32_t src_dtype,
                       void* k_cache, void* v_cache, const pkv_cache_desc* cache,
                       const float* k_scale, const float* v_scale,
                       int64_t scale_row_stride, pkv_stream_t stream);
+
+/*
+ * pkv_read_tokens — token rows read back from the cache: what pkv_append wrote,
+ * as values (a prefix handed to a dense attention or to another pool, rows to
+ * be turned or scaled anew; [UI] "C++ Block Scheduler and Asynchronous Fetch
+ * Kernel": cached tokens leave for another tier).
+ *
+ *   slot_mapping   int64 [n_tokens]: row i is read from this flat slot; a
+ *                  negative slot gives zeros, one past the cache too and is
+ *                  recorded (PKV_DEVERR_SLOT).
+ *   k_scale, v_scale  as pkv_append: row i and KV head h use [i *
+ *                  scale_row_stride + h].
+ *   k_out, v_out   [n_tokens, num_kv_heads, head_dim] of out_dtype (PKV_BF16 or
+ *                  PKV_F32), 16-byte aligned.  The value is the product of code
+ *                  and scales in binary32 (one rounding; the code and an E2M1
+ *                  group's scale multiply exactly), rounded to bf16 if asked;
+ *                  bf16 caches to bf16 outputs bit for bit.
+ * n_tokens == 0 is a no-op.
+ */
+pkv_status pkv_read_tokens(const int64_t* slot_mapping, int64_t n_tokens, const void* k_cache, const void* v_cache,
+                           const pkv_cache_desc* cache, const float* k_scale, const float* v_scale,
+                           int64_t scale_row_stride, void* k_out, void* v_out, int32_t out_dtype,
+                           pkv_stream_t stream);
 
 /*
  * pkv_slot_mapping — the flat cache slot of each new token, from the block
@@ -526,6 +566,27 @@ pkv_status pkv_rotary_append(const void* q, int64_t q_stride, const void* k, int
                              pkv_stream_t stream);
 
 /*
+ * pkv_rotary_append_axes — pkv_rotary_append for tokens with a position along
+ * each of several axes (time, height and width in images and video).
+ *
+ *   positions      int64 [num_axes] rows of n_tokens, position_stride >= 0
+ *                  elements apart (0: the same positions along every axis).
+ *   axes           int32 [rotary_dim / 2] (device): pair i turns by the position
+ *                  along axis axes[i] times inv_freq[i].  NULL with one axis.  An
+ *                  entry outside [0, num_axes) is recorded (PKV_DEVERR_AXIS) and
+ *                  its pair not turned.
+ * Everything else as pkv_rotary_append.
+ */
+pkv_status pkv_rotary_append_axes(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                  int64_t v_stride, int32_t src_dtype, int64_t n_tokens, int32_t num_q_heads,
+                                  const int64_t* positions, int64_t position_stride, int32_t num_axes,
+                                  const int32_t* axes, const double* inv_freq, int32_t rotary_dim,
+                                  int32_t interleaved, float magnitude, const int64_t* slot_mapping, void* k_cache,
+                                  void* v_cache, const pkv_cache_desc* cache, const float* k_scale,
+                                  const float* v_scale, int64_t scale_row_stride, void* q_out, int64_t out_stride,
+                                  pkv_stream_t stream);
+
+/*
  * pkv_compact_tokens — in-place compaction: entry j of sequence b moves K and V
  * rows of logical position keep[keep_starts[b] + j] to logical position
  * dst_start[b] + j ([UI] "Predictive Prefetching and Attention-Salience
@@ -561,7 +622,8 @@ enum {
   PKV_DEVERR_WAIT_TIMEOUT = 1,    /* a pipeline wait gave up (bounded spin)     */
   PKV_DEVERR_BLOCK_ID = 2,        /* block table entry outside [0, num_blocks)  */
   PKV_DEVERR_CONTEXT_LEN = 3,     /* context length beyond the table or bound   */
-  PKV_DEVERR_SLOT = 4             /* append slot beyond the cache               */
+  PKV_DEVERR_SLOT = 4,            /* slot beyond the cache                      */
+  PKV_DEVERR_AXIS = 5             /* rotary axis that is none of the call's     */
 };
 
 /*
@@ -600,7 +662,7 @@ int32_t pkv_abi_version(void);
  * the number of launches and their summed device time; it then clears the
  * buffer.  Kinds: 0 append, 1 decode split, 2 combine, 3 cascade prefix,
  * 4 block copy, 5 multi-token query, 6 slot mapping, 7 chunk attention,
- * 8 rotary append, 9 token compaction.
+ * 8 rotary append, 9 token compaction, 10 token read.
  */
 typedef struct {
   int32_t kind;

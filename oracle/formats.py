@@ -161,3 +161,81 @@ def e4m3_encode_exhaustive(y, chunk=1 << 16):
 def f32_div(x, s):
     """IEEE binary32 division x / s, correctly rounded (numpy float32)."""
     return (np.asarray(x, dtype=np.float32) / np.asarray(s, dtype=np.float32)).astype(np.float32)
+
+
+# --------------------------------------------------------------------------
+# E2M1 with an E4M3 scale for every 16 elements
+#
+# OCP 4-bit floating point, "E2M1": 1 sign bit, 2 exponent bits with bias 1, 1
+# mantissa bit; no infinities, no NaN.  A group's value is its E4M3 scale times
+# the code's.
+# --------------------------------------------------------------------------
+
+E2M1_GROUP = 16
+
+
+def _e2m1_value(code):
+    s, e, m = (code >> 3) & 1, (code >> 1) & 3, code & 1
+    mag = 0.5 * m if e == 0 else (1.0 + 0.5 * m) * 2.0 ** (e - 1)
+    return -mag if s else mag
+
+
+# Value of each of the 16 codes, float64.
+E2M1_VALUES = np.array([_e2m1_value(c) for c in range(16)], dtype=np.float64)
+
+
+def e2m1_encode(y):
+    """E2M1 codes of binary32 values: the nearest of the eight magnitudes by
+    exact float64 distance, the even code on a tie; magnitudes from 6 on,
+    infinities included, give 6.  The sign is kept.  NaN is not encoded (its
+    group's scale says it)."""
+    y = np.asarray(y, dtype=np.float32)
+    a = np.minimum(np.abs(y.astype(np.float64)), 6.0)
+    dist = np.abs(a[..., None] - E2M1_VALUES[:8])
+    near = dist == np.nanmin(dist, axis=-1, keepdims=True)
+    even = near & (np.arange(8) % 2 == 0)
+    code = np.where(even.any(-1), even.argmax(-1), near.argmax(-1)).astype(np.uint8)
+    return code | (np.signbit(y).astype(np.uint8) << np.uint8(3))
+
+
+def e2m1_rows(x, scale=None):
+    """(codes [..., D], scale codes [..., D / 16]) of binary32 rows; `scale`:
+    binary32, one per row (broadcast), that divides them first."""
+    x = np.asarray(x, dtype=np.float32)
+    if scale is not None:
+        x = f32_div(x, np.broadcast_to(np.asarray(scale, dtype=np.float32)[..., None], x.shape))
+    g = x.reshape(x.shape[:-1] + (-1, E2M1_GROUP))
+    amax = np.abs(g).max(axis=-1)                       # NaN if the group holds one
+    sc = e4m3_encode(f32_div(amax, np.float32(6.0)))
+    s = e4m3_to_f64(sc).astype(np.float32)[..., None]
+    ok = s > 0
+    code = np.where(ok, e2m1_encode(f32_div(g, np.where(ok, s, np.float32(1.0)))), np.uint8(0))
+    return code.reshape(x.shape), sc
+
+
+def e2m1_pack(codes, scales):
+    """The bytes of token rows as the cache holds them: codes [..., bs, D] and
+    scale codes [..., bs, D / 16] of every (block, head) -> uint8 [..., bs,
+    D / 2 + D / 16] (all rows of codes first, then all rows of scales)."""
+    c = np.asarray(codes, dtype=np.uint8)
+    bs, D = c.shape[-2:]
+    by = (c[..., 0::2] | (c[..., 1::2] << np.uint8(4))).reshape(c.shape[:-2] + (bs * D // 2,))
+    sc = np.asarray(scales, dtype=np.uint8).reshape(c.shape[:-2] + (bs * D // 16,))
+    return np.concatenate([by, sc], axis=-1).reshape(c.shape[:-2] + (bs, D // 2 + D // 16))
+
+
+def e2m1_unpack(cache):
+    """(codes [..., bs, D], scale codes [..., bs, D / 16]) of a cache's bytes."""
+    b = np.asarray(cache, dtype=np.uint8)
+    bs, row = b.shape[-2:]
+    D = row * 16 // 9
+    flat = b.reshape(b.shape[:-2] + (bs * row,))
+    by = flat[..., :bs * D // 2].reshape(b.shape[:-2] + (bs, D // 2))
+    sc = flat[..., bs * D // 2:].reshape(b.shape[:-2] + (bs, D // 16))
+    return np.stack([by & 15, by >> 4], axis=-1).reshape(b.shape[:-2] + (bs, D)), sc
+
+
+def e2m1_values(cache):
+    """Float64 values [..., bs, D] of an E2M1 cache's bytes (without the heads' scales)."""
+    codes, sc = e2m1_unpack(cache)
+    return E2M1_VALUES[codes] * np.repeat(e4m3_to_f64(sc), E2M1_GROUP, axis=-1)

@@ -4,8 +4,8 @@ Every function here only checks tensor shapes / dtypes and hands raw device
 pointers plus the current CUDA stream to the C ABI (include/pkv.h); all of the
 computation runs in the library's sm_103a kernels.  PyTorch supplies device
 memory and streams.  The calls made once per layer and step on a few tokens
-(chunk_attention, rotary_append, compact_tokens) do this in a compiled module
-(csrc/binding.cpp), the others through ctypes.
+(chunk_attention, rotary_append, compact_tokens, read_tokens) do this in a
+compiled module (csrc/binding.cpp), the others through ctypes.
 
     append(k_new, v_new, slot_mapping, k_cache, v_cache[, k_scale, v_scale])
     decode_attention(q, k_cache, v_cache, block_tables, context_lens, scale
@@ -14,9 +14,12 @@ memory and streams.  The calls made once per layer and step on a few tokens
     rotary_append(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache) -> q turned (bf16)
     chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_starts, scale) -> out (bf16)
     compact_tokens(k_cache, v_cache, block_tables, keep, keep_starts)
+    read_tokens(slot_mapping, k_cache, v_cache[, k_scale, v_scale]) -> k, v
 
 Cache tensors are [num_blocks, H_kv, block_size, head_dim], bf16 or E4M3
-(torch.uint8 or torch.float8_e4m3fn storage).
+(torch.uint8 or torch.float8_e4m3fn storage), or E2M1: 4-bit codes with an
+8-bit scale for every 16 of them, torch.uint8 [num_blocks, H_kv, block_size,
+head_dim / 2 + head_dim / 16] (e2m1_cache; layout in include/pkv.h).
 """
 
 import ctypes
@@ -26,19 +29,20 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._lib import (PKV_BF16, PKV_E4M3, PKV_F32, CacheDesc, DecodePlan, PkvError,  # noqa: F401
+from ._lib import (PKV_BF16, PKV_E2M1, PKV_E4M3, PKV_F32, CacheDesc, DecodePlan, PkvError,  # noqa: F401
                    TraceEntry)
 
 __all__ = ["append", "decode_attention", "decode_plan", "cache_desc", "slot_mapping",
            "cascade_plan", "cascade_decode_attention", "multi_query_plan", "multi_query_attention",
-           "chunk_plan", "chunk_attention", "rotary_frequencies", "rotary_append", "compact_tokens",
+           "chunk_plan", "chunk_attention", "rotary_frequencies", "rotary_axes", "rotary_append", "compact_tokens",
+           "e2m1_cache", "read_tokens",
            "BlockManager", "OutOfBlocks", "copy_blocks",
            "host_pool_like", "copy_blocks_between",
            "device_error", "trace_enable", "trace_read", "library", "PkvError"]
 
 KERNEL_KINDS = {0: "append", 1: "decode_split", 2: "combine", 3: "cascade_prefix", 4: "block_copy",
                 5: "multi_query", 6: "slot_mapping", 7: "chunk_attention", 8: "rotary_append",
-                9: "compact_tokens"}
+                9: "compact_tokens", 10: "read_tokens"}
 
 
 def library():
@@ -62,11 +66,26 @@ def _cache_dtype(t):
     raise TypeError(f"cache dtype {t.dtype}: expected bfloat16 or uint8/float8_e4m3fn")
 
 
+# row bytes of an E2M1 cache (head_dim / 2 of codes, head_dim / 16 of scales) -> head_dim
+_E2M1_ROWS = {36: 64, 72: 128}
+
+
+def e2m1_cache(num_blocks, num_kv_heads, block_size, head_dim, device=None):
+    """An E2M1 cache of zeros: uint8 [num_blocks, num_kv_heads, block_size,
+    head_dim / 2 + head_dim / 16], 4.5 bits per element."""
+    if head_dim not in _E2M1_ROWS.values():
+        raise ValueError(f"head_dim {head_dim}: an E2M1 cache has 64 or 128")
+    return torch.zeros((num_blocks, num_kv_heads, block_size, head_dim // 2 + head_dim // 16), dtype=torch.uint8,
+                       device=device if device is not None else "cuda")
+
+
 def cache_desc(k_cache):
     """C descriptor of a [num_blocks, H_kv, block_size, head_dim] cache tensor."""
     if k_cache.dim() != 4:
         raise ValueError("cache must be [num_blocks, num_kv_heads, block_size, head_dim]")
     nb, hkv, bs, d = k_cache.shape
+    if k_cache.dtype == torch.uint8 and d in _E2M1_ROWS:
+        return CacheDesc(nb, bs, hkv, _E2M1_ROWS[d], PKV_E2M1)
     return CacheDesc(nb, bs, hkv, d, _cache_dtype(k_cache))
 
 
@@ -95,12 +114,18 @@ def append(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=N
     slot_mapping[i] (int64; phys * block_size + offset; < 0 skips).
 
     E4M3 caches need k_scale / v_scale (float32): [N, H_kv] per-row scales, or
-    [H_kv] per-head scales (then scale_row_stride defaults to 0).
+    [H_kv] per-head scales (then scale_row_stride defaults to 0).  E2M1 caches
+    take them or go without; every group of 16 elements gets a scale of its own
+    besides.
     """
     lib = library()
     _check_pair(k_cache, v_cache)
     dev = k_cache.device
     desc = cache_desc(k_cache)
+    if desc.dtype == PKV_E2M1:
+        _lib.check(_lib.binding().append(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale,
+                                         scale_row_stride), "pkv_append")
+        return
     if k_new.shape != v_new.shape or k_new.dim() != 3:
         raise ValueError("k_new / v_new must both be [N, H_kv, D]")
     n, hkv, d = k_new.shape
@@ -130,6 +155,20 @@ def append(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=N
                         _ptr(v_cache), ctypes.byref(desc), _ptr(k_scale), _ptr(v_scale),
                         int(scale_row_stride), _stream(dev))
     _lib.check(st, "pkv_append")
+
+
+def read_tokens(slot_mapping, k_cache, v_cache, k_scale=None, v_scale=None, scale_row_stride=None,
+                dtype=torch.bfloat16):
+    """Token rows read back from flat slots slot_mapping[i] (int64; < 0 gives
+    zeros): (k, v), both [N, H_kv, D] of `dtype` (bfloat16 or float32), what
+    `append` wrote there times the scales it was given (scales as `append`)."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"dtype {dtype}: expected bfloat16 or float32")
+    r = _lib.binding().read_tokens(slot_mapping, k_cache, v_cache, k_scale, v_scale, scale_row_stride,
+                                   dtype == torch.float32)
+    if type(r) is int:
+        _lib.check(r, "pkv_read_tokens")
+    return r
 
 
 def decode_plan(batch, num_q_heads, k_cache_or_desc, max_context_len, split_tokens=0, num_sms=0):
@@ -396,8 +435,23 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, origi
     return f.to(device) if device is not None else f
 
 
+def rotary_axes(sections, mixed=False, device=None):
+    """The axis of every rotary pair (int32 [sum(sections)]) for tokens with a
+    position along each of len(sections) axes: sections[a] pairs turn by axis a.
+    One axis after another, or with `mixed` a pair of each axis in turn while it
+    has any left."""
+    left = [int(n) for n in sections]
+    if not left or min(left) < 0 or sum(left) == 0:
+        raise ValueError("sections must be numbers of pairs, one per axis")
+    if mixed:
+        axes = [a for i in range(max(left)) for a, n in enumerate(left) if i < n]
+    else:
+        axes = [a for a, n in enumerate(left) for _ in range(n)]
+    return torch.tensor(axes, dtype=torch.int32, device=device)
+
+
 def rotary_append(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=None,
-                  magnitude=1.0, interleaved=False, out=None, scale_row_stride=None):
+                  magnitude=1.0, interleaved=False, out=None, scale_row_stride=None, axes=None):
     """Turn new tokens' queries and keys by their rotary angles, append keys
     and values to their slots, and return the queries (bf16 [N, H_q, D]).
 
@@ -407,9 +461,13 @@ def rotary_append(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, 
     i + rotary_dim / 2) of a head, or (2i, 2i + 1) if interleaved; elements past
     rotary_dim pass through.  slot_mapping and scales as `append` (a negative
     slot stores nothing; its query is still returned).  `out` may be q itself.
+
+    With `axes` (int32 [rotary_dim / 2] on the device, rotary_axes) positions is
+    int64 [num_axes, N], a position along each axis (rows contiguous, any stride
+    between them), and pair i turns by the position along axis axes[i].
     """
     r = _lib.binding().rotary_append(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, k_scale, v_scale,
-                                     magnitude, interleaved, out, scale_row_stride)
+                                     magnitude, interleaved, out, scale_row_stride, axes)
     if type(r) is int:
         _lib.check(r, "pkv_rotary_append")
     return r

@@ -20,9 +20,10 @@ PKV_ERR_OUT_OF_BLOCKS = 5
 PKV_BF16 = 0
 PKV_F32 = 1
 PKV_E4M3 = 2
+PKV_E2M1 = 3
 
 DEVERR_NAMES = {0: "none", 1: "wait timeout", 2: "block id out of range",
-                3: "context length out of range", 4: "slot out of range"}
+                3: "context length out of range", 4: "slot out of range", 5: "rotary axis out of range"}
 
 
 class CacheDesc(ctypes.Structure):
@@ -54,6 +55,7 @@ _F = ctypes.c_float
 
 SIGNATURES = {
     "pkv_append": (_I32, [_P, _P, _I32, _I64, _P, _P, _P, ctypes.POINTER(CacheDesc), _P, _P, _I64, _P]),
+    "pkv_read_tokens": (_I32, [_P, _I64, _P, _P, ctypes.POINTER(CacheDesc), _P, _P, _I64, _P, _P, _I32, _P]),
     "pkv_slot_mapping": (_I32, [_P, _I32, _I32, _P, _P, _I64, ctypes.POINTER(CacheDesc), _P, _P]),
     "pkv_decode_attention": (_I32, [_P, _I32, _I32, _P, _P, ctypes.POINTER(CacheDesc), _P, _I32, _P,
                                     _I32, _F, _P, _P, _P, _I64, _P]),
@@ -81,6 +83,8 @@ SIGNATURES = {
                                    _I32, _P]),
     "pkv_rotary_append": (_I32, [_P, _I64, _P, _I64, _P, _I64, _I32, _I64, _I32, _P, _P, _I32, _I32, _F, _P, _P, _P,
                                  ctypes.POINTER(CacheDesc), _P, _P, _I64, _P, _I64, _P]),
+    "pkv_rotary_append_axes": (_I32, [_P, _I64, _P, _I64, _P, _I64, _I32, _I64, _I32, _P, _I64, _I32, _P, _P, _I32,
+                                      _I32, _F, _P, _P, _P, ctypes.POINTER(CacheDesc), _P, _P, _I64, _P, _I64, _P]),
     "pkv_compact_tokens": (_I32, [_P, _P, ctypes.POINTER(CacheDesc), _P, _I32, _I32, _P, _I32, _P, _P, _I32, _P]),
     "pkv_copy_blocks": (_I32, [_P, _P, ctypes.POINTER(CacheDesc), _P, _P, _I32, _P]),
     "pkv_bm_create": (_I32, [_I64, _I32, ctypes.POINTER(_P)]),
@@ -158,7 +162,8 @@ def binding():
                                    "`python -m paged_kv_cache_222_gb300.build`, which prints why where it does not "
                                    "compile") from e
             mod.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
-                       for f in ("pkv_chunk_plan", "pkv_chunk_attention", "pkv_rotary_append", "pkv_compact_tokens")))
+                       for f in ("pkv_chunk_plan", "pkv_chunk_attention", "pkv_rotary_append_axes", "pkv_compact_tokens",
+                                 "pkv_append", "pkv_read_tokens")))
             _binding = mod
     return _binding
 

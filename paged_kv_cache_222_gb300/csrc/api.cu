@@ -228,10 +228,13 @@ cudaError_t traced(int kind, cudaStream_t stream, F&& launch) {
 
 // ------------------------------------------------------------ checks
 
-pkv_status check_cache(const pkv_cache_desc* c) {
+// `e2m1`: the call takes 4-bit caches too.
+pkv_status check_cache(const pkv_cache_desc* c, bool e2m1 = false) {
   if (c == nullptr) return fail(PKV_ERR_INVALID_ARG, "cache descriptor is NULL");
-  if (c->dtype != PKV_BF16 && c->dtype != PKV_E4M3)
-    return fail(PKV_ERR_INVALID_ARG, "cache dtype %d (want PKV_BF16 or PKV_E4M3)", c->dtype);
+  if (c->dtype == PKV_E2M1 && !e2m1)
+    return fail(PKV_ERR_UNSUPPORTED, "E2M1 caches are attended by pkv_chunk_attention");
+  if (c->dtype != PKV_BF16 && c->dtype != PKV_E4M3 && c->dtype != PKV_E2M1)
+    return fail(PKV_ERR_INVALID_ARG, "cache dtype %d (want PKV_BF16, PKV_E4M3 or PKV_E2M1)", c->dtype);
   if (c->block_size != 16 && c->block_size != 32)
     return fail(PKV_ERR_UNSUPPORTED, "block_size %d (16 or 32)", c->block_size);
   if (c->head_dim != 64 && c->head_dim != 128)
@@ -240,6 +243,25 @@ pkv_status check_cache(const pkv_cache_desc* c) {
     return fail(PKV_ERR_INVALID_ARG, "num_kv_heads %d", c->num_kv_heads);
   if (c->num_blocks < 1 || c->num_blocks > 0x7FFFFFFFll)
     return fail(PKV_ERR_INVALID_ARG, "num_blocks %lld", static_cast<long long>(c->num_blocks));
+  return PKV_OK;
+}
+
+// Bytes of one (block, head) of K or V.
+int64_t tile_bytes(const pkv_cache_desc& c) {
+  if (c.dtype == PKV_E2M1) return pkv::e2m1_tile_bytes(c.head_dim, c.block_size);
+  return static_cast<int64_t>(c.block_size) * c.head_dim * (c.dtype == PKV_E4M3 ? 1 : 2);
+}
+
+// Scales of K and V: an E4M3 cache has both, an E2M1 cache both or neither, a
+// bf16 cache none.
+pkv_status check_scales(const pkv_cache_desc& c, const float* k_scale, const float* v_scale, int64_t stride) {
+  if (c.dtype == PKV_E4M3 && (k_scale == nullptr || v_scale == nullptr))
+    return fail(PKV_ERR_INVALID_ARG, "E4M3 cache needs k_scale and v_scale");
+  if (c.dtype == PKV_E2M1 && (k_scale == nullptr) != (v_scale == nullptr))
+    return fail(PKV_ERR_INVALID_ARG, "E2M1 cache takes both k_scale and v_scale, or neither");
+  if (c.dtype == PKV_BF16 && (k_scale != nullptr || v_scale != nullptr))
+    return fail(PKV_ERR_INVALID_ARG, "scales given for a bf16 cache");
+  if (stride < 0) return fail(PKV_ERR_INVALID_ARG, "scale_row_stride < 0");
   return PKV_OK;
 }
 
@@ -363,8 +385,8 @@ struct DecodeArgs {
   int32_t new_dtype = -1;
 };
 
-pkv_status check_decode(const DecodeArgs& a) {
-  pkv_status s = check_cache(a.cache);
+pkv_status check_decode(const DecodeArgs& a, bool e2m1 = false) {
+  pkv_status s = check_cache(a.cache, e2m1);
   if (s != PKV_OK) return s;
   const pkv_cache_desc& c = *a.cache;
   if (a.batch < 0 || a.batch > 65535) return fail(PKV_ERR_INVALID_ARG, "batch %d", a.batch);
@@ -378,12 +400,8 @@ pkv_status check_decode(const DecodeArgs& a) {
   if (a.max_ctx < 0 || static_cast<int64_t>(a.max_ctx) > static_cast<int64_t>(a.max_blocks) * c.block_size)
     return fail(PKV_ERR_INVALID_ARG, "max_context_len %d outside [0, max_blocks_per_seq * block_size]",
                 a.max_ctx);
-  const bool fp8 = c.dtype == PKV_E4M3;
-  if (fp8 && (a.k_scale == nullptr || a.v_scale == nullptr))
-    return fail(PKV_ERR_INVALID_ARG, "E4M3 cache needs k_scale and v_scale");
-  if (!fp8 && (a.k_scale != nullptr || a.v_scale != nullptr))
-    return fail(PKV_ERR_INVALID_ARG, "scales given for a bf16 cache");
-  if (a.scale_stride < 0) return fail(PKV_ERR_INVALID_ARG, "scale_row_stride < 0");
+  s = check_scales(c, a.k_scale, a.v_scale, a.scale_stride);
+  if (s != PKV_OK) return s;
   if (a.batch == 0) return PKV_OK;
   if (a.q == nullptr || a.k_cache == nullptr || a.v_cache == nullptr || a.out == nullptr ||
       a.block_tables == nullptr || a.context_lens == nullptr)
@@ -392,7 +410,7 @@ pkv_status check_decode(const DecodeArgs& a) {
     return fail(PKV_ERR_INVALID_ARG, "q, caches and out must be 16-byte aligned");
   if (!aligned(a.block_tables, 4) || !aligned(a.context_lens, 4))
     return fail(PKV_ERR_INVALID_ARG, "block_tables / context_lens must be 4-byte aligned");
-  if (fp8 && (!aligned(a.k_scale, 4) || !aligned(a.v_scale, 4)))
+  if (!aligned(a.k_scale, 4) || !aligned(a.v_scale, 4))
     return fail(PKV_ERR_INVALID_ARG, "scales must be 4-byte aligned");
   if (a.new_dtype != -1) {
     if (a.new_dtype != PKV_BF16 && a.new_dtype != PKV_F32)
@@ -513,17 +531,13 @@ pkv_status pkv_append(const void* k_new, const void* v_new, int32_t src_dtype, i
                       const int64_t* slot_mapping, void* k_cache, void* v_cache,
                       const pkv_cache_desc* cache, const float* k_scale, const float* v_scale,
                       int64_t scale_row_stride, pkv_stream_t stream) {
-  pkv_status s = check_cache(cache);
+  pkv_status s = check_cache(cache, true);
   if (s != PKV_OK) return s;
   if (src_dtype != PKV_BF16 && src_dtype != PKV_F32)
     return fail(PKV_ERR_INVALID_ARG, "source dtype %d (PKV_BF16 or PKV_F32)", src_dtype);
   if (n_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "n_tokens %lld", static_cast<long long>(n_tokens));
-  const bool fp8 = cache->dtype == PKV_E4M3;
-  if (fp8 && (k_scale == nullptr || v_scale == nullptr))
-    return fail(PKV_ERR_INVALID_ARG, "E4M3 cache needs k_scale and v_scale");
-  if (!fp8 && (k_scale != nullptr || v_scale != nullptr))
-    return fail(PKV_ERR_INVALID_ARG, "scales given for a bf16 cache");
-  if (scale_row_stride < 0) return fail(PKV_ERR_INVALID_ARG, "scale_row_stride < 0");
+  s = check_scales(*cache, k_scale, v_scale, scale_row_stride);
+  if (s != PKV_OK) return s;
   if (n_tokens == 0) return PKV_OK;
   if (k_new == nullptr || v_new == nullptr || slot_mapping == nullptr || k_cache == nullptr ||
       v_cache == nullptr)
@@ -531,7 +545,7 @@ pkv_status pkv_append(const void* k_new, const void* v_new, int32_t src_dtype, i
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
     return fail(PKV_ERR_INVALID_ARG, "k_new, v_new and caches must be 16-byte aligned");
   if (!aligned(slot_mapping, 8)) return fail(PKV_ERR_INVALID_ARG, "slot_mapping must be 8-byte aligned");
-  if (fp8 && (!aligned(k_scale, 4) || !aligned(v_scale, 4)))
+  if (!aligned(k_scale, 4) || !aligned(v_scale, 4))
     return fail(PKV_ERR_INVALID_ARG, "scales must be 4-byte aligned");
 
   int dev;
@@ -561,10 +575,55 @@ pkv_status pkv_append(const void* k_new, const void* v_new, int32_t src_dtype, i
   return PKV_OK;
 }
 
+pkv_status pkv_read_tokens(const int64_t* slot_mapping, int64_t n_tokens, const void* k_cache, const void* v_cache,
+                           const pkv_cache_desc* cache, const float* k_scale, const float* v_scale,
+                           int64_t scale_row_stride, void* k_out, void* v_out, int32_t out_dtype,
+                           pkv_stream_t stream) {
+  pkv_status s = check_cache(cache, true);
+  if (s != PKV_OK) return s;
+  if (out_dtype != PKV_BF16 && out_dtype != PKV_F32)
+    return fail(PKV_ERR_INVALID_ARG, "output dtype %d (PKV_BF16 or PKV_F32)", out_dtype);
+  if (n_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "n_tokens %lld", static_cast<long long>(n_tokens));
+  s = check_scales(*cache, k_scale, v_scale, scale_row_stride);
+  if (s != PKV_OK) return s;
+  if (n_tokens == 0) return PKV_OK;
+  if (slot_mapping == nullptr || k_cache == nullptr || v_cache == nullptr || k_out == nullptr || v_out == nullptr)
+    return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return fail(PKV_ERR_INVALID_ARG, "outputs and caches must be 16-byte aligned");
+  if (!aligned(slot_mapping, 8)) return fail(PKV_ERR_INVALID_ARG, "slot_mapping must be 8-byte aligned");
+  if (!aligned(k_scale, 4) || !aligned(v_scale, 4)) return fail(PKV_ERR_INVALID_ARG, "scales must be 4-byte aligned");
+  int dev;
+  DeviceState* st;
+  s = current_device(&dev, &st);
+  if (s != PKV_OK) return s;
+  pkv::ReadParams p = {};
+  p.slots = slot_mapping;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.scale_stride = scale_row_stride;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.n_tokens = n_tokens;
+  p.num_slots = cache->num_blocks * cache->block_size;
+  p.block_size = cache->block_size;
+  p.num_kv_heads = cache->num_kv_heads;
+  p.head_dim = cache->head_dim;
+  p.out_dtype = out_dtype;
+  p.cache_dtype = cache->dtype;
+  p.err = st->err;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = traced(pkv::kKindRead, cs, [&] { return pkv::launch_read(p, cs); });
+  if (e != cudaSuccess) return cuda_fail(e, "token read launch");
+  return PKV_OK;
+}
+
 pkv_status pkv_slot_mapping(const int32_t* block_tables, int32_t num_seqs, int32_t max_blocks_per_seq,
                             const int64_t* seq_index, const int64_t* positions, int64_t n_tokens,
                             const pkv_cache_desc* cache, int64_t* slot_mapping, pkv_stream_t stream) {
-  pkv_status s = check_cache(cache);
+  pkv_status s = check_cache(cache, true);
   if (s != PKV_OK) return s;
   if (n_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "n_tokens %lld", static_cast<long long>(n_tokens));
   if (num_seqs < 0) return fail(PKV_ERR_INVALID_ARG, "num_seqs %d", num_seqs);
@@ -602,7 +661,7 @@ pkv_status pkv_slot_mapping(const int32_t* block_tables, int32_t num_seqs, int32
 pkv_status pkv_copy_blocks(void* k_cache, void* v_cache, const pkv_cache_desc* cache,
                            const int32_t* src_blocks, const int32_t* dst_blocks, int32_t n_pairs,
                            pkv_stream_t stream) {
-  pkv_status s = check_cache(cache);
+  pkv_status s = check_cache(cache, true);
   if (s != PKV_OK) return s;
   if (n_pairs < 0) return fail(PKV_ERR_INVALID_ARG, "n_pairs %d", n_pairs);
   if (n_pairs == 0) return PKV_OK;
@@ -616,7 +675,6 @@ pkv_status pkv_copy_blocks(void* k_cache, void* v_cache, const pkv_cache_desc* c
   DeviceState* st;
   s = current_device(&dev, &st);
   if (s != PKV_OK) return s;
-  const int64_t esz = cache->dtype == PKV_E4M3 ? 1 : 2;
   pkv::CopyParams p = {};
   p.k_src = k_cache;
   p.v_src = v_cache;
@@ -625,7 +683,7 @@ pkv_status pkv_copy_blocks(void* k_cache, void* v_cache, const pkv_cache_desc* c
   p.src = src_blocks;
   p.dst = dst_blocks;
   p.n_pairs = n_pairs;
-  p.block_vec = static_cast<int64_t>(cache->num_kv_heads) * cache->block_size * cache->head_dim * esz / 16;
+  p.block_vec = static_cast<int64_t>(cache->num_kv_heads) * tile_bytes(*cache) / 16;
   p.src_blocks = cache->num_blocks;
   p.dst_blocks = cache->num_blocks;
   p.err = st->err;
@@ -640,7 +698,7 @@ pkv_status pkv_copy_blocks_between(const void* src_k, const void* src_v, int64_t
                                    const pkv_cache_desc* cache, const int32_t* src_blocks,
                                    const int32_t* dst_blocks, int32_t n_pairs, int32_t max_ctas,
                                    pkv_stream_t stream) {
-  pkv_status s = check_cache(cache);
+  pkv_status s = check_cache(cache, true);
   if (s != PKV_OK) return s;
   if (n_pairs < 0) return fail(PKV_ERR_INVALID_ARG, "n_pairs %d", n_pairs);
   if (max_ctas < 0) return fail(PKV_ERR_INVALID_ARG, "max_ctas %d", max_ctas);
@@ -659,7 +717,6 @@ pkv_status pkv_copy_blocks_between(const void* src_k, const void* src_v, int64_t
   DeviceState* st;
   s = current_device(&dev, &st);
   if (s != PKV_OK) return s;
-  const int64_t esz = cache->dtype == PKV_E4M3 ? 1 : 2;
   pkv::CopyParams p = {};
   p.k_src = src_k;
   p.v_src = src_v;
@@ -668,7 +725,7 @@ pkv_status pkv_copy_blocks_between(const void* src_k, const void* src_v, int64_t
   p.src = src_blocks;
   p.dst = dst_blocks;
   p.n_pairs = n_pairs;
-  p.block_vec = static_cast<int64_t>(cache->num_kv_heads) * cache->block_size * cache->head_dim * esz / 16;
+  p.block_vec = static_cast<int64_t>(cache->num_kv_heads) * tile_bytes(*cache) / 16;
   p.src_blocks = src_num_blocks;
   p.dst_blocks = dst_num_blocks;
   if (max_ctas == 0) {
@@ -1483,13 +1540,13 @@ extern "C" pkv_status pkv_chunk_attention(
   return PKV_OK;
 }
 
-extern "C" pkv_status pkv_rotary_append(
+extern "C" pkv_status pkv_rotary_append_axes(
     const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
-    int32_t src_dtype, int64_t n_tokens, int32_t num_q_heads, const int64_t* positions, const double* inv_freq,
-    int32_t rotary_dim, int32_t interleaved, float magnitude, const int64_t* slot_mapping, void* k_cache,
+    int32_t src_dtype, int64_t n_tokens, int32_t num_q_heads, const int64_t* positions, int64_t position_stride,
+    int32_t num_axes, const int32_t* axes, const double* inv_freq, int32_t rotary_dim, int32_t interleaved, float magnitude, const int64_t* slot_mapping, void* k_cache,
     void* v_cache, const pkv_cache_desc* cache, const float* k_scale, const float* v_scale,
     int64_t scale_row_stride, void* q_out, int64_t out_stride, pkv_stream_t stream) {
-  pkv_status s = check_cache(cache);
+  pkv_status s = check_cache(cache, true);
   if (s != PKV_OK) return s;
   const pkv_cache_desc& c = *cache;
   if (src_dtype != PKV_BF16 && src_dtype != PKV_F32)
@@ -1506,23 +1563,22 @@ extern "C" pkv_status pkv_rotary_append(
     return fail(PKV_ERR_INVALID_ARG, "a token stride is smaller than the token's heads");
   if (q_stride * esz % 16 || k_stride * esz % 16 || v_stride * esz % 16 || out_stride * 2 % 16)
     return fail(PKV_ERR_INVALID_ARG, "token strides must be multiples of 16 bytes");
-  const bool fp8 = c.dtype == PKV_E4M3;
-  if (fp8 && (k_scale == nullptr || v_scale == nullptr))
-    return fail(PKV_ERR_INVALID_ARG, "E4M3 cache needs k_scale and v_scale");
-  if (!fp8 && (k_scale != nullptr || v_scale != nullptr))
-    return fail(PKV_ERR_INVALID_ARG, "scales given for a bf16 cache");
-  if (scale_row_stride < 0) return fail(PKV_ERR_INVALID_ARG, "scale_row_stride < 0");
+  if (num_axes < 1 || num_axes > 65535) return fail(PKV_ERR_INVALID_ARG, "num_axes %d", num_axes);
+  if (position_stride < 0)
+    return fail(PKV_ERR_INVALID_ARG, "position_stride %lld", static_cast<long long>(position_stride));
+  s = check_scales(c, k_scale, v_scale, scale_row_stride);
+  if (s != PKV_OK) return s;
   if (n_tokens == 0) return PKV_OK;
   if (q == nullptr || k == nullptr || v == nullptr || q_out == nullptr || positions == nullptr ||
-      inv_freq == nullptr || slot_mapping == nullptr || k_cache == nullptr || v_cache == nullptr)
+      inv_freq == nullptr || (num_axes > 1 && axes == nullptr) || slot_mapping == nullptr || k_cache == nullptr || v_cache == nullptr)
     return fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_cache, 16) ||
       !aligned(v_cache, 16))
     return fail(PKV_ERR_INVALID_ARG, "q, k, v, q_out and the caches must be 16-byte aligned");
   if (!aligned(positions, 8) || !aligned(inv_freq, 8) || !aligned(slot_mapping, 8))
     return fail(PKV_ERR_INVALID_ARG, "positions, inv_freq and slot_mapping must be 8-byte aligned");
-  if (fp8 && (!aligned(k_scale, 4) || !aligned(v_scale, 4)))
-    return fail(PKV_ERR_INVALID_ARG, "scales must be 4-byte aligned");
+  if (!aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(axes, 4))
+    return fail(PKV_ERR_INVALID_ARG, "scales and axes must be 4-byte aligned");
   if (q == q_out && (src_dtype != PKV_BF16 || q_stride != out_stride))
     return fail(PKV_ERR_INVALID_ARG, "q turned in place needs bf16 and equal strides");
   int dev;
@@ -1539,6 +1595,9 @@ extern "C" pkv_status pkv_rotary_append(
   p.v_stride = v_stride;
   p.out_stride = out_stride;
   p.positions = positions;
+  p.position_stride = position_stride;
+  p.axes = axes;
+  p.num_axes = num_axes;
   p.inv_freq = inv_freq;
   p.magnitude = magnitude;
   p.slots = slot_mapping;
@@ -1556,7 +1615,7 @@ extern "C" pkv_status pkv_rotary_append(
   p.rotary_dim = rotary_dim;
   p.interleaved = interleaved;
   p.src_dtype = src_dtype == PKV_BF16 ? pkv::kEncBF16 : pkv::kEncF32;
-  p.cache_dtype = fp8 ? pkv::kEncE4M3 : pkv::kEncBF16;
+  p.cache_dtype = c.dtype;
   p.err = st->err;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = traced(pkv::kKindRotary, cs, [&] { return pkv::launch_rotary(p, cs); });
@@ -1564,11 +1623,22 @@ extern "C" pkv_status pkv_rotary_append(
   return PKV_OK;
 }
 
+extern "C" pkv_status pkv_rotary_append(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+    int32_t src_dtype, int64_t n_tokens, int32_t num_q_heads, const int64_t* positions, const double* inv_freq,
+    int32_t rotary_dim, int32_t interleaved, float magnitude, const int64_t* slot_mapping, void* k_cache,
+    void* v_cache, const pkv_cache_desc* cache, const float* k_scale, const float* v_scale,
+    int64_t scale_row_stride, void* q_out, int64_t out_stride, pkv_stream_t stream) {
+  return pkv_rotary_append_axes(q, q_stride, k, k_stride, v, v_stride, src_dtype, n_tokens, num_q_heads, positions, 0,
+                                1, nullptr, inv_freq, rotary_dim, interleaved, magnitude, slot_mapping, k_cache,
+                                v_cache, cache, k_scale, v_scale, scale_row_stride, q_out, out_stride, stream);
+}
+
 extern "C" pkv_status pkv_compact_tokens(void* k_cache, void* v_cache, const pkv_cache_desc* cache,
                                          const int32_t* block_tables, int32_t max_blocks_per_seq, int32_t batch,
                                          const int32_t* keep, int32_t n_keep, const int32_t* keep_starts,
                                          const int32_t* dst_start, int32_t max_keep, pkv_stream_t stream) {
-  pkv_status s = check_cache(cache);
+  pkv_status s = check_cache(cache, true);
   if (s != PKV_OK) return s;
   const pkv_cache_desc& c = *cache;
   if (batch < 0) return fail(PKV_ERR_INVALID_ARG, "batch %d", batch);
@@ -1600,10 +1670,16 @@ extern "C" pkv_status pkv_compact_tokens(void* k_cache, void* v_cache, const pkv
   p.max_blocks = max_blocks_per_seq;
   p.block_size = c.block_size;
   p.num_kv_heads = c.num_kv_heads;
-  p.row_bytes = c.head_dim * (c.dtype == PKV_E4M3 ? 1 : 2);
+  p.row_bytes = static_cast<int32_t>(c.dtype == PKV_E2M1 ? pkv::e2m1_code_row(c.head_dim) : tile_bytes(c) / c.block_size);
+  p.tile_bytes = static_cast<int32_t>(tile_bytes(c));
   p.err = st->err;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = traced(pkv::kKindCompact, cs, [&] { return pkv::launch_compact(p, cs); });
+  if (e == cudaSuccess && c.dtype == PKV_E2M1) {  // the rows of scales
+    p.row_bytes = pkv::e2m1_scale_row(c.head_dim);
+    p.tile_offset = c.block_size * pkv::e2m1_code_row(c.head_dim);
+    e = traced(pkv::kKindCompact, cs, [&] { return pkv::launch_compact(p, cs); });
+  }
   if (e != cudaSuccess) return cuda_fail(e, "token compaction launch");
   return PKV_OK;
 }

@@ -19,6 +19,8 @@
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
+#include <initializer_list>
+#include <utility>
 
 #include "pkv.h"
 
@@ -29,8 +31,10 @@ using at::Tensor;
 // Entry points of the loaded library, handed over by bind().
 decltype(&pkv_chunk_plan) g_chunk_plan = nullptr;
 decltype(&pkv_chunk_attention) g_chunk_attention = nullptr;
-decltype(&pkv_rotary_append) g_rotary_append = nullptr;
+decltype(&pkv_rotary_append_axes) g_rotary_append = nullptr;
 decltype(&pkv_compact_tokens) g_compact_tokens = nullptr;
+decltype(&pkv_append) g_append = nullptr;
+decltype(&pkv_read_tokens) g_read_tokens = nullptr;
 
 // A Python exception has been set.
 struct Raised {};
@@ -104,18 +108,24 @@ Caches caches(PyObject* ko, PyObject* vo) {
   if (!k.is_contiguous() || !v.is_contiguous()) raise(PyExc_ValueError, "caches must be contiguous");
   if (k.device() != v.device() || !k.is_cuda()) raise(PyExc_ValueError, "caches must be CUDA tensors on one device");
   int32_t dtype;
-  if (k.scalar_type() == at::kBFloat16)
+  int64_t d_row = k.size(3);
+  if (k.scalar_type() == at::kBFloat16) {
     dtype = PKV_BF16;
-  else if (k.scalar_type() == at::kByte || k.scalar_type() == at::kFloat8_e4m3fn)
+  } else if (k.scalar_type() == at::kByte && (d_row == 36 || d_row == 72)) {
+    dtype = PKV_E2M1;  // rows of head_dim / 2 + head_dim / 16 bytes
+    d_row = d_row / 9 * 16;
+  } else if (k.scalar_type() == at::kByte || k.scalar_type() == at::kFloat8_e4m3fn) {
     dtype = PKV_E4M3;
-  else
+  } else {
     raise(PyExc_TypeError, "cache dtype %s: expected bfloat16 or uint8/float8_e4m3fn", type_name(k.scalar_type()));
+  }
   pkv_cache_desc d = {k.size(0), size32(k.size(2), "block_size"), size32(k.size(1), "num_kv_heads"),
-                      size32(k.size(3), "head_dim"), dtype};
+                      size32(d_row, "head_dim"), dtype};
   return Caches{k, v, d, k.device()};
 }
 
-// Scales of an E4M3 cache, [rows, H_kv] or [H_kv] each; their row stride.
+// Scales of an E4M3 or E2M1 cache, [rows, H_kv] or [H_kv] each (an E2M1 cache
+// may have none); their row stride.
 struct Scales {
   const float* k = nullptr;
   const float* v = nullptr;
@@ -124,11 +134,12 @@ struct Scales {
 
 Scales scales(PyObject* ko, PyObject* vo, PyObject* so, const Caches& c, int64_t rows) {
   Scales s;
-  if (c.desc.dtype != PKV_E4M3) {
+  if (c.desc.dtype == PKV_E2M1 && ko == Py_None && vo == Py_None) return s;
+  if (c.desc.dtype == PKV_BF16) {
     if (ko != Py_None || vo != Py_None) raise(PyExc_ValueError, "scales given for a bf16 cache");
     return s;
   }
-  if (ko == Py_None || vo == Py_None) raise(PyExc_ValueError, "E4M3 cache needs k_scale and v_scale");
+  if (ko == Py_None || vo == Py_None) raise(PyExc_ValueError, "k_scale and v_scale are both needed");
   const Tensor &k = dense(ko, at::kFloat, "k_scale", c.dev), &v = dense(vo, at::kFloat, "v_scale", c.dev);
   if (k.sizes() != v.sizes()) raise(PyExc_ValueError, "k_scale and v_scale differ in shape");
   const int64_t heads = c.desc.num_kv_heads;
@@ -165,6 +176,22 @@ pkv_status on_stream(at::Device dev, F&& call) {
   pkv_stream_t stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
   const Unlocked unlocked;
   return call(stream);
+}
+
+// A Python tuple of the tensors.
+PyObject* tuple(std::initializer_list<Tensor> tensors) {
+  PyObject* t = PyTuple_New(static_cast<Py_ssize_t>(tensors.size()));
+  if (t == nullptr) throw Raised{};
+  Py_ssize_t i = 0;
+  for (const Tensor& x : tensors) {
+    PyObject* o = THPVariable_Wrap(x);
+    if (o == nullptr) {
+      Py_DECREF(t);
+      throw Raised{};
+    }
+    PyTuple_SET_ITEM(t, i++, o);
+  }
+  return t;
 }
 
 void expect(Py_ssize_t got, Py_ssize_t want) {
@@ -252,7 +279,7 @@ int64_t token_rows(const Tensor& t, const char* name, at::ScalarType type, at::D
 }
 
 PyObject* rotary_append(PyObject* const* a, Py_ssize_t n_args) {
-  expect(n_args, 14);
+  expect(n_args, 15);
   const Caches c = caches(a[6], a[7]);
   const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
   if (q.dim() != 3) raise(PyExc_ValueError, "q must be [N, H_q, D]");
@@ -263,11 +290,26 @@ PyObject* rotary_append(PyObject* const* a, Py_ssize_t n_args) {
     raise(PyExc_TypeError, "q dtype %s: expected bfloat16 or float32", type_name(type));
   const int64_t q_st = token_rows(q, "q", type, c.dev, n, hq, d), k_st = token_rows(k, "k", type, c.dev, n, hkv, d),
                 v_st = token_rows(v, "v", type, c.dev, n, hkv, d);
-  const Tensor& pos = dense(a[3], at::kLong, "positions", c.dev);
+  const Tensor& pos = tensor(a[3], "positions");
   const Tensor& freq = dense(a[4], at::kDouble, "inv_freq", c.dev);
   const Tensor& slots = dense(a[5], at::kLong, "slot_mapping", c.dev);
-  if (pos.dim() != 1 || pos.size(0) != n || slots.dim() != 1 || slots.size(0) != n)
-    raise(PyExc_ValueError, "positions and slot_mapping must have one entry per token");
+  if (pos.scalar_type() != at::kLong)
+    raise(PyExc_TypeError, "positions must be %s, got %s", type_name(at::kLong), type_name(pos.scalar_type()));
+  if (pos.device() != c.dev) raise(PyExc_ValueError, "positions must be on %s", c.dev.str().c_str());
+  const bool many = a[14] != Py_None;  // [axes, N], an axis' positions contiguous
+  const int64_t along = many ? 1 : 0;
+  if (pos.dim() != 1 + along || pos.size(along) != n || slots.dim() != 1 || slots.size(0) != n)
+    raise(PyExc_ValueError, many ? "positions must be [num_axes, N] and slot_mapping [N]"
+                                 : "positions and slot_mapping must have one entry per token");
+  if (n > 1 && pos.stride(along) != 1) raise(PyExc_ValueError, "positions must be contiguous");
+  const int32_t* axes = nullptr;
+  int32_t num_axes = 1;
+  if (many) {
+    const Tensor& t = dense(a[14], at::kInt, "axes", c.dev);
+    if (t.dim() != 1 || t.size(0) != freq.numel()) raise(PyExc_ValueError, "axes must be [rotary_dim / 2]");
+    axes = t.const_data_ptr<int32_t>();
+    num_axes = size32(pos.size(0), "num_axes");
+  }
   if (freq.dim() != 1) raise(PyExc_ValueError, "inv_freq must be [rotary_dim / 2]");
   const int32_t heads = size32(hq, "H_q"), rotary_dim = size32(2 * freq.size(0), "rotary_dim");
   const Scales sc = scales(a[8], a[9], a[13], c, n);
@@ -285,7 +327,7 @@ PyObject* rotary_append(PyObject* const* a, Py_ssize_t n_args) {
   const pkv_status st = on_stream(c.dev, [&](pkv_stream_t stream) {
     return g_rotary_append(q.data_ptr(), q_st, k.data_ptr(), k_st, v.data_ptr(), v_st,
                            type == at::kBFloat16 ? PKV_BF16 : PKV_F32, n, heads, pos.const_data_ptr<int64_t>(),
-                           freq.const_data_ptr<double>(), rotary_dim, interleaved, magnitude,
+                           many ? pos.stride(0) : 0, num_axes, axes, freq.const_data_ptr<double>(), rotary_dim, interleaved, magnitude,
                            slots.const_data_ptr<int64_t>(), c.k.data_ptr(), c.v.data_ptr(), &c.desc, sc.k, sc.v,
                            sc.stride, out.data_ptr(), o_st, stream);
   });
@@ -322,14 +364,62 @@ PyObject* compact_tokens(PyObject* const* a, Py_ssize_t n_args) {
   return PyLong_FromLong(st);
 }
 
+// Appends to an E2M1 cache (the other types' appends are checked in Python).
+PyObject* append(PyObject* const* a, Py_ssize_t n_args) {
+  expect(n_args, 8);
+  const Caches c = caches(a[3], a[4]);
+  const Tensor &k = tensor(a[0], "k_new"), &v = tensor(a[1], "v_new");
+  if (k.dim() != 3 || k.sizes() != v.sizes()) raise(PyExc_ValueError, "k_new / v_new must both be [N, H_kv, D]");
+  const int64_t n = k.size(0);
+  if (k.size(1) != c.desc.num_kv_heads || k.size(2) != c.desc.head_dim)
+    raise(PyExc_ValueError, "k_new heads / head_dim do not match the cache");
+  const at::ScalarType type = k.scalar_type();
+  if (type != at::kBFloat16 && type != at::kFloat)
+    raise(PyExc_TypeError, "k_new dtype %s: expected bfloat16 or float32", type_name(type));
+  dense(a[0], type, "k_new", c.dev);
+  dense(a[1], type, "v_new", c.dev);
+  const Tensor& slots = dense(a[2], at::kLong, "slot_mapping", c.dev);
+  if (slots.numel() != n) raise(PyExc_ValueError, "slot_mapping must have one entry per row");
+  const Scales sc = scales(a[5], a[6], a[7], c, n);
+  const pkv_status st = on_stream(c.dev, [&](pkv_stream_t stream) {
+    return g_append(k.data_ptr(), v.data_ptr(), type == at::kBFloat16 ? PKV_BF16 : PKV_F32, n,
+                    slots.const_data_ptr<int64_t>(), c.k.data_ptr(), c.v.data_ptr(), &c.desc, sc.k, sc.v, sc.stride,
+                    stream);
+  });
+  return PyLong_FromLong(st);
+}
+
+PyObject* read_tokens(PyObject* const* a, Py_ssize_t n_args) {
+  expect(n_args, 7);
+  const Caches c = caches(a[1], a[2]);
+  const Tensor& slots = dense(a[0], at::kLong, "slot_mapping", c.dev);
+  if (slots.dim() != 1) raise(PyExc_ValueError, "slot_mapping must be [N]");
+  const int64_t n = slots.size(0);
+  const Scales sc = scales(a[3], a[4], a[5], c, n);
+  const int f32 = PyObject_IsTrue(a[6]);
+  if (f32 < 0) throw Raised{};
+  const auto options = c.k.options().dtype(f32 ? at::kFloat : at::kBFloat16);
+  const int64_t shape[3] = {n, c.desc.num_kv_heads, c.desc.head_dim};
+  Tensor k = at::empty(shape, options), v = at::empty(shape, options);
+  const pkv_status st = on_stream(c.dev, [&](pkv_stream_t stream) {
+    return g_read_tokens(slots.const_data_ptr<int64_t>(), n, c.k.data_ptr(), c.v.data_ptr(), &c.desc, sc.k, sc.v,
+                         sc.stride, k.data_ptr(), v.data_ptr(), f32 ? PKV_F32 : PKV_BF16, stream);
+  });
+  if (st != PKV_OK) return PyLong_FromLong(st);
+  return tuple({std::move(k), std::move(v)});
+}
+
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
-  expect(n, 4);
-  void* p[4];
-  for (int i = 0; i < 4; ++i) p[i] = reinterpret_cast<void*>(static_cast<uintptr_t>(integer(a[i], "address")));
+  constexpr int kCalls = 6;
+  expect(n, kCalls);
+  void* p[kCalls];
+  for (int i = 0; i < kCalls; ++i) p[i] = reinterpret_cast<void*>(static_cast<uintptr_t>(integer(a[i], "address")));
   g_chunk_plan = reinterpret_cast<decltype(g_chunk_plan)>(p[0]);
   g_chunk_attention = reinterpret_cast<decltype(g_chunk_attention)>(p[1]);
   g_rotary_append = reinterpret_cast<decltype(g_rotary_append)>(p[2]);
   g_compact_tokens = reinterpret_cast<decltype(g_compact_tokens)>(p[3]);
+  g_append = reinterpret_cast<decltype(g_append)>(p[4]);
+  g_read_tokens = reinterpret_cast<decltype(g_read_tokens)>(p[5]);
   Py_RETURN_NONE;
 }
 
@@ -348,7 +438,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<name>)), METH_FASTCALL, nullptr}
 
 PyMethodDef g_methods[] = {PKV_ENTRY(bind), PKV_ENTRY(chunk_attention), PKV_ENTRY(rotary_append),
-                           PKV_ENTRY(compact_tokens), {nullptr, nullptr, 0, nullptr}};
+                           PKV_ENTRY(compact_tokens), PKV_ENTRY(append), PKV_ENTRY(read_tokens), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", "Compiled calls of the paged-KV library.", -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

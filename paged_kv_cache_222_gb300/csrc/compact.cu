@@ -17,7 +17,8 @@
 // A CTA takes one (sequence, head, K or V, column band) and walks its rows in
 // order; columns are independent, so few sequences are cut into bands of at
 // least 64 bytes.  The rows' addresses (keep list, then block table) are
-// looked up 256 at a time, a batch ahead.  Bound: the moved bytes, each read
+// looked up 256 at a time, a batch ahead.  E2M1 caches take a second launch for
+// the rows of scales.  Bound: the moved bytes, each read
 // and written once: half of 32 x 4096 tokens of 8 heads of 128 (536 MB) takes
 // 86.5 us, 6.2 TB/s, 93 % of the measured copy (without the next step's loads
 // ahead 90 us; twice the rows per step 100, half of them 104; 128-byte bands
@@ -37,9 +38,12 @@ __device__ __forceinline__ int64_t compact_row(const CompactParams& p, const int
     bad = kDevErrBlockId;
     return -1;
   }
-  return (static_cast<int64_t>(blk) * p.num_kv_heads + h) * p.block_size + pos % p.block_size;
+  return (static_cast<int64_t>(blk) * p.num_kv_heads + h) * p.tile_bytes + (pos % p.block_size) * p.row_bytes;
 }
 
+// W: the word that moves (rows of codes or whole elements: 16 bytes; rows of
+// an E2M1 cache's scales: 8 or 4).
+template <class W>
 __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactParams p, int band_bytes) {
   __shared__ int64_t s_src[2][kCompactThreads], s_dst[2][kCompactThreads];
   wait_prior_grid();
@@ -48,7 +52,7 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
   const int b = blockIdx.x;
   const int band = blockIdx.y % bands, hv = blockIdx.y / bands;
   const int h = hv >> 1;
-  char* cache = static_cast<char*>((hv & 1) ? p.v_cache : p.k_cache) + band * band_bytes;
+  char* cache = static_cast<char*>((hv & 1) ? p.v_cache : p.k_cache) + p.tile_offset + band * band_bytes;
   const bool note = blockIdx.y == 0;  // one CTA of the sequence records what it refuses
   const int k0 = p.keep_starts[b], k1 = p.keep_starts[b + 1];
   const int first = p.dst_start != nullptr ? p.dst_start[b] : 0;
@@ -78,15 +82,13 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
       src = dst = -1;
       return;
     }
-    src *= p.row_bytes;
-    dst *= p.row_bytes;
   };
 
-  // a step: 256 threads x 4 x 16 bytes; per_pass rows per 256 threads
-  const int words = band_bytes / 16;
+  // a step: 256 threads x 4 words; per_pass rows per 256 threads
+  const int words = band_bytes / static_cast<int>(sizeof(W));
   const int per_pass = kCompactThreads / words;
   const int per_step = per_pass * kCompactUnroll;
-  const int my_row = threadIdx.x / words, my_off = (threadIdx.x % words) * 16;
+  const int my_row = threadIdx.x / words, my_off = (threadIdx.x % words) * static_cast<int>(sizeof(W));
   int64_t ns, nd;
   lookup(threadIdx.x, ns, nd);
   for (int base = 0, buf = 0; base < n; base += kCompactThreads, buf ^= 1) {
@@ -96,13 +98,13 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
     __syncthreads();
     lookup(base + kCompactThreads + threadIdx.x, ns, nd);  // the next batch, in flight while this one moves
     const int here = min(n - base, kCompactThreads);
-    uint4 v[kCompactUnroll], w[kCompactUnroll];
-    auto load = [&](int r0, uint4 (&to)[kCompactUnroll]) {
+    W v[kCompactUnroll], w[kCompactUnroll];
+    auto load = [&](int r0, W (&to)[kCompactUnroll]) {
 #pragma unroll
       for (int u = 0; u < kCompactUnroll; ++u) {
         const int row = r0 + u * per_pass + my_row;
         const int64_t src = row < here ? s_src[buf][row] : -1;
-        if (src >= 0) to[u] = __ldcg(reinterpret_cast<const uint4*>(cache + src + my_off));
+        if (src >= 0) to[u] = __ldcg(reinterpret_cast<const W*>(cache + src + my_off));
       }
     };
     load(0, v);
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
       for (int u = 0; u < kCompactUnroll; ++u) {
         const int row = r0 + u * per_pass + my_row;
         const int64_t dst = row < here ? s_dst[buf][row] : -1;
-        if (dst >= 0) *reinterpret_cast<uint4*>(cache + dst + my_off) = v[u];
+        if (dst >= 0) *reinterpret_cast<W*>(cache + dst + my_off) = v[u];
       }
 #pragma unroll
       for (int u = 0; u < kCompactUnroll; ++u) v[u] = w[u];
@@ -124,11 +126,17 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
 }  // namespace
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
+  if (p.row_bytes < 16) {  // an E2M1 cache's scales
+    const dim3 grid(p.batch, p.num_kv_heads * 2);
+    return p.row_bytes == 8
+               ? launch_pdl(compact_kernel<uint2>, grid, dim3(kCompactThreads), 0, stream, p, p.row_bytes)
+               : launch_pdl(compact_kernel<uint32_t>, grid, dim3(kCompactThreads), 0, stream, p, p.row_bytes);
+  }
   // column bands of at least 64 bytes while the CTAs are fewer than two per SM
   int band = p.row_bytes;
   while (band > 64 && static_cast<int64_t>(p.batch) * p.num_kv_heads * 2 * (p.row_bytes / band) < 2 * 152) band /= 2;
   const dim3 grid(p.batch, p.num_kv_heads * 2 * (p.row_bytes / band));
-  return launch_pdl(compact_kernel, grid, dim3(kCompactThreads), 0, stream, p, band);
+  return launch_pdl(compact_kernel<uint4>, grid, dim3(kCompactThreads), 0, stream, p, band);
 }
 
 }  // namespace pkv

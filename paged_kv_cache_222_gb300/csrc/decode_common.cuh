@@ -13,7 +13,7 @@
 namespace pkv {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr int kE4M3 = 2;
+constexpr int kE4M3 = 2, kE2M1 = 3;
 
 template <int D, bool FP8>
 struct Layout {

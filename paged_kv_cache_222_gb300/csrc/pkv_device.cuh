@@ -194,6 +194,48 @@ __device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi) {
   return d;
 }
 
+// Eight floats -> eight E2M1 codes, RNE with saturation to +-6; v[0] in bits 0..3.
+__device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&v)[8]) {
+  uint32_t d;
+  asm("{\n\t.reg .b8 a, b, c, e;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 e, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, e};\n\t}"
+      : "=r"(d)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return d;
+}
+
+// Eight E2M1 codes -> four f16x2 (exact), in the order of the bytes: 1.3 cycles
+// per pair and sub-partition.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t codes, uint32_t (&d)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, e;\n\t"
+      "mov.b32 {a, b, c, e}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, e;\n\t}"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(codes));
+}
+
+// Product of two f16 pairs.  A code times its group's scale is exact: at most
+// six significant bits, a multiple of 2^-10 and at most 2688.
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Larger of two values, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // Byte permute: picks bytes of {b:a} by the 4 selector nibbles.
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t d;
@@ -266,6 +308,28 @@ __device__ __forceinline__ void enc_store8(void* cache, int64_t elem, const floa
     o.y = w[2] | (w[3] << 16);
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + elem) = o;
   }
+}
+
+// E2M1 rows: a group of 16 elements has the scale s = E4M3(max |x| / 6), RNE
+// and saturating, and the codes E2M1(x / s), both quotients IEEE binary32 ones.
+// A NaN in the group makes its scale NaN, so that the group reads as NaN; a
+// scale that rounds to zero leaves zeros.
+__device__ __forceinline__ float abs_max8(const float (&x)[8]) {
+  float m = fabsf(x[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(x[i]));
+  return m;
+}
+__device__ __forceinline__ uint8_t e2m1_group_scale(float abs_max) {
+  return static_cast<uint8_t>(f32x2_to_e4m3x2(__fdiv_rn(abs_max, 6.f), 0.f) & 0xFFu);
+}
+__device__ __forceinline__ uint32_t e2m1_codes8(const float (&x)[8], uint8_t scale_code) {
+  const float s = f16lo_to_f32(e4m3x2_to_f16x2(scale_code));
+  if (!(s > 0.f)) return 0u;
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+  return f32x8_to_e2m1x8(y);
 }
 
 // 2^x on the special-function unit.

@@ -14,6 +14,7 @@ constexpr int kDevErrWaitTimeout = 1;
 constexpr int kDevErrBlockId = 2;
 constexpr int kDevErrContextLen = 3;
 constexpr int kDevErrSlot = 4;
+constexpr int kDevErrAxis = 5;
 
 // Tokens per pipeline tile: one mma M dimension of keys.
 constexpr int kTileTokens = 16;
@@ -31,7 +32,8 @@ enum KernelKind {
   kKindChunk = 7,
   kKindRotary = 8,
   kKindCompact = 9,
-  kNumKernelKinds = 10  // the trace aggregates by kind
+  kKindRead = 10,
+  kNumKernelKinds = 11  // the trace aggregates by kind
 };
 
 // Decode work split: balanced stream-K ranges over the flattened
@@ -57,7 +59,27 @@ struct AppendParams {
   int32_t num_kv_heads;
   int32_t head_dim;
   int32_t src_dtype;    // PKV_BF16 / PKV_F32
-  int32_t cache_dtype;  // PKV_BF16 / PKV_E4M3
+  int32_t cache_dtype;  // PKV_BF16 / PKV_E4M3 / PKV_E2M1
+  int* err;
+};
+
+// Token rows read back from the cache (append.cu).
+struct ReadParams {
+  const int64_t* slots;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  int64_t scale_stride;
+  void* k_out;
+  void* v_out;
+  int64_t n_tokens;
+  int64_t num_slots;  // num_blocks * block_size
+  int32_t block_size;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t out_dtype;    // PKV_BF16 / PKV_F32
+  int32_t cache_dtype;  // PKV_BF16 / PKV_E4M3 / PKV_E2M1
   int* err;
 };
 
@@ -76,8 +98,18 @@ struct SlotParams {
 };
 
 // Element types of K / V rows being encoded into the cache: the sources of
-// an append (bf16, f32) and the cache's own (bf16, E4M3).
-constexpr int kEncBF16 = 0, kEncF32 = 1, kEncE4M3 = 2;
+// an append (bf16, f32) and the cache's own (bf16, E4M3, E2M1).
+constexpr int kEncBF16 = 0, kEncF32 = 1, kEncE4M3 = 2, kEncE2M1 = 3;
+
+// E2M1 caches: the bytes of one (block, head) are block_size rows of D / 2 code
+// bytes, then block_size rows of D / 16 scale bytes.  Codes and scales apart keep
+// both of them in 16-byte pieces that the TMA unit moves.
+constexpr int kE2M1Group = 16;  // elements that share a scale
+constexpr int e2m1_code_row(int head_dim) { return head_dim / 2; }
+constexpr int e2m1_scale_row(int head_dim) { return head_dim / kE2M1Group; }
+constexpr int e2m1_tile_bytes(int head_dim, int block_size) {
+  return block_size * (e2m1_code_row(head_dim) + e2m1_scale_row(head_dim));
+}
 
 struct DecodeParams {
   const void* q;              // bf16 [B, H_q, D]
@@ -193,7 +225,10 @@ struct RotaryParams {
   const void* v;
   void* q_out;                   // bf16
   int64_t q_stride, k_stride, v_stride, out_stride;  // elements between tokens
-  const int64_t* positions;
+  const int64_t* positions;      // [num_axes] rows of one per token, position_stride apart
+  int64_t position_stride;
+  const int32_t* axes;           // [rotary_dim / 2]: the axis of each pair, or NULL: axis 0
+  int32_t num_axes;
   const double* inv_freq;        // [rotary_dim / 2], radians per position
   float magnitude;
   const int64_t* slots;
@@ -211,7 +246,7 @@ struct RotaryParams {
   int32_t rotary_dim;
   int32_t interleaved;
   int32_t src_dtype;             // PKV_BF16 / PKV_F32
-  int32_t cache_dtype;           // PKV_BF16 / PKV_E4M3
+  int32_t cache_dtype;           // PKV_BF16 / PKV_E4M3 / PKV_E2M1
   int* err;
 };
 
@@ -231,6 +266,8 @@ struct CompactParams {
   int32_t block_size;
   int32_t num_kv_heads;
   int32_t row_bytes;             // bytes of one token row of one head
+  int32_t tile_bytes;            // from one (block, head) to the next
+  int32_t tile_offset;           // of a (block, head)'s first row
   int* err;
 };
 
@@ -244,6 +281,7 @@ int config_epoch();
 // Launchers (return the launch's cudaError_t; nothing is synchronised).
 cudaError_t launch_copy_blocks(const CopyParams& p, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
+cudaError_t launch_read(const ReadParams& p, cudaStream_t stream);
 cudaError_t launch_slot_mapping(const SlotParams& p, cudaStream_t stream);
 cudaError_t launch_decode_split(const DecodeParams& p, const CUtensorMap& tmap_k,
                                 const CUtensorMap& tmap_v, cudaStream_t stream);

@@ -7,8 +7,11 @@
 // Pair i of a head's first rotary_dim elements, (x1, x2) = (x[i], x[i + rd/2])
 // in the half layout and (x[2i], x[2i+1]) in the interleaved one, becomes
 //   (x1 c - x2 s, x2 c + x1 s),   c = mag cos(pos f_i), s = mag sin(pos f_i);
-// the other elements pass through.  All in binary32, rounded once to bf16 or
-// quantised once to E4M3.
+// the other elements pass through.  With several axes (time, height, width of
+// images and video) pos is the token's position along the pair's own axis.  All
+// in binary32, rounded once to bf16 or
+// quantised once to E4M3 or E2M1 (whose groups of 16 elements may lie in two
+// items: their largest magnitudes are exchanged between the row's lanes).
 //
 // Angles of far positions: f_i / 2 pi is taken as a 64-bit fixed-point
 // fraction of a turn, so that pos * f_i modulo one turn is one wrapping 64-bit
@@ -82,6 +85,43 @@ struct Raw8 {
   }
 };
 
+// The lanes of a row (D / 16, all of them here) hold its elements in pieces of
+// eight: this one x, piece px, and y, piece py.  Which lane holds a piece, and
+// as which of the two: in the half layout pieces below half_pieces are x of
+// their own number's lane and those up to turned_pieces y, half_pieces further
+// on; any other lies at its place.  A group's scale needs both of its pieces'
+// largest magnitude.
+template <int D>
+__device__ __forceinline__ void store_e2m1(uint8_t* tile, int block_size, int off, int px, int py, int half_pieces,
+                                           int turned_pieces, float (&x)[8], float (&y)[8], float scale, bool scaled) {
+  constexpr int LANES = D / 16;
+  const int lane = threadIdx.x & 31, first = lane & ~(LANES - 1);
+  const unsigned mask = ((1u << LANES) - 1u) << first;
+  if (scaled) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = __fdiv_rn(x[i], scale);
+      y[i] = __fdiv_rn(y[i], scale);
+    }
+  }
+  const float mx = abs_max8(x), my = abs_max8(y);
+  auto from = [&](int piece) {  // the largest magnitude of a piece
+    const bool split = piece < turned_pieces && half_pieces > 0;
+    const bool low = split && piece < half_pieces;
+    const int at = first + (split ? (low ? piece : piece - half_pieces) : piece / 2);
+    const float a = __shfl_sync(mask, mx, at), b = __shfl_sync(mask, my, at);
+    return (split ? low : piece % 2 == 0) ? a : b;
+  };
+  const uint8_t sx = e2m1_group_scale(max_nan(mx, from(px ^ 1)));
+  const uint8_t sy = e2m1_group_scale(max_nan(my, from(py ^ 1)));
+  uint8_t* codes = tile + off * (D / 2);
+  uint8_t* scales = tile + block_size * (D / 2) + off * LANES;
+  *reinterpret_cast<uint32_t*>(codes + px * 4) = e2m1_codes8(x, sx);
+  *reinterpret_cast<uint32_t*>(codes + py * 4) = e2m1_codes8(y, sy);
+  if (px % 2 == 0) scales[px / 2] = sx;
+  if (py % 2 == 0) scales[py / 2] = sy;
+}
+
 template <int D, int SRC, int DST, bool INTER>
 __global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const RotaryParams p) {
   __shared__ __align__(16) float2 s_cs[D / 2];  // read two at a time
@@ -119,7 +159,13 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const Rot
   load(cur);  // in flight while the angles are computed
   const int64_t slot = p.slots[tok];
   if (threadIdx.x < half) {
-    const uint64_t turn = turn_step(p.inv_freq[threadIdx.x]) * static_cast<uint64_t>(p.positions[tok]);
+    const int axis = p.axes != nullptr ? p.axes[threadIdx.x] : 0;
+    int64_t pos = 0;  // an axis that is none: not turned
+    if (axis >= 0 && axis < p.num_axes)
+      pos = p.positions[axis * p.position_stride + tok];
+    else
+      record_error(p.err, kDevErrAxis);
+    const uint64_t turn = turn_step(p.inv_freq[threadIdx.x]) * static_cast<uint64_t>(pos);
     float sn, cs;
     sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077392578125e-10f, &sn, &cs);
     s_cs[threadIdx.x] = make_float2(cs * p.magnitude, sn * p.magnitude);
@@ -172,10 +218,15 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_append_kernel(const Rot
         if (cur.r == hq && c == 0) record_error(p.err, kDevErrSlot);
       } else if (slot >= 0) {
         const int64_t blk = p.block_size == 16 ? slot >> 4 : slot >> 5;
-        const int64_t dst = ((blk * hk + h) * p.block_size + (slot & (p.block_size - 1))) * D;
+        const int off = static_cast<int>(slot & (p.block_size - 1));
+        const int64_t dst = ((blk * hk + h) * p.block_size + off) * D;
         void* cache = kind == 1 ? p.k_cache : p.v_cache;
-        const float sc = DST == kEncE4M3 ? (kind == 1 ? p.k_scale : p.v_scale)[tok * p.scale_stride + h] : 1.f;
-        if (turned) {
+        const float* scales = kind == 1 ? p.k_scale : p.v_scale;
+        const float sc = DST != kEncBF16 && scales != nullptr ? scales[tok * p.scale_stride + h] : 1.f;
+        if constexpr (DST == kEncE2M1) {
+          store_e2m1<D>(static_cast<uint8_t*>(cache) + (blk * hk + h) * e2m1_tile_bytes(D, p.block_size), p.block_size,
+                        off, e0 / 8, e1 / 8, turned && !INTER ? half / 8 : 0, p.rotary_dim / 8, x, y, sc, scales != nullptr);
+        } else if (turned) {
           enc_store8<kEncF32, DST>(cache, dst + e0, x, uint4{}, sc);
           enc_store8<kEncF32, DST>(cache, dst + e1, y, uint4{}, sc);
         } else {
@@ -209,6 +260,8 @@ cudaError_t launch_rotary(const RotaryParams& p, cudaStream_t stream) {
   const bool bf = p.src_dtype == kEncBF16;
   if (p.cache_dtype == kEncBF16)
     return bf ? launch_rotary_sd<kEncBF16, kEncBF16>(p, stream) : launch_rotary_sd<kEncF32, kEncBF16>(p, stream);
+  if (p.cache_dtype == kEncE2M1)
+    return bf ? launch_rotary_sd<kEncBF16, kEncE2M1>(p, stream) : launch_rotary_sd<kEncF32, kEncE2M1>(p, stream);
   return bf ? launch_rotary_sd<kEncBF16, kEncE4M3>(p, stream) : launch_rotary_sd<kEncF32, kEncE4M3>(p, stream);
 }
 

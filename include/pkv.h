@@ -85,8 +85,9 @@ typedef enum {
  * 4.5 bits per element.  The head_dim / 2 + head_dim / 16 bytes per row are
  * laid out per (block, head): block_size rows of head_dim / 2 code bytes
  * (element 2 i in the low half of byte i), then block_size rows of head_dim / 16
- * scale bytes.  Taken by pkv_append, pkv_rotary_append, pkv_read_tokens,
- * pkv_compact_tokens, pkv_slot_mapping and the block copies; the others return
+ * scale bytes.  Attended by pkv_chunk_attention (single tokens and chunks), and
+ * taken by pkv_append, pkv_rotary_append, pkv_read_tokens, pkv_compact_tokens,
+ * pkv_slot_mapping and the block copies; the other attention calls return
  * PKV_ERR_UNSUPPORTED.
  */
 typedef struct {
@@ -484,11 +485,12 @@ pkv_status pkv_multi_query_attention(const void* q, int32_t batch, int32_t q_len
  *   scale          finite, > 0.
  *   out            bf16 [n_tokens, num_q_heads, head_dim], 16-byte aligned.
  *                  The weights are rounded to the cache's 16-bit type (bf16, or
- *                  f16 for E4M3 caches, whose q is taken as f16 too: finite
- *                  below 65520, and held to 2^-25 below 2^-14) and sums are
+ *                  f16 for E4M3 and E2M1 caches, whose q is taken as f16 too:
+ *                  finite below 65520, and held to 2^-25 below 2^-14) and sums are
  *                  binary32; pkv_decode_attention holds weights over bf16 caches
  *                  to 16 bits.
- *   k_scale, v_scale  as pkv_decode_attention; positive.
+ *   k_scale, v_scale  as pkv_decode_attention; positive.  E2M1 caches: both or
+ *                  neither (neither: 1).
  *   split_tokens   0 = automatic, else visible tokens per split (a multiple of
  *                  128, at most 1024 * block_size).
  *   workspace      device scratch of plan.workspace_bytes from pkv_chunk_plan

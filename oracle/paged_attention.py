@@ -43,6 +43,7 @@ from .formats import bf16_bits_to_f64, e4m3_to_f64, e4m3_encode, f32_to_bf16_bit
 BF16 = "bf16"
 F32 = "f32"
 E4M3 = "e4m3"
+VALUES = 'values'
 
 
 def slot_of(block_table_row, pos, block_size):
@@ -64,7 +65,10 @@ def gather_sequence(cache, block_table_row, ctx, h, block_size):
 
 
 def dequantize(raw, cache_dtype, scale=None):
-    """Exact float64 value of raw cache words (times the FP8 scale if any)."""
+    """Exact float64 value of raw cache words (times the FP8 scale if any).  A
+    cache of VALUES is float64 already (formats.e2m1_values)."""
+    if cache_dtype == VALUES:
+        return raw if scale is None else raw * np.float64(np.float32(scale))
     if cache_dtype == BF16:
         return bf16_bits_to_f64(raw)
     if cache_dtype == E4M3:

@@ -390,7 +390,7 @@ def chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_starts, s
     slopes[hq] * (t - pos) with slopes (float32 [H_q]).  A query at position
     pos sees key t iff t < prefix_lens[b] (int32 [B]) or pos - window < t <=
     pos (window 0: t <= pos).  E4M3 caches take k_scale / v_scale float32 [B,
-    H_kv] or [H_kv].
+    H_kv] or [H_kv]; E2M1 caches take them or go without.
     """
     r = _lib.binding().chunk_attention(q, k_cache, v_cache, block_tables, context_lens, q_starts, scale, max_q_len,
                                        max_context_len, k_scale, v_scale, softcap, window, slopes, prefix_lens, out,

@@ -156,6 +156,31 @@ pkv_status make_cache_tmap(CUtensorMap* tm, const void* base, const pkv_cache_de
   return PKV_OK;
 }
 
+// 4-D view of the code rows (byte of a row, token in block, KV head, block) or
+// of the scale rows (byte of the block's scales, one, KV head, block) of an E2M1
+// cache.  A box is `box_tokens` token rows; code rows of 64 or 32 bytes are
+// swizzled over their own width.
+pkv_status make_e2m1_tmap(CUtensorMap* tm, const void* base, const pkv_cache_desc& c, int box_tokens, bool scales) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  const int codes = pkv::e2m1_code_row(c.head_dim), row = pkv::e2m1_scale_row(c.head_dim);
+  const cuuint64_t tile = static_cast<cuuint64_t>(pkv::e2m1_tile_bytes(c.head_dim, c.block_size));
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(scales ? row * c.block_size : codes),
+                        static_cast<cuuint64_t>(scales ? 1 : c.block_size), static_cast<cuuint64_t>(c.num_kv_heads),
+                        static_cast<cuuint64_t>(c.num_blocks)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(scales ? tile : codes), tile, tile * c.num_kv_heads};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(scales ? row * box_tokens : codes),
+                       static_cast<cuuint32_t>(scales ? 1 : box_tokens), 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  const char* from = static_cast<const char*>(base) + (scales ? codes * c.block_size : 0);
+  CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<char*>(from), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  scales ? CU_TENSOR_MAP_SWIZZLE_NONE : (codes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B),
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled(E2M1) failed (%d)", int(r));
+  return PKV_OK;
+}
+
 // 4-D view (d, head of the group, KV head, token) of the queries [T, H_q, D]: a
 // box is the rows (token, head) of `box_tokens` tokens and one KV head, 128
 // bytes (64 columns) of each, 128B-swizzled; tokens past T read as zeros.
@@ -1307,12 +1332,12 @@ namespace {
 // Rows (new tokens x query heads of a KV head) of one row tile: the mma.sync
 // kernel when every sequence's rows fit one of its tiles, else the tcgen05
 // kernel's 256.
-bool chunk_small(int32_t max_q_len, int32_t group) {
-  return static_cast<int64_t>(max_q_len) * group <= pkv::kChunkSmallRows;
+bool chunk_small(int32_t max_q_len, int32_t group, int32_t dtype) {
+  return dtype != PKV_E2M1 && static_cast<int64_t>(max_q_len) * group <= pkv::kChunkSmallRows;
 }
 
-int32_t chunk_tile_q(int32_t max_q_len, int32_t group) {
-  return (chunk_small(max_q_len, group) ? pkv::kChunkSmallRows : pkv::kChunkTcRows) / group;
+int32_t chunk_tile_q(int32_t max_q_len, int32_t group, int32_t dtype) {
+  return (chunk_small(max_q_len, group, dtype) ? pkv::kChunkSmallRows : pkv::kChunkTcRows) / group;
 }
 
 // Key tiles per split of the tcgen05 kernel: the number of splits that
@@ -1342,7 +1367,7 @@ int64_t tc_split_tiles(int64_t n_tokens, int64_t batch, int64_t tile_q, int64_t 
 pkv_status chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_t num_q_heads,
                       const pkv_cache_desc* c, int32_t max_ctx, int32_t window, bool has_prefix,
                       int32_t split_tokens, int32_t sms, pkv_decode_plan_t* out) {
-  pkv_status s = check_cache(c);
+  pkv_status s = check_cache(c, true);
   if (s != PKV_OK) return s;
   if (n_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "n_tokens %d", n_tokens);
   if (batch < 0 || batch > 65535) return fail(PKV_ERR_INVALID_ARG, "batch %d", batch);
@@ -1360,8 +1385,8 @@ pkv_status chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_
     return fail(PKV_ERR_INVALID_ARG, "split_tokens %d (0, or a multiple of 128 up to %lld)", split_tokens,
                 static_cast<long long>(max_st));
   if (sms <= 0) sms = kDefaultSms;
-  const bool small = chunk_small(max_q_len, group);
-  const int64_t tile_q = chunk_tile_q(max_q_len, group), nk = small ? pkv::kChunkSmallTile : pkv::kChunkTcTile;
+  const bool small = chunk_small(max_q_len, group, c->dtype);
+  const int64_t tile_q = chunk_tile_q(max_q_len, group, c->dtype), nk = small ? pkv::kChunkSmallTile : pkv::kChunkTcTile;
   // visible keys of one row tile, in tiles of nk
   int64_t tiles = ceil_div(max_ctx, nk);
   if (window > 0 && !has_prefix) {
@@ -1442,7 +1467,7 @@ extern "C" pkv_status pkv_chunk_attention(
   DecodeArgs a = {q, some, num_q_heads, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
                   context_lens, max_context_len, scale, static_cast<float*>(out), k_scale, v_scale,
                   scale_row_stride};
-  pkv_status s = check_decode(a);
+  pkv_status s = check_decode(a, true);
   if (s != PKV_OK) return s;
   if (!(scale > 0.f)) return fail(PKV_ERR_INVALID_ARG, "scale must be positive");
   pkv_score_mods m = {};
@@ -1477,17 +1502,19 @@ extern "C" pkv_status pkv_chunk_attention(
   }
   const pkv_cache_desc& c = *cache;
   const int32_t group = num_q_heads / c.num_kv_heads;
-  CUtensorMap tk, tv;
-  const bool small = pl.workers == 1;
-  CUtensorMap tq = {};
-  if (!small) {
-    s = make_query_tmap(&tq, q, c, n_tokens, group, chunk_tile_q(max_q_len, group));
-    if (s != PKV_OK) return s;
+  const bool small = pl.workers == 1, e2m1 = c.dtype == PKV_E2M1;
+  pkv::ChunkMaps maps = {};
+  if (!small) s = make_query_tmap(&maps.q, q, c, n_tokens, group, chunk_tile_q(max_q_len, group, c.dtype));
+  if (s == PKV_OK && e2m1) {
+    s = make_e2m1_tmap(&maps.k, k_cache, c, c.block_size, false);
+    if (s == PKV_OK) s = make_e2m1_tmap(&maps.v, v_cache, c, c.block_size, false);
+    if (s == PKV_OK) s = make_e2m1_tmap(&maps.k_scales, k_cache, c, c.block_size, true);
+    if (s == PKV_OK) s = make_e2m1_tmap(&maps.v_scales, v_cache, c, c.block_size, true);
+  } else if (s == PKV_OK) {
+    const int box = small ? pkv::kTileTokens : c.block_size;  // token rows per TMA box
+    s = make_cache_tmap(&maps.k, k_cache, c, box);
+    if (s == PKV_OK) s = make_cache_tmap(&maps.v, v_cache, c, box);
   }
-  const int box = small ? pkv::kTileTokens : c.block_size;  // token rows per TMA box
-  s = make_cache_tmap(&tk, k_cache, c, box);
-  if (s != PKV_OK) return s;
-  s = make_cache_tmap(&tv, v_cache, c, box);
   if (s != PKV_OK) return s;
   pkv::ChunkParams p = {};
   p.q = q;
@@ -1519,7 +1546,7 @@ extern "C" pkv_status pkv_chunk_attention(
   p.window = m.window;
   p.split_tokens = pl.split_tokens;
   p.max_splits = pl.max_splits;
-  p.tile_q = chunk_tile_q(max_q_len, group);
+  p.tile_q = chunk_tile_q(max_q_len, group, c.dtype);
   p.qk_log2 = qk_log2;
   p.cap_log2 = m.softcap * kLog2e;
   pkv::cap_coefficients(m.softcap, p.cap_c, p.cap_y_max);
@@ -1528,12 +1555,12 @@ extern "C" pkv_status pkv_chunk_attention(
   p.err = st->err;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = traced(pkv::kKindChunk, cs, [&] {
-    return small ? pkv::launch_chunk_small(p, tk, tv, cs) : pkv::launch_chunk_tc(p, tq, tk, tv, cs);
+    return small ? pkv::launch_chunk_small(p, maps.k, maps.v, cs) : pkv::launch_chunk_tc(p, maps, cs);
   });
   if (e == cudaSuccess && pl.max_splits > 1)
     e = traced(pkv::kKindCombine, cs, [&] {
       const int nk = small ? pkv::kChunkSmallTile
-                           : pkv::chunk_tc_tile(c.head_dim, c.dtype == PKV_E4M3, m.softcap > 0.f || m.slopes != nullptr);
+                           : pkv::chunk_tc_tile(c.head_dim, c.dtype != PKV_BF16, m.softcap > 0.f || m.slopes != nullptr);
       return pkv::launch_chunk_combine(p, nk, cs);
     });
   if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");

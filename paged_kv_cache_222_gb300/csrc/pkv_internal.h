@@ -218,6 +218,12 @@ struct ChunkParams {
   int* err;
 };
 
+// Tensor maps of a chunk attention call: the queries (tcgen05 kernel), the
+// caches' rows (E2M1: of codes) and an E2M1 cache's rows of scales.
+struct ChunkMaps {
+  CUtensorMap q, k, v, k_scales, v_scales;
+};
+
 // Rotary positions and append of new tokens (rotary.cu).
 struct RotaryParams {
   const void* q;
@@ -298,8 +304,8 @@ cudaError_t launch_multi_query_tc(const DecodeParams& p, const CUtensorMap& tmap
 // kernel (row tiles of up to 256 rows) and the merge of their split pieces.
 cudaError_t launch_chunk_small(const ChunkParams& p, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
                                cudaStream_t stream);
-cudaError_t launch_chunk_tc(const ChunkParams& p, const CUtensorMap& tmap_q, const CUtensorMap& tmap_k,
-                            const CUtensorMap& tmap_v, cudaStream_t stream);
+cudaError_t launch_chunk_tc(const ChunkParams& p, const ChunkMaps& maps, cudaStream_t stream);
+cudaError_t launch_chunk_tc_e2m1(const ChunkParams& p, const ChunkMaps& maps, cudaStream_t stream);
 // `nk`: keys per tile of the kernel that wrote the pieces.
 cudaError_t launch_chunk_combine(const ChunkParams& p, int nk, cudaStream_t stream);
 cudaError_t launch_rotary(const RotaryParams& p, cudaStream_t stream);

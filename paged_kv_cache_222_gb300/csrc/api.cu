@@ -1332,12 +1332,12 @@ namespace {
 // Rows (new tokens x query heads of a KV head) of one row tile: the mma.sync
 // kernel when every sequence's rows fit one of its tiles, else the tcgen05
 // kernel's 256.
-bool chunk_small(int32_t max_q_len, int32_t group, int32_t dtype) {
-  return dtype != PKV_E2M1 && static_cast<int64_t>(max_q_len) * group <= pkv::kChunkSmallRows;
+bool chunk_small(int32_t max_q_len, int32_t group) {
+  return static_cast<int64_t>(max_q_len) * group <= pkv::kChunkSmallRows;
 }
 
-int32_t chunk_tile_q(int32_t max_q_len, int32_t group, int32_t dtype) {
-  return (chunk_small(max_q_len, group, dtype) ? pkv::kChunkSmallRows : pkv::kChunkTcRows) / group;
+int32_t chunk_tile_q(int32_t max_q_len, int32_t group) {
+  return (chunk_small(max_q_len, group) ? pkv::kChunkSmallRows : pkv::kChunkTcRows) / group;
 }
 
 // Key tiles per split of the tcgen05 kernel: the number of splits that
@@ -1385,8 +1385,9 @@ pkv_status chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_
     return fail(PKV_ERR_INVALID_ARG, "split_tokens %d (0, or a multiple of 128 up to %lld)", split_tokens,
                 static_cast<long long>(max_st));
   if (sms <= 0) sms = kDefaultSms;
-  const bool small = chunk_small(max_q_len, group, c->dtype);
-  const int64_t tile_q = chunk_tile_q(max_q_len, group, c->dtype), nk = small ? pkv::kChunkSmallTile : pkv::kChunkTcTile;
+  const bool small = chunk_small(max_q_len, group), e2m1 = c->dtype == PKV_E2M1;
+  const int64_t tile_q = chunk_tile_q(max_q_len, group);
+  const int64_t nk = !small ? pkv::kChunkTcTile : (e2m1 ? pkv::kChunkE2M1Tile : pkv::kChunkSmallTile);
   // visible keys of one row tile, in tiles of nk
   int64_t tiles = ceil_div(max_ctx, nk);
   if (window > 0 && !has_prefix) {
@@ -1413,7 +1414,9 @@ pkv_status chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_
       // are eight and more (16 of 511-8191: 45 us with 2048, 32 with 1024), or one
       // each of up to 2048 tokens that nearly fill the round (64 of 1k-2k: 43 us,
       // two splits 49).  Else as for decode, from 1024 tokens.
-      const int64_t slots = sms * pkv::chunk_small_ctas(c->head_dim, c->dtype == PKV_E4M3, max_q_len * group <= 8);
+      const bool eight = max_q_len * group <= 8;
+      const int64_t slots = sms * (e2m1 ? pkv::chunk_e2m1_ctas(c->head_dim, eight)
+                                        : pkv::chunk_small_ctas(c->head_dim, c->dtype == PKV_E4M3, eight));
       const int64_t n = units > 0 ? slots / units : slots;
       st = n > 0 && !(all <= 1024 && units >= sms) ? ceil_div(ceil_div(all, n), 128) * 128 : all;
       if (st < 256) st = 256;
@@ -1421,6 +1424,7 @@ pkv_status chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_
         st = decode_split_tokens(static_cast<int32_t>(row_tiles < 0x7FFFFFFF ? row_tiles : 0x7FFFFFFF), c->num_kv_heads,
                                  static_cast<int32_t>(all < 0x7FFFFFC0 ? all : 0x7FFFFFC0), sms);
         while (st < 1024 && st < all) st += 64;
+        st = ceil_div(st, nk) * nk;
       }
       if (st > max_st) st = max_st;
     } else {
@@ -1504,7 +1508,7 @@ extern "C" pkv_status pkv_chunk_attention(
   const int32_t group = num_q_heads / c.num_kv_heads;
   const bool small = pl.workers == 1, e2m1 = c.dtype == PKV_E2M1;
   pkv::ChunkMaps maps = {};
-  if (!small) s = make_query_tmap(&maps.q, q, c, n_tokens, group, chunk_tile_q(max_q_len, group, c.dtype));
+  if (!small) s = make_query_tmap(&maps.q, q, c, n_tokens, group, chunk_tile_q(max_q_len, group));
   if (s == PKV_OK && e2m1) {
     s = make_e2m1_tmap(&maps.k, k_cache, c, c.block_size, false);
     if (s == PKV_OK) s = make_e2m1_tmap(&maps.v, v_cache, c, c.block_size, false);
@@ -1546,7 +1550,7 @@ extern "C" pkv_status pkv_chunk_attention(
   p.window = m.window;
   p.split_tokens = pl.split_tokens;
   p.max_splits = pl.max_splits;
-  p.tile_q = chunk_tile_q(max_q_len, group, c.dtype);
+  p.tile_q = chunk_tile_q(max_q_len, group);
   p.qk_log2 = qk_log2;
   p.cap_log2 = m.softcap * kLog2e;
   pkv::cap_coefficients(m.softcap, p.cap_c, p.cap_y_max);
@@ -1555,11 +1559,12 @@ extern "C" pkv_status pkv_chunk_attention(
   p.err = st->err;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = traced(pkv::kKindChunk, cs, [&] {
-    return small ? pkv::launch_chunk_small(p, maps.k, maps.v, cs) : pkv::launch_chunk_tc(p, maps, cs);
+    if (!small) return pkv::launch_chunk_tc(p, maps, cs);
+    return e2m1 ? pkv::launch_chunk_e2m1(p, maps, cs) : pkv::launch_chunk_small(p, maps.k, maps.v, cs);
   });
   if (e == cudaSuccess && pl.max_splits > 1)
     e = traced(pkv::kKindCombine, cs, [&] {
-      const int nk = small ? pkv::kChunkSmallTile
+      const int nk = small ? (e2m1 ? pkv::kChunkE2M1Tile : pkv::kChunkSmallTile)
                            : pkv::chunk_tc_tile(c.head_dim, c.dtype != PKV_BF16, m.softcap > 0.f || m.slopes != nullptr);
       return pkv::launch_chunk_combine(p, nk, cs);
     });

@@ -1,0 +1,461 @@
+// Attention of ragged chunks over E2M1 caches, row tiles of up to 16 rows (single
+// tokens of up to 16 query heads per KV head, a few tokens of smaller groups);
+// what it computes: chunk_common.cuh, what a cache holds: pkv.h.
+//
+// A CTA takes the rows of one tile of one (sequence, KV head) over one split of
+// its visible keys, in 128-key steps: warp w loads keys 32w..32w+31 of every
+// step by TMA (a box of codes and a box of scales per block, of K and of V) into
+// a ring of its own on barriers of its own, and refills a slot as soon as it has
+// read it; the warps merge (m, l, O) through shared memory at the end.
+//
+// Both products have keys as the first operand's rows or columns and up to 8
+// tile rows as the second's columns (NT of them: 1 or 2), mma.sync m16n8k16 of
+// f16 with fp32 sums, so that the codes, widened once, serve every row:
+//   S^T = K Q^T.  A lane's word of an ldmatrix row is 8 codes of one key: two
+//     products' worth, whose order of d is Q's to follow.  cvt makes f16 pairs of
+//     its bytes, which are multiplied by the key's scale of that group, in pairs
+//     too: exact, so S is that of the cache's values.
+//   O^T += V^T P^T.  A lane needs pairs of keys at one d where the cache has
+//     pairs of d of one key: it reads the same D / 8 d of its four keys, widens
+//     and interleaves them (one byte permute per pair).  All of them lie in one
+//     group, so that a pair of keys has one pair of scales.
+// Keys take the products' rows in an order (key_of) that keeps those reads free
+// of bank conflicts.  P is rounded to f16: at most 2^-11 of each weight, next to
+// the output's own 2^-8.  V past the sequence's end has scale 0 (its codes are
+// finite whatever they are).
+
+#include "chunk_common.cuh"
+
+namespace pkv {
+namespace {
+
+template <int D, int NT>
+struct E2M1Shape {
+  static constexpr int STEP = kChunkE2M1Tile, KEYS = STEP / 4;  // keys of a step, and of a warp
+  static constexpr int ROWB = D / 2, SROWB = D / 16;      // bytes of a row's codes and scales
+  static constexpr int CODEB = KEYS * ROWB;               // codes of K (or V) of a warp's step
+  static constexpr int SCALEB = 256;                      // its scales: boxes of 64 bytes or more, 128 apart
+  static constexpr int CTAS = chunk_e2m1_ctas(D, NT == 1);
+  static constexpr int NS = D == 128 ? 2 : 4;
+  static constexpr int STAGE = 4 * 2 * CODEB;
+  static constexpr int DP = D + 4, R = 8 * NT;
+  static constexpr int MERGE = 4 * R * DP * 4 + 4 * R * 2 * 4;
+  static constexpr int RING = NS * (STAGE + 4 * 2 * SCALEB);
+  static constexpr int BYTES = (RING > MERGE ? RING : MERGE) + 4 * NS * 8 + kChunkMaxSplitBlocks * 4 + 1024;
+};
+
+// Key of a 16-key group that is row i of the products.  128-wide heads: rows
+// 2 j and 2 j + 1 are keys {0, 1, 4, 5}[j] and {2, 3, 6, 7}[j], 64-wide ones: j
+// and j + 4.
+template <int D>
+__device__ __forceinline__ int key_of(int i) {
+  return D == 128 ? (i & 12) | ((i & 1) << 1) | ((i >> 1) & 1) : (i & 8) | ((i & 1) << 2) | ((i >> 1) & 3);
+}
+
+template <int D, int NT, bool FAR>
+__global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
+    chunk_e2m1_kernel(const __grid_constant__ ChunkMaps maps, const ChunkParams p) {
+  using C = E2M1Shape<D, NT>;
+  constexpr int NS = C::NS, DP = C::DP, KS = D / 16, CH = D / 32;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = lane >> 2, j = lane & 3;
+  const int G = p.group, H_q = p.num_q_heads;
+  const int ntq = (p.max_q_len + p.tile_q - 1) / p.tile_q;
+  const int h = blockIdx.y / ntq;
+  const int i0 = (blockIdx.y - h * ntq) * p.tile_q;
+  const int b = blockIdx.z, split = blockIdx.x;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + (C::RING > C::MERGE ? C::RING : C::MERGE));  // [NS][4]
+  int* s_blk = reinterpret_cast<int*>(full + 4 * NS);
+  // stage s of this warp: codes of K and of V, scales of K and of V
+  const uint32_t codes0 = smem_u32(smem) + warp * 2 * C::CODEB;
+  const uint32_t scales0 = smem_u32(smem) + NS * C::STAGE + warp * 2 * C::SCALEB;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 4 * NS; ++s) mbar_init(smem_u32(full + s), 1);
+    fence_mbar_init();
+    prefetch_tmap(&maps.k);
+    prefetch_tmap(&maps.v);
+    prefetch_tmap(&maps.k_scales);
+    prefetch_tmap(&maps.v_scales);
+  }
+  wait_prior_grid();
+
+  const ChunkSeq sq = chunk_seq(p, b, split == 0 && blockIdx.y == 0 && threadIdx.x == 0);
+  if (i0 >= sq.n) return;
+  const int i1 = min(sq.n, i0 + p.tile_q) - 1;
+  const int rows = (i1 - i0 + 1) * G;
+  const ChunkRange rg = chunk_range<C::STEP>(p, sq, i0, i1);
+  const ChunkSplit sp(rg.n, p.split_tokens / C::STEP, split);
+  const int nsplit = sp.nsplit, k0 = sp.k0, ntile = sp.ntile;
+  if (split >= nsplit) return;
+  const int64_t row_base = static_cast<int64_t>(sq.start + i0) * H_q + h * G;  // of row (0, g = 0)
+  auto out_row = [&](int row) { return row_base + static_cast<int64_t>(row / G) * H_q + row % G; };
+
+  // block ids of the split's keys; blocks that no row sees (behind the window,
+  // past the last query) are not looked up and read as zeros
+  const int bshift = p.block_size == 16 ? 4 : 5;
+  const int per_tile = C::STEP >> bshift;
+  const int32_t* tbl = p.block_tables + static_cast<int64_t>(b) * p.max_blocks;
+  for (int i = threadIdx.x; i < ntile * per_tile; i += blockDim.x) {
+    const int t0 = rg.tile(k0 + i / per_tile) * C::STEP + (i % per_tile) * p.block_size;
+    int phys = -1;  // outside the tensor map: the TMA unit fills zeros
+    if (rg.sees(t0, t0 + p.block_size)) {
+      phys = tbl[t0 >> bshift];
+      if (phys < 0 || phys >= p.num_blocks) {
+        record_error(p.err, kDevErrBlockId);
+        phys = -1;
+      }
+    }
+    s_blk[i] = phys;
+  }
+  __syncthreads();
+
+  // a warp's 32 keys are one or two blocks: lane 4 bx + w loads block bx of codes
+  // of K, of V, scales of K, of V
+  const int nbox = C::KEYS >> bshift;
+  const int box_scales = p.block_size * C::SROWB < 128 ? 128 : p.block_size * C::SROWB;
+  const int group_scales = bshift == 4 ? box_scales : 16 * C::SROWB;  // from a 16-key group's scales to the next's
+  const int what = lane & 3, bx = lane >> 2;
+  const CUtensorMap* tmap = what == 0 ? &maps.k : (what == 1 ? &maps.v : (what == 2 ? &maps.k_scales : &maps.v_scales));
+  const uint32_t box_to = what < 2 ? codes0 + what * C::CODEB + bx * p.block_size * C::ROWB
+                                   : scales0 + (what - 2) * C::SCALEB + bx * box_scales;
+  const uint32_t stage_step = what < 2 ? C::STAGE : 4 * 2 * C::SCALEB;
+  auto issue = [&](int k) {
+    const int s = k % NS;
+    const uint32_t bar = smem_u32(full + 4 * s + warp);
+    if (lane == 0) {
+      fence_proxy_async_smem();  // this warp's reads of the slot come before the copy
+      mbar_arrive_expect_tx(bar, 2 * C::KEYS * (C::ROWB + C::SROWB));
+    }
+    __syncwarp();
+    if (bx < nbox)
+      tma_load_4d(box_to + s * stage_step, tmap, bar, 0, 0, h,
+                  s_blk[k * per_tile + ((warp * C::KEYS) >> bshift) + bx]);
+  };
+  int issued = 0;
+  for (; issued < ntile && issued < NS; ++issued) issue(issued);
+
+  // Q as the second operand: row r of each n-tile; chunk c of 32 d is two
+  // products, of the lane's d 32 c + 8 j + 0..3 and + 4..7
+  uint32_t qb[NT][KS][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int row = 8 * nt + r;
+    const uint16_t* q = static_cast<const uint16_t*>(p.q) + out_row(row) * D;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const uint4 w = row < rows ? *reinterpret_cast<const uint4*>(q + 32 * c + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
+      qb[nt][2 * c][0] = pack_f16x2(bf16lo_to_f32(w.x), bf16hi_to_f32(w.x));
+      qb[nt][2 * c][1] = pack_f16x2(bf16lo_to_f32(w.y), bf16hi_to_f32(w.y));
+      qb[nt][2 * c + 1][0] = pack_f16x2(bf16lo_to_f32(w.z), bf16hi_to_f32(w.z));
+      qb[nt][2 * c + 1][1] = pack_f16x2(bf16lo_to_f32(w.w), bf16hi_to_f32(w.w));
+    }
+  }
+  // this lane's rows of the tile: 8 nt + 2 j and + 1.  Per row: position (-1
+  // where it sees nothing), first key of the window, end of the prefix, bias
+  constexpr float kLog2e = 1.4426950408889634f;
+  int pos[NT][2], lo[NT][2], pf[NT][2];
+  float slope[NT][2], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = 8 * nt + 2 * j + e;
+      pos[nt][e] = row < rows ? sq.ctx - sq.n + i0 + row / G : -1;
+      lo[nt][e] = p.window > 0 && pos[nt][e] >= p.window ? pos[nt][e] - p.window + 1 : 0;
+      pf[nt][e] = pos[nt][e] >= 0 ? sq.prefix : 0;
+      slope[nt][e] = p.slopes != nullptr && row < rows ? p.slopes[h * G + row % G] * kLog2e : 0.f;
+      m[nt][e] = -CUDART_INF_F;
+      l[nt][e] = 0.f;
+    }
+  float qk_mult = p.qk_log2, v_mult = 1.f;
+  if (p.k_scale != nullptr) {
+    qk_mult *= p.k_scale[static_cast<int64_t>(b) * p.scale_stride + h];
+    v_mult = p.v_scale[static_cast<int64_t>(b) * p.scale_stride + h];
+  }
+  const CapPoly<FAR> poly(qk_mult, p);
+  const float ex_mult = p.cap_log2 > 0.f || p.slopes != nullptr ? 1.f : qk_mult;  // scores to log2 weights
+
+  float o[NT][KS][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int mt = 0; mt < KS; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
+
+  // K by ldmatrix: keys key_of(0-7), chunk 2 i; key_of(8-15), chunk 2 i; the same of chunk 2 i + 1
+  const int key_k = key_of<D>((lane & 7) + ((lane >> 3) & 1) * 8), ch_k = lane >> 4;
+  auto code_at = [](int key, int chunk) {  // 16-byte chunk of a row, as the TMA unit stores it
+    return key * C::ROWB + ((chunk ^ (D == 128 ? (key >> 1) & 3 : (key >> 2) & 1)) << 4);
+  };
+  // V: this lane's keys of the products' columns 2 j, 2 j + 1, 2 j + 8, 2 j + 9
+  const int kv0 = key_of<D>(2 * j), kv1 = key_of<D>(2 * j + 1);
+  constexpr int VB = D / 16;                       // code bytes of a lane per key: D / 8 d
+  const int kr = key_of<D>(r);                     // key of score rows r (and r + 8, eight further)
+
+  bool healthy = true;
+  for (int k = 0; k < ntile; ++k) {
+    const int s = k % NS;
+    const bool arrived = mbar_wait(smem_u32(full + 4 * s + warp), static_cast<uint32_t>((k / NS) & 1), p.err);
+    if (!__all_sync(kFull, arrived)) healthy = false;
+    const uint32_t kc = codes0 + s * C::STAGE, vc = kc + C::CODEB;
+    const uint32_t ksc = scales0 + s * (4 * 2 * C::SCALEB), vsc = ksc + C::SCALEB;
+    const int t_warp = rg.tile(k0 + k) * C::STEP + warp * C::KEYS;  // this warp's first key
+    if (healthy) {
+      // ---- S^T of two groups of 16 keys: rows r, r + 8 (e >= 2) are keys kr and
+      // kr + 8, columns 2 j, 2 j + 1 (odd e)
+      float sc[2][NT][4];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) sc[g][nt][0] = sc[g][nt][1] = sc[g][nt][2] = sc[g][nt][3] = 0.f;
+        // scale pairs of keys kr and kr + 8: of chunk c, the group that holds the lane's eight d
+        uint32_t s2[2][CH];
+        const uint32_t sel = j < 2 ? 0x2200u : 0x3311u;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t w[CH / 2];
+          lds_words(ksc + g * group_scales + (kr + 8 * e) * C::SROWB, w);
+#pragma unroll
+          for (int i = 0; i < CH / 2; ++i) {
+            const uint32_t d = prmt(w[i], 0u, sel);
+            s2[e][2 * i] = e4m3x2_to_f16x2(static_cast<uint16_t>(d & 0xFFFFu));
+            s2[e][2 * i + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(d >> 16));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < CH / 2; ++i) {
+          uint32_t R[4];
+          ldsm_x4(kc + g * 16 * C::ROWB + code_at(key_k, 2 * i + ch_k), R);
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            const int c = 2 * i + cc;
+            uint32_t x[4], y[4];  // of keys kr and kr + 8
+            e2m1x8_to_f16x2(R[2 * cc], x);
+            e2m1x8_to_f16x2(R[2 * cc + 1], y);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              x[q] = mul_f16x2(x[q], s2[0][c]);
+              y[q] = mul_f16x2(y[q], s2[1][c]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t a[4] = {x[2 * e], y[2 * e], x[2 * e + 1], y[2 * e + 1]};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_f16_16816(sc[g][nt], a, qb[nt][2 * c + e][0], qb[nt][2 * c + e][1]);
+            }
+          }
+        }
+      }
+      // ---- scores, masks, online softmax with a lazy maximum (it moves when it
+      // grows by more than 2^8, so that weights stay within 2^8)
+      if (p.cap_log2 > 0.f) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[g][nt][e] = capped<FAR>(sc[g][nt][e], qk_mult, p.cap_log2, poly);
+      }
+      auto key_at = [&](int g, int e) { return t_warp + 16 * g + kr + (e < 2 ? 0 : 8); };
+      if (p.slopes != nullptr) {
+        const float mult = p.cap_log2 > 0.f ? 1.f : qk_mult;
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              sc[g][nt][e] = fmaf(sc[g][nt][e], mult, slope[nt][e & 1] * static_cast<float>(key_at(g, e) - pos[nt][e & 1]));
+      }
+      bool whole = true;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          whole = whole && ((t_warp + C::KEYS - 1 <= pos[nt][e] && t_warp >= lo[nt][e]) || t_warp + C::KEYS <= pf[nt][e]);
+      if (!__all_sync(kFull, whole)) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int t = key_at(g, e), x = e & 1;
+              if (!((t <= pos[nt][x] && t >= lo[nt][x]) || t < pf[nt][x])) sc[g][nt][e] = -CUDART_INF_F;
+            }
+      }
+      float mx[NT][2];
+      bool up[NT][2], any = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][e + 2]), fmaxf(sc[1][nt][e], sc[1][nt][e + 2]));
+#pragma unroll
+          for (int sh = 4; sh < 32; sh <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, sh));
+          mx[nt][e] = x * ex_mult;
+          up[nt][e] = mx[nt][e] > m[nt][e] + 8.f;
+          any = any || up[nt][e];
+        }
+      if (__any_sync(kFull, any)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float al = up[nt][e] ? fast_exp2(m[nt][e] - mx[nt][e]) : 1.f;
+            if (up[nt][e]) m[nt][e] = mx[nt][e];
+            l[nt][e] *= al;
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt) {
+              o[nt][mt][e] *= al;
+              o[nt][mt][e + 2] *= al;
+            }
+          }
+      }
+      uint32_t pb[2][NT][2];  // P^T as the second operand
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float mu[2] = {m[nt][0] == -CUDART_INF_F ? 0.f : m[nt][0], m[nt][1] == -CUDART_INF_F ? 0.f : m[nt][1]};
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[g][nt][e] = fast_exp2(fmaf(sc[g][nt][e], ex_mult, -mu[e & 1]));
+          l[nt][0] += sc[g][nt][0] + sc[g][nt][2];
+          l[nt][1] += sc[g][nt][1] + sc[g][nt][3];
+          pb[g][nt][0] = movmatrix_trans(pack_f16x2(sc[g][nt][0], sc[g][nt][1]));
+          pb[g][nt][1] = movmatrix_trans(pack_f16x2(sc[g][nt][2], sc[g][nt][3]));
+        }
+      }
+      // ---- O^T += V^T P^T: product mt's rows r and r + 8 are d = r D / 8 + 2 mt and + 1
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int valid = sq.ctx - t_warp - 16 * g;
+        auto pair_scale = [&](int ka, int kb) {
+          const uint32_t at = vsc + g * group_scales + (D == 128 ? r : r >> 1);
+          const uint32_t sa = ka < valid ? lds_byte(at + ka * C::SROWB) : 0u;
+          const uint32_t sb = kb < valid ? lds_byte(at + kb * C::SROWB) : 0u;
+          return e4m3x2_to_f16x2(static_cast<uint16_t>(sa | (sb << 8)));
+        };
+        const uint32_t s01 = pair_scale(kv0, kv1), s23 = pair_scale(kv0 + 8, kv1 + 8);
+        uint32_t w[4][VB / 4];  // the lane's codes of its four keys
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = (i & 1 ? kv1 : kv0) + (i & 2 ? 8 : 0);
+          lds_words(vc + g * 16 * C::ROWB + code_at(key, D == 128 ? r >> 1 : r >> 2) +
+                        (D == 128 ? (r & 1) * 8 : (r & 3) * 4),
+                    w[i]);
+        }
+#pragma unroll
+        for (int q = 0; q < VB / 4; ++q) {
+          uint32_t x[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e2m1x8_to_f16x2(w[i][q], x[i]);
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            const uint32_t a[4] = {mul_f16x2(prmt(x[0][mt], x[1][mt], 0x5410u), s01),
+                                   mul_f16x2(prmt(x[0][mt], x[1][mt], 0x7632u), s01),
+                                   mul_f16x2(prmt(x[2][mt], x[3][mt], 0x5410u), s23),
+                                   mul_f16x2(prmt(x[2][mt], x[3][mt], 0x7632u), s23)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][4 * q + mt], a, pb[g][nt][0], pb[g][nt][1]);
+          }
+        }
+      }
+    }
+    __syncwarp();  // this warp has read its part of the slot: refill it
+    if (healthy && k + NS < ntile) issue(issued++);
+  }
+  if (!healthy && lane == 0) {
+    // a copy of this warp's may still be landing: one more bounded wait each
+    for (int kk = issued > NS ? issued - NS : 0; kk < issued; ++kk)
+      mbar_wait(smem_u32(full + 4 * (kk % NS) + warp), static_cast<uint32_t>((kk / NS) & 1), nullptr);
+  }
+  allow_next_grid();
+
+  // ---- row sums over the lanes that share a row; the warps' results merge through shared memory
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int sh = 4; sh < 32; sh <<= 1) l[nt][e] += __shfl_xor_sync(kFull, l[nt][e], sh);
+  __syncthreads();  // every warp is done with the stages
+  float* s_o = reinterpret_cast<float*>(smem);  // [4 warps][R][DP]
+  float* s_ml = s_o + 4 * C::R * DP;            // [4 warps][R][2]
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = 8 * nt + 2 * j + e;
+      float* to = s_o + (warp * C::R + row) * DP + r * (D / 8);
+#pragma unroll
+      for (int mt = 0; mt < KS; mt += 2)
+        *reinterpret_cast<float4*>(to + 2 * mt) =
+            make_float4(o[nt][mt][e], o[nt][mt][e + 2], o[nt][mt + 1][e], o[nt][mt + 1][e + 2]);
+      if (r == 0) {
+        s_ml[(warp * C::R + row) * 2] = m[nt][e];
+        s_ml[(warp * C::R + row) * 2 + 1] = l[nt][e];
+      }
+    }
+  __syncthreads();
+
+  for (int idx = threadIdx.x; idx < rows * (D / 2); idx += blockDim.x) {
+    const int row = idx / (D / 2), d = 2 * (idx - row * (D / 2));
+    float M = -CUDART_INF_F;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) M = fmaxf(M, s_ml[(w * C::R + row) * 2]);
+    float a0 = 0.f, a1 = 0.f, lsum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float2 ml = *reinterpret_cast<const float2*>(s_ml + (w * C::R + row) * 2);
+      const float wt = ml.x == -CUDART_INF_F ? 0.f : fast_exp2(ml.x - M);
+      const float2 v = *reinterpret_cast<const float2*>(s_o + (w * C::R + row) * DP + d);
+      a0 += wt * v.x;
+      a1 += wt * v.y;
+      lsum += wt * ml.y;
+    }
+    const int64_t orow = out_row(row);
+    if (nsplit == 1) {
+      const float inv = lsum > 0.f ? v_mult / lsum : 0.f;
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + orow * D + d) = pack_bf16x2(a0 * inv, a1 * inv);
+    } else {
+      const int64_t slot = orow * p.max_splits + split;
+      *reinterpret_cast<float2*>(p.ws_o + slot * D + d) = make_float2(a0 * v_mult, a1 * v_mult);
+      if (d == 0) {
+        p.ws_ml[slot * 2] = M;
+        p.ws_ml[slot * 2 + 1] = lsum;
+      }
+    }
+  }
+}
+
+template <int D, int NT, bool FAR>
+cudaError_t launch_t(const ChunkParams& p, const ChunkMaps& m, cudaStream_t stream) {
+  auto kern = chunk_e2m1_kernel<D, NT, FAR>;
+  constexpr int smem = E2M1Shape<D, NT>::BYTES;
+  static int configured[64] = {};
+  cudaError_t e = set_smem_once(kern, smem, configured);
+  if (e != cudaSuccess) return e;
+  const int ntq = (p.max_q_len + p.tile_q - 1) / p.tile_q;
+  return launch_pdl(kern, dim3(p.max_splits, p.num_kv_heads * ntq, p.batch), dim3(128), smem, stream, m, p);
+}
+
+template <int D>
+cudaError_t launch_d(const ChunkParams& p, const ChunkMaps& m, cudaStream_t stream) {
+  if (p.max_q_len * p.group > 8)
+    return p.cap_far ? launch_t<D, 2, true>(p, m, stream) : launch_t<D, 2, false>(p, m, stream);
+  return p.cap_far ? launch_t<D, 1, true>(p, m, stream) : launch_t<D, 1, false>(p, m, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_e2m1(const ChunkParams& p, const ChunkMaps& m, cudaStream_t stream) {
+  return p.head_dim == 128 ? launch_d<128>(p, m, stream) : launch_d<64>(p, m, stream);
+}
+
+}  // namespace pkv

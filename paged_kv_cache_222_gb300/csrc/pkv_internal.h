@@ -304,6 +304,7 @@ cudaError_t launch_multi_query_tc(const DecodeParams& p, const CUtensorMap& tmap
 // kernel (row tiles of up to 256 rows) and the merge of their split pieces.
 cudaError_t launch_chunk_small(const ChunkParams& p, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
                                cudaStream_t stream);
+cudaError_t launch_chunk_e2m1(const ChunkParams& p, const ChunkMaps& maps, cudaStream_t stream);
 cudaError_t launch_chunk_tc(const ChunkParams& p, const ChunkMaps& maps, cudaStream_t stream);
 cudaError_t launch_chunk_tc_e2m1(const ChunkParams& p, const ChunkMaps& maps, cudaStream_t stream);
 // `nk`: keys per tile of the kernel that wrote the pieces.
@@ -335,10 +336,12 @@ constexpr int kChunkMaxSplitBlocks = 1024;
 // Longest context: the end of its last key tile, and of the tile after it, are
 // still 32-bit numbers.
 constexpr int kChunkMaxContext = 0x7FFFFF00;
-// Keys per tile: of the mma.sync kernel; of the tcgen05 kernel at most, and by
+// Keys per tile: of the mma.sync kernels; of the tcgen05 kernel at most, and by
 // its variant (chunk_tc.cu: whether S(k+1) is issued ahead of P(k)'s product).
-constexpr int kChunkSmallTile = 64, kChunkTcTile = 128;
-// CTAs per SM of the mma.sync kernel, by the bytes of a 64-key step (chunk.cu).
+constexpr int kChunkSmallTile = 64, kChunkE2M1Tile = 128, kChunkTcTile = 128;
+// CTAs per SM of the mma.sync kernels, by the bytes of a 64-key step (chunk.cu),
+// and over E2M1 caches (chunk_e2m1.cu).
+constexpr int chunk_e2m1_ctas(int head_dim, bool eight_rows) { return eight_rows ? 4 : 3; }
 constexpr int chunk_small_ctas(int head_dim, bool fp8, bool eight_rows) {
   const int stage = 2 * kChunkSmallTile * head_dim * (fp8 ? 1 : 2);
   return !eight_rows || stage >= 32768 ? 3 : (stage == 16384 ? 4 : 5);

@@ -16,9 +16,10 @@
 //     its bytes, which are multiplied by the key's scale of that group, in pairs
 //     too: exact, so S is that of the cache's values.
 //   O^T += V^T P^T.  A lane needs pairs of keys at one d where the cache has
-//     pairs of d of one key: it reads the same D / 8 d of its four keys, widens
-//     and interleaves them (one byte permute per pair).  All of them lie in one
-//     group, so that a pair of keys has one pair of scales.
+//     pairs of d of one key: it reads the same D / 8 d of its four keys and swaps
+//     halves of their bytes before it widens them (a shift and a select for four
+//     pairs).  All of them lie in one group, so that a pair of keys has one pair
+//     of scales.
 // Keys take the products' rows in an order (key_of) that keeps those reads free
 // of bank conflicts.  P is rounded to f16: at most 2^-11 of each weight, next to
 // the output's own 2^-8.  V past the sequence's end has scale 0 (its codes are
@@ -334,14 +335,18 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
       // ---- O^T += V^T P^T: product mt's rows r and r + 8 are d = r D / 8 + 2 mt and + 1
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const int valid = sq.ctx - t_warp - 16 * g;
-        auto pair_scale = [&](int ka, int kb) {
-          const uint32_t at = vsc + g * group_scales + (D == 128 ? r : r >> 1);
-          const uint32_t sa = ka < valid ? lds_byte(at + ka * C::SROWB) : 0u;
-          const uint32_t sb = kb < valid ? lds_byte(at + kb * C::SROWB) : 0u;
-          return e4m3x2_to_f16x2(static_cast<uint16_t>(sa | (sb << 8)));
-        };
-        const uint32_t s01 = pair_scale(kv0, kv1), s23 = pair_scale(kv0 + 8, kv1 + 8);
+        const int valid = sq.ctx - t_warp - 16 * g;  // keys from here on are past the end
+        const uint32_t at = vsc + g * group_scales + (D == 128 ? r : r >> 1);
+        uint32_t sv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sv[i] = lds_byte(at + ((i & 1 ? kv1 : kv0) + (i & 2 ? 8 : 0)) * C::SROWB);
+        if (valid < 16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((i & 1 ? kv1 : kv0) + (i & 2 ? 8 : 0) >= valid) sv[i] = 0u;
+        }
+        const uint32_t s01 = e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(sv[0], sv[1], 0x0040u))),
+                       s23 = e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(sv[2], sv[3], 0x0040u)));
         uint32_t w[4][VB / 4];  // the lane's codes of its four keys
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -352,15 +357,18 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
         }
 #pragma unroll
         for (int q = 0; q < VB / 4; ++q) {
-          uint32_t x[4][4];
+          // bytes of a pair of keys at one d: its even d, and its odd ones
+          uint32_t x[2][2][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e2m1x8_to_f16x2(w[i][q], x[i]);
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t ka = w[2 * i][q], kb = w[2 * i + 1][q];
+            e2m1x8_to_f16x2(bit_select(0x0F0F0F0Fu, ka, kb << 4), x[i][0]);
+            e2m1x8_to_f16x2(bit_select(0x0F0F0F0Fu, ka >> 4, kb), x[i][1]);
+          }
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt) {
-            const uint32_t a[4] = {mul_f16x2(prmt(x[0][mt], x[1][mt], 0x5410u), s01),
-                                   mul_f16x2(prmt(x[0][mt], x[1][mt], 0x7632u), s01),
-                                   mul_f16x2(prmt(x[2][mt], x[3][mt], 0x5410u), s23),
-                                   mul_f16x2(prmt(x[2][mt], x[3][mt], 0x7632u), s23)};
+            const uint32_t a[4] = {mul_f16x2(x[0][0][mt], s01), mul_f16x2(x[0][1][mt], s01),
+                                   mul_f16x2(x[1][0][mt], s23), mul_f16x2(x[1][1][mt], s23)};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][4 * q + mt], a, pb[g][nt][0], pb[g][nt][1]);
           }

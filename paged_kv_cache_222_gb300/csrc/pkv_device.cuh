@@ -249,6 +249,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
+// Bits of a where the mask is set, of b elsewhere.
+__device__ __forceinline__ uint32_t bit_select(uint32_t mask, uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xCA;" : "=r"(d) : "r"(mask), "r"(a), "r"(b));
+  return d;
+}
+
 // Byte permute: picks bytes of {b:a} by the 4 selector nibbles.
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t d;

@@ -126,20 +126,22 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
   const uint32_t box_to = what < 2 ? codes0 + what * C::CODEB + bx * p.block_size * C::ROWB
                                    : scales0 + (what - 2) * C::SCALEB + bx * box_scales;
   const uint32_t stage_step = what < 2 ? C::STAGE : 4 * 2 * C::SCALEB;
-  auto issue = [&](int k) {
-    const int s = k % NS;
-    const uint32_t bar = smem_u32(full + 4 * s + warp);
+  const uint32_t bar0 = smem_u32(full) + 8 * warp;  // of stage 0; 32 bytes on to the next stage's
+  const uint32_t blk0 = smem_u32(s_blk) + 4 * (((warp * C::KEYS) >> bshift) + bx);
+  auto issue = [&](int k, int s) {  // step k into stage s
     if (lane == 0) {
       fence_proxy_async_smem();  // this warp's reads of the slot come before the copy
-      mbar_arrive_expect_tx(bar, 2 * C::KEYS * (C::ROWB + C::SROWB));
+      mbar_arrive_expect_tx(bar0 + 32 * s, 2 * C::KEYS * (C::ROWB + C::SROWB));
     }
     __syncwarp();
-    if (bx < nbox)
-      tma_load_4d(box_to + s * stage_step, tmap, bar, 0, 0, h,
-                  s_blk[k * per_tile + ((warp * C::KEYS) >> bshift) + bx]);
+    if (bx < nbox) {
+      uint32_t phys[1];
+      lds_words(blk0 + k * (4 * per_tile), phys);
+      tma_load_4d(box_to + s * stage_step, tmap, bar0 + 32 * s, 0, 0, h, static_cast<int>(phys[0]));
+    }
   };
   int issued = 0;
-  for (; issued < ntile && issued < NS; ++issued) issue(issued);
+  for (; issued < ntile && issued < NS; ++issued) issue(issued, issued);
 
   // Q as the second operand: row r of each n-tile; chunk c of 32 d is two
   // products, of the lane's d 32 c + 8 j + 0..3 and + 4..7
@@ -157,8 +159,9 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
       qb[nt][2 * c + 1][1] = pack_f16x2(bf16lo_to_f32(w.w), bf16hi_to_f32(w.w));
     }
   }
-  // this lane's rows of the tile: 8 nt + 2 j and + 1.  Per row: position (-1
-  // where it sees nothing), first key of the window, end of the prefix, bias
+  // this lane's rows of the tile: 8 nt + 2 j and + 1.  Per row: position, first
+  // key of the window, end of the prefix, bias; a row past the tile's takes no
+  // mask (nothing of it is ever written)
   constexpr float kLog2e = 1.4426950408889634f;
   int pos[NT][2], lo[NT][2], pf[NT][2];
   float slope[NT][2], m[NT][2], l[NT][2];
@@ -167,13 +170,27 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int row = 8 * nt + 2 * j + e;
-      pos[nt][e] = row < rows ? sq.ctx - sq.n + i0 + row / G : -1;
-      lo[nt][e] = p.window > 0 && pos[nt][e] >= p.window ? pos[nt][e] - p.window + 1 : 0;
+      constexpr int kFarPos = 0x7FFFFFFF;
+      pos[nt][e] = row < rows ? sq.ctx - sq.n + i0 + row / G : kFarPos;
+      lo[nt][e] = p.window > 0 && row < rows && pos[nt][e] >= p.window ? pos[nt][e] - p.window + 1 : 0;
       pf[nt][e] = pos[nt][e] >= 0 ? sq.prefix : 0;
       slope[nt][e] = p.slopes != nullptr && row < rows ? p.slopes[h * G + row % G] * kLog2e : 0.f;
       m[nt][e] = -CUDART_INF_F;
       l[nt][e] = 0.f;
     }
+  // of all rows: keys [lo_all, hi_all] and those before pf_all are seen by every one
+  int hi_all = 0x7FFFFFFF, lo_all = 0, pf_all = 0x7FFFFFFF;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      hi_all = min(hi_all, pos[nt][e]);
+      lo_all = max(lo_all, lo[nt][e]);
+      pf_all = min(pf_all, pf[nt][e]);
+    }
+  hi_all = __reduce_min_sync(kFull, hi_all);
+  lo_all = __reduce_max_sync(kFull, lo_all);
+  pf_all = __reduce_min_sync(kFull, pf_all);
   float qk_mult = p.qk_log2, v_mult = 1.f;
   if (p.k_scale != nullptr) {
     qk_mult *= p.k_scale[static_cast<int64_t>(b) * p.scale_stride + h];
@@ -191,20 +208,28 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
   // K by ldmatrix: keys key_of(0-7), chunk 2 i; key_of(8-15), chunk 2 i; the same of chunk 2 i + 1
   const int key_k = key_of<D>((lane & 7) + ((lane >> 3) & 1) * 8), ch_k = lane >> 4;
   auto code_at = [](int key, int chunk) {  // 16-byte chunk of a row, as the TMA unit stores it
-    return key * C::ROWB + ((chunk ^ (D == 128 ? (key >> 1) & 3 : (key >> 2) & 1)) << 4);
+    return static_cast<uint32_t>(key * C::ROWB + ((chunk ^ (D == 128 ? (key >> 1) & 3 : (key >> 2) & 1)) << 4));
   };
+  const uint32_t at_k = codes0 + code_at(key_k, ch_k);  // chunks 2 i + ch_k: the address with bit 5 flipped for i = 1
   // V: this lane's keys of the products' columns 2 j, 2 j + 1, 2 j + 8, 2 j + 9
+  // (the last two: 8 rows on), and its D / 8 d of them
   const int kv0 = key_of<D>(2 * j), kv1 = key_of<D>(2 * j + 1);
-  constexpr int VB = D / 16;                       // code bytes of a lane per key: D / 8 d
+  constexpr int VB = D / 16;                       // their code bytes
+  const uint32_t v_in = D == 128 ? (r & 1) * 8 : (r & 3) * 4;
+  const uint32_t at_v0 = codes0 + C::CODEB + code_at(kv0, D == 128 ? r >> 1 : r >> 2) + v_in,
+                 at_v1 = codes0 + C::CODEB + code_at(kv1, D == 128 ? r >> 1 : r >> 2) + v_in;
   const int kr = key_of<D>(r);                     // key of score rows r (and r + 8, eight further)
+  const uint32_t at_ks = scales0 + kr * C::SROWB, at_vs = scales0 + C::SCALEB + (D == 128 ? r : r >> 1);
+  const uint32_t at_vs0 = at_vs + kv0 * C::SROWB, at_vs1 = at_vs + kv1 * C::SROWB;
+  const uint32_t sel = j < 2 ? 0x2200u : 0x3311u;  // of four groups' scales those of the lane's d, each twice
 
   bool healthy = true;
+  int s = 0;
+  uint32_t parity = 0;
   for (int k = 0; k < ntile; ++k) {
-    const int s = k % NS;
-    const bool arrived = mbar_wait(smem_u32(full + 4 * s + warp), static_cast<uint32_t>((k / NS) & 1), p.err);
+    const bool arrived = mbar_wait(bar0 + 32 * s, parity, p.err);
     if (!__all_sync(kFull, arrived)) healthy = false;
-    const uint32_t kc = codes0 + s * C::STAGE, vc = kc + C::CODEB;
-    const uint32_t ksc = scales0 + s * (4 * 2 * C::SCALEB), vsc = ksc + C::SCALEB;
+    const uint32_t code_s = s * C::STAGE, scale_s = s * (4 * 2 * C::SCALEB);
     const int t_warp = rg.tile(k0 + k) * C::STEP + warp * C::KEYS;  // this warp's first key
     if (healthy) {
       // ---- S^T of two groups of 16 keys: rows r, r + 8 (e >= 2) are keys kr and
@@ -216,11 +241,10 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
         for (int nt = 0; nt < NT; ++nt) sc[g][nt][0] = sc[g][nt][1] = sc[g][nt][2] = sc[g][nt][3] = 0.f;
         // scale pairs of keys kr and kr + 8: of chunk c, the group that holds the lane's eight d
         uint32_t s2[2][CH];
-        const uint32_t sel = j < 2 ? 0x2200u : 0x3311u;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           uint32_t w[CH / 2];
-          lds_words(ksc + g * group_scales + (kr + 8 * e) * C::SROWB, w);
+          lds_words(at_ks + scale_s + g * group_scales + 8 * e * C::SROWB, w);
 #pragma unroll
           for (int i = 0; i < CH / 2; ++i) {
             const uint32_t d = prmt(w[i], 0u, sel);
@@ -231,7 +255,7 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
 #pragma unroll
         for (int i = 0; i < CH / 2; ++i) {
           uint32_t R[4];
-          ldsm_x4(kc + g * 16 * C::ROWB + code_at(key_k, 2 * i + ch_k), R);
+          ldsm_x4((at_k ^ (32 * i)) + code_s + g * 16 * C::ROWB, R);
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
             const int c = 2 * i + cc;
@@ -273,13 +297,7 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
             for (int e = 0; e < 4; ++e)
               sc[g][nt][e] = fmaf(sc[g][nt][e], mult, slope[nt][e & 1] * static_cast<float>(key_at(g, e) - pos[nt][e & 1]));
       }
-      bool whole = true;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          whole = whole && ((t_warp + C::KEYS - 1 <= pos[nt][e] && t_warp >= lo[nt][e]) || t_warp + C::KEYS <= pf[nt][e]);
-      if (!__all_sync(kFull, whole)) {
+      if (!((t_warp + C::KEYS - 1 <= hi_all && t_warp >= lo_all) || t_warp + C::KEYS <= pf_all)) {
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
@@ -290,26 +308,27 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
               if (!((t <= pos[nt][x] && t >= lo[nt][x]) || t < pf[nt][x])) sc[g][nt][e] = -CUDART_INF_F;
             }
       }
+      // (-inf: nothing seen yet, any seen key moves it)
       float mx[NT][2];
-      bool up[NT][2], any = false;
+      bool up = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][e + 2]), fmaxf(sc[1][nt][e], sc[1][nt][e + 2]));
-#pragma unroll
-          for (int sh = 4; sh < 32; sh <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, sh));
-          mx[nt][e] = x * ex_mult;
-          up[nt][e] = mx[nt][e] > m[nt][e] + 8.f;
-          any = any || up[nt][e];
+          mx[nt][e] = ex_mult * fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][e + 2]), fmaxf(sc[1][nt][e], sc[1][nt][e + 2]));
+          up = up || mx[nt][e] > m[nt][e] + 8.f;
         }
-      if (__any_sync(kFull, any)) {
+      if (__any_sync(kFull, up)) {  // rare: only then the rows' maxima are put together
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float al = up[nt][e] ? fast_exp2(m[nt][e] - mx[nt][e]) : 1.f;
-            if (up[nt][e]) m[nt][e] = mx[nt][e];
+            float x = mx[nt][e];
+#pragma unroll
+            for (int sh = 4; sh < 32; sh <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, sh));
+            const bool moves = x > m[nt][e] + 8.f;
+            const float al = moves ? fast_exp2(m[nt][e] - x) : 1.f;
+            if (moves) m[nt][e] = x;
             l[nt][e] *= al;
 #pragma unroll
             for (int mt = 0; mt < KS; ++mt) {
@@ -336,10 +355,10 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const int valid = sq.ctx - t_warp - 16 * g;  // keys from here on are past the end
-        const uint32_t at = vsc + g * group_scales + (D == 128 ? r : r >> 1);
         uint32_t sv[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sv[i] = lds_byte(at + ((i & 1 ? kv1 : kv0) + (i & 2 ? 8 : 0)) * C::SROWB);
+        for (int i = 0; i < 4; ++i)
+          sv[i] = lds_byte((i & 1 ? at_vs1 : at_vs0) + scale_s + g * group_scales + (i & 2 ? 8 * C::SROWB : 0));
         if (valid < 16) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -349,12 +368,8 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
                        s23 = e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(sv[2], sv[3], 0x0040u)));
         uint32_t w[4][VB / 4];  // the lane's codes of its four keys
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = (i & 1 ? kv1 : kv0) + (i & 2 ? 8 : 0);
-          lds_words(vc + g * 16 * C::ROWB + code_at(key, D == 128 ? r >> 1 : r >> 2) +
-                        (D == 128 ? (r & 1) * 8 : (r & 3) * 4),
-                    w[i]);
-        }
+        for (int i = 0; i < 4; ++i)
+          lds_words((i & 1 ? at_v1 : at_v0) + code_s + g * 16 * C::ROWB + (i & 2 ? 8 * C::ROWB : 0), w[i]);
 #pragma unroll
         for (int q = 0; q < VB / 4; ++q) {
           // bytes of a pair of keys at one d: its even d, and its odd ones
@@ -376,12 +391,16 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
       }
     }
     __syncwarp();  // this warp has read its part of the slot: refill it
-    if (healthy && k + NS < ntile) issue(issued++);
+    if (healthy && issued < ntile) issue(issued++, s);
+    if (++s == NS) {
+      s = 0;
+      parity ^= 1u;
+    }
   }
   if (!healthy && lane == 0) {
     // a copy of this warp's may still be landing: one more bounded wait each
     for (int kk = issued > NS ? issued - NS : 0; kk < issued; ++kk)
-      mbar_wait(smem_u32(full + 4 * (kk % NS) + warp), static_cast<uint32_t>((kk / NS) & 1), nullptr);
+      mbar_wait(bar0 + 32 * (kk % NS), static_cast<uint32_t>((kk / NS) & 1), nullptr);
   }
   allow_next_grid();
 

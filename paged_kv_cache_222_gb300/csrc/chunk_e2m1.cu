@@ -53,7 +53,8 @@ __device__ __forceinline__ int key_of(int i) {
   return D == 128 ? (i & 12) | ((i & 1) << 1) | ((i >> 1) & 1) : (i & 8) | ((i & 1) << 2) | ((i >> 1) & 3);
 }
 
-template <int D, int NT, bool FAR>
+// MODS: scores that are capped or biased.  FAR: a cap above kCapNear.
+template <int D, int NT, bool MODS, bool FAR>
 __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
     chunk_e2m1_kernel(const __grid_constant__ ChunkMaps maps, const ChunkParams p) {
   using C = E2M1Shape<D, NT>;
@@ -234,72 +235,82 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
     if (healthy) {
       // ---- S^T of two groups of 16 keys: rows r, r + 8 (e >= 2) are keys kr and
       // kr + 8, columns 2 j, 2 j + 1 (odd e)
-      float sc[2][NT][4];
+      uint32_t kw[2][CH / 2][4], ksw[2][2][CH / 2];  // codes; scale codes of keys kr and kr + 8
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
 #pragma unroll
+        for (int e = 0; e < 2; ++e) lds_words(at_ks + scale_s + g * group_scales + 8 * e * C::SROWB, ksw[g][e]);
+#pragma unroll
+        for (int i = 0; i < CH / 2; ++i) ldsm_x4((at_k ^ (32 * i)) + code_s + g * 16 * C::ROWB, kw[g][i]);
+      }
+      float sc[2][NT][4];
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
         for (int nt = 0; nt < NT; ++nt) sc[g][nt][0] = sc[g][nt][1] = sc[g][nt][2] = sc[g][nt][3] = 0.f;
-        // scale pairs of keys kr and kr + 8: of chunk c, the group that holds the lane's eight d
-        uint32_t s2[2][CH];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t w[CH / 2];
-          lds_words(at_ks + scale_s + g * group_scales + 8 * e * C::SROWB, w);
+      for (int i = 0; i < CH / 2; ++i)
 #pragma unroll
-          for (int i = 0; i < CH / 2; ++i) {
-            const uint32_t d = prmt(w[i], 0u, sel);
-            s2[e][2 * i] = e4m3x2_to_f16x2(static_cast<uint16_t>(d & 0xFFFFu));
-            s2[e][2 * i + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(d >> 16));
-          }
-        }
+        for (int cc = 0; cc < 2; ++cc) {
+          const int c = 2 * i + cc;
 #pragma unroll
-        for (int i = 0; i < CH / 2; ++i) {
-          uint32_t R[4];
-          ldsm_x4((at_k ^ (32 * i)) + code_s + g * 16 * C::ROWB, R);
-#pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            const int c = 2 * i + cc;
+          for (int g = 0; g < 2; ++g) {
             uint32_t x[4], y[4];  // of keys kr and kr + 8
-            e2m1x8_to_f16x2(R[2 * cc], x);
-            e2m1x8_to_f16x2(R[2 * cc + 1], y);
+            e2m1x8_to_f16x2(kw[g][i][2 * cc], x);
+            e2m1x8_to_f16x2(kw[g][i][2 * cc + 1], y);
+            // their scale pairs of the group that holds the lane's eight d
+            const uint32_t sx = e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(ksw[g][0][i], 0u, sel) >> (16 * cc))),
+                           sy = e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(ksw[g][1][i], 0u, sel) >> (16 * cc)));
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              x[q] = mul_f16x2(x[q], s2[0][c]);
-              y[q] = mul_f16x2(y[q], s2[1][c]);
+              x[q] = mul_f16x2(x[q], sx);
+              y[q] = mul_f16x2(y[q], sy);
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const uint32_t a[4] = {x[2 * e], y[2 * e], x[2 * e + 1], y[2 * e + 1]};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16_16816(sc[g][nt], a, qb[nt][2 * c + e][0], qb[nt][2 * c + e][1]);
+              for (int nt = 0; nt < NT; ++nt) mma_f16_pure(sc[g][nt], a, qb[nt][2 * c + e][0], qb[nt][2 * c + e][1]);
             }
           }
         }
-      }
+      // ---- V's codes and scales: the slot can be refilled under the softmax and P V
+      uint32_t vw[2][4][VB / 4], sv[2][4];  // of the lane's four keys
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          lds_words((i & 1 ? at_v1 : at_v0) + code_s + g * 16 * C::ROWB + (i & 2 ? 8 * C::ROWB : 0), vw[g][i]);
+          sv[g][i] = lds_byte((i & 1 ? at_vs1 : at_vs0) + scale_s + g * group_scales + (i & 2 ? 8 * C::SROWB : 0));
+        }
+      __syncwarp();
+      if (issued < ntile) issue(issued++, s);
       // ---- scores, masks, online softmax with a lazy maximum (it moves when it
       // grows by more than 2^8, so that weights stay within 2^8)
-      if (p.cap_log2 > 0.f) {
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[g][nt][e] = capped<FAR>(sc[g][nt][e], qk_mult, p.cap_log2, poly);
-      }
       auto key_at = [&](int g, int e) { return t_warp + 16 * g + kr + (e < 2 ? 0 : 8); };
-      if (p.slopes != nullptr) {
-        const float mult = p.cap_log2 > 0.f ? 1.f : qk_mult;
+      if constexpr (MODS) {
+        if (p.cap_log2 > 0.f) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+          for (int g = 0; g < 2; ++g)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              sc[g][nt][e] = fmaf(sc[g][nt][e], mult, slope[nt][e & 1] * static_cast<float>(key_at(g, e) - pos[nt][e & 1]));
+              for (int e = 0; e < 4; ++e) sc[g][nt][e] = capped<FAR>(sc[g][nt][e], qk_mult, p.cap_log2, poly);
+        }
+        if (p.slopes != nullptr) {
+          const float mult = p.cap_log2 > 0.f ? 1.f : qk_mult;
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                sc[g][nt][e] = fmaf(sc[g][nt][e], mult, slope[nt][e & 1] * static_cast<float>(key_at(g, e) - pos[nt][e & 1]));
+        }
       }
       if (!((t_warp + C::KEYS - 1 <= hi_all && t_warp >= lo_all) || t_warp + C::KEYS <= pf_all)) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+        for (int g = 0; g < 2; ++g) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -307,6 +318,11 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
               const int t = key_at(g, e), x = e & 1;
               if (!((t <= pos[nt][x] && t >= lo[nt][x]) || t < pf[nt][x])) sc[g][nt][e] = -CUDART_INF_F;
             }
+          // (a key past the sequence's end is seen by no row, so that this is reached)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (t_warp + 16 * g + (i & 1 ? kv1 : kv0) + (i & 2 ? 8 : 0) >= sq.ctx) sv[g][i] = 0u;
+        }
       }
       // (-inf: nothing seen yet, any seen key moves it)
       float mx[NT][2];
@@ -354,29 +370,15 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
       // ---- O^T += V^T P^T: product mt's rows r and r + 8 are d = r D / 8 + 2 mt and + 1
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const int valid = sq.ctx - t_warp - 16 * g;  // keys from here on are past the end
-        uint32_t sv[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          sv[i] = lds_byte((i & 1 ? at_vs1 : at_vs0) + scale_s + g * group_scales + (i & 2 ? 8 * C::SROWB : 0));
-        if (valid < 16) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if ((i & 1 ? kv1 : kv0) + (i & 2 ? 8 : 0) >= valid) sv[i] = 0u;
-        }
-        const uint32_t s01 = e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(sv[0], sv[1], 0x0040u))),
-                       s23 = e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(sv[2], sv[3], 0x0040u)));
-        uint32_t w[4][VB / 4];  // the lane's codes of its four keys
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          lds_words((i & 1 ? at_v1 : at_v0) + code_s + g * 16 * C::ROWB + (i & 2 ? 8 * C::ROWB : 0), w[i]);
+        const uint32_t s01 = e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(sv[g][0], sv[g][1], 0x0040u))),
+                       s23 = e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(sv[g][2], sv[g][3], 0x0040u)));
 #pragma unroll
         for (int q = 0; q < VB / 4; ++q) {
           // bytes of a pair of keys at one d: its even d, and its odd ones
           uint32_t x[2][2][4];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t ka = w[2 * i][q], kb = w[2 * i + 1][q];
+            const uint32_t ka = vw[g][2 * i][q], kb = vw[g][2 * i + 1][q];
             e2m1x8_to_f16x2(bit_select(0x0F0F0F0Fu, ka, kb << 4), x[i][0]);
             e2m1x8_to_f16x2(bit_select(0x0F0F0F0Fu, ka >> 4, kb), x[i][1]);
           }
@@ -385,13 +387,11 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
             const uint32_t a[4] = {mul_f16x2(x[0][0][mt], s01), mul_f16x2(x[0][1][mt], s01),
                                    mul_f16x2(x[1][0][mt], s23), mul_f16x2(x[1][1][mt], s23)};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][4 * q + mt], a, pb[g][nt][0], pb[g][nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_f16_pure(o[nt][4 * q + mt], a, pb[g][nt][0], pb[g][nt][1]);
           }
         }
       }
     }
-    __syncwarp();  // this warp has read its part of the slot: refill it
-    if (healthy && issued < ntile) issue(issued++, s);
     if (++s == NS) {
       s = 0;
       parity ^= 1u;
@@ -461,9 +461,9 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
   }
 }
 
-template <int D, int NT, bool FAR>
+template <int D, int NT, bool MODS, bool FAR>
 cudaError_t launch_t(const ChunkParams& p, const ChunkMaps& m, cudaStream_t stream) {
-  auto kern = chunk_e2m1_kernel<D, NT, FAR>;
+  auto kern = chunk_e2m1_kernel<D, NT, MODS, FAR>;
   constexpr int smem = E2M1Shape<D, NT>::BYTES;
   static int configured[64] = {};
   cudaError_t e = set_smem_once(kern, smem, configured);
@@ -472,11 +472,16 @@ cudaError_t launch_t(const ChunkParams& p, const ChunkMaps& m, cudaStream_t stre
   return launch_pdl(kern, dim3(p.max_splits, p.num_kv_heads * ntq, p.batch), dim3(128), smem, stream, m, p);
 }
 
+template <int D, int NT>
+cudaError_t launch_n(const ChunkParams& p, const ChunkMaps& m, cudaStream_t stream) {
+  if (p.cap_far) return launch_t<D, NT, true, true>(p, m, stream);
+  return p.cap_log2 > 0.f || p.slopes != nullptr ? launch_t<D, NT, true, false>(p, m, stream)
+                                                 : launch_t<D, NT, false, false>(p, m, stream);
+}
+
 template <int D>
 cudaError_t launch_d(const ChunkParams& p, const ChunkMaps& m, cudaStream_t stream) {
-  if (p.max_q_len * p.group > 8)
-    return p.cap_far ? launch_t<D, 2, true>(p, m, stream) : launch_t<D, 2, false>(p, m, stream);
-  return p.cap_far ? launch_t<D, 1, true>(p, m, stream) : launch_t<D, 1, false>(p, m, stream);
+  return p.max_q_len * p.group > 8 ? launch_n<D, 2>(p, m, stream) : launch_n<D, 1>(p, m, stream);
 }
 
 }  // namespace

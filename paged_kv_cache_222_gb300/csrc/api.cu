@@ -1509,12 +1509,12 @@ extern "C" pkv_status pkv_chunk_attention(
   const bool small = pl.workers == 1, e2m1 = c.dtype == PKV_E2M1;
   pkv::ChunkMaps maps = {};
   if (!small) s = make_query_tmap(&maps.q, q, c, n_tokens, group, chunk_tile_q(max_q_len, group));
-  if (s == PKV_OK && e2m1) {
+  if (s == PKV_OK && e2m1 && !small) {
     s = make_e2m1_tmap(&maps.k, k_cache, c, c.block_size, false);
     if (s == PKV_OK) s = make_e2m1_tmap(&maps.v, v_cache, c, c.block_size, false);
     if (s == PKV_OK) s = make_e2m1_tmap(&maps.k_scales, k_cache, c, c.block_size, true);
     if (s == PKV_OK) s = make_e2m1_tmap(&maps.v_scales, v_cache, c, c.block_size, true);
-  } else if (s == PKV_OK) {
+  } else if (s == PKV_OK && !e2m1) {
     const int box = small ? pkv::kTileTokens : c.block_size;  // token rows per TMA box
     s = make_cache_tmap(&maps.k, k_cache, c, box);
     if (s == PKV_OK) s = make_cache_tmap(&maps.v, v_cache, c, box);
@@ -1522,6 +1522,8 @@ extern "C" pkv_status pkv_chunk_attention(
   if (s != PKV_OK) return s;
   pkv::ChunkParams p = {};
   p.q = q;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
   p.out = out;
   p.q_starts = q_starts;
   p.block_tables = block_tables;
@@ -1560,7 +1562,7 @@ extern "C" pkv_status pkv_chunk_attention(
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = traced(pkv::kKindChunk, cs, [&] {
     if (!small) return pkv::launch_chunk_tc(p, maps, cs);
-    return e2m1 ? pkv::launch_chunk_e2m1(p, maps, cs) : pkv::launch_chunk_small(p, maps.k, maps.v, cs);
+    return e2m1 ? pkv::launch_chunk_e2m1(p, cs) : pkv::launch_chunk_small(p, maps.k, maps.v, cs);
   });
   if (e == cudaSuccess && pl.max_splits > 1)
     e = traced(pkv::kKindCombine, cs, [&] {

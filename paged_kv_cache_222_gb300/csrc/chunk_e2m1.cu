@@ -3,15 +3,16 @@
 // what it computes: chunk_common.cuh, what a cache holds: pkv.h.
 //
 // A CTA takes the rows of one tile of one (sequence, KV head) over one split of
-// its visible keys, in 128-key steps: warp w loads keys 32w..32w+31 of every
-// step by TMA (a box of codes and a box of scales per block, of K and of V) into
-// a ring of its own on barriers of its own, and refills a slot as soon as it has
-// read it; the warps merge (m, l, O) through shared memory at the end.
+// its visible keys, in 128-key steps: a warp loads its 32 or 64 keys of every step
+// (one bulk copy per block, of K and of V: a block's codes and scales lie behind
+// one another) into a ring of its own on barriers of its own, and refills a slot
+// as soon as it has read it; the warps merge (m, l, O) through shared memory at
+// the end.
 //
 // Both products have keys as the first operand's rows or columns and up to 8
 // tile rows as the second's columns (NT of them: 1 or 2), mma.sync m16n8k16 of
 // f16 with fp32 sums, so that the codes, widened once, serve every row:
-//   S^T = K Q^T.  A lane's word of an ldmatrix row is 8 codes of one key: two
+//   S^T = K Q^T.  A lane reads a quarter of a key's row, 8 codes a word, two
 //     products' worth, whose order of d is Q's to follow.  cvt makes f16 pairs of
 //     its bytes, which are multiplied by the key's scale of that group, in pairs
 //     too: exact, so S is that of the cache's values.
@@ -20,45 +21,61 @@
 //     halves of their bytes before it widens them (a shift and a select for four
 //     pairs).  All of them lie in one group, so that a pair of keys has one pair
 //     of scales.
-// Keys take the products' rows in an order (key_of) that keeps those reads free
-// of bank conflicts.  P is rounded to f16: at most 2^-11 of each weight, next to
-// the output's own 2^-8.  V past the sequence's end has scale 0 (its codes are
-// finite whatever they are).
+// Keys take the products' rows in an order (key_of) that spreads those reads over
+// the banks.  P is rounded to f16: at most 2^-11 of each weight, next to the
+// output's own 2^-8.  V past the sequence's end, and K and V of blocks that no
+// row sees, have scale 0 (codes are finite whatever they are).
 
 #include "chunk_common.cuh"
 
 namespace pkv {
 namespace {
 
-template <int D, int NT>
+template <int D, int NT, int BS>
 struct E2M1Shape {
-  static constexpr int STEP = kChunkE2M1Tile, KEYS = STEP / 4;  // keys of a step, and of a warp
-  static constexpr int ROWB = D / 2, SROWB = D / 16;      // bytes of a row's codes and scales
-  static constexpr int CODEB = KEYS * ROWB;               // codes of K (or V) of a warp's step
-  static constexpr int SCALEB = 256;                      // its scales: boxes of 64 bytes or more, 128 apart
+  static constexpr int STEP = kChunkE2M1Tile;               // keys of a step,
+  static constexpr int KEYS = chunk_e2m1_keys(D, NT == 1);  // and of a warp
+  static constexpr int WARPS = STEP / KEYS, THREADS = 32 * WARPS, NG = KEYS / 16;
+  static constexpr int ROWB = D / 2, SROWB = D / 16;        // bytes of a row's codes and scales
+  static constexpr int TILE = BS * (ROWB + SROWB);          // of a block: its rows of codes, then of scales
+  static constexpr int NBLK = KEYS / BS;                    // blocks of a warp's step
+  static constexpr int STAGE = 2 * NBLK * TILE;             // a warp's step: K, then V
   static constexpr int CTAS = chunk_e2m1_ctas(D, NT == 1);
-  static constexpr int NS = D == 128 ? 2 : 4;
-  static constexpr int STAGE = 4 * 2 * CODEB;
+  static constexpr int NS = 2;
   static constexpr int DP = D + 4, R = 8 * NT;
-  static constexpr int MERGE = 4 * R * DP * 4 + 4 * R * 2 * 4;
-  static constexpr int RING = NS * (STAGE + 4 * 2 * SCALEB);
-  static constexpr int BYTES = (RING > MERGE ? RING : MERGE) + 4 * NS * 8 + kChunkMaxSplitBlocks * 4 + 1024;
+  static constexpr int MERGE = WARPS * R * DP * 4 + WARPS * R * 2 * 4;
+  static constexpr int RING = NS * WARPS * STAGE;
+  static constexpr int BYTES = (RING > MERGE ? RING : MERGE) + WARPS * NS * 8 +
+                               kChunkMaxSplitBlocks * 4 + 128;
+  // codes and scales of a group of 16 keys, from K's or V's start in a stage
+  static constexpr int code_of(int g) { return 16 * g / BS * TILE + 16 * g % BS * ROWB; }
+  static constexpr int scale_of(int g) { return 16 * g / BS * TILE + BS * ROWB + 16 * g % BS * SROWB; }
 };
 
-// Key of a 16-key group that is row i of the products.  128-wide heads: rows
-// 2 j and 2 j + 1 are keys {0, 1, 4, 5}[j] and {2, 3, 6, 7}[j], 64-wide ones: j
-// and j + 4.
+// Key of a 16-key group that is row i = 8 n + 4 j1 + 2 j0 + e of the products: the
+// eight lanes that read 128 bytes of K together, and the lanes that read the same
+// d of V, then have keys in different halves (64-byte rows) or quarters (32-byte
+// rows) of 128 bytes.
 template <int D>
 __device__ __forceinline__ int key_of(int i) {
-  return D == 128 ? (i & 12) | ((i & 1) << 1) | ((i >> 1) & 1) : (i & 8) | ((i & 1) << 2) | ((i >> 1) & 3);
+  return (i & 14) | ((i & 1) ^ (D == 128 ? (i >> 1) & 1 : (i >> 2) & 1));
+}
+
+// Bulk copy global -> shared of `bytes` (a multiple of 16; both addresses 16-byte
+// aligned), completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
 }
 
 // MODS: scores that are capped or biased.  FAR: a cap above kCapNear.
-template <int D, int NT, bool MODS, bool FAR>
-__global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
-    chunk_e2m1_kernel(const __grid_constant__ ChunkMaps maps, const ChunkParams p) {
-  using C = E2M1Shape<D, NT>;
-  constexpr int NS = C::NS, DP = C::DP, KS = D / 16, CH = D / 32;
+template <int D, int NT, int BS, bool MODS, bool FAR>
+__global__ void __launch_bounds__(E2M1Shape<D, NT, BS>::THREADS, E2M1Shape<D, NT, BS>::CTAS)
+    chunk_e2m1_kernel(const ChunkParams p) {
+  using C = E2M1Shape<D, NT, BS>;
+  constexpr int NS = C::NS, DP = C::DP, KS = D / 16, NG = C::NG, WARPS = C::WARPS;
+  constexpr int KW = D / 32;  // words of codes that a lane takes of a key of K
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, j = lane & 3;
@@ -70,20 +87,14 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + (C::RING > C::MERGE ? C::RING : C::MERGE));  // [NS][4]
-  int* s_blk = reinterpret_cast<int*>(full + 4 * NS);
-  // stage s of this warp: codes of K and of V, scales of K and of V
-  const uint32_t codes0 = smem_u32(smem) + warp * 2 * C::CODEB;
-  const uint32_t scales0 = smem_u32(smem) + NS * C::STAGE + warp * 2 * C::SCALEB;
+      (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + (C::RING > C::MERGE ? C::RING : C::MERGE));  // [NS][WARPS]
+  int* s_blk = reinterpret_cast<int*>(full + WARPS * NS);
+  const uint32_t stage0 = smem_u32(smem) + warp * NS * C::STAGE;  // of this warp's ring
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 4 * NS; ++s) mbar_init(smem_u32(full + s), 1);
+    for (int s = 0; s < WARPS * NS; ++s) mbar_init(smem_u32(full + s), 1);
     fence_mbar_init();
-    prefetch_tmap(&maps.k);
-    prefetch_tmap(&maps.v);
-    prefetch_tmap(&maps.k_scales);
-    prefetch_tmap(&maps.v_scales);
   }
   wait_prior_grid();
 
@@ -100,14 +111,13 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
 
   // block ids of the split's keys; blocks that no row sees (behind the window,
   // past the last query) are not looked up and read as zeros
-  const int bshift = p.block_size == 16 ? 4 : 5;
-  const int per_tile = C::STEP >> bshift;
+  constexpr int per_tile = C::STEP / BS;
   const int32_t* tbl = p.block_tables + static_cast<int64_t>(b) * p.max_blocks;
   for (int i = threadIdx.x; i < ntile * per_tile; i += blockDim.x) {
-    const int t0 = rg.tile(k0 + i / per_tile) * C::STEP + (i % per_tile) * p.block_size;
-    int phys = -1;  // outside the tensor map: the TMA unit fills zeros
-    if (rg.sees(t0, t0 + p.block_size)) {
-      phys = tbl[t0 >> bshift];
+    const int t0 = rg.tile(k0 + i / per_tile) * C::STEP + (i % per_tile) * BS;
+    int phys = -1;
+    if (rg.sees(t0, t0 + BS)) {
+      phys = tbl[t0 / BS];
       if (phys < 0 || phys >= p.num_blocks) {
         record_error(p.err, kDevErrBlockId);
         phys = -1;
@@ -117,43 +127,46 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
   }
   __syncthreads();
 
-  // a warp's 32 keys are one or two blocks: lane 4 bx + w loads block bx of codes
-  // of K, of V, scales of K, of V
-  const int nbox = C::KEYS >> bshift;
-  const int box_scales = p.block_size * C::SROWB < 128 ? 128 : p.block_size * C::SROWB;
-  const int group_scales = bshift == 4 ? box_scales : 16 * C::SROWB;  // from a 16-key group's scales to the next's
-  const int what = lane & 3, bx = lane >> 2;
-  const CUtensorMap* tmap = what == 0 ? &maps.k : (what == 1 ? &maps.v : (what == 2 ? &maps.k_scales : &maps.v_scales));
-  const uint32_t box_to = what < 2 ? codes0 + what * C::CODEB + bx * p.block_size * C::ROWB
-                                   : scales0 + (what - 2) * C::SCALEB + bx * box_scales;
-  const uint32_t stage_step = what < 2 ? C::STAGE : 4 * 2 * C::SCALEB;
-  const uint32_t bar0 = smem_u32(full) + 8 * warp;  // of stage 0; 32 bytes on to the next stage's
-  const uint32_t blk0 = smem_u32(s_blk) + 4 * (((warp * C::KEYS) >> bshift) + bx);
-  auto issue = [&](int k, int s) {  // step k into stage s
+  // a warp's keys are one to four blocks: lane 2 bx + v loads block bx of K or V
+  constexpr uint32_t BAR = 8 * WARPS;                  // from a stage's barrier to the next's
+  const uint32_t bar0 = smem_u32(full) + 8 * warp;     // of stage 0
+  const int v = lane & 1, bx = lane >> 1;
+  const uint32_t box_to = stage0 + (v * C::NBLK + bx) * C::TILE;
+  const uint32_t blk0 = smem_u32(s_blk) + 4 * (warp * C::NBLK + bx);
+  const uint8_t* cache = static_cast<const uint8_t*>(v ? p.v_cache : p.k_cache) + static_cast<int64_t>(h) * C::TILE;
+  const int64_t block_bytes = static_cast<int64_t>(p.num_kv_heads) * C::TILE;
+  auto issue = [&](int k, int s) {  // step k into stage s, which this warp has read
+    uint32_t phys[1] = {0u};
+    if (bx < C::NBLK) lds_words(blk0 + k * (4 * per_tile), phys);
+    const bool there = bx < C::NBLK && static_cast<int>(phys[0]) >= 0;
+    const uint32_t bytes = __popc(__ballot_sync(kFull, there)) * C::TILE;
     if (lane == 0) {
-      fence_proxy_async_smem();  // this warp's reads of the slot come before the copy
-      mbar_arrive_expect_tx(bar0 + 32 * s, 2 * C::KEYS * (C::ROWB + C::SROWB));
+      fence_proxy_async_smem();  // this warp's reads of the slot come before the copies
+      mbar_arrive_expect_tx(bar0 + BAR * s, bytes);
     }
     __syncwarp();
-    if (bx < nbox) {
-      uint32_t phys[1];
-      lds_words(blk0 + k * (4 * per_tile), phys);
-      tma_load_4d(box_to + s * stage_step, tmap, bar0 + 32 * s, 0, 0, h, static_cast<int>(phys[0]));
+    const uint32_t to = box_to + s * C::STAGE;
+    if (there) {
+      bulk_load(to, cache + static_cast<int64_t>(phys[0]) * block_bytes, C::TILE, bar0 + BAR * s);
+    } else if (bx < C::NBLK) {  // no row sees the block: zeros
+      for (int i = 0; i < BS * C::SROWB; i += 16)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to + BS * C::ROWB + i), "r"(0u) : "memory");
     }
+    __syncwarp();
   };
   int issued = 0;
   for (; issued < ntile && issued < NS; ++issued) issue(issued, issued);
 
-  // Q as the second operand: row r of each n-tile; chunk c of 32 d is two
-  // products, of the lane's d 32 c + 8 j + 0..3 and + 4..7
+  // Q as the second operand: row r of each n-tile; word c of the lane's quarter of
+  // a row is two products, of d j D / 4 + 8 c + 0..3 and + 4..7
   uint32_t qb[NT][KS][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int row = 8 * nt + r;
-    const uint16_t* q = static_cast<const uint16_t*>(p.q) + out_row(row) * D;
+    const uint16_t* q = static_cast<const uint16_t*>(p.q) + out_row(row) * D + j * (D / 4);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const uint4 w = row < rows ? *reinterpret_cast<const uint4*>(q + 32 * c + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
+    for (int c = 0; c < KW; ++c) {
+      const uint4 w = row < rows ? *reinterpret_cast<const uint4*>(q + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
       qb[nt][2 * c][0] = pack_f16x2(bf16lo_to_f32(w.x), bf16hi_to_f32(w.x));
       qb[nt][2 * c][1] = pack_f16x2(bf16lo_to_f32(w.y), bf16hi_to_f32(w.y));
       qb[nt][2 * c + 1][0] = pack_f16x2(bf16lo_to_f32(w.z), bf16hi_to_f32(w.z));
@@ -206,92 +219,96 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
 #pragma unroll
     for (int mt = 0; mt < KS; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
 
-  // K by ldmatrix: keys key_of(0-7), chunk 2 i; key_of(8-15), chunk 2 i; the same of chunk 2 i + 1
-  const int key_k = key_of<D>((lane & 7) + ((lane >> 3) & 1) * 8), ch_k = lane >> 4;
-  auto code_at = [](int key, int chunk) {  // 16-byte chunk of a row, as the TMA unit stores it
-    return static_cast<uint32_t>(key * C::ROWB + ((chunk ^ (D == 128 ? (key >> 1) & 3 : (key >> 2) & 1)) << 4));
-  };
-  const uint32_t at_k = codes0 + code_at(key_k, ch_k);  // chunks 2 i + ch_k: the address with bit 5 flipped for i = 1
-  // V: this lane's keys of the products' columns 2 j, 2 j + 1, 2 j + 8, 2 j + 9
-  // (the last two: 8 rows on), and its D / 8 d of them
-  const int kv0 = key_of<D>(2 * j), kv1 = key_of<D>(2 * j + 1);
-  constexpr int VB = D / 16;                       // their code bytes
-  const uint32_t v_in = D == 128 ? (r & 1) * 8 : (r & 3) * 4;
-  const uint32_t at_v0 = codes0 + C::CODEB + code_at(kv0, D == 128 ? r >> 1 : r >> 2) + v_in,
-                 at_v1 = codes0 + C::CODEB + code_at(kv1, D == 128 ? r >> 1 : r >> 2) + v_in;
-  const int kr = key_of<D>(r);                     // key of score rows r (and r + 8, eight further)
-  const uint32_t at_ks = scales0 + kr * C::SROWB, at_vs = scales0 + C::SCALEB + (D == 128 ? r : r >> 1);
-  const uint32_t at_vs0 = at_vs + kv0 * C::SROWB, at_vs1 = at_vs + kv1 * C::SROWB;
-  const uint32_t sel = j < 2 ? 0x2200u : 0x3311u;  // of four groups' scales those of the lane's d, each twice
+  // K: key of score rows r (and r + 8, eight further); V: keys of the products'
+  // columns 2 j, 2 j + 1 (and 2 j + 8, 2 j + 9), the lane's D / 8 d of them
+  const int kr = key_of<D>(r), kv0 = key_of<D>(2 * j), kv1 = key_of<D>(2 * j + 1);
+  constexpr int VB = D / 16, GL = D / 64;  // code bytes of a lane per key of V; groups of its quarter of K
+  constexpr int VAT = C::NBLK * C::TILE;   // V behind K
+  const uint32_t at_k = stage0 + kr * C::ROWB + j * (4 * KW), at_ks = stage0 + kr * C::SROWB + j * GL;
+  const uint32_t at_v0 = stage0 + VAT + kv0 * C::ROWB + r * VB, at_v1 = stage0 + VAT + kv1 * C::ROWB + r * VB;
+  const uint32_t at_vs0 = stage0 + VAT + kv0 * C::SROWB + r * VB / 8, at_vs1 = stage0 + VAT + kv1 * C::SROWB + r * VB / 8;
 
   bool healthy = true;
   int s = 0;
   uint32_t parity = 0;
   for (int k = 0; k < ntile; ++k) {
-    const bool arrived = mbar_wait(bar0 + 32 * s, parity, p.err);
+    const bool arrived = mbar_wait(bar0 + BAR * s, parity, p.err);
     if (!__all_sync(kFull, arrived)) healthy = false;
-    const uint32_t code_s = s * C::STAGE, scale_s = s * (4 * 2 * C::SCALEB);
+    const uint32_t stage = s * C::STAGE;
     const int t_warp = rg.tile(k0 + k) * C::STEP + warp * C::KEYS;  // this warp's first key
     if (healthy) {
-      // ---- S^T of two groups of 16 keys: rows r, r + 8 (e >= 2) are keys kr and
-      // kr + 8, columns 2 j, 2 j + 1 (odd e)
-      uint32_t kw[2][CH / 2][4], ksw[2][2][CH / 2];  // codes; scale codes of keys kr and kr + 8
+      // ---- S^T of groups of 16 keys, two at a time: rows r, r + 8 (e >= 2) are keys
+      // kr and kr + 8, columns 2 j, 2 j + 1 (odd e)
+      float sc[NG][NT][4];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) lds_words(at_ks + scale_s + g * group_scales + 8 * e * C::SROWB, ksw[g][e]);
-#pragma unroll
-        for (int i = 0; i < CH / 2; ++i) ldsm_x4((at_k ^ (32 * i)) + code_s + g * 16 * C::ROWB, kw[g][i]);
-      }
-      float sc[2][NT][4];
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
+      for (int g = 0; g < NG; ++g)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) sc[g][nt][0] = sc[g][nt][1] = sc[g][nt][2] = sc[g][nt][3] = 0.f;
 #pragma unroll
-      for (int i = 0; i < CH / 2; ++i)
+      for (int g0 = 0; g0 < NG; g0 += 2) {
+        uint32_t kw[2][2][KW], ks[2][2];  // codes and scale codes of keys kr and kr + 8
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          const int c = 2 * i + cc;
+        for (int g = 0; g < 2; ++g)
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            uint32_t x[4], y[4];  // of keys kr and kr + 8
-            e2m1x8_to_f16x2(kw[g][i][2 * cc], x);
-            e2m1x8_to_f16x2(kw[g][i][2 * cc + 1], y);
-            // their scale pairs of the group that holds the lane's eight d
-            const uint32_t sx = e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(ksw[g][0][i], 0u, sel) >> (16 * cc))),
-                           sy = e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(ksw[g][1][i], 0u, sel) >> (16 * cc)));
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              x[q] = mul_f16x2(x[q], sx);
-              y[q] = mul_f16x2(y[q], sy);
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t a[4] = {x[2 * e], y[2 * e], x[2 * e + 1], y[2 * e + 1]};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16_pure(sc[g][nt], a, qb[nt][2 * c + e][0], qb[nt][2 * c + e][1]);
-            }
+          for (int x = 0; x < 2; ++x) {
+            lds_words(at_k + stage + C::code_of(g0 + g) + 8 * x * C::ROWB, kw[g][x]);
+            const uint32_t at = at_ks + stage + C::scale_of(g0 + g) + 8 * x * C::SROWB;
+            ks[g][x] = GL == 2 ? lds_half(at) : lds_byte(at);
           }
+#pragma unroll
+        for (int gl = 0; gl < GL; ++gl) {  // words 2 gl and 2 gl + 1 lie in one group
+          uint32_t s2[2][2];
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              s2[g][x] = e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(ks[g][x], 0u, gl == 0 ? 0x4400u : 0x4411u)));
+#pragma unroll
+          for (int c = 2 * gl; c < 2 * gl + 2; ++c)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              uint32_t x[4], y[4];  // of keys kr and kr + 8
+              e2m1x8_to_f16x2(kw[g][0][c], x);
+              e2m1x8_to_f16x2(kw[g][1][c], y);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                x[q] = mul_f16x2(x[q], s2[g][0]);
+                y[q] = mul_f16x2(y[q], s2[g][1]);
+              }
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t a[4] = {x[2 * e], y[2 * e], x[2 * e + 1], y[2 * e + 1]};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_f16_pure(sc[g0 + g][nt], a, qb[nt][2 * c + e][0], qb[nt][2 * c + e][1]);
+              }
+            }
         }
-      // ---- V's codes and scales: the slot can be refilled under the softmax and P V
+      }
+      // ---- V's codes and scales of the first two groups (with no more of them the
+      // slot can be refilled under the softmax and P V)
       uint32_t vw[2][4][VB / 4], sv[2][4];  // of the lane's four keys
+      auto load_v = [&](int g0) {
 #pragma unroll
-      for (int g = 0; g < 2; ++g)
+        for (int g = 0; g < 2; ++g)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          lds_words((i & 1 ? at_v1 : at_v0) + code_s + g * 16 * C::ROWB + (i & 2 ? 8 * C::ROWB : 0), vw[g][i]);
-          sv[g][i] = lds_byte((i & 1 ? at_vs1 : at_vs0) + scale_s + g * group_scales + (i & 2 ? 8 * C::SROWB : 0));
+          for (int i = 0; i < 4; ++i) {
+            lds_words((i & 1 ? at_v1 : at_v0) + stage + C::code_of(g0 + g) + (i & 2 ? 8 * C::ROWB : 0), vw[g][i]);
+            sv[g][i] = lds_byte((i & 1 ? at_vs1 : at_vs0) + stage + C::scale_of(g0 + g) + (i & 2 ? 8 * C::SROWB : 0));
+          }
+        if (g0 + 2 == NG) {
+          __syncwarp();
+          if (issued < ntile) issue(issued++, s);
         }
-      __syncwarp();
-      if (issued < ntile) issue(issued++, s);
+      };
+      load_v(0);
       // ---- scores, masks, online softmax with a lazy maximum (it moves when it
       // grows by more than 2^8, so that weights stay within 2^8)
       auto key_at = [&](int g, int e) { return t_warp + 16 * g + kr + (e < 2 ? 0 : 8); };
       if constexpr (MODS) {
         if (p.cap_log2 > 0.f) {
 #pragma unroll
-          for (int g = 0; g < 2; ++g)
+          for (int g = 0; g < NG; ++g)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -300,7 +317,7 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
         if (p.slopes != nullptr) {
           const float mult = p.cap_log2 > 0.f ? 1.f : qk_mult;
 #pragma unroll
-          for (int g = 0; g < 2; ++g)
+          for (int g = 0; g < NG; ++g)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -308,9 +325,10 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
                 sc[g][nt][e] = fmaf(sc[g][nt][e], mult, slope[nt][e & 1] * static_cast<float>(key_at(g, e) - pos[nt][e & 1]));
         }
       }
-      if (!((t_warp + C::KEYS - 1 <= hi_all && t_warp >= lo_all) || t_warp + C::KEYS <= pf_all)) {
+      const bool whole = (t_warp + C::KEYS - 1 <= hi_all && t_warp >= lo_all) || t_warp + C::KEYS <= pf_all;
+      if (!whole) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < NG; ++g) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -318,10 +336,6 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
               const int t = key_at(g, e), x = e & 1;
               if (!((t <= pos[nt][x] && t >= lo[nt][x]) || t < pf[nt][x])) sc[g][nt][e] = -CUDART_INF_F;
             }
-          // (a key past the sequence's end is seen by no row, so that this is reached)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (t_warp + 16 * g + (i & 1 ? kv1 : kv0) + (i & 2 ? 8 : 0) >= sq.ctx) sv[g][i] = 0u;
         }
       }
       // (-inf: nothing seen yet, any seen key moves it)
@@ -331,7 +345,10 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mx[nt][e] = ex_mult * fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][e + 2]), fmaxf(sc[1][nt][e], sc[1][nt][e + 2]));
+          float x = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
+#pragma unroll
+          for (int g = 1; g < NG; ++g) x = fmaxf(x, fmaxf(sc[g][nt][e], sc[g][nt][e + 2]));
+          mx[nt][e] = ex_mult * x;
           up = up || mx[nt][e] > m[nt][e] + 8.f;
         }
       if (__any_sync(kFull, up)) {  // rare: only then the rows' maxima are put together
@@ -353,12 +370,12 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
             }
           }
       }
-      uint32_t pb[2][NT][2];  // P^T as the second operand
+      uint32_t pb[NG][NT][2];  // P^T as the second operand
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float mu[2] = {m[nt][0] == -CUDART_INF_F ? 0.f : m[nt][0], m[nt][1] == -CUDART_INF_F ? 0.f : m[nt][1]};
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < NG; ++g) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[g][nt][e] = fast_exp2(fmaf(sc[g][nt][e], ex_mult, -mu[e & 1]));
           l[nt][0] += sc[g][nt][0] + sc[g][nt][2];
@@ -369,25 +386,37 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
       }
       // ---- O^T += V^T P^T: product mt's rows r and r + 8 are d = r D / 8 + 2 mt and + 1
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const uint32_t s01 = e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(sv[g][0], sv[g][1], 0x0040u))),
-                       s23 = e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(sv[g][2], sv[g][3], 0x0040u)));
+      for (int g0 = 0; g0 < NG; g0 += 2) {
+        if (g0 > 0) load_v(g0);
+        if (!whole) {  // keys past the sequence's end (a row that sees them all there is none): zeros
 #pragma unroll
-        for (int q = 0; q < VB / 4; ++q) {
-          // bytes of a pair of keys at one d: its even d, and its odd ones
-          uint32_t x[2][2][4];
+          for (int g = 0; g < 2; ++g)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t ka = vw[g][2 * i][q], kb = vw[g][2 * i + 1][q];
-            e2m1x8_to_f16x2(bit_select(0x0F0F0F0Fu, ka, kb << 4), x[i][0]);
-            e2m1x8_to_f16x2(bit_select(0x0F0F0F0Fu, ka >> 4, kb), x[i][1]);
-          }
+            for (int i = 0; i < 4; ++i)
+              if (t_warp + 16 * (g0 + g) + (i & 1 ? kv1 : kv0) + (i & 2 ? 8 : 0) >= sq.ctx) sv[g][i] = 0u;
+        }
 #pragma unroll
-          for (int mt = 0; mt < 4; ++mt) {
-            const uint32_t a[4] = {mul_f16x2(x[0][0][mt], s01), mul_f16x2(x[0][1][mt], s01),
-                                   mul_f16x2(x[1][0][mt], s23), mul_f16x2(x[1][1][mt], s23)};
+        for (int g = 0; g < 2; ++g) {
+          const uint32_t s01 = e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(sv[g][0], sv[g][1], 0x0040u))),
+                         s23 = e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(sv[g][2], sv[g][3], 0x0040u)));
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16_pure(o[nt][4 * q + mt], a, pb[g][nt][0], pb[g][nt][1]);
+          for (int q = 0; q < VB / 4; ++q) {
+            // bytes of a pair of keys at one d: its even d, and its odd ones
+            uint32_t x[2][2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t ka = vw[g][2 * i][q], kb = vw[g][2 * i + 1][q];
+              e2m1x8_to_f16x2(bit_select(0x0F0F0F0Fu, ka, kb << 4), x[i][0]);
+              e2m1x8_to_f16x2(bit_select(0x0F0F0F0Fu, ka >> 4, kb), x[i][1]);
+            }
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+              const uint32_t a[4] = {mul_f16x2(x[0][0][mt], s01), mul_f16x2(x[0][1][mt], s01),
+                                     mul_f16x2(x[1][0][mt], s23), mul_f16x2(x[1][1][mt], s23)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16_pure(o[nt][4 * q + mt], a, pb[g0 + g][nt][0], pb[g0 + g][nt][1]);
+            }
           }
         }
       }
@@ -400,7 +429,7 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
   if (!healthy && lane == 0) {
     // a copy of this warp's may still be landing: one more bounded wait each
     for (int kk = issued > NS ? issued - NS : 0; kk < issued; ++kk)
-      mbar_wait(bar0 + 32 * (kk % NS), static_cast<uint32_t>((kk / NS) & 1), nullptr);
+      mbar_wait(bar0 + BAR * (kk % NS), static_cast<uint32_t>((kk / NS) & 1), nullptr);
   }
   allow_next_grid();
 
@@ -412,8 +441,8 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
 #pragma unroll
       for (int sh = 4; sh < 32; sh <<= 1) l[nt][e] += __shfl_xor_sync(kFull, l[nt][e], sh);
   __syncthreads();  // every warp is done with the stages
-  float* s_o = reinterpret_cast<float*>(smem);  // [4 warps][R][DP]
-  float* s_ml = s_o + 4 * C::R * DP;            // [4 warps][R][2]
+  float* s_o = reinterpret_cast<float*>(smem);  // [WARPS][R][DP]
+  float* s_ml = s_o + WARPS * C::R * DP;        // [WARPS][R][2]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -435,10 +464,10 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
     const int row = idx / (D / 2), d = 2 * (idx - row * (D / 2));
     float M = -CUDART_INF_F;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) M = fmaxf(M, s_ml[(w * C::R + row) * 2]);
+    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_ml[(w * C::R + row) * 2]);
     float a0 = 0.f, a1 = 0.f, lsum = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       const float2 ml = *reinterpret_cast<const float2*>(s_ml + (w * C::R + row) * 2);
       const float wt = ml.x == -CUDART_INF_F ? 0.f : fast_exp2(ml.x - M);
       const float2 v = *reinterpret_cast<const float2*>(s_o + (w * C::R + row) * DP + d);
@@ -461,33 +490,38 @@ __global__ void __launch_bounds__(128, E2M1Shape<D, NT>::CTAS)
   }
 }
 
-template <int D, int NT, bool MODS, bool FAR>
-cudaError_t launch_t(const ChunkParams& p, const ChunkMaps& m, cudaStream_t stream) {
-  auto kern = chunk_e2m1_kernel<D, NT, MODS, FAR>;
-  constexpr int smem = E2M1Shape<D, NT>::BYTES;
+template <int D, int NT, int BS, bool MODS, bool FAR>
+cudaError_t launch_t(const ChunkParams& p, cudaStream_t stream) {
+  using C = E2M1Shape<D, NT, BS>;
+  auto kern = chunk_e2m1_kernel<D, NT, BS, MODS, FAR>;
   static int configured[64] = {};
-  cudaError_t e = set_smem_once(kern, smem, configured);
+  cudaError_t e = set_smem_once(kern, C::BYTES, configured);
   if (e != cudaSuccess) return e;
   const int ntq = (p.max_q_len + p.tile_q - 1) / p.tile_q;
-  return launch_pdl(kern, dim3(p.max_splits, p.num_kv_heads * ntq, p.batch), dim3(128), smem, stream, m, p);
+  return launch_pdl(kern, dim3(p.max_splits, p.num_kv_heads * ntq, p.batch), dim3(C::THREADS), C::BYTES, stream, p);
+}
+
+template <int D, int NT, int BS>
+cudaError_t launch_n(const ChunkParams& p, cudaStream_t stream) {
+  if (p.cap_far) return launch_t<D, NT, BS, true, true>(p, stream);
+  return p.cap_log2 > 0.f || p.slopes != nullptr ? launch_t<D, NT, BS, true, false>(p, stream)
+                                                 : launch_t<D, NT, BS, false, false>(p, stream);
 }
 
 template <int D, int NT>
-cudaError_t launch_n(const ChunkParams& p, const ChunkMaps& m, cudaStream_t stream) {
-  if (p.cap_far) return launch_t<D, NT, true, true>(p, m, stream);
-  return p.cap_log2 > 0.f || p.slopes != nullptr ? launch_t<D, NT, true, false>(p, m, stream)
-                                                 : launch_t<D, NT, false, false>(p, m, stream);
+cudaError_t launch_b(const ChunkParams& p, cudaStream_t stream) {
+  return p.block_size == 16 ? launch_n<D, NT, 16>(p, stream) : launch_n<D, NT, 32>(p, stream);
 }
 
 template <int D>
-cudaError_t launch_d(const ChunkParams& p, const ChunkMaps& m, cudaStream_t stream) {
-  return p.max_q_len * p.group > 8 ? launch_n<D, 2>(p, m, stream) : launch_n<D, 1>(p, m, stream);
+cudaError_t launch_d(const ChunkParams& p, cudaStream_t stream) {
+  return p.max_q_len * p.group > 8 ? launch_b<D, 2>(p, stream) : launch_b<D, 1>(p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_e2m1(const ChunkParams& p, const ChunkMaps& m, cudaStream_t stream) {
-  return p.head_dim == 128 ? launch_d<128>(p, m, stream) : launch_d<64>(p, m, stream);
+cudaError_t launch_chunk_e2m1(const ChunkParams& p, cudaStream_t stream) {
+  return p.head_dim == 128 ? launch_d<128>(p, stream) : launch_d<64>(p, stream);
 }
 
 }  // namespace pkv

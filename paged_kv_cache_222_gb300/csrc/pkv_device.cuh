@@ -138,7 +138,12 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr));
 }
 
-// One byte, and one or two words, of shared memory.
+// One or two bytes, and one to four words, of shared memory.
+__device__ __forceinline__ uint32_t lds_half(uint32_t addr) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ uint32_t lds_byte(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
@@ -149,6 +154,12 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[1]) {
 }
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[2]) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+}
+
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[4]) {
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(addr));
 }
 
 // Transpose of an 8x8 b16 matrix held one row pair per lane (ldmatrix layout).

@@ -183,6 +183,8 @@ struct CopyParams {
 // query i of its n sits at position context_lens[b] - n + i.
 struct ChunkParams {
   const void* q;                 // bf16 [T, H_q, D]
+  const void* k_cache;
+  const void* v_cache;
   void* out;                     // bf16 [T, H_q, D]
   const int32_t* q_starts;       // [B + 1]
   const int32_t* block_tables;   // [B, MB]
@@ -304,7 +306,7 @@ cudaError_t launch_multi_query_tc(const DecodeParams& p, const CUtensorMap& tmap
 // kernel (row tiles of up to 256 rows) and the merge of their split pieces.
 cudaError_t launch_chunk_small(const ChunkParams& p, const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
                                cudaStream_t stream);
-cudaError_t launch_chunk_e2m1(const ChunkParams& p, const ChunkMaps& maps, cudaStream_t stream);
+cudaError_t launch_chunk_e2m1(const ChunkParams& p, cudaStream_t stream);
 cudaError_t launch_chunk_tc(const ChunkParams& p, const ChunkMaps& maps, cudaStream_t stream);
 cudaError_t launch_chunk_tc_e2m1(const ChunkParams& p, const ChunkMaps& maps, cudaStream_t stream);
 // `nk`: keys per tile of the kernel that wrote the pieces.
@@ -341,7 +343,10 @@ constexpr int kChunkMaxContext = 0x7FFFFF00;
 constexpr int kChunkSmallTile = 64, kChunkE2M1Tile = 128, kChunkTcTile = 128;
 // CTAs per SM of the mma.sync kernels, by the bytes of a 64-key step (chunk.cu),
 // and over E2M1 caches (chunk_e2m1.cu).
-constexpr int chunk_e2m1_ctas(int head_dim, bool eight_rows) { return eight_rows ? 4 : 3; }
+constexpr int chunk_e2m1_keys(int head_dim, bool eight_rows) { return 32; }  // of a warp's step
+constexpr int chunk_e2m1_ctas(int head_dim, bool eight_rows) {
+  return (eight_rows ? 4 : 3) * (chunk_e2m1_keys(head_dim, eight_rows) / 32);
+}
 constexpr int chunk_small_ctas(int head_dim, bool fp8, bool eight_rows) {
   const int stage = 2 * kChunkSmallTile * head_dim * (fp8 ? 1 : 2);
   return !eight_rows || stage >= 32768 ? 3 : (stage == 16384 ? 4 : 5);

@@ -664,7 +664,7 @@ int32_t pkv_abi_version(void);
  * the number of launches and their summed device time; it then clears the
  * buffer.  Kinds: 0 append, 1 decode split, 2 combine, 3 cascade prefix,
  * 4 block copy, 5 multi-token query, 6 slot mapping, 7 chunk attention,
- * 8 rotary append, 9 token compaction, 10 token read.
+ * 8 rotary append, 9 token compaction, 10 token read, 11 tables.
  */
 typedef struct {
   int32_t kind;

@@ -112,6 +112,82 @@ pkv_status pkv_bm_block_tables(pkv_block_manager* bm, int32_t n_seqs, const int6
                                 int32_t max_blocks_per_seq, int32_t* block_tables,
                                 int32_t* context_lens);
 
+/* ------------------------------------------------------------ device tables
+ *
+ * The same growth and shrinkage of block tables done on the GPU, for requests
+ * whose lengths live there: a serving step then needs no number on the host and
+ * can be captured in a graph.  The free pool is a stack in device memory:
+ * free_blocks int32 [free_capacity], of which the first free_count[0] entries are
+ * free, the last of them the next to go.  Blocks belong to one request each (no
+ * reference counts: shared prefixes are pkv_bm_*'s).
+ *
+ * pkv_extend_tables — new tokens of every request get their blocks, slots and
+ * positions.
+ *
+ *   block_tables   int32 [batch, max_blocks_per_seq], written where a block is
+ *                  added; entries past a request's last block may hold anything.
+ *                  batch 0..65535; max_blocks_per_seq * block_size < 2^31.
+ *   past_lens, new_lens  int32 [batch]: tokens that request b holds, and gets.
+ *                  One of a negative number, or of more tokens than its table
+ *                  holds, is recorded (PKV_DEVERR_CONTEXT_LEN) and gets none.
+ *   cache          block size and number of blocks (any dtype).
+ *   max_tokens     host-side bound on the new tokens, and the size of
+ *                  slot_mapping and positions (up to 2^31 - 1).
+ *   out            device arrays:
+ *     context_lens   [batch] past_lens[b] + new_lens[b] (may be past_lens itself)
+ *     q_starts       [batch + 1] new tokens of the requests before b
+ *     block_starts   [batch + 1] new blocks of the requests before b
+ *     slot_mapping, positions  int64 [max_tokens]: flat slot and position of each
+ *                    new token, request after request; -1 past the last
+ *     free_count     [1] entries left (may be the input's)
+ *     lacking        [1] blocks that were missing, 0 if there were enough
+ * New block i of request b is free_blocks[count - 1 - (block_starts[b] + i)].  All or
+ * nothing: with too few free blocks, more tokens than max_tokens (recorded as
+ * PKV_DEVERR_CONTEXT_LEN) or a count outside [0, free_capacity] (recorded as
+ * PKV_DEVERR_BLOCK_ID) no request gets any, tables and free_count stay, q_starts
+ * and block_starts are 0 and every slot is -1, so that what runs on them does
+ * nothing.  A block id outside [0, num_blocks), free or in the table's last
+ * entry, is recorded (PKV_DEVERR_BLOCK_ID), its tokens get slot -1 and a new entry
+ * is -1.
+ */
+typedef struct {
+  int32_t* context_lens;
+  int32_t* q_starts;
+  int32_t* block_starts;
+  int64_t* slot_mapping;
+  int64_t* positions;
+  int32_t* free_count;
+  int32_t* lacking;
+} pkv_table_step;
+
+pkv_status pkv_extend_tables(int32_t* block_tables, int32_t max_blocks_per_seq, int32_t batch,
+                             const int32_t* past_lens, const int32_t* new_lens, const int32_t* free_blocks,
+                             int32_t free_capacity, const int32_t* free_count, const pkv_cache_desc* cache,
+                             int64_t max_tokens, const pkv_table_step* out, pkv_stream_t stream);
+
+/*
+ * pkv_truncate_tables — every request keeps its first keep_lens[b] of
+ * context_lens[b] tokens (finished requests none, a rejected draft's the tokens
+ * before it); the blocks behind them go back on the stack, in the order that
+ * undoes pkv_extend_tables.
+ *
+ *   block_tables   read; entries of the blocks given back stay as they are (they
+ *                  are past the request's end now).
+ *   free_blocks    written from entry free_count[0] on.
+ *   block_starts   int32 [batch + 1], written: blocks given back by the requests
+ *                  before b.
+ *   free_count_out [1], written (may be free_count): entries afterwards.
+ * A request with keep < 0, keep > context or more tokens than its table holds is
+ * recorded (PKV_DEVERR_CONTEXT_LEN) and gives nothing back.  All or nothing: if
+ * the blocks do not fit free_capacity or the count is negative, that is recorded
+ * (PKV_DEVERR_BLOCK_ID) and nothing changes.  An entry outside [0, num_blocks) is
+ * recorded (PKV_DEVERR_BLOCK_ID) and goes on the stack as -1.
+ */
+pkv_status pkv_truncate_tables(const int32_t* block_tables, int32_t max_blocks_per_seq, int32_t batch,
+                               const int32_t* context_lens, const int32_t* keep_lens, int32_t* free_blocks,
+                               int32_t free_capacity, const int32_t* free_count, const pkv_cache_desc* cache,
+                               int32_t* block_starts, int32_t* free_count_out, pkv_stream_t stream);
+
 /*
  * pkv_copy_blocks — device copy-on-write step: for each pair i,
  * k_cache[dst[i]] = k_cache[src[i]] and v_cache[dst[i]] = v_cache[src[i]]

@@ -4,8 +4,9 @@ Every function here only checks tensor shapes / dtypes and hands raw device
 pointers plus the current CUDA stream to the C ABI (include/pkv.h); all of the
 computation runs in the library's sm_103a kernels.  PyTorch supplies device
 memory and streams.  The calls made once per layer and step on a few tokens
-(chunk_attention, rotary_append, compact_tokens, read_tokens) do this in a
-compiled module (csrc/binding.cpp), the others through ctypes.
+(chunk_attention, rotary_append, compact_tokens, read_tokens, extend_tables,
+truncate_tables) do this in a compiled module (csrc/binding.cpp), the others
+through ctypes.
 
     append(k_new, v_new, slot_mapping, k_cache, v_cache[, k_scale, v_scale])
     decode_attention(q, k_cache, v_cache, block_tables, context_lens, scale
@@ -16,12 +17,16 @@ compiled module (csrc/binding.cpp), the others through ctypes.
     compact_tokens(k_cache, v_cache, block_tables, keep, keep_starts)
     read_tokens(slot_mapping, k_cache, v_cache[, k_scale, v_scale]) -> k, v
 
+    extend_tables(block_tables, past_lens, new_lens, free_blocks, free_count, k_cache, max_tokens)
+    truncate_tables(block_tables, context_lens, keep_lens, free_blocks, free_count, k_cache)
+
 Cache tensors are [num_blocks, H_kv, block_size, head_dim], bf16 or E4M3
 (torch.uint8 or torch.float8_e4m3fn storage), or E2M1: 4-bit codes with an
 8-bit scale for every 16 of them, torch.uint8 [num_blocks, H_kv, block_size,
 head_dim / 2 + head_dim / 16] (e2m1_cache; layout in include/pkv.h).
 """
 
+import collections
 import ctypes
 import math
 
@@ -35,14 +40,14 @@ from ._lib import (PKV_BF16, PKV_E2M1, PKV_E4M3, PKV_F32, CacheDesc, DecodePlan,
 __all__ = ["append", "decode_attention", "decode_plan", "cache_desc", "slot_mapping",
            "cascade_plan", "cascade_decode_attention", "multi_query_plan", "multi_query_attention",
            "chunk_plan", "chunk_attention", "rotary_frequencies", "rotary_axes", "rotary_append", "compact_tokens",
-           "e2m1_cache", "read_tokens",
+           "e2m1_cache", "read_tokens", "ExtendedTables", "extend_tables", "truncate_tables",
            "BlockManager", "OutOfBlocks", "copy_blocks",
            "host_pool_like", "copy_blocks_between",
            "device_error", "trace_enable", "trace_read", "library", "PkvError"]
 
 KERNEL_KINDS = {0: "append", 1: "decode_split", 2: "combine", 3: "cascade_prefix", 4: "block_copy",
                 5: "multi_query", 6: "slot_mapping", 7: "chunk_attention", 8: "rotary_append",
-                9: "compact_tokens", 10: "read_tokens"}
+                9: "compact_tokens", 10: "read_tokens", 11: "tables"}
 
 
 def library():
@@ -484,6 +489,47 @@ def compact_tokens(k_cache, v_cache, block_tables, keep, keep_starts, dst_start=
     """
     _lib.check(_lib.binding().compact_tokens(k_cache, v_cache, block_tables, keep, keep_starts, dst_start, max_keep),
                "pkv_compact_tokens")
+
+
+ExtendedTables = collections.namedtuple(
+    "ExtendedTables", "context_lens q_starts slot_mapping positions block_starts free_count lacking")
+
+
+def extend_tables(block_tables, past_lens, new_lens, free_blocks, free_count, k_cache, max_tokens, out=None):
+    """Blocks, slots and positions of every request's new tokens, on the GPU.
+
+    Request b holds past_lens[b] tokens and gets new_lens[b] more (int32 [B]);
+    the blocks they need come from the top of the stack free_blocks (int32, its
+    first free_count[0] entries are free) and are entered in block_tables (int32
+    [B, MB], in place).  `k_cache` gives block size and number of blocks, max_tokens
+    (a host number) bounds the new tokens.  Returns ExtendedTables:
+
+      context_lens [B]   past + new      q_starts, block_starts [B + 1]  sums of new tokens, blocks
+      slot_mapping, positions   int64 [max_tokens], request after request, -1 past the last
+      free_count [1]     what is left (the argument stays as it was)
+      lacking [1]        blocks that were missing: if any, nothing was done and no slot is given
+
+    which is what rotary_append / append and chunk_attention take.  `out` (an
+    ExtendedTables, or a tuple like it) is written and returned instead; its
+    context_lens may be past_lens and its free_count the argument, so that a
+    captured step advances them.
+    """
+    r = _lib.binding().extend_tables(block_tables, past_lens, new_lens, free_blocks, free_count, k_cache, max_tokens,
+                                     out)
+    if type(r) is int:
+        _lib.check(r, "pkv_extend_tables")
+    return r if out is not None else ExtendedTables._make(r)
+
+
+def truncate_tables(block_tables, context_lens, keep_lens, free_blocks, free_count, k_cache, out=None):
+    """Requests keep their first keep_lens[b] of context_lens[b] tokens (int32
+    [B]); the blocks behind them go back on the stack (free_blocks in place, in
+    the order that undoes extend_tables).  Returns the new free_count (int32 [1],
+    or `out`, which may be free_count itself)."""
+    r = _lib.binding().truncate_tables(block_tables, context_lens, keep_lens, free_blocks, free_count, k_cache, out)
+    if type(r) is int:
+        _lib.check(r, "pkv_truncate_tables")
+    return r
 
 
 def slot_mapping(block_tables, positions, k_cache, seq_index=None, out=None):

@@ -44,6 +44,11 @@ class ScoreMods(ctypes.Structure):
                 ("slopes", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p)]
 
 
+class TableStep(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("context_lens", "q_starts", "block_starts", "slot_mapping", "positions",
+                                               "free_count", "lacking")]
+
+
 class TraceEntry(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("launches", ctypes.c_int32), ("total_ms", ctypes.c_double)]
 
@@ -86,6 +91,9 @@ SIGNATURES = {
     "pkv_rotary_append_axes": (_I32, [_P, _I64, _P, _I64, _P, _I64, _I32, _I64, _I32, _P, _I64, _I32, _P, _P, _I32,
                                       _I32, _F, _P, _P, _P, ctypes.POINTER(CacheDesc), _P, _P, _I64, _P, _I64, _P]),
     "pkv_compact_tokens": (_I32, [_P, _P, ctypes.POINTER(CacheDesc), _P, _I32, _I32, _P, _I32, _P, _P, _I32, _P]),
+    "pkv_extend_tables": (_I32, [_P, _I32, _I32, _P, _P, _P, _I32, _P, ctypes.POINTER(CacheDesc), _I64,
+                                 ctypes.POINTER(TableStep), _P]),
+    "pkv_truncate_tables": (_I32, [_P, _I32, _I32, _P, _P, _P, _I32, _P, ctypes.POINTER(CacheDesc), _P, _P, _P]),
     "pkv_copy_blocks": (_I32, [_P, _P, ctypes.POINTER(CacheDesc), _P, _P, _I32, _P]),
     "pkv_bm_create": (_I32, [_I64, _I32, ctypes.POINTER(_P)]),
     "pkv_bm_destroy": (None, [_P]),
@@ -163,7 +171,7 @@ def binding():
                                    "compile") from e
             mod.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                        for f in ("pkv_chunk_plan", "pkv_chunk_attention", "pkv_rotary_append_axes", "pkv_compact_tokens",
-                                 "pkv_append", "pkv_read_tokens")))
+                                 "pkv_append", "pkv_read_tokens", "pkv_extend_tables", "pkv_truncate_tables")))
             _binding = mod
     return _binding
 

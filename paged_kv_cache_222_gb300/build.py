@@ -29,7 +29,7 @@ LIB_PATH = os.path.join(PKG, "libpkv.so")
 BINDING_PATH = os.path.join(PKG, "_binding.so")
 
 SOURCES = ["api.cu", "append.cu", "decode.cu", "cascade.cu", "multi_query.cu", "blocks.cu", "chunk.cu", "chunk_e2m1.cu", "chunk_tc.cu", "chunk_tc_e2m1.cu", "rotary.cu",
-           "compact.cu", "block_manager.cpp"]
+           "compact.cu", "tables.cu", "block_manager.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -683,6 +683,112 @@ pkv_status pkv_slot_mapping(const int32_t* block_tables, int32_t num_seqs, int32
   return PKV_OK;
 }
 
+namespace {
+
+// What pkv_extend_tables and pkv_truncate_tables check alike.
+pkv_status check_tables(const pkv_cache_desc* cache, int32_t batch, int32_t max_blocks, int32_t free_capacity) {
+  pkv_status s = check_cache(cache, true);
+  if (s != PKV_OK) return s;
+  if (batch < 0 || batch > 65535) return fail(PKV_ERR_INVALID_ARG, "batch %d", batch);
+  if (max_blocks < 1 || static_cast<int64_t>(max_blocks) * cache->block_size > 0x7FFFFFFFll)
+    return fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq %d", max_blocks);
+  if (free_capacity < 0) return fail(PKV_ERR_INVALID_ARG, "free_capacity %d", free_capacity);
+  return PKV_OK;
+}
+
+}  // namespace
+
+pkv_status pkv_extend_tables(int32_t* block_tables, int32_t max_blocks_per_seq, int32_t batch,
+                             const int32_t* past_lens, const int32_t* new_lens, const int32_t* free_blocks,
+                             int32_t free_capacity, const int32_t* free_count, const pkv_cache_desc* cache,
+                             int64_t max_tokens, const pkv_table_step* out, pkv_stream_t stream) {
+  pkv_status s = check_tables(cache, batch, max_blocks_per_seq, free_capacity);
+  if (s != PKV_OK) return s;
+  if (max_tokens < 0 || max_tokens > 0x7FFFFFFFll)
+    return fail(PKV_ERR_INVALID_ARG, "max_tokens %lld", static_cast<long long>(max_tokens));
+  if (out == nullptr || free_count == nullptr || out->q_starts == nullptr || out->block_starts == nullptr ||
+      out->free_count == nullptr || out->lacking == nullptr ||
+      (batch > 0 && (block_tables == nullptr || past_lens == nullptr || new_lens == nullptr || out->context_lens == nullptr)) ||
+      (free_capacity > 0 && free_blocks == nullptr) ||
+      (max_tokens > 0 && (out->slot_mapping == nullptr || out->positions == nullptr)))
+    return fail(PKV_ERR_INVALID_ARG, "NULL pointer");
+  for (const void* t : {static_cast<const void*>(block_tables), static_cast<const void*>(past_lens),
+                        static_cast<const void*>(new_lens), static_cast<const void*>(free_blocks),
+                        static_cast<const void*>(free_count), static_cast<const void*>(out->context_lens),
+                        static_cast<const void*>(out->q_starts), static_cast<const void*>(out->block_starts),
+                        static_cast<const void*>(out->free_count), static_cast<const void*>(out->lacking)})
+    if (!aligned(t, 4)) return fail(PKV_ERR_INVALID_ARG, "32-bit arrays must be 4-byte aligned");
+  if (!aligned(out->slot_mapping, 8) || !aligned(out->positions, 8))
+    return fail(PKV_ERR_INVALID_ARG, "slot_mapping and positions must be 8-byte aligned");
+  int dev;
+  DeviceState* st;
+  s = current_device(&dev, &st);
+  if (s != PKV_OK) return s;
+  pkv::ExtendParams p = {};
+  p.block_tables = block_tables;
+  p.past_lens = past_lens;
+  p.new_lens = new_lens;
+  p.free_blocks = free_blocks;
+  p.free_count = free_count;
+  p.context_lens = out->context_lens;
+  p.q_starts = out->q_starts;
+  p.block_starts = out->block_starts;
+  p.slots = out->slot_mapping;
+  p.positions = out->positions;
+  p.free_count_out = out->free_count;
+  p.lacking = out->lacking;
+  p.num_blocks = cache->num_blocks;
+  p.max_tokens = max_tokens;
+  p.free_capacity = free_capacity;
+  p.batch = batch;
+  p.max_blocks = max_blocks_per_seq;
+  p.block_size = cache->block_size;
+  p.err = st->err;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = traced(pkv::kKindTables, cs, [&] { return pkv::launch_extend(p, cs); });
+  if (e != cudaSuccess) return cuda_fail(e, "table extension launch");
+  return PKV_OK;
+}
+
+pkv_status pkv_truncate_tables(const int32_t* block_tables, int32_t max_blocks_per_seq, int32_t batch,
+                               const int32_t* context_lens, const int32_t* keep_lens, int32_t* free_blocks,
+                               int32_t free_capacity, const int32_t* free_count, const pkv_cache_desc* cache,
+                               int32_t* block_starts, int32_t* free_count_out, pkv_stream_t stream) {
+  pkv_status s = check_tables(cache, batch, max_blocks_per_seq, free_capacity);
+  if (s != PKV_OK) return s;
+  if (free_count == nullptr || block_starts == nullptr || free_count_out == nullptr ||
+      (batch > 0 && (block_tables == nullptr || context_lens == nullptr || keep_lens == nullptr)) ||
+      (free_capacity > 0 && free_blocks == nullptr))
+    return fail(PKV_ERR_INVALID_ARG, "NULL pointer");
+  for (const void* t : {static_cast<const void*>(block_tables), static_cast<const void*>(context_lens),
+                        static_cast<const void*>(keep_lens), static_cast<const void*>(free_blocks),
+                        static_cast<const void*>(free_count), static_cast<const void*>(block_starts),
+                        static_cast<const void*>(free_count_out)})
+    if (!aligned(t, 4)) return fail(PKV_ERR_INVALID_ARG, "32-bit arrays must be 4-byte aligned");
+  int dev;
+  DeviceState* st;
+  s = current_device(&dev, &st);
+  if (s != PKV_OK) return s;
+  pkv::TruncateParams p = {};
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.keep_lens = keep_lens;
+  p.free_blocks = free_blocks;
+  p.free_count = free_count;
+  p.block_starts = block_starts;
+  p.free_count_out = free_count_out;
+  p.num_blocks = cache->num_blocks;
+  p.free_capacity = free_capacity;
+  p.batch = batch;
+  p.max_blocks = max_blocks_per_seq;
+  p.block_size = cache->block_size;
+  p.err = st->err;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = traced(pkv::kKindTables, cs, [&] { return pkv::launch_truncate(p, cs); });
+  if (e != cudaSuccess) return cuda_fail(e, "table truncation launch");
+  return PKV_OK;
+}
+
 pkv_status pkv_copy_blocks(void* k_cache, void* v_cache, const pkv_cache_desc* cache,
                            const int32_t* src_blocks, const int32_t* dst_blocks, int32_t n_pairs,
                            pkv_stream_t stream) {

@@ -23,6 +23,7 @@
 #include <utility>
 
 #include "pkv.h"
+#include "pkv_blocks.h"
 
 namespace {
 
@@ -35,6 +36,8 @@ decltype(&pkv_rotary_append_axes) g_rotary_append = nullptr;
 decltype(&pkv_compact_tokens) g_compact_tokens = nullptr;
 decltype(&pkv_append) g_append = nullptr;
 decltype(&pkv_read_tokens) g_read_tokens = nullptr;
+decltype(&pkv_extend_tables) g_extend_tables = nullptr;
+decltype(&pkv_truncate_tables) g_truncate_tables = nullptr;
 
 // A Python exception has been set.
 struct Raised {};
@@ -409,8 +412,111 @@ PyObject* read_tokens(PyObject* const* a, Py_ssize_t n_args) {
   return tuple({std::move(k), std::move(v)});
 }
 
+// `n` elements of a one-dimensional tensor from `at` on, as a tensor of their own
+// on the same storage.
+Tensor part(const Tensor& base, int64_t at, int64_t n) {
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()), base.key_set(), base.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(base.storage_offset() + at);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  return t;
+}
+
+// The geometry that tables are made for: one cache tensor.
+Caches one_cache(PyObject* ko) { return caches(ko, ko); }
+
+const Tensor& ints(PyObject* o, const char* name, at::Device dev, int64_t n) {
+  const Tensor& t = dense(o, at::kInt, name, dev);
+  if (t.dim() != 1 || t.size(0) != n) raise(PyExc_ValueError, "%s must be [%lld]", name, static_cast<long long>(n));
+  return t;
+}
+
+// The stack of free blocks and its count.
+struct Stack {
+  const Tensor& blocks;
+  const Tensor& count;
+  int32_t capacity;
+};
+Stack stack(PyObject* blocks, PyObject* count, at::Device dev) {
+  const Tensor& t = dense(blocks, at::kInt, "free_blocks", dev);
+  if (t.dim() != 1) raise(PyExc_ValueError, "free_blocks must be 1-D");
+  return Stack{t, ints(count, "free_count", dev, 1), size32(t.size(0), "free_blocks")};
+}
+
+PyObject* extend_tables(PyObject* const* a, Py_ssize_t n_args) {
+  expect(n_args, 8);
+  const Caches c = one_cache(a[5]);
+  const Tensor& tables = dense(a[0], at::kInt, "block_tables", c.dev);
+  if (tables.dim() != 2) raise(PyExc_ValueError, "block_tables must be [B, MB]");
+  const int64_t b = tables.size(0);
+  const int32_t batch = size32(b, "B"), mb = size32(tables.size(1), "MB");
+  const Tensor &past = ints(a[1], "past_lens", c.dev, b), &news = ints(a[2], "new_lens", c.dev, b);
+  const Stack st = stack(a[3], a[4], c.dev);
+  const int64_t most = integer(a[6], "max_tokens");
+  if (most < 0) raise(PyExc_ValueError, "max_tokens %lld", static_cast<long long>(most));
+  Tensor r[7];  // context_lens, q_starts, slot_mapping, positions, block_starts, free_count, lacking
+  const int64_t sizes[7] = {b, b + 1, most, most, b + 1, 1, 1};
+  static const char* const names[7] = {"out.context_lens", "out.q_starts",   "out.slot_mapping", "out.positions",
+                                       "out.block_starts", "out.free_count", "out.lacking"};
+  if (a[7] == Py_None) {
+    const Tensor i32 = at::empty({3 * b + 4}, tables.options()), i64 = at::empty({2 * most}, tables.options().dtype(at::kLong));
+    int64_t at32 = 0, at64 = 0;
+    for (int i = 0; i < 7; ++i) {
+      const bool wide = i == 2 || i == 3;
+      r[i] = part(wide ? i64 : i32, wide ? at64 : at32, sizes[i]);
+      (wide ? at64 : at32) += sizes[i];
+    }
+  } else {
+    if (!PyTuple_Check(a[7]) || PyTuple_GET_SIZE(a[7]) != 7) raise(PyExc_TypeError, "out must be seven tensors");
+    for (int i = 0; i < 7; ++i) {
+      const Tensor& t = dense(PyTuple_GET_ITEM(a[7], i), i == 2 || i == 3 ? at::kLong : at::kInt, names[i], c.dev);
+      if (t.dim() != 1 || t.size(0) != sizes[i])
+        raise(PyExc_ValueError, "%s must be [%lld]", names[i], static_cast<long long>(sizes[i]));
+      r[i] = t;
+    }
+  }
+  const pkv_table_step out = {r[0].data_ptr<int32_t>(), r[1].data_ptr<int32_t>(), r[4].data_ptr<int32_t>(),
+                              r[2].data_ptr<int64_t>(), r[3].data_ptr<int64_t>(), r[5].data_ptr<int32_t>(),
+                              r[6].data_ptr<int32_t>()};
+  const pkv_status s = on_stream(c.dev, [&](pkv_stream_t stream) {
+    return g_extend_tables(tables.data_ptr<int32_t>(), mb, batch, past.const_data_ptr<int32_t>(),
+                           news.const_data_ptr<int32_t>(), st.blocks.const_data_ptr<int32_t>(), st.capacity,
+                           st.count.const_data_ptr<int32_t>(), &c.desc, most, &out, stream);
+  });
+  if (s != PKV_OK) return PyLong_FromLong(s);
+  if (a[7] != Py_None) {
+    Py_INCREF(a[7]);
+    return a[7];
+  }
+  return tuple({r[0], r[1], r[2], r[3], r[4], r[5], r[6]});
+}
+
+PyObject* truncate_tables(PyObject* const* a, Py_ssize_t n_args) {
+  expect(n_args, 7);
+  const Caches c = one_cache(a[5]);
+  const Tensor& tables = dense(a[0], at::kInt, "block_tables", c.dev);
+  if (tables.dim() != 2) raise(PyExc_ValueError, "block_tables must be [B, MB]");
+  const int64_t b = tables.size(0);
+  const int32_t batch = size32(b, "B"), mb = size32(tables.size(1), "MB");
+  const Tensor &ctx = ints(a[1], "context_lens", c.dev, b), &keep = ints(a[2], "keep_lens", c.dev, b);
+  const Stack st = stack(a[3], a[4], c.dev);
+  const Tensor mine = at::empty({b + 2}, tables.options());
+  const Tensor count = a[6] == Py_None ? part(mine, b + 1, 1) : ints(a[6], "out", c.dev, 1);
+  const pkv_status s = on_stream(c.dev, [&](pkv_stream_t stream) {
+    return g_truncate_tables(tables.const_data_ptr<int32_t>(), mb, batch, ctx.const_data_ptr<int32_t>(),
+                             keep.const_data_ptr<int32_t>(), st.blocks.data_ptr<int32_t>(), st.capacity,
+                             st.count.const_data_ptr<int32_t>(), &c.desc, mine.data_ptr<int32_t>(),
+                             count.data_ptr<int32_t>(), stream);
+  });
+  if (s != PKV_OK) return PyLong_FromLong(s);
+  if (a[6] != Py_None) {
+    Py_INCREF(a[6]);
+    return a[6];
+  }
+  return THPVariable_Wrap(count);
+}
+
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
-  constexpr int kCalls = 6;
+  constexpr int kCalls = 8;
   expect(n, kCalls);
   void* p[kCalls];
   for (int i = 0; i < kCalls; ++i) p[i] = reinterpret_cast<void*>(static_cast<uintptr_t>(integer(a[i], "address")));
@@ -420,6 +526,8 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   g_compact_tokens = reinterpret_cast<decltype(g_compact_tokens)>(p[3]);
   g_append = reinterpret_cast<decltype(g_append)>(p[4]);
   g_read_tokens = reinterpret_cast<decltype(g_read_tokens)>(p[5]);
+  g_extend_tables = reinterpret_cast<decltype(g_extend_tables)>(p[6]);
+  g_truncate_tables = reinterpret_cast<decltype(g_truncate_tables)>(p[7]);
   Py_RETURN_NONE;
 }
 
@@ -438,7 +546,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<name>)), METH_FASTCALL, nullptr}
 
 PyMethodDef g_methods[] = {PKV_ENTRY(bind), PKV_ENTRY(chunk_attention), PKV_ENTRY(rotary_append),
-                           PKV_ENTRY(compact_tokens), PKV_ENTRY(append), PKV_ENTRY(read_tokens), {nullptr, nullptr, 0, nullptr}};
+                           PKV_ENTRY(compact_tokens), PKV_ENTRY(append), PKV_ENTRY(read_tokens),
+                           PKV_ENTRY(extend_tables), PKV_ENTRY(truncate_tables), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", "Compiled calls of the paged-KV library.", -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

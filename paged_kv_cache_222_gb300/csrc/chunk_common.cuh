@@ -40,27 +40,6 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int b, bool 
   return s;
 }
 
-// Largest b in [0, n) with key(b) <= x, for keys that do not decrease and
-// key(0) <= x: a whole warp looks at 32 places of the range per round, so a
-// thousand sequences take two dependent loads.  (Keys that do decrease give
-// some b of the range.)
-template <class F>
-__device__ __forceinline__ int warp_search(int n, int x, F&& key) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, len = n;
-  while (len > 1) {
-    const int step = (len + 31) / 32;
-    const int at = lane * step;
-    const bool le = at < len && (lane == 0 || key(lo + at) <= x);
-    const unsigned m = __ballot_sync(kFull, le);
-    const int last = 31 - __clz(m);   // lane 0's bit is always set
-    const int off = last * step;
-    lo += off;
-    len = min(step, len - off);
-  }
-  return lo;
-}
-
 // Row tiles of the tcgen05 kernel: sequence b's tiles take numbers from
 // floor(q_starts[b] / tile_q) + b on, which leaves each one room for its
 // ceil(n / tile_q) tiles and needs no prefix sum; some numbers stay unused.

@@ -59,6 +59,27 @@ __device__ __forceinline__ void allow_next_grid() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Largest b in [0, n) with key(b) <= x, for keys that do not decrease and
+// key(0) <= x: a whole warp looks at 32 places of the range per round, so a
+// thousand sequences take two dependent loads.  (Keys that do decrease give
+// some b of the range.)
+template <class F>
+__device__ __forceinline__ int warp_search(int n, int x, F&& key) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = n;
+  while (len > 1) {
+    const int step = (len + 31) / 32;
+    const int at = lane * step;
+    const bool le = at < len && (lane == 0 || key(lo + at) <= x);
+    const unsigned m = __ballot_sync(kFull, le);
+    const int last = 31 - __clz(m);   // lane 0's bit is always set
+    const int off = last * step;
+    lo += off;
+    len = min(step, len - off);
+  }
+  return lo;
+}
+
 // Launch with programmatic dependent launch allowed: the kernel may be
 // scheduled while its predecessor in the stream drains; it waits for the
 // predecessor's completion (griddepcontrol.wait) before touching its data.

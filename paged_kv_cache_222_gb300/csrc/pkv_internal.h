@@ -33,7 +33,8 @@ enum KernelKind {
   kKindRotary = 8,
   kKindCompact = 9,
   kKindRead = 10,
-  kNumKernelKinds = 11  // the trace aggregates by kind
+  kKindTables = 11,
+  kNumKernelKinds = 12  // the trace aggregates by kind
 };
 
 // Decode work split: balanced stream-K ranges over the flattened
@@ -279,6 +280,46 @@ struct CompactParams {
   int* err;
 };
 
+// Tables, slots and positions of requests' new tokens (tables.cu).
+struct ExtendParams {
+  int32_t* block_tables;         // [B, MB]
+  const int32_t* past_lens;      // [B]
+  const int32_t* new_lens;       // [B]
+  const int32_t* free_blocks;    // stack
+  const int32_t* free_count;
+  int32_t* context_lens;         // [B], may be past_lens
+  int32_t* q_starts;             // [B + 1]
+  int32_t* block_starts;         // [B + 1]
+  int64_t* slots;                // [max_tokens]
+  int64_t* positions;            // [max_tokens]
+  int32_t* free_count_out;       // may be free_count
+  int32_t* lacking;
+  int64_t num_blocks;
+  int64_t max_tokens;
+  int32_t free_capacity;
+  int32_t batch;
+  int32_t max_blocks;
+  int32_t block_size;
+  int* err;
+};
+
+// Blocks that requests give back (tables.cu).
+struct TruncateParams {
+  const int32_t* block_tables;   // [B, MB]
+  const int32_t* context_lens;   // [B]
+  const int32_t* keep_lens;      // [B]
+  int32_t* free_blocks;          // stack
+  const int32_t* free_count;
+  int32_t* block_starts;         // [B + 1]
+  int32_t* free_count_out;       // may be free_count
+  int64_t num_blocks;
+  int32_t free_capacity;
+  int32_t batch;
+  int32_t max_blocks;
+  int32_t block_size;
+  int* err;
+};
+
 // Message returned by pkv_last_error() on this host thread.
 void set_last_error(const char* msg);
 
@@ -290,6 +331,8 @@ int config_epoch();
 cudaError_t launch_copy_blocks(const CopyParams& p, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_read(const ReadParams& p, cudaStream_t stream);
+cudaError_t launch_extend(const ExtendParams& p, cudaStream_t stream);
+cudaError_t launch_truncate(const TruncateParams& p, cudaStream_t stream);
 cudaError_t launch_slot_mapping(const SlotParams& p, cudaStream_t stream);
 cudaError_t launch_decode_split(const DecodeParams& p, const CUtensorMap& tmap_k,
                                 const CUtensorMap& tmap_v, cudaStream_t stream);

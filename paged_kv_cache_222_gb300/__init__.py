@@ -123,14 +123,14 @@ def append(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=N
     take them or go without; every group of 16 elements gets a scale of its own
     besides.
     """
+    if k_cache.dtype == torch.uint8 and k_cache.shape[-1] in _E2M1_ROWS:
+        _lib.check(_lib.binding().append(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale,
+                                         scale_row_stride), "pkv_append")
+        return
     lib = library()
     _check_pair(k_cache, v_cache)
     dev = k_cache.device
     desc = cache_desc(k_cache)
-    if desc.dtype == PKV_E2M1:
-        _lib.check(_lib.binding().append(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale,
-                                         scale_row_stride), "pkv_append")
-        return
     if k_new.shape != v_new.shape or k_new.dim() != 3:
         raise ValueError("k_new / v_new must both be [N, H_kv, D]")
     n, hkv, d = k_new.shape

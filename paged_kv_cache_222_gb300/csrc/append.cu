@@ -12,10 +12,10 @@
 // (E4M3) stores; loads are 16-byte (bf16 source) or 2x16-byte (f32 source).
 // Grid-stride, so any number of rows fits a bounded grid.
 //
-// E2M1 caches: a thread per group of 16 elements, which it reads whole, scales
-// and packs into 8 code bytes and a scale byte (pkv_device.cuh).
+// E2M1 caches: a thread per group of 16 elements, 8 code bytes and a scale byte
+// (how codes are found without dividing: pkv_device.cuh).
 //
-// read_kernel is the way back: a thread per 16 elements of a (token, head) row
+// read_kernel is the way back: a thread per 8 elements of a (token, head) row
 // widens them (codes times scales; every code and code-times-scale product is
 // exact in binary32), multiplies by the head's scale and rounds once.
 //
@@ -73,156 +73,186 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
   }
 }
 
-template <int SRC>
+// Pieces of (token, head) rows, `per_tok` of a token: a CTA takes whole tokens,
+// threadIdx.y one of them and threadIdx.x its piece, so that nothing is divided.
+template <class F>
+__device__ __forceinline__ void for_pieces(int64_t n_tokens, int per_tok, F&& f) {
+  for (int64_t tok = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y; tok < n_tokens;
+       tok += static_cast<int64_t>(gridDim.x) * blockDim.y)
+    for (int i = threadIdx.x; i < per_tok; i += blockDim.x) f(tok, i);
+}
+
+// Byte of a block's first tile: blocks and a block's bytes are 32-bit numbers.
+__device__ __forceinline__ int64_t tile_at(int64_t block, int block_bytes) {
+  return static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(block)) * static_cast<uint32_t>(block_bytes));
+}
+
+// A thread per group of 16 elements of K or of V.  SCALED: with heads' scales.
+template <int SRC, bool SCALED>
 __global__ void __launch_bounds__(256) append_e2m1_kernel(AppendParams p) {
   wait_prior_grid();
   allow_next_grid();
-  const int D = p.head_dim, H = p.num_kv_heads;
-  const int per_row = D / kE2M1Group;
-  const int64_t total = p.n_tokens * H * per_row;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  const int64_t tile = e2m1_tile_bytes(D, p.block_size);
-  for (int64_t idx = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; idx < total; idx += stride) {
-    const int64_t row = idx / per_row;  // token * H + head
-    const int part = static_cast<int>(idx - row * per_row);
-    const int64_t tok = row / H;
-    const int h = static_cast<int>(row - tok * H);
+  const int D = p.head_dim, H = p.num_kv_heads, shift = p.block_size == 16 ? 4 : 5, to_row = D == 128 ? 3 : 2;
+  const int tile = e2m1_tile_bytes(D, p.block_size), groups = H << to_row;
+  for_pieces(p.n_tokens, 2 * groups, [&](int64_t tok, int i) {
     const int64_t slot = p.slots[tok];
-    if (slot < 0) continue;
+    const bool kv = i >= groups;
+    const int g = kv ? i - groups : i, h = g >> to_row, part = g & ((1 << to_row) - 1);
+    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const char*>(kv ? p.v_new : p.k_new) +
+                                                       (tok * (H * D) + g * 16) * (SRC == kBF16 ? 2 : 4));
+    uint4 w[SRC == kBF16 ? 2 : 4];
+#pragma unroll
+    for (int q = 0; q < (SRC == kBF16 ? 2 : 4); ++q) w[q] = from[q];
+    if (slot < 0) return;
     if (slot >= p.num_slots) {
-      if (part == 0 && h == 0) record_error(p.err, kDevErrSlot);
-      continue;
+      if (i == 0) record_error(p.err, kDevErrSlot);
+      return;
     }
-    const int64_t blk = slot / p.block_size;
-    const int off = static_cast<int>(slot - blk * p.block_size);
-    const int64_t base = (blk * H + h) * tile;
+    float x[2][8], amax;
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      float x[2][8];
-      uint4 raw;
-      const void* src = kv ? p.v_new : p.k_new;
-      enc_load8<SRC>(src, row * D + part * kE2M1Group, x[0], raw);
-      enc_load8<SRC>(src, row * D + part * kE2M1Group + 8, x[1], raw);
-      const float* scale = kv ? p.v_scale : p.k_scale;
-      if (scale != nullptr) {
-        const float s = scale[tok * p.scale_stride + h];
+    for (int q = 0; q < 2; ++q) {
+      if constexpr (SRC == kBF16) {
+        const uint32_t v[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[0][i] = __fdiv_rn(x[0][i], s);
-          x[1][i] = __fdiv_rn(x[1][i], s);
+        for (int e = 0; e < 4; ++e) {
+          x[q][2 * e] = bf16lo_to_f32(v[e]);
+          x[q][2 * e + 1] = bf16hi_to_f32(v[e]);
         }
+      } else {
+        const uint4 a = w[SRC == kBF16 ? 0 : 2 * q], c = w[SRC == kBF16 ? 0 : 2 * q + 1];
+        const uint32_t v[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[q][e] = __uint_as_float(v[e]);
       }
-      const uint8_t sc = e2m1_group_scale(max_nan(abs_max8(x[0]), abs_max8(x[1])));
-      uint8_t* to = static_cast<uint8_t*>(kv ? p.v_cache : p.k_cache) + base;
-      *reinterpret_cast<uint2*>(to + off * (D / 2) + part * 8) =
-          make_uint2(e2m1_codes8(x[0], sc), e2m1_codes8(x[1], sc));
-      to[p.block_size * (D / 2) + off * per_row + part] = sc;
+      if constexpr (SCALED) {
+        const float s = (kv ? p.v_scale : p.k_scale)[tok * p.scale_stride + h];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[q][e] = __fdiv_rn(x[q][e], s);
+      }
     }
-  }
+    if constexpr (SRC == kBF16 && !SCALED) {  // on pairs
+      uint32_t m = 0u;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t v[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = max_nan_bf16x2(m, v[e] & 0x7FFF7FFFu);
+      }
+      amax = max_nan(bf16lo_to_f32(m), bf16hi_to_f32(m));
+    } else {
+      amax = max_nan(abs_max8(x[0]), abs_max8(x[1]));
+    }
+    const int off = static_cast<int>(slot) & (p.block_size - 1);
+    uint8_t* to = static_cast<uint8_t*>(kv ? p.v_cache : p.k_cache) + tile_at(slot >> shift, H * tile) + h * tile;
+    const uint8_t sc = e2m1_group_scale(amax);
+    constexpr bool SHORT = SRC == kBF16 && !SCALED;
+    *reinterpret_cast<uint2*>(to + off * (D / 2) + part * 8) =
+        make_uint2(e2m1_codes8<SHORT>(x[0], amax, sc), e2m1_codes8<SHORT>(x[1], amax, sc));
+    to[p.block_size * (D / 2) + off * (D / 16) + part] = sc;
+  });
 }
 
-// Sixteen results at element `elem`.
-template <int DST>
-__device__ __forceinline__ void store16(void* base, int64_t elem, const float (&x)[16]) {
-  if constexpr (DST == kBF16) {
-    uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + elem);
+// Eight elements of a row, piece `part` of it, as they lie in the tile of their
+// block and head.
+template <int SRC>
+struct Raw8 {
+  uint4 w;
+  __device__ __forceinline__ void load(const uint8_t* tile, int D, int block_size, int off, int part) {
+    if constexpr (SRC == kBF16) {
+      w = *reinterpret_cast<const uint4*>(tile + (off * D + part * 8) * 2);
+    } else if constexpr (SRC == kE4M3) {
+      const uint2 c = *reinterpret_cast<const uint2*>(tile + off * D + part * 8);
+      w.x = c.x;
+      w.y = c.y;
+    } else {
+      w.x = *reinterpret_cast<const uint32_t*>(tile + off * (D / 2) + part * 4);
+      w.y = tile[block_size * (D / 2) + off * (D / 16) + part / 2];
+    }
+  }
+  __device__ __forceinline__ void widen(float (&x)[8]) const {
+    if constexpr (SRC == kBF16) {
+      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      to[i] = make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]), pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
-                         pack_bf16x2(x[8 * i + 4], x[8 * i + 5]), pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16lo_to_f32(v[i]);
+        x[2 * i + 1] = bf16hi_to_f32(v[i]);
+      }
+    } else {
+      uint32_t h[4];
+      if constexpr (SRC == kE4M3) {
+        h[0] = e4m3x2_to_f16x2(static_cast<uint16_t>(w.x & 0xFFFFu));
+        h[1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w.x >> 16));
+        h[2] = e4m3x2_to_f16x2(static_cast<uint16_t>(w.y & 0xFFFFu));
+        h[3] = e4m3x2_to_f16x2(static_cast<uint16_t>(w.y >> 16));
+      } else {
+        const uint32_t s = e4m3x2_to_f16x2(static_cast<uint16_t>(w.y | (w.y << 8)));
+        e2m1x8_to_f16x2(w.x, h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = mul_f16x2(h[i], s);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = f16lo_to_f32(h[i]);
+        x[2 * i + 1] = f16hi_to_f32(h[i]);
+      }
+    }
+  }
+};
+
+// Eight results at element `elem`.
+template <int DST>
+__device__ __forceinline__ void store8(void* base, int64_t elem, const float (&x)[8]) {
+  if constexpr (DST == kBF16) {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + elem) =
+        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
   } else {
     float4* to = reinterpret_cast<float4*>(static_cast<float*>(base) + elem);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) to[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    to[0] = make_float4(x[0], x[1], x[2], x[3]);
+    to[1] = make_float4(x[4], x[5], x[6], x[7]);
   }
 }
 
-// Eight f16x2 as floats.
-__device__ __forceinline__ void widen16(const uint32_t (&h)[8], float (&x)[16]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = f16lo_to_f32(h[i]);
-    x[2 * i + 1] = f16hi_to_f32(h[i]);
-  }
-}
-
+// A thread per 8 elements of K and of V: 16 bytes of bf16, so that a warp writes
+// whole lines.
 template <int SRC, int DST>
 __global__ void __launch_bounds__(256) read_kernel(ReadParams p) {
   wait_prior_grid();
   allow_next_grid();
-  const int D = p.head_dim, H = p.num_kv_heads;
-  const int per_row = D / 16;
-  const int64_t total = p.n_tokens * H * per_row;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  const int64_t tile = SRC == kE2M1 ? e2m1_tile_bytes(D, p.block_size)
-                                    : static_cast<int64_t>(p.block_size) * D * (SRC == kBF16 ? 2 : 1);
-  for (int64_t idx = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; idx < total; idx += stride) {
-    const int64_t row = idx / per_row;  // token * H + head
-    const int part = static_cast<int>(idx - row * per_row);
-    const int64_t tok = row / H;
-    const int h = static_cast<int>(row - tok * H);
-    const int64_t slot = p.slots[tok];
-    const bool live = slot >= 0 && slot < p.num_slots;
-    if (slot >= p.num_slots && part == 0 && h == 0) record_error(p.err, kDevErrSlot);
-    const int64_t blk = live ? slot / p.block_size : 0;
-    const int off = live ? static_cast<int>(slot - blk * p.block_size) : 0;
+  const int D = p.head_dim, H = p.num_kv_heads, shift = p.block_size == 16 ? 4 : 5, to_row = D == 128 ? 4 : 3;
+  const int tile = SRC == kE2M1 ? e2m1_tile_bytes(D, p.block_size) : p.block_size * D * (SRC == kBF16 ? 2 : 1);
+  for_pieces(p.n_tokens, H << to_row, [&](int64_t tok, int i) {
+    const int64_t slot = p.slots[tok], to = tok * (H * D) + i * 8;
+    if (slot < 0 || slot >= p.num_slots) {
+      if (slot >= 0 && i == 0) record_error(p.err, kDevErrSlot);
+      const float zero[8] = {};
+      store8<DST>(p.k_out, to, zero);
+      store8<DST>(p.v_out, to, zero);
+      return;
+    }
+    const int h = i >> to_row, part = i & ((1 << to_row) - 1);
+    const int64_t base = tile_at(slot >> shift, H * tile) + h * tile;
+    const int off = static_cast<int>(slot) & (p.block_size - 1);
+    Raw8<SRC> raw[2];  // K's and V's, read together
+    raw[0].load(static_cast<const uint8_t*>(p.k_cache) + base, D, p.block_size, off, part);
+    raw[1].load(static_cast<const uint8_t*>(p.v_cache) + base, D, p.block_size, off, part);
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      float x[16];
-      if (live) {
-        const uint8_t* from = static_cast<const uint8_t*>(kv ? p.v_cache : p.k_cache) + (blk * H + h) * tile;
-        uint32_t hw[8];
-        if constexpr (SRC == kBF16) {
-          const uint4* q = reinterpret_cast<const uint4*>(from + (off * D + part * 16) * 2);
-          const uint4 a = q[0], b = q[1];
-          if constexpr (DST == kBF16) {  // bit for bit
-            uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(kv ? p.v_out : p.k_out) + row * D + part * 16);
-            to[0] = a;
-            to[1] = b;
-            continue;
-          }
-          const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[2 * i] = bf16lo_to_f32(w[i]);
-            x[2 * i + 1] = bf16hi_to_f32(w[i]);
-          }
-        } else if constexpr (SRC == kE4M3) {
-          const uint4 a = *reinterpret_cast<const uint4*>(from + off * D + part * 16);
-          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            hw[2 * i] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] & 0xFFFFu));
-            hw[2 * i + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i] >> 16));
-          }
-          widen16(hw, x);
-        } else {
-          const uint2 a = *reinterpret_cast<const uint2*>(from + off * (D / 2) + part * 8);
-          const uint32_t sc = from[p.block_size * (D / 2) + off * per_row + part];
-          const uint32_t s2 = e4m3x2_to_f16x2(static_cast<uint16_t>(sc | (sc << 8)));
-          uint32_t lo[4], hi[4];
-          e2m1x8_to_f16x2(a.x, lo);
-          e2m1x8_to_f16x2(a.y, hi);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            hw[i] = mul_f16x2(lo[i], s2);
-            hw[4 + i] = mul_f16x2(hi[i], s2);
-          }
-          widen16(hw, x);
-        }
+      void* out = kv ? p.v_out : p.k_out;
+      if constexpr (SRC == kBF16 && DST == kBF16) {  // bit for bit
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + to) = raw[kv].w;
+      } else {
+        float x[8];
+        raw[kv].widen(x);
         const float* scale = kv ? p.v_scale : p.k_scale;
         if (scale != nullptr) {
           const float s = scale[tok * p.scale_stride + h];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] *= s;
+          for (int e = 0; e < 8; ++e) x[e] *= s;
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = 0.f;
+        store8<DST>(out, to, x);
       }
-      store16<DST>(kv ? p.v_out : p.k_out, row * D + part * 16, x);
     }
-  }
+  });
 }
 
 // Slot of each new token: the block table's entry for the token's logical
@@ -253,6 +283,14 @@ __global__ void __launch_bounds__(256) slot_mapping_kernel(SlotParams p) {
   }
 }
 
+// for_pieces over tokens of `per_tok` pieces.
+template <class P>
+cudaError_t launch_pieces(void (*kern)(P), const P& p, int64_t per_tok, cudaStream_t stream) {
+  const dim3 block = per_tok < 256 ? dim3(static_cast<unsigned>(per_tok), static_cast<unsigned>(256 / per_tok)) : dim3(256);
+  const int64_t want = (p.n_tokens + block.y - 1) / block.y;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(want < 152 * 256 ? want : 152 * 256)), block, 0, stream, p);
+}
+
 }  // namespace
 
 cudaError_t launch_slot_mapping(const SlotParams& p, cudaStream_t stream) {
@@ -273,8 +311,6 @@ cudaError_t launch_slot_mapping(const SlotParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_read(const ReadParams& p, cudaStream_t stream) {
-  const int64_t want = (p.n_tokens * p.num_kv_heads * (p.head_dim / 16) + 255) / 256;
-  const dim3 grid(static_cast<unsigned>(want < 152 * 32 ? want : 152 * 32));
   void (*kern)(ReadParams);
   const bool bf = p.out_dtype == kBF16;
   if (p.cache_dtype == kBF16)
@@ -283,15 +319,15 @@ cudaError_t launch_read(const ReadParams& p, cudaStream_t stream) {
     kern = bf ? read_kernel<kE4M3, kBF16> : read_kernel<kE4M3, kF32>;
   else
     kern = bf ? read_kernel<kE2M1, kBF16> : read_kernel<kE2M1, kF32>;
-  return launch_pdl(kern, grid, dim3(256), 0, stream, p);
+  return launch_pieces(kern, p, static_cast<int64_t>(p.num_kv_heads) * (p.head_dim / 8), stream);
 }
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
   if (p.cache_dtype == kE2M1) {
-    const int64_t want = (p.n_tokens * p.num_kv_heads * (p.head_dim / kE2M1Group) + 255) / 256;
-    const dim3 grid(static_cast<unsigned>(want < 152 * 32 ? want : 152 * 32));
-    return launch_pdl(p.src_dtype == kBF16 ? append_e2m1_kernel<kBF16> : append_e2m1_kernel<kF32>, grid, dim3(256), 0,
-                      stream, p);
+    const bool bf = p.src_dtype == kBF16, scaled = p.k_scale != nullptr;
+    return launch_pieces(scaled ? (bf ? append_e2m1_kernel<kBF16, true> : append_e2m1_kernel<kF32, true>)
+                                : (bf ? append_e2m1_kernel<kBF16, false> : append_e2m1_kernel<kF32, false>),
+                         p, static_cast<int64_t>(p.num_kv_heads) * (p.head_dim / 8), stream);
   }
   const int64_t work = p.n_tokens * p.num_kv_heads * (p.head_dim / 8);
   if (work == 0) return cudaSuccess;

@@ -134,12 +134,6 @@ struct TcUnit {
   }
 };
 
-__device__ __forceinline__ float min_nan(float a, float b) {  // NaN if one is
-  float d;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
 // x := cap * tanh(x / cap) in log2 units for any x: a polynomial up to 0.35 of
 // the cap, else 1 - 2 / (e^2y + 1), one reciprocal shared by four scores,
 // 1 / a = b c d / (a b c d); 2y is held below 28 log2 units, where tanh is 1 to

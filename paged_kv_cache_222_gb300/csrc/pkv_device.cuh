@@ -275,6 +275,13 @@ __device__ __forceinline__ uint32_t bit_select(uint32_t mask, uint32_t a, uint32
   return d;
 }
 
+// The same of two bf16 pairs.
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // Byte permute: picks bytes of {b:a} by the 4 selector nibbles.
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t d;
@@ -359,15 +366,50 @@ __device__ __forceinline__ float abs_max8(const float (&x)[8]) {
   for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(x[i]));
   return m;
 }
-__device__ __forceinline__ uint8_t e2m1_group_scale(float abs_max) {
-  return static_cast<uint8_t>(f32x2_to_e4m3x2(__fdiv_rn(abs_max, 6.f), 0.f) & 0xFFu);
+// Which code a quotient x / s rounds to is decided by the side of the codes' borders
+// on which it lies (E2M1: 1/4, 3/4, 5/4, 7/4, 5/2, 7/2, 5; E4M3: numbers of five
+// bits); binary32 division puts it on a border t only if x = t s exactly, since
+// else it is further from t than half a last bit of t.  The same side without
+// dividing: y = x r with r near 1 / s is off by less than 2^-21 of itself; rounded to
+// 12 bits after the point it is t if x = t s, and x - y s is exact then, whose sign
+// moves it off again if x is not.
+__device__ __forceinline__ float side_of_quotient(float x, float s, float r) {
+  const float y = __uint_as_float((__float_as_uint(x * r) + 0x400u) & 0xFFFFF800u);
+  return fmaf(fmaf(-y, s, x), r, y);
 }
-__device__ __forceinline__ uint32_t e2m1_codes8(const float (&x)[8], uint8_t scale_code) {
+__device__ __forceinline__ float min_nan(float a, float b) {  // NaN if one is
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ uint8_t e2m1_group_scale(float abs_max) {
+  const float x = min_nan(abs_max, 3.4028234663852886e38f);  // (infinity minus infinity would be NaN)
+  return static_cast<uint8_t>(f32x2_to_e4m3x2(side_of_quotient(x, 6.f, 0.16666667f), 0.f) & 0xFFu);
+}
+// SHORT: sources of 8 bits (bf16 that no head's scale divides) need no second step:
+// X / (S t) with X < 256, S < 16 and t's two bits is 1 or at least 2^-8 away from it.
+// Borders are not reached past 8 s, where a group's scale has saturated: that is
+// divided.  Appending 16,384 tokens of 8 heads of 128 from bf16: 31.9 us with 17
+// divisions a group, 25.6 without; from binary32 34.4 and 30.6.
+template <bool SHORT>
+__device__ __forceinline__ uint32_t e2m1_codes8(const float (&x)[8], float abs_max, uint8_t scale_code) {
   const float s = f16lo_to_f32(e4m3x2_to_f16x2(scale_code));
   if (!(s > 0.f)) return 0u;
   float y[8];
+  if (abs_max <= 3584.f) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (SHORT)
+        y[i] = __uint_as_float((__float_as_uint(x[i] * r) + 0x400u) & 0xFFFFF800u);
+      else  // (the sign bit: of a negative zero's)
+        y[i] = __uint_as_float(__float_as_uint(side_of_quotient(x[i], s, r)) | (__float_as_uint(x[i]) & 0x80000000u));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+  }
   return f32x8_to_e2m1x8(y);
 }
 

@@ -112,12 +112,12 @@ __device__ __forceinline__ void store_e2m1(uint8_t* tile, int block_size, int of
     const float a = __shfl_sync(mask, mx, at), b = __shfl_sync(mask, my, at);
     return (split ? low : piece % 2 == 0) ? a : b;
   };
-  const uint8_t sx = e2m1_group_scale(max_nan(mx, from(px ^ 1)));
-  const uint8_t sy = e2m1_group_scale(max_nan(my, from(py ^ 1)));
+  const float gx = max_nan(mx, from(px ^ 1)), gy = max_nan(my, from(py ^ 1));  // of the pieces' groups
+  const uint8_t sx = e2m1_group_scale(gx), sy = e2m1_group_scale(gy);
   uint8_t* codes = tile + off * (D / 2);
   uint8_t* scales = tile + block_size * (D / 2) + off * LANES;
-  *reinterpret_cast<uint32_t*>(codes + px * 4) = e2m1_codes8(x, sx);
-  *reinterpret_cast<uint32_t*>(codes + py * 4) = e2m1_codes8(y, sy);
+  *reinterpret_cast<uint32_t*>(codes + px * 4) = e2m1_codes8<false>(x, gx, sx);
+  *reinterpret_cast<uint32_t*>(codes + py * 4) = e2m1_codes8<false>(y, gy, sy);
   if (px % 2 == 0) scales[px / 2] = sx;
   if (py % 2 == 0) scales[py / 2] = sy;
 }

@@ -169,6 +169,38 @@ __device__ __forceinline__ void cap_scores(float* x, float w_mult, float cap_log
   }
 }
 
+// tanh(y) = y P(y^2) for |y| <= kMidLimit, off by less than 4.4e-7 with binary32's own
+// rounding: 100 times that (the largest cap of these kernels) is below 2^-13 of a
+// weight.  The coefficients of the least largest error, the last one positive so
+// that -inf, a hidden score, stays that.  Ten packed FMA-pipe operations for two
+// weights' exponents, where the exponential form takes 2.25 special-function and
+// about 15 other operations for each: E2M1 caches, whose scores the groups' largest
+// channels bring past 0.35 of a cap, 3 chunks of 2000 over 1000 of 128-wide heads
+// with cap 30 1383 -> 730 us.
+constexpr float kMidLimit = 1.25f;
+__device__ __forceinline__ float2 mid_tanh(float2 x, float y_mult) {
+  const float2 u = __fmul2_rn(x, make_float2(y_mult, y_mult)), t = __fmul2_rn(u, u);
+  float2 q = make_float2(0.000525482697f, 0.000525482697f);
+  q = __ffma2_rn(q, t, make_float2(-0.00432548998f, -0.00432548998f));
+  q = __ffma2_rn(q, t, make_float2(0.0176362358f, 0.0176362358f));
+  q = __ffma2_rn(q, t, make_float2(-0.0516446903f, -0.0516446903f));
+  q = __ffma2_rn(q, t, make_float2(0.132648036f, 0.132648036f));
+  q = __ffma2_rn(q, t, make_float2(-0.333242148f, -0.333242148f));
+  q = __ffma2_rn(q, t, make_float2(0.999996483f, 0.999996483f));
+  return __fmul2_rn(u, q);
+}
+
+// Largest of N magnitudes.
+template <int N>
+__device__ __forceinline__ float abs_max(const float* x) {
+  float am[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) am[j] = max3f(am[j], fabsf(x[i + 2 * j]), fabsf(x[i + 2 * j + 1]));
+  return fmaxf(max3f(am[0], am[1], am[2]), am[3]);
+}
+
 // x := -inf where the key is not seen; words that every lane sees whole are
 // passed over.
 template <int N>
@@ -339,6 +371,7 @@ __global__ void __launch_bounds__(TcShape<D, KV, MODE>::THREADS, 1)
   constexpr int M = C::M, NK = C::NK, NS = C::NS, NR = C::NR, GROUPS = C::GROUPS, RU = C::RU;
   constexpr bool EARLY = C::EARLY, FAR = (MODE & kFar) != 0;
   constexpr int SCORE = MODE & ~kFar;
+  constexpr bool MID = KV == kE2M1 && !FAR;  // scores past the small ones' polynomial, up to kMidLimit caps
   // + g * NK, + g * (EARLY ? NK / 2 : NK), + g * D
   constexpr uint32_t COL_S = 0, COL_P = EARLY ? GROUPS * NK : COL_S, COL_O = COL_P + GROUPS * (EARLY ? NK / 2 : NK);
   constexpr uint32_t P_STEP = EARLY ? NK / 2 : NK;
@@ -787,16 +820,26 @@ __global__ void __launch_bounds__(TcShape<D, KV, MODE>::THREADS, 1)
           }
           // Capped: the row maximum is taken of the raw products (a cap does not
           // change which is the largest), the cap enters with the exponent.
-          bool small = false;
+          bool small = false, mid = false;
           if constexpr (SCORE == kCapped) {
-            float am[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < NK; i += 8)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) am[j] = max3f(am[j], fabsf(x[i + 2 * j]), fabsf(x[i + 2 * j + 1]));
-            small = __all_sync(kFull, poly.holds(fmaxf(max3f(am[0], am[1], am[2]), am[3])));
+            const float am = abs_max<NK>(x);
+            small = __all_sync(kFull, poly.holds(am));
+            if constexpr (MID) mid = !small && __all_sync(kFull, am * poly.y_mult <= kMidLimit);
           }
-          if constexpr (SCORE == kCappedBiased) cap_scores<NK, FAR>(x, qk, p.cap_log2, poly, masked, see);
+          if constexpr (SCORE == kCappedBiased) {
+            if constexpr (MID) mid = __all_sync(kFull, abs_max<NK>(x) * poly.y_mult <= kMidLimit);
+            if (mid) {
+#pragma unroll
+              for (int i = 0; i < NK; i += 2) {
+                const float2 z = __fmul2_rn(mid_tanh(make_float2(x[i], x[i + 1]), poly.y_mult),
+                                            make_float2(p.cap_log2, p.cap_log2));
+                x[i] = z.x;
+                x[i + 1] = z.y;
+              }
+            } else {
+              cap_scores<NK, FAR>(x, qk, p.cap_log2, poly, masked, see);
+            }
+          }
           if constexpr (SCORE == kBiased || SCORE == kCappedBiased) {
             const float mult = SCORE == kBiased ? qk : 1.f, base = slope * static_cast<float>(t0 - pos);
             const float2 mult2 = make_float2(mult, mult), slope2 = make_float2(slope, slope);
@@ -856,9 +899,11 @@ __global__ void __launch_bounds__(TcShape<D, KV, MODE>::THREADS, 1)
           }
           const float mu = m_used == -CUDART_INF_F ? 0.f : m_used;
           const float2 neg_mu = make_float2(-mu, -mu), mult2 = make_float2(qk, qk);
+          [[maybe_unused]] const float2 cap2 = make_float2(p.cap_log2, p.cap_log2);
           float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           // weights of the row, 2^(score - m), into S's columns; WAY: the scores
-          // are raw products, raw products to be capped, or done
+          // are raw products, raw products to be capped (small ones), done, or raw
+          // products to be capped (up to kMidLimit caps)
           auto weights = [&](auto way) {
             constexpr int WAY = decltype(way)::value;
 #pragma unroll
@@ -869,7 +914,8 @@ __global__ void __launch_bounds__(TcShape<D, KV, MODE>::THREADS, 1)
                 const float2 xx = make_float2(x[32 * c + 2 * i], x[32 * c + 2 * i + 1]);
                 const float2 e = WAY == 0   ? __ffma2_rn(xx, mult2, neg_mu)
                                  : WAY == 1 ? poly.minus(xx, neg_mu)
-                                            : __fadd2_rn(xx, neg_mu);
+                                 : WAY == 2 ? __fadd2_rn(xx, neg_mu)
+                                            : __ffma2_rn(mid_tanh(xx, poly.y_mult), cap2, neg_mu);
                 const float2 pp = make_float2(fast_exp2(e.x), fast_exp2(e.y));
                 ls[i & 1] = __fadd2_rn(ls[i & 1], pp);
                 hi[i] = WIDE ? pack_f16x2(pp.x, pp.y) : pack_bf16x2(pp.x, pp.y);
@@ -882,6 +928,8 @@ __global__ void __launch_bounds__(TcShape<D, KV, MODE>::THREADS, 1)
           } else if constexpr (SCORE == kCapped) {
             if (small) {
               weights(std::integral_constant<int, 1>{});
+            } else if (mid) {
+              weights(std::integral_constant<int, 3>{});
             } else {
               cap_scores<NK, FAR>(x, qk, p.cap_log2, poly, masked, see);
               if (masked) mask_scores<NK>(x, see);

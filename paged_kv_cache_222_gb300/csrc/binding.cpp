@@ -412,11 +412,12 @@ PyObject* read_tokens(PyObject* const* a, Py_ssize_t n_args) {
   return tuple({std::move(k), std::move(v)});
 }
 
-// `n` elements of a one-dimensional tensor from `at` on, as a tensor of their own
-// on the same storage.
-Tensor part(const Tensor& base, int64_t at, int64_t n) {
-  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()), base.key_set(), base.dtype());
-  t.unsafeGetTensorImpl()->set_storage_offset(base.storage_offset() + at);
+// `n` elements of `type` from byte `at` of a tensor's storage on, as a tensor of
+// their own.
+Tensor part(const Tensor& base, at::ScalarType type, int64_t at, int64_t n) {
+  const auto meta = c10::scalarTypeToTypeMeta(type);
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()), base.key_set(), meta);
+  t.unsafeGetTensorImpl()->set_storage_offset(at / static_cast<int64_t>(meta.itemsize()));
   t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
   return t;
 }
@@ -458,12 +459,13 @@ PyObject* extend_tables(PyObject* const* a, Py_ssize_t n_args) {
   static const char* const names[7] = {"out.context_lens", "out.q_starts",   "out.slot_mapping", "out.positions",
                                        "out.block_starts", "out.free_count", "out.lacking"};
   if (a[7] == Py_None) {
-    const Tensor i32 = at::empty({3 * b + 4}, tables.options()), i64 = at::empty({2 * most}, tables.options().dtype(at::kLong));
-    int64_t at32 = 0, at64 = 0;
+    // one allocation: the 64-bit arrays first
+    const Tensor all = at::empty({16 * most + 4 * (3 * b + 4)}, tables.options().dtype(at::kByte));
+    int64_t at64 = 0, at32 = 16 * most;
     for (int i = 0; i < 7; ++i) {
       const bool wide = i == 2 || i == 3;
-      r[i] = part(wide ? i64 : i32, wide ? at64 : at32, sizes[i]);
-      (wide ? at64 : at32) += sizes[i];
+      r[i] = part(all, wide ? at::kLong : at::kInt, wide ? at64 : at32, sizes[i]);
+      (wide ? at64 : at32) += (wide ? 8 : 4) * sizes[i];
     }
   } else {
     if (!PyTuple_Check(a[7]) || PyTuple_GET_SIZE(a[7]) != 7) raise(PyExc_TypeError, "out must be seven tensors");
@@ -500,7 +502,7 @@ PyObject* truncate_tables(PyObject* const* a, Py_ssize_t n_args) {
   const Tensor &ctx = ints(a[1], "context_lens", c.dev, b), &keep = ints(a[2], "keep_lens", c.dev, b);
   const Stack st = stack(a[3], a[4], c.dev);
   const Tensor mine = at::empty({b + 2}, tables.options());
-  const Tensor count = a[6] == Py_None ? part(mine, b + 1, 1) : ints(a[6], "out", c.dev, 1);
+  const Tensor count = a[6] == Py_None ? part(mine, at::kInt, 4 * (b + 1), 1) : ints(a[6], "out", c.dev, 1);
   const pkv_status s = on_stream(c.dev, [&](pkv_stream_t stream) {
     return g_truncate_tables(tables.const_data_ptr<int32_t>(), mb, batch, ctx.const_data_ptr<int32_t>(),
                              keep.const_data_ptr<int32_t>(), st.blocks.data_ptr<int32_t>(), st.capacity,

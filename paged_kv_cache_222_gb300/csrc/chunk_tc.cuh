@@ -95,7 +95,7 @@ struct TcShape {
   static constexpr int CODES = NK * RAWROW;
   static constexpr int RAW = CODES + (KV == kE2M1 ? 1024 : 0);
   static constexpr int NS = WIDE ? (D == 128 ? 3 : 6) : 131072 / TILE;
-  static constexpr int NR = WIDE ? (D == 128 ? 3 : 6) : 0;
+  static constexpr int NR = WIDE ? (D == 128 ? (KV == kE2M1 ? 4 : 3) : 6) : 0;
   static constexpr int SB = 64;                    // output staging of a softmax warp: SB bytes of its 32 rows
   static constexpr int STAGE = 32 * SB;
   static constexpr int RU = 4;                     // units in flight between the roles
@@ -108,8 +108,9 @@ struct TcShape {
   // get (a row's 128 scores; bf16 caches at 192 instead of 224: 570 us where it
   // takes 521); with E4M3 caches 200 / 56 spill least for plain scores of
   // 128-wide heads (614 us, 192 / 64: 617), 192 / 64 for all others (capped 862
-  // us, 200 / 56: 880)
-  static constexpr int REGS_SOFTMAX = !WIDE ? 224 : (D == 128 && MODE == kPlain ? 200 : 192);
+  // us, 200 / 56: 880); E2M1's widening has more to hold (12 chunks of 1-512: 200 /
+  // 56 264 us, 192 / 64 259, 184 / 72 261, 176 / 80 268)
+  static constexpr int REGS_SOFTMAX = !WIDE ? 224 : (D == 128 && MODE == kPlain && KV == kE4M3 ? 200 : 192);
   static constexpr int REGS_OTHER = WIDE && REGS_SOFTMAX == 192 ? 64 : 56;
   static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * (WIDE ? 128 : 168), "register file");
 };

@@ -3,11 +3,11 @@
 // what it computes: chunk_common.cuh, what a cache holds: pkv.h.
 //
 // A CTA takes the rows of one tile of one (sequence, KV head) over one split of
-// its visible keys, in 128-key steps: a warp loads its 32 or 64 keys of every step
-// (one bulk copy per block, of K and of V: a block's codes and scales lie behind
-// one another) into a ring of its own on barriers of its own, and refills a slot
-// as soon as it has read it; the warps merge (m, l, O) through shared memory at
-// the end.
+// its visible keys, in 128-key steps: a warp copies its 32 keys of every step (a
+// block's codes and scales lie behind one another) into a ring of its own and
+// refills a slot as soon as it has read it, waiting for no other warp; the warps
+// merge (m, l, O) through shared memory at the end.  The copies are the lanes' own
+// 16-byte ones: @@@
 //
 // Both products have keys as the first operand's rows or columns and up to 8
 // tile rows as the second's columns (NT of them: 1 or 2), mma.sync m16n8k16 of
@@ -45,8 +45,7 @@ struct E2M1Shape {
   static constexpr int DP = D + 4, R = 8 * NT;
   static constexpr int MERGE = WARPS * R * DP * 4 + WARPS * R * 2 * 4;
   static constexpr int RING = NS * WARPS * STAGE;
-  static constexpr int BYTES = (RING > MERGE ? RING : MERGE) + WARPS * NS * 8 +
-                               kChunkMaxSplitBlocks * 4 + 128;
+  static constexpr int BYTES = (RING > MERGE ? RING : MERGE) + kChunkMaxSplitBlocks * 4 + 128;
   // codes and scales of a group of 16 keys, from K's or V's start in a stage
   static constexpr int code_of(int g) { return 16 * g / BS * TILE + 16 * g % BS * ROWB; }
   static constexpr int scale_of(int g) { return 16 * g / BS * TILE + BS * ROWB + 16 * g % BS * SROWB; }
@@ -61,12 +60,15 @@ __device__ __forceinline__ int key_of(int i) {
   return (i & 14) | ((i & 1) ^ (D == 128 ? (i >> 1) & 1 : (i >> 2) & 1));
 }
 
-// Bulk copy global -> shared of `bytes` (a multiple of 16; both addresses 16-byte
-// aligned), completing on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
+// Copy 16 bytes global -> shared behind the thread's back, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait until the copies of all of this thread's groups but the last N have landed.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // MODS: scores that are capped or biased.  FAR: a cap above kCapNear.
@@ -88,14 +90,9 @@ __global__ void __launch_bounds__(E2M1Shape<D, NT, BS>::THREADS, E2M1Shape<D, NT
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + (C::RING > C::MERGE ? C::RING : C::MERGE));  // [NS][WARPS]
-  int* s_blk = reinterpret_cast<int*>(full + WARPS * NS);
+  int* s_blk = reinterpret_cast<int*>(smem + (C::RING > C::MERGE ? C::RING : C::MERGE));
   const uint32_t stage0 = smem_u32(smem) + warp * NS * C::STAGE;  // of this warp's ring
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < WARPS * NS; ++s) mbar_init(smem_u32(full + s), 1);
-    fence_mbar_init();
-  }
   wait_prior_grid();
 
   const ChunkSeq sq = chunk_seq(p, b, split == 0 && blockIdx.y == 0 && threadIdx.x == 0);
@@ -127,35 +124,33 @@ __global__ void __launch_bounds__(E2M1Shape<D, NT, BS>::THREADS, E2M1Shape<D, NT
   }
   __syncthreads();
 
-  // a warp's keys are one to four blocks: lane 2 bx + v loads block bx of K or V
-  constexpr uint32_t BAR = 8 * WARPS;                  // from a stage's barrier to the next's
-  const uint32_t bar0 = smem_u32(full) + 8 * warp;     // of stage 0
-  const int v = lane & 1, bx = lane >> 1;
-  const uint32_t box_to = stage0 + (v * C::NBLK + bx) * C::TILE;
-  const uint32_t blk0 = smem_u32(s_blk) + 4 * (warp * C::NBLK + bx);
-  const uint8_t* cache = static_cast<const uint8_t*>(v ? p.v_cache : p.k_cache) + static_cast<int64_t>(h) * C::TILE;
+  // A warp's step is K's blocks and then V's, as they lie in the cache: PER lanes
+  // copy one of them, 16 bytes each in turn, so that eight lanes read a line.
+  constexpr int PIECES = 2 * C::NBLK, PER = 32 / PIECES, TURNS = (C::TILE / 16 + PER - 1) / PER;
+  const int copied = lane / PER, sub = lane % PER;
+  const bool is_v = copied >= C::NBLK;
+  const uint8_t* cache = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache) +
+                         static_cast<int64_t>(h) * C::TILE + sub * 16;
   const int64_t block_bytes = static_cast<int64_t>(p.num_kv_heads) * C::TILE;
+  const uint32_t copy_to = stage0 + copied * C::TILE + sub * 16;
+  const uint32_t blk0 = smem_u32(s_blk) + 4 * (warp * C::NBLK + (is_v ? copied - C::NBLK : copied));
   auto issue = [&](int k, int s) {  // step k into stage s, which this warp has read
-    uint32_t phys[1] = {0u};
-    if (bx < C::NBLK) lds_words(blk0 + k * (4 * per_tile), phys);
-    const bool there = bx < C::NBLK && static_cast<int>(phys[0]) >= 0;
-    const uint32_t bytes = __popc(__ballot_sync(kFull, there)) * C::TILE;
-    if (lane == 0) {
-      fence_proxy_async_smem();  // this warp's reads of the slot come before the copies
-      mbar_arrive_expect_tx(bar0 + BAR * s, bytes);
-    }
-    __syncwarp();
-    const uint32_t to = box_to + s * C::STAGE;
-    if (there) {
-      bulk_load(to, cache + static_cast<int64_t>(phys[0]) * block_bytes, C::TILE, bar0 + BAR * s);
-    } else if (bx < C::NBLK) {  // no row sees the block: zeros
-      for (int i = 0; i < BS * C::SROWB; i += 16)
-        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to + BS * C::ROWB + i), "r"(0u) : "memory");
-    }
-    __syncwarp();
+    uint32_t phys[1];
+    lds_words(blk0 + k * (4 * per_tile), phys);
+    const bool there = static_cast<int>(phys[0]) >= 0;  // else no row sees the block: zeros
+    const uint8_t* from = there ? cache + static_cast<int64_t>(phys[0]) * block_bytes : cache;
+    const uint32_t to = copy_to + s * C::STAGE;
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i)
+      if ((i + 1) * PER * 16 <= C::TILE || i * PER + sub < C::TILE / 16)
+        copy16(to + i * PER * 16, from + i * PER * 16, there);
   };
   int issued = 0;
-  for (; issued < ntile && issued < NS; ++issued) issue(issued, issued);
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {  // a group per step, empty past the last
+    if (issued < ntile) issue(issued++, i);
+    copies_end();
+  }
 
   // Q as the second operand: row r of each n-tile; word c of the lane's quarter of
   // a row is two products, of d j D / 4 + 8 c + 0..3 and + 4..7
@@ -228,15 +223,13 @@ __global__ void __launch_bounds__(E2M1Shape<D, NT, BS>::THREADS, E2M1Shape<D, NT
   const uint32_t at_v0 = stage0 + VAT + kv0 * C::ROWB + r * VB, at_v1 = stage0 + VAT + kv1 * C::ROWB + r * VB;
   const uint32_t at_vs0 = stage0 + VAT + kv0 * C::SROWB + r * VB / 8, at_vs1 = stage0 + VAT + kv1 * C::SROWB + r * VB / 8;
 
-  bool healthy = true;
   int s = 0;
-  uint32_t parity = 0;
   for (int k = 0; k < ntile; ++k) {
-    const bool arrived = mbar_wait(bar0 + BAR * s, parity, p.err);
-    if (!__all_sync(kFull, arrived)) healthy = false;
+    copies_wait<NS - 1>();
+    __syncwarp();  // every lane's copies of this step have landed
     const uint32_t stage = s * C::STAGE;
     const int t_warp = rg.tile(k0 + k) * C::STEP + warp * C::KEYS;  // this warp's first key
-    if (healthy) {
+    {
       // ---- S^T of groups of 16 keys, two at a time: rows r, r + 8 (e >= 2) are keys
       // kr and kr + 8, columns 2 j, 2 j + 1 (odd e)
       float sc[NG][NT][4];
@@ -297,8 +290,9 @@ __global__ void __launch_bounds__(E2M1Shape<D, NT, BS>::THREADS, E2M1Shape<D, NT
             sv[g][i] = lds_byte((i & 1 ? at_vs1 : at_vs0) + stage + C::scale_of(g0 + g) + (i & 2 ? 8 * C::SROWB : 0));
           }
         if (g0 + 2 == NG) {
-          __syncwarp();
+          __syncwarp();  // every lane has read the slot
           if (issued < ntile) issue(issued++, s);
+          copies_end();
         }
       };
       load_v(0);
@@ -421,15 +415,7 @@ __global__ void __launch_bounds__(E2M1Shape<D, NT, BS>::THREADS, E2M1Shape<D, NT
         }
       }
     }
-    if (++s == NS) {
-      s = 0;
-      parity ^= 1u;
-    }
-  }
-  if (!healthy && lane == 0) {
-    // a copy of this warp's may still be landing: one more bounded wait each
-    for (int kk = issued > NS ? issued - NS : 0; kk < issued; ++kk)
-      mbar_wait(bar0 + BAR * (kk % NS), static_cast<uint32_t>((kk / NS) & 1), nullptr);
+    if (++s == NS) s = 0;
   }
   allow_next_grid();
 

@@ -110,7 +110,9 @@ typedef struct {
  *                  s = physical_block * block_size + offset; s < 0 skips the
  *                  row (padding).  s >= num_blocks * block_size is recorded in
  *                  the device error word and skipped.  Two rows with the same
- *                  slot in one call: which one lands is unspecified.
+ *                  slot in one call: which one lands is unspecified, and may be
+ *                  another one for each piece of the row (in an E2M1 cache for a
+ *                  group's codes and its scale).
  *   k_cache, v_cache  written in place (only the addressed slots change).
  *   k_scale, v_scale  E4M3 caches only (NULL otherwise): float32, row i and
  *                  KV head h use element [i * scale_row_stride + h];

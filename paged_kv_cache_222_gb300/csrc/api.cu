@@ -1521,7 +1521,7 @@ pkv_status chunk_plan(int32_t n_tokens, int32_t batch, int32_t max_q_len, int32_
       // each of up to 2048 tokens that nearly fill the round (64 of 1k-2k: 43 us,
       // two splits 49).  Else as for decode, from 1024 tokens.
       const bool eight = max_q_len * group <= 8;
-      const int64_t slots = sms * (e2m1 ? pkv::chunk_e2m1_ctas(c->head_dim, eight)
+      const int64_t slots = sms * (e2m1 ? pkv::chunk_e2m1_ctas(eight)
                                         : pkv::chunk_small_ctas(c->head_dim, c->dtype == PKV_E4M3, eight));
       const int64_t n = units > 0 ? slots / units : slots;
       st = n > 0 && !(all <= 1024 && units >= sms) ? ceil_div(ceil_div(all, n), 128) * 128 : all;

@@ -1,4 +1,5 @@
-// Pieces shared by the ragged-chunk attention kernels (chunk.cu, chunk_tc.cu):
+// Pieces shared by the ragged-chunk attention kernels (chunk.cu, chunk_e2m1.cu,
+// chunk_tc.cuh):
 // which sequence a token or a row tile belongs to, which keys a row tile sees,
 // and the scores' definition.
 //

@@ -7,7 +7,10 @@
 // block's codes and scales lie behind one another) into a ring of its own and
 // refills a slot as soon as it has read it, waiting for no other warp; the warps
 // merge (m, l, O) through shared memory at the end.  The copies are the lanes' own
-// 16-byte ones: @@@
+// 16-byte ones: a block of one head is 1152 bytes (576 with 64-wide heads), and
+// bulk copies of that size came no faster than one per 58 cycles and SM whatever
+// they hold (64 sequences of 512-8192 tokens, 64 + 8 heads of 128, 16-token blocks:
+// 85.5 us where this takes 77; tensor-map boxes of codes and of scales 90.5).
 //
 // Both products have keys as the first operand's rows or columns and up to 8
 // tile rows as the second's columns (NT of them: 1 or 2), mma.sync m16n8k16 of
@@ -25,6 +28,18 @@
 // the banks.  P is rounded to f16: at most 2^-11 of each weight, next to the
 // output's own 2^-8.  V past the sequence's end, and K and V of blocks that no
 // row sees, have scale 0 (codes are finite whatever they are).
+//
+// Bound: the HBM stream of 9/8 D bytes per visible key and KV head, and close
+// behind it the ALU: per 32 keys of 128 a warp issues about 600 instructions, 148
+// of them conversions, at half rate, of the 784 cycles that the stream leaves it.
+// 8 sequences of 131,072 tokens: 196 us with the merge, 6.2 TB/s, 91 % of the
+// measured copy; 64 of 512-8192 77 us, 4.5 TB/s, 66 %: CTAs of 16 steps, whose
+// start (lengths, table, first keys, one after another) and merge take 5 us, two
+// of them behind one another; 64-wide heads 50 us, 51 %, with the same overhead for
+// half the bytes.  Measured and not kept: five CTAs per SM (82 and 221 us: 96
+// registers), two warps of 32 keys per CTA and eight CTAs (80-93 and 196; windowed
+// single tokens 64 for 72, up to 16 rows 120 for 110), 64 keys per warp, equal
+// ranges of all steps per CTA (88 us: an SM's four CTAs even each other out already).
 
 #include "chunk_common.cuh"
 
@@ -33,14 +48,13 @@ namespace {
 
 template <int D, int NT, int BS>
 struct E2M1Shape {
-  static constexpr int STEP = kChunkE2M1Tile;               // keys of a step,
-  static constexpr int KEYS = chunk_e2m1_keys(D, NT == 1);  // and of a warp
+  static constexpr int STEP = kChunkE2M1Tile, KEYS = 32;    // keys of a step, and of a warp
   static constexpr int WARPS = STEP / KEYS, THREADS = 32 * WARPS, NG = KEYS / 16;
   static constexpr int ROWB = D / 2, SROWB = D / 16;        // bytes of a row's codes and scales
   static constexpr int TILE = BS * (ROWB + SROWB);          // of a block: its rows of codes, then of scales
   static constexpr int NBLK = KEYS / BS;                    // blocks of a warp's step
   static constexpr int STAGE = 2 * NBLK * TILE;             // a warp's step: K, then V
-  static constexpr int CTAS = chunk_e2m1_ctas(D, NT == 1);
+  static constexpr int CTAS = chunk_e2m1_ctas(NT == 1);
   static constexpr int NS = 2;
   static constexpr int DP = D + 4, R = 8 * NT;
   static constexpr int MERGE = WARPS * R * DP * 4 + WARPS * R * 2 * 4;

@@ -180,7 +180,7 @@ struct CopyParams {
 };
 
 // Attention of ragged chunks of new tokens over the paged cache (chunk.cu,
-// chunk_tc.cu).  Sequence b owns query rows [q_starts[b], q_starts[b + 1]);
+// chunk_e2m1.cu, chunk_tc.cuh).  Sequence b owns query rows [q_starts[b], q_starts[b + 1]);
 // query i of its n sits at position context_lens[b] - n + i.
 struct ChunkParams {
   const void* q;                 // bf16 [T, H_q, D]
@@ -382,14 +382,11 @@ constexpr int kChunkMaxSplitBlocks = 1024;
 // still 32-bit numbers.
 constexpr int kChunkMaxContext = 0x7FFFFF00;
 // Keys per tile: of the mma.sync kernels; of the tcgen05 kernel at most, and by
-// its variant (chunk_tc.cu: whether S(k+1) is issued ahead of P(k)'s product).
+// its variant (chunk_tc.cuh: whether S(k+1) is issued ahead of P(k)'s product).
 constexpr int kChunkSmallTile = 64, kChunkE2M1Tile = 128, kChunkTcTile = 128;
-// CTAs per SM of the mma.sync kernels, by the bytes of a 64-key step (chunk.cu),
-// and over E2M1 caches (chunk_e2m1.cu).
-constexpr int chunk_e2m1_keys(int head_dim, bool eight_rows) { return 32; }  // of a warp's step
-constexpr int chunk_e2m1_ctas(int head_dim, bool eight_rows) {
-  return (eight_rows ? 4 : 3) * (chunk_e2m1_keys(head_dim, eight_rows) / 32);
-}
+// CTAs per SM of the mma.sync kernels: over E2M1 caches (chunk_e2m1.cu), and by
+// the bytes of a 64-key step over others (chunk.cu).
+constexpr int chunk_e2m1_ctas(bool eight_rows) { return eight_rows ? 4 : 3; }
 constexpr int chunk_small_ctas(int head_dim, bool fp8, bool eight_rows) {
   const int stage = 2 * kChunkSmallTile * head_dim * (fp8 ? 1 : 2);
   return !eight_rows || stage >= 32768 ? 3 : (stage == 16384 ? 4 : 5);

@@ -17,7 +17,9 @@
 // may have the plan overwrite in place: past_b = context_b - new_b, the old count
 // = the new one + what was taken.  Up to kInline items the plan's own CTA fills
 // (one launch).  Bound: latency, of a launch, the lengths, the scan, a free id or
-// table entry, a store; 16 bytes per token written.
+// table entry, a store.  On the GPU 256 single tokens take 3.3 us, 120,570 tokens of
+// 1024 requests 7.5 (two launches), 69,000 freed blocks 3.9; a call costs 6.5-10 us
+// of the host's time, most of it for the seven outputs.
 
 #include <algorithm>
 

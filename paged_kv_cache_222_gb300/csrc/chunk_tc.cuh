@@ -179,16 +179,22 @@ __device__ __forceinline__ void cap_scores(float* x, float w_mult, float cap_log
 // channels bring past 0.35 of a cap, 3 chunks of 2000 over 1000 of 128-wide heads
 // with cap 30 1383 -> 730 us.
 constexpr float kMidLimit = 1.25f;
-__device__ __forceinline__ float2 mid_tanh(float2 x, float y_mult) {
-  const float2 u = __fmul2_rn(x, make_float2(y_mult, y_mult)), t = __fmul2_rn(u, u);
-  float2 q = make_float2(0.000525482697f, 0.000525482697f);
-  q = __ffma2_rn(q, t, make_float2(-0.00432548998f, -0.00432548998f));
-  q = __ffma2_rn(q, t, make_float2(0.0176362358f, 0.0176362358f));
-  q = __ffma2_rn(q, t, make_float2(-0.0516446903f, -0.0516446903f));
-  q = __ffma2_rn(q, t, make_float2(0.132648036f, 0.132648036f));
-  q = __ffma2_rn(q, t, make_float2(-0.333242148f, -0.333242148f));
-  q = __ffma2_rn(q, t, make_float2(0.999996483f, 0.999996483f));
-  return __fmul2_rn(u, q);
+template <int N>
+__device__ __forceinline__ void mid_tanh(float2* x, float y_mult) {
+  constexpr float kC[7] = {0.999996483f, -0.333242148f, 0.132648036f, -0.0516446903f, 0.0176362358f, -0.00432548998f, 0.000525482697f};
+  float2 t[N], q[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = __fmul2_rn(x[i], make_float2(y_mult, y_mult));
+    t[i] = __fmul2_rn(x[i], x[i]);
+    q[i] = make_float2(kC[6], kC[6]);
+  }
+#pragma unroll
+  for (int c = 5; c >= 0; --c)
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = __ffma2_rn(q[i], t[i], make_float2(kC[c], kC[c]));
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = __fmul2_rn(x[i], q[i]);
 }
 
 // Largest of N magnitudes.
@@ -200,6 +206,20 @@ __device__ __forceinline__ float abs_max(const float* x) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) am[j] = max3f(am[j], fabsf(x[i + 2 * j]), fabsf(x[i + 2 * j + 1]));
   return fmaxf(max3f(am[0], am[1], am[2]), am[3]);
+}
+
+// Largest of N scores.
+template <int N>
+__device__ __forceinline__ float row_max(const float* x) {
+  float mp[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    mp[j] = max3f(x[j], x[8 + j], x[16 + j]);
+#pragma unroll
+    for (int i = 24; i + 8 < N; i += 16) mp[j] = max3f(mp[j], x[i + j], x[i + 8 + j]);
+    mp[j] = fmaxf(mp[j], x[N - 8 + j]);
+  }
+  return max3f(max3f(mp[0], mp[1], mp[2]), max3f(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
 }
 
 // x := -inf where the key is not seen; words that every lane sees whole are
@@ -373,6 +393,7 @@ __global__ void __launch_bounds__(TcShape<D, KV, MODE>::THREADS, 1)
   constexpr bool EARLY = C::EARLY, FAR = (MODE & kFar) != 0;
   constexpr int SCORE = MODE & ~kFar;
   constexpr bool MID = KV == kE2M1 && !FAR;  // scores past the small ones' polynomial, up to kMidLimit caps
+  constexpr bool PARTS = MID && SCORE == kCapped;
   // + g * NK, + g * (EARLY ? NK / 2 : NK), + g * D
   constexpr uint32_t COL_S = 0, COL_P = EARLY ? GROUPS * NK : COL_S, COL_O = COL_P + GROUPS * (EARLY ? NK / 2 : NK);
   constexpr uint32_t P_STEP = EARLY ? NK / 2 : NK;
@@ -797,92 +818,29 @@ __global__ void __launch_bounds__(TcShape<D, KV, MODE>::THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         if (warp_ok) {
-          float x[NK];
-#pragma unroll
-          for (int c = 0; c < NK / 32; ++c) tmem_ld32(t_s + 32 * c, x + 32 * c);
-          tmem_wait_ld();
-          if constexpr (EARLY) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(sfree + grp));  // S may be overwritten
-          }
           const int t0 = u.tile(k) * NK;
           const bool whole = (t0 + NK - 1 <= pos && t0 >= lo) || t0 + NK <= pf;
           const bool masked = !__all_sync(kFull, whole);
-          uint32_t see[NK / 32];  // bit i of word w: key t0 + 32 w + i is seen
-          if (masked) {
-            auto below = [&](int n, int w) {  // the first n keys of the tile
-              n -= 32 * w;
-              return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
-            };
-#pragma unroll
-            for (int w = 0; w < NK / 32; ++w)
-              see[w] = (below(pos - t0 + 1, w) & ~below(lo - t0, w)) | below(pf - t0, w);
-          }
-          // Capped: the row maximum is taken of the raw products (a cap does not
-          // change which is the largest), the cap enters with the exponent.
-          bool small = false, mid = false;
-          if constexpr (SCORE == kCapped) {
-            const float am = abs_max<NK>(x);
-            small = __all_sync(kFull, poly.holds(am));
-            if constexpr (MID) mid = !small && __all_sync(kFull, am * poly.y_mult <= kMidLimit);
-          }
-          if constexpr (SCORE == kCappedBiased) {
-            if constexpr (MID) mid = __all_sync(kFull, abs_max<NK>(x) * poly.y_mult <= kMidLimit);
-            if (mid) {
-#pragma unroll
-              for (int i = 0; i < NK; i += 2) {
-                const float2 z = __fmul2_rn(mid_tanh(make_float2(x[i], x[i + 1]), poly.y_mult),
-                                            make_float2(p.cap_log2, p.cap_log2));
-                x[i] = z.x;
-                x[i + 1] = z.y;
-              }
-            } else {
-              cap_scores<NK, FAR>(x, qk, p.cap_log2, poly, masked, see);
-            }
-          }
-          if constexpr (SCORE == kBiased || SCORE == kCappedBiased) {
-            const float mult = SCORE == kBiased ? qk : 1.f, base = slope * static_cast<float>(t0 - pos);
-            const float2 mult2 = make_float2(mult, mult), slope2 = make_float2(slope, slope);
-            const float2 base2 = make_float2(base, base);
-#pragma unroll
-            for (int i = 0; i < NK; i += 2) {
-              const float2 at = make_float2(static_cast<float>(i), static_cast<float>(i + 1));
-              const float2 z = __ffma2_rn(make_float2(x[i], x[i + 1]), mult2, __ffma2_rn(slope2, at, base2));
-              x[i] = z.x;
-              x[i + 1] = z.y;
-            }
-          }
-          if (masked) mask_scores<NK>(x, see);
-          float mt;
-          {
-            float mp[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              mp[j] = max3f(x[j], x[8 + j], x[16 + j]);
-#pragma unroll
-              for (int i = 24; i + 8 < NK; i += 16) mp[j] = max3f(mp[j], x[i + j], x[i + 8 + j]);
-              mp[j] = fmaxf(mp[j], x[NK - 8 + j]);
-            }
-            mt = max3f(max3f(mp[0], mp[1], mp[2]), max3f(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7]));
-            if constexpr (SCORE == kPlain) mt *= qk;
-            if constexpr (SCORE == kCapped) mt = mt == -CUDART_INF_F ? mt : capped<FAR>(mt, qk, p.cap_log2, poly);
-          }
+          auto below = [&](int n, int w) {  // the first n keys of the tile, as bits of word w
+            n -= 32 * w;
+            return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
+          };
+          auto seen = [&](int w) {  // bit i: key t0 + 32 w + i is seen
+            return (below(pos - t0 + 1, w) & ~below(lo - t0, w)) | below(pf - t0, w);
+          };
           float alpha = 1.f;
           bool resc = false;
-          if (m_used == -CUDART_INF_F) {
-            m_used = mt;  // nothing accumulated yet for this row
-          } else if (row_ok && mt > m_used + 8.f) {
-            alpha = fast_exp2(m_used - mt);
-            m_used = mt;
-            resc = true;
-          }
-          if (EARLY && sk > 0) {  // P(k-1)'s product has read it (and O holds tiles 0..k-1)
-            ok = wait(pfree + grp, sk - 1);
-            if (!ok) break;
-            tc_fence_after();
-          }
-          if (__any_sync(kFull, resc)) {  // O holds tiles 0..k-1 (else PV(k-1) came before S(k))
+          auto grow = [&](float mt) {  // the row's maximum of this tile
+            if (m_used == -CUDART_INF_F) {
+              m_used = mt;  // nothing accumulated yet for this row
+            } else if (row_ok && mt > m_used + 8.f) {
+              alpha = fast_exp2(m_used - mt);
+              m_used = mt;
+              resc = true;
+            }
+          };
+          auto rescale = [&]() {
+            if (!__any_sync(kFull, resc)) return;  // O holds tiles 0..k-1 (else PV(k-1) came before S(k))
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += 32) {
               uint32_t u[2][16];
@@ -897,47 +855,169 @@ __global__ void __launch_bounds__(TcShape<D, KV, MODE>::THREADS, 1)
               tmem_st16(t_o + c0 + 16, u[1]);
             }
             lsum *= alpha;
-          }
-          const float mu = m_used == -CUDART_INF_F ? 0.f : m_used;
-          const float2 neg_mu = make_float2(-mu, -mu), mult2 = make_float2(qk, qk);
-          [[maybe_unused]] const float2 cap2 = make_float2(p.cap_log2, p.cap_log2);
+          };
           float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          // weights of the row, 2^(score - m), into S's columns; WAY: the scores
-          // are raw products, raw products to be capped (small ones), done, or raw
+          // weights of 32 keys, 2^(score - m), into S's columns; WAY: the scores are
+          // raw products, raw products to be capped (small ones), done, or raw
           // products to be capped (up to kMidLimit caps)
-          auto weights = [&](auto way) {
+          auto weights = [&](auto way, int c, const float* x) {
             constexpr int WAY = decltype(way)::value;
+            const float mu = m_used == -CUDART_INF_F ? 0.f : m_used;
+            const float2 neg_mu = make_float2(-mu, -mu), mult2 = make_float2(qk, qk);
+            [[maybe_unused]] const float2 cap2 = make_float2(p.cap_log2, p.cap_log2);
+            uint32_t hi[16];
+            float2 e[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 xx = make_float2(x[2 * i], x[2 * i + 1]);
+              if constexpr (WAY == 3)
+                e[i] = xx;
+              else
+                e[i] = WAY == 0 ? __ffma2_rn(xx, mult2, neg_mu) : WAY == 1 ? poly.minus(xx, neg_mu) : __fadd2_rn(xx, neg_mu);
+            }
+            if constexpr (WAY == 3) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                mid_tanh<4>(e + i, poly.y_mult);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) e[i + j] = __ffma2_rn(e[i + j], cap2, neg_mu);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 pp = make_float2(fast_exp2(e[i].x), fast_exp2(e[i].y));
+              ls[i & 1] = __fadd2_rn(ls[i & 1], pp);
+              hi[i] = WIDE ? pack_f16x2(pp.x, pp.y) : pack_bf16x2(pp.x, pp.y);
+            }
+            tmem_st16(t_p + 16 * c, hi);
+          };
+          if constexpr (PARTS) {
+            // Scores that are not all small are read again, in parts of 32 that each
+            // take their own way, by a loop whose code stays in the instruction cache
+            // (the whole row's code for each way: 5 prompts of 301-1777, 28 + 4 heads
+            // of 64, cap 30 75 us, this 62; all rows in parts 60, but 437 us for 345
+            // where all are small, 4 chunks of 512 over 3584 of 128-wide heads).  P's
+            // part takes columns that have been read.
+            uint32_t ways = 0u;  // of each part: 0 small, 1 up to kMidLimit caps, 2 beyond
+            float x[NK];
+#pragma unroll
+            for (int c = 0; c < NK / 32; ++c) tmem_ld32(t_s + 32 * c, x + 32 * c);
+            tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < NK / 32; ++c) {
-              uint32_t hi[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float2 xx = make_float2(x[32 * c + 2 * i], x[32 * c + 2 * i + 1]);
-                const float2 e = WAY == 0   ? __ffma2_rn(xx, mult2, neg_mu)
-                                 : WAY == 1 ? poly.minus(xx, neg_mu)
-                                 : WAY == 2 ? __fadd2_rn(xx, neg_mu)
-                                            : __ffma2_rn(mid_tanh(xx, poly.y_mult), cap2, neg_mu);
-                const float2 pp = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-                ls[i & 1] = __fadd2_rn(ls[i & 1], pp);
-                hi[i] = WIDE ? pack_f16x2(pp.x, pp.y) : pack_bf16x2(pp.x, pp.y);
-              }
-              tmem_st16(t_p + 16 * c, hi);
+              const float am = abs_max<32>(x + 32 * c);
+              const bool small = __all_sync(kFull, poly.holds(am)), mid = __all_sync(kFull, am * poly.y_mult <= kMidLimit);
+              ways |= (small ? 0u : mid ? 1u : 2u) << (2 * c);
             }
-          };
-          if constexpr (SCORE == kPlain) {
-            weights(std::integral_constant<int, 0>{});
-          } else if constexpr (SCORE == kCapped) {
-            if (small) {
-              weights(std::integral_constant<int, 1>{});
-            } else if (mid) {
-              weights(std::integral_constant<int, 3>{});
+            if (masked) {
+#pragma unroll
+              for (int c = 0; c < NK / 32; ++c) {
+                const uint32_t see = seen(c);
+                mask_scores<32>(x + 32 * c, &see);
+              }
+            }
+            float mt = row_max<NK>(x);
+            mt = mt == -CUDART_INF_F ? mt : capped<FAR>(mt, qk, p.cap_log2, poly);
+            grow(mt);
+            rescale();
+            if (ways == 0u) {
+#pragma unroll
+              for (int c = 0; c < NK / 32; ++c) weights(std::integral_constant<int, 1>{}, c, x + 32 * c);
             } else {
-              cap_scores<NK, FAR>(x, qk, p.cap_log2, poly, masked, see);
-              if (masked) mask_scores<NK>(x, see);
-              weights(std::integral_constant<int, 2>{});
+#pragma unroll 1
+              for (int c = 0; c < NK / 32; ++c, ways >>= 2) {
+                float x[32];
+                tmem_ld32(t_s + 32 * c, x);
+                tmem_wait_ld();
+                const uint32_t way = ways & 3u, see = masked ? seen(c) : 0xFFFFFFFFu;
+                if (way == 2u) cap_scores<32, FAR>(x, qk, p.cap_log2, poly, masked, &see);
+                if (masked) mask_scores<32>(x, &see);
+                if (way == 0u)
+                  weights(std::integral_constant<int, 1>{}, c, x);
+                else if (way == 1u)
+                  weights(std::integral_constant<int, 3>{}, c, x);
+                else
+                  weights(std::integral_constant<int, 2>{}, c, x);
+              }
             }
           } else {
-            weights(std::integral_constant<int, 2>{});
+            float x[NK];
+#pragma unroll
+            for (int c = 0; c < NK / 32; ++c) tmem_ld32(t_s + 32 * c, x + 32 * c);
+            tmem_wait_ld();
+            if constexpr (EARLY) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(sfree + grp));  // S may be overwritten
+            }
+            uint32_t see[NK / 32];
+            if (masked) {
+#pragma unroll
+              for (int w = 0; w < NK / 32; ++w) see[w] = seen(w);
+            }
+            // Capped: the row maximum is taken of the raw products (a cap does not
+            // change which is the largest), the cap enters with the exponent.
+            bool small = false, mid = false;
+            if constexpr (SCORE == kCapped) small = __all_sync(kFull, poly.holds(abs_max<NK>(x)));
+            if constexpr (SCORE == kCappedBiased) {
+              if constexpr (MID) mid = __all_sync(kFull, abs_max<NK>(x) * poly.y_mult <= kMidLimit);
+              if (mid) {
+#pragma unroll
+                for (int i = 0; i < NK; i += 16) {
+                  float2 z[8];
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) z[j] = make_float2(x[i + 2 * j], x[i + 2 * j + 1]);
+                  mid_tanh<8>(z, poly.y_mult);
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) {
+                    x[i + 2 * j] = z[j].x * p.cap_log2;
+                    x[i + 2 * j + 1] = z[j].y * p.cap_log2;
+                  }
+                }
+              } else {
+                cap_scores<NK, FAR>(x, qk, p.cap_log2, poly, masked, see);
+              }
+            }
+            if constexpr (SCORE == kBiased || SCORE == kCappedBiased) {
+              const float mult = SCORE == kBiased ? qk : 1.f, base = slope * static_cast<float>(t0 - pos);
+              const float2 mult2 = make_float2(mult, mult), slope2 = make_float2(slope, slope);
+              const float2 base2 = make_float2(base, base);
+#pragma unroll
+              for (int i = 0; i < NK; i += 2) {
+                const float2 at = make_float2(static_cast<float>(i), static_cast<float>(i + 1));
+                const float2 z = __ffma2_rn(make_float2(x[i], x[i + 1]), mult2, __ffma2_rn(slope2, at, base2));
+                x[i] = z.x;
+                x[i + 1] = z.y;
+              }
+            }
+            if (masked) mask_scores<NK>(x, see);
+            float mt = row_max<NK>(x);
+            if constexpr (SCORE == kPlain) mt *= qk;
+            if constexpr (SCORE == kCapped) mt = mt == -CUDART_INF_F ? mt : capped<FAR>(mt, qk, p.cap_log2, poly);
+            grow(mt);
+            if (EARLY && sk > 0) {  // P(k-1)'s product has read it (and O holds tiles 0..k-1)
+              ok = wait(pfree + grp, sk - 1);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            rescale();
+            auto each = [&](auto way) {
+#pragma unroll
+              for (int c = 0; c < NK / 32; ++c) weights(way, c, x + 32 * c);
+            };
+            if constexpr (SCORE == kPlain) {
+              each(std::integral_constant<int, 0>{});
+            } else if constexpr (SCORE == kCapped) {
+              if (small) {
+                each(std::integral_constant<int, 1>{});
+              } else {
+                cap_scores<NK, FAR>(x, qk, p.cap_log2, poly, masked, see);
+                if (masked) mask_scores<NK>(x, see);
+                each(std::integral_constant<int, 2>{});
+              }
+            } else {
+              each(std::integral_constant<int, 2>{});
+            }
           }
           lsum += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
           tmem_wait_st();

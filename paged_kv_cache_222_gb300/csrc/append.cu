@@ -15,7 +15,7 @@
 // E2M1 caches: a thread per group of 16 elements, 8 code bytes and a scale byte
 // (how codes are found without dividing: pkv_device.cuh).  Bound: the bytes, and
 // the ALU beside them (14 instructions per element): 16,384 tokens of 8 heads of 128
-// from bf16 25.6 us, 3.4 TB/s; 8 elements of K and of V per thread, whose group's
+// from bf16 21.9 us, 3.9 TB/s; 8 elements of K and of V per thread, whose group's
 // largest magnitude two lanes exchange, 26-34 us.
 //
 // read_kernel is the way back: a thread per 8 elements of a (token, head) row
@@ -93,8 +93,10 @@ __device__ __forceinline__ int64_t tile_at(int64_t block, int block_bytes) {
 }
 
 // A thread per group of 16 elements of K or of V.  SCALED: with heads' scales.
+// From bf16, held to the 40 registers of 6 CTAs per SM (45 and 5: 24.2 us for 21.9; 7
+// CTAs 25.7).
 template <int SRC, bool SCALED>
-__global__ void __launch_bounds__(256) append_e2m1_kernel(AppendParams p) {
+__global__ void __launch_bounds__(256, SRC == kBF16 ? 6 : 1) append_e2m1_kernel(AppendParams p) {
   wait_prior_grid();
   allow_next_grid();
   const int D = p.head_dim, H = p.num_kv_heads, shift = p.block_size == 16 ? 4 : 5, to_row = D == 128 ? 3 : 2;

@@ -453,7 +453,7 @@ PyObject* extend_tables(PyObject* const* a, Py_ssize_t n_args) {
   const Tensor &past = ints(a[1], "past_lens", c.dev, b), &news = ints(a[2], "new_lens", c.dev, b);
   const Stack st = stack(a[3], a[4], c.dev);
   const int64_t most = integer(a[6], "max_tokens");
-  if (most < 0) raise(PyExc_ValueError, "max_tokens %lld", static_cast<long long>(most));
+  if (most < 0 || most > 0x7FFFFFFF) raise(PyExc_ValueError, "max_tokens %lld", static_cast<long long>(most));
   Tensor r[7];  // context_lens, q_starts, slot_mapping, positions, block_starts, free_count, lacking
   const int64_t sizes[7] = {b, b + 1, most, most, b + 1, 1, 1};
   static const char* const names[7] = {"out.context_lens", "out.q_starts",   "out.slot_mapping", "out.positions",

@@ -30,16 +30,17 @@
 // row sees, have scale 0 (codes are finite whatever they are).
 //
 // Bound: the HBM stream of 9/8 D bytes per visible key and KV head, and close
-// behind it the ALU: per 32 keys of 128 a warp issues about 600 instructions, 148
-// of them conversions, at half rate, of the 784 cycles that the stream leaves it.
-// 8 sequences of 131,072 tokens: 196 us with the merge, 6.2 TB/s, 91 % of the
-// measured copy; 64 of 512-8192 77 us, 4.5 TB/s, 66 %: CTAs of 16 steps, whose
-// start (lengths, table, first keys, one after another) and merge take 5 us, two
-// of them behind one another; 64-wide heads 50 us, 51 %, with the same overhead for
-// half the bytes.  Measured and not kept: five CTAs per SM (82 and 221 us: 96
-// registers), two warps of 32 keys per CTA and eight CTAs (80-93 and 196; windowed
+// behind it the instructions: 647 of a warp per 32 keys of 128 (253 of them the
+// ALU's, 148 of those conversions), of the 800 cycles that the stream leaves it.
+// 8 sequences of 131,072 tokens: 195 us with the merge, 6.2 TB/s, 91 % of the
+// measured copy; 64 of 512-8192 76 us, 4.6 TB/s, 68 %: a CTA's start (lengths,
+// table, first keys, one after another) and end cost 1.2 us of its SM's time each
+// time (200 sequences of 200: 23 us for 7.5 of bytes), and shorter ones, longer ones
+// or none ahead of others come to the same; 64-wide heads 50 us, 51 %, with the same
+// cost for half the bytes.  Measured and not kept: five CTAs per SM (83 and 221 us:
+// 96 registers), two warps of 32 keys per CTA and eight CTAs (80-93 and 196; windowed
 // single tokens 64 for 72, up to 16 rows 120 for 110), 64 keys per warp, equal
-// ranges of all steps per CTA (88 us: an SM's four CTAs even each other out already).
+// ranges of all steps per CTA (88 us for 85 before the lanes' copies).
 
 #include "chunk_common.cuh"
 

@@ -309,3 +309,13 @@ def test_a_serving_run(captured):
         assert n == nb - sum(map(len, held))
         assert sorted(free[:n].tolist() + sum(held, [])) == list(range(nb))
         lens.copy_(keep)                             # the next step's past
+
+
+@pytest.mark.parametrize("most", [1 << 31, 1 << 62, -1])
+def test_more_tokens_than_a_call_takes_are_refused_before_memory_is_taken(most):
+    table, free, nb = make([10], [1], 16)
+    t, p, n, f, c, cache = up(table), up([10]), up([1]), up(free), up([len(free)]), cache_of(nb, 16)
+    held = torch.cuda.memory_allocated()
+    with pytest.raises(ValueError):
+        pkv.extend_tables(t, p, n, f, c, cache, most)
+    assert torch.cuda.memory_allocated() == held

@@ -179,22 +179,16 @@ __device__ __forceinline__ void cap_scores(float* x, float w_mult, float cap_log
 // channels bring past 0.35 of a cap, 3 chunks of 2000 over 1000 of 128-wide heads
 // with cap 30 1383 -> 730 us.
 constexpr float kMidLimit = 1.25f;
-template <int N>
-__device__ __forceinline__ void mid_tanh(float2* x, float y_mult) {
-  constexpr float kC[7] = {0.999996483f, -0.333242148f, 0.132648036f, -0.0516446903f, 0.0176362358f, -0.00432548998f, 0.000525482697f};
-  float2 t[N], q[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    x[i] = __fmul2_rn(x[i], make_float2(y_mult, y_mult));
-    t[i] = __fmul2_rn(x[i], x[i]);
-    q[i] = make_float2(kC[6], kC[6]);
-  }
-#pragma unroll
-  for (int c = 5; c >= 0; --c)
-#pragma unroll
-    for (int i = 0; i < N; ++i) q[i] = __ffma2_rn(q[i], t[i], make_float2(kC[c], kC[c]));
-#pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = __fmul2_rn(x[i], q[i]);
+__device__ __forceinline__ float2 mid_tanh(float2 x, float y_mult) {
+  const float2 u = __fmul2_rn(x, make_float2(y_mult, y_mult)), t = __fmul2_rn(u, u);
+  float2 q = make_float2(0.000525482697f, 0.000525482697f);
+  q = __ffma2_rn(q, t, make_float2(-0.00432548998f, -0.00432548998f));
+  q = __ffma2_rn(q, t, make_float2(0.0176362358f, 0.0176362358f));
+  q = __ffma2_rn(q, t, make_float2(-0.0516446903f, -0.0516446903f));
+  q = __ffma2_rn(q, t, make_float2(0.132648036f, 0.132648036f));
+  q = __ffma2_rn(q, t, make_float2(-0.333242148f, -0.333242148f));
+  q = __ffma2_rn(q, t, make_float2(0.999996483f, 0.999996483f));
+  return __fmul2_rn(u, q);
 }
 
 // Largest of N magnitudes.
@@ -819,8 +813,7 @@ __global__ void __launch_bounds__(TcShape<D, KV, MODE>::THREADS, 1)
         tc_fence_after();
         if (warp_ok) {
           const int t0 = u.tile(k) * NK;
-          const bool whole = (t0 + NK - 1 <= pos && t0 >= lo) || t0 + NK <= pf;
-          const bool masked = !__all_sync(kFull, whole);
+          auto is_masked = [&]() { return !__all_sync(kFull, (t0 + NK - 1 <= pos && t0 >= lo) || t0 + NK <= pf); };
           auto below = [&](int n, int w) {  // the first n keys of the tile, as bits of word w
             n -= 32 * w;
             return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
@@ -866,26 +859,14 @@ __global__ void __launch_bounds__(TcShape<D, KV, MODE>::THREADS, 1)
             const float2 neg_mu = make_float2(-mu, -mu), mult2 = make_float2(qk, qk);
             [[maybe_unused]] const float2 cap2 = make_float2(p.cap_log2, p.cap_log2);
             uint32_t hi[16];
-            float2 e[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float2 xx = make_float2(x[2 * i], x[2 * i + 1]);
-              if constexpr (WAY == 3)
-                e[i] = xx;
-              else
-                e[i] = WAY == 0 ? __ffma2_rn(xx, mult2, neg_mu) : WAY == 1 ? poly.minus(xx, neg_mu) : __fadd2_rn(xx, neg_mu);
-            }
-            if constexpr (WAY == 3) {
-#pragma unroll
-              for (int i = 0; i < 16; i += 4) {
-                mid_tanh<4>(e + i, poly.y_mult);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) e[i + j] = __ffma2_rn(e[i + j], cap2, neg_mu);
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 pp = make_float2(fast_exp2(e[i].x), fast_exp2(e[i].y));
+              const float2 e = WAY == 0   ? __ffma2_rn(xx, mult2, neg_mu)
+                               : WAY == 1 ? poly.minus(xx, neg_mu)
+                               : WAY == 2 ? __fadd2_rn(xx, neg_mu)
+                                          : __ffma2_rn(mid_tanh(xx, poly.y_mult), cap2, neg_mu);
+              const float2 pp = make_float2(fast_exp2(e.x), fast_exp2(e.y));
               ls[i & 1] = __fadd2_rn(ls[i & 1], pp);
               hi[i] = WIDE ? pack_f16x2(pp.x, pp.y) : pack_bf16x2(pp.x, pp.y);
             }
@@ -903,6 +884,7 @@ __global__ void __launch_bounds__(TcShape<D, KV, MODE>::THREADS, 1)
 #pragma unroll
             for (int c = 0; c < NK / 32; ++c) tmem_ld32(t_s + 32 * c, x + 32 * c);
             tmem_wait_ld();
+            const bool masked = is_masked();
 #pragma unroll
             for (int c = 0; c < NK / 32; ++c) {
               const float am = abs_max<32>(x + 32 * c);
@@ -950,6 +932,7 @@ __global__ void __launch_bounds__(TcShape<D, KV, MODE>::THREADS, 1)
               __syncwarp();
               if (lane == 0) mbar_arrive(smem_u32(sfree + grp));  // S may be overwritten
             }
+            const bool masked = is_masked();
             uint32_t see[NK / 32];
             if (masked) {
 #pragma unroll
@@ -963,16 +946,11 @@ __global__ void __launch_bounds__(TcShape<D, KV, MODE>::THREADS, 1)
               if constexpr (MID) mid = __all_sync(kFull, abs_max<NK>(x) * poly.y_mult <= kMidLimit);
               if (mid) {
 #pragma unroll
-                for (int i = 0; i < NK; i += 16) {
-                  float2 z[8];
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) z[j] = make_float2(x[i + 2 * j], x[i + 2 * j + 1]);
-                  mid_tanh<8>(z, poly.y_mult);
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) {
-                    x[i + 2 * j] = z[j].x * p.cap_log2;
-                    x[i + 2 * j + 1] = z[j].y * p.cap_log2;
-                  }
+                for (int i = 0; i < NK; i += 2) {
+                  const float2 z = __fmul2_rn(mid_tanh(make_float2(x[i], x[i + 1]), poly.y_mult),
+                                              make_float2(p.cap_log2, p.cap_log2));
+                  x[i] = z.x;
+                  x[i + 1] = z.y;
                 }
               } else {
                 cap_scores<NK, FAR>(x, qk, p.cap_log2, poly, masked, see);

@@ -821,6 +821,9 @@ __global__ void __launch_bounds__(TcShape<D, KV, MODE>::THREADS, 1)
           auto seen = [&](int w) {  // bit i: key t0 + 32 w + i is seen
             return (below(pos - t0 + 1, w) & ~below(lo - t0, w)) | below(pf - t0, w);
           };
+          // rows past the tile's last hold what was in their shared memory: they do not
+          // choose how the warp's scores are capped
+          auto magnitude = [&](float abs_max) { return row_ok ? abs_max : 0.f; };
           float alpha = 1.f;
           bool resc = false;
           auto grow = [&](float mt) {  // the row's maximum of this tile
@@ -887,7 +890,7 @@ __global__ void __launch_bounds__(TcShape<D, KV, MODE>::THREADS, 1)
             const bool masked = is_masked();
 #pragma unroll
             for (int c = 0; c < NK / 32; ++c) {
-              const float am = abs_max<32>(x + 32 * c);
+              const float am = magnitude(abs_max<32>(x + 32 * c));
               const bool small = __all_sync(kFull, poly.holds(am)), mid = __all_sync(kFull, am * poly.y_mult <= kMidLimit);
               ways |= (small ? 0u : mid ? 1u : 2u) << (2 * c);
             }
@@ -941,9 +944,9 @@ __global__ void __launch_bounds__(TcShape<D, KV, MODE>::THREADS, 1)
             // Capped: the row maximum is taken of the raw products (a cap does not
             // change which is the largest), the cap enters with the exponent.
             bool small = false, mid = false;
-            if constexpr (SCORE == kCapped) small = __all_sync(kFull, poly.holds(abs_max<NK>(x)));
+            if constexpr (SCORE == kCapped) small = __all_sync(kFull, poly.holds(magnitude(abs_max<NK>(x))));
             if constexpr (SCORE == kCappedBiased) {
-              if constexpr (MID) mid = __all_sync(kFull, abs_max<NK>(x) * poly.y_mult <= kMidLimit);
+              if constexpr (MID) mid = __all_sync(kFull, magnitude(abs_max<NK>(x)) * poly.y_mult <= kMidLimit);
               if (mid) {
 #pragma unroll
                 for (int i = 0; i < NK; i += 2) {

@@ -262,3 +262,35 @@ def test_refusals():
             pkv.chunk_attention(*args, **dict(kw, **bad))
     with pytest.raises(ValueError):               # 64-wide queries over 128-wide caches
         pkv.chunk_attention(args[0][:, :, :64].contiguous(), *args[1:], **kw)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kind", ["e2m1", "e4m3", "bf16"])
+def test_what_ran_before_does_not_matter(kind, D):
+    # 7 query heads per KV head leave four rows of a tile of 256 without queries; what
+    # an earlier call left there must not choose how scores are capped
+    g = torch.Generator().manual_seed(9)
+    n, hkv, bs = 700, 2, 16
+    blocks = -(-n // bs)
+    if kind == "e2m1":
+        kc, vc = (E.pool(g, blocks, hkv, bs, D, loud=False).to(DEV) for _ in range(2))
+    else:
+        kc, vc = (torch.randn((blocks, hkv, bs, D), generator=g).to(DEV, torch.bfloat16) for _ in range(2))
+    ones = None if kind == "bf16" else torch.ones(hkv, device=DEV)
+    if kind == "e4m3":
+        kc, vc = kc.to(torch.float8_e4m3fn), vc.to(torch.float8_e4m3fn)
+    table = torch.arange(blocks, dtype=torch.int32, device=DEV)[None]
+    ctx, starts = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([n], [0, n]))
+    q = torch.randn((n, 8 * hkv, D), generator=g).to(DEV, torch.bfloat16)
+
+    def run(q):
+        return pkv.chunk_attention(q, kc, vc, table, ctx, starts, D ** -0.5, max_q_len=n, max_context_len=n, softcap=30.0,
+                                   k_scale=ones, v_scale=ones)
+
+    outs = []
+    for mult in (1e-3, 1e4):
+        for _ in range(20):
+            run(q * mult)                            # all 256 rows of every tile, on every SM
+        outs.append(run(q[:, : 7 * hkv].contiguous()))
+    assert pkv.device_error(DEV) == 0
+    assert torch.equal(outs[0], outs[1])

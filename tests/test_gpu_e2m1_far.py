@@ -43,3 +43,23 @@ def test_far_blocks(src):
     ids = torch.tensor([[3], [5]], dtype=torch.int32, device=DEV)
     both(lambda kc, vc, s, first: pkv.copy_blocks(kc, vc, ids[0] + first, ids[1] + first))
     assert (big[0][:near] == 7).all() and (big[1][:near] == 7).all()
+
+
+@pytest.mark.parametrize("n,H,D,bs", [(5000, 8, 128, 16), (40_001, 3, 64, 32)])
+@pytest.mark.parametrize("src", [torch.bfloat16, torch.float32])
+def test_more_rows_than_a_grid(src, n, H, D, bs):
+    # CTAs that take rows in turn write and read what calls of a few rows do
+    g = torch.Generator(device=DEV).manual_seed(4)
+    nb = -(-n // bs) + 3
+    k, v = (torch.randn((n, H, D), generator=g, device=DEV).to(src) for _ in range(2))
+    slots = torch.randperm(nb * bs, generator=g, device=DEV)[:n]
+    slots[::97] = -1
+    one, few = ([pkv.e2m1_cache(nb, H, bs, D, device=DEV).zero_() for _ in range(2)] for _ in range(2))
+    pkv.append(k, v, slots, *one)
+    for i in range(0, n, 1000):
+        pkv.append(k[i:i + 1000].contiguous(), v[i:i + 1000].contiguous(), slots[i:i + 1000].contiguous(), *few)
+    assert all(torch.equal(a, b) and a.any() for a, b in zip(one, few))
+    got = pkv.read_tokens(slots, *one, dtype=src)
+    want = [pkv.read_tokens(slots[i:i + 1000].contiguous(), *one, dtype=src) for i in range(0, n, 1000)]
+    assert all(torch.equal(a, torch.cat(b)) and a.any() for a, b in zip(got, zip(*want)))
+    assert pkv.device_error(DEV) == 0

@@ -295,8 +295,8 @@ template <class P>
 cudaError_t launch_pieces(void (*kern)(P), const P& p, int64_t per_tok, cudaStream_t stream) {
   const dim3 block = per_tok < 256 ? dim3(static_cast<unsigned>(per_tok), static_cast<unsigned>(256 / per_tok)) : dim3(256);
   const int64_t want = (p.n_tokens + block.y - 1) / block.y;
-  // two rounds of the six CTAs that an SM holds (8192 tokens of 8 heads of 128 appended
-  // and read back 19.4 us; one round 20.8, four 19.5, a CTA per two tokens 20.1)
+  // two waves of the six CTAs that an SM holds (8192 tokens of 8 heads of 128 appended
+  // and read back 19.4 us; one wave 20.8, four 19.5, a CTA per two tokens 20.1)
   return launch_pdl(kern, dim3(static_cast<unsigned>(want < 152 * 12 ? want : 152 * 12)), block, 0, stream, p);
 }
 

@@ -140,13 +140,16 @@ pkv_status pkv_bm_block_tables(pkv_block_manager* bm, int32_t n_seqs, const int6
  *     slot_mapping, positions  int64 [max_tokens]: flat slot and position of each
  *                    new token, request after request; -1 past the last
  *     free_count     [1] entries left (may be the input's)
- *     lacking        [1] blocks that were missing, 0 if there were enough
+ *     lacking        [1] 0 if the step went through; else blocks that were
+ *                    missing, or -1 if none was and it was refused all the same
  * New block i of request b is free_blocks[count - 1 - (block_starts[b] + i)].  All or
  * nothing: with too few free blocks, more tokens than max_tokens (recorded as
  * PKV_DEVERR_CONTEXT_LEN) or a count outside [0, free_capacity] (recorded as
  * PKV_DEVERR_BLOCK_ID) no request gets any, tables and free_count stay, q_starts
  * and block_starts are 0 and every slot is -1, so that what runs on them does
- * nothing.  A block id outside [0, num_blocks), free or in the table's last
+ * nothing, and lacking is not 0, so that it shows on the device (what one request
+ * got is q_starts[b + 1] - q_starts[b]: lacking does not tell of a single one that
+ * got none).  A block id outside [0, num_blocks), free or in the table's last
  * entry, is recorded (PKV_DEVERR_BLOCK_ID), its tokens get slot -1 and a new entry
  * is -1.
  */

@@ -10,7 +10,8 @@ import numpy as np
 def extend(table, past, new, free, count, block_size, max_tokens, num_blocks):
     """(table, context_lens, q_starts, slots, positions, block_starts, count,
     lacking, good) of giving request b new[b] tokens behind its past[b]; `good`
-    is false where something was refused or a block id was bad."""
+    is false where something was refused or a block id was bad; `lacking` is -1
+    where the whole step was, with no block missing."""
     table = table.copy()
     B, MB = table.shape
     good, plan = True, []
@@ -25,6 +26,7 @@ def extend(table, past, new, free, count, block_size, max_tokens, num_blocks):
     in_range = 0 <= count <= len(free)
     lacking = max(0, need - count) if in_range else need
     goes = in_range and need <= count and tokens <= max_tokens
+    lacking = -1 if not goes and not lacking else lacking
     good = good and in_range and tokens <= max_tokens
     slots = np.full(max_tokens, -1, dtype=np.int64)
     positions = np.full(max_tokens, -1, dtype=np.int64)

@@ -507,7 +507,8 @@ def extend_tables(block_tables, past_lens, new_lens, free_blocks, free_count, k_
       context_lens [B]   past + new      q_starts, block_starts [B + 1]  sums of new tokens, blocks
       slot_mapping, positions   int64 [max_tokens], request after request, -1 past the last
       free_count [1]     what is left (the argument stays as it was)
-      lacking [1]        blocks that were missing: if any, nothing was done and no slot is given
+      lacking [1]        0, or nothing was done and no slot is given: blocks that were missing, or -1 if
+                         more tokens than max_tokens or a bad free_count were the reason
 
     which is what rotary_append / append and chunk_attention take.  `out` (an
     ExtendedTables, or a tuple like it) is written and returned instead; its

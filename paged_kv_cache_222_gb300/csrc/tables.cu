@@ -158,7 +158,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendP
     p.block_starts[p.batch] = goes ? static_cast<int32_t>(total.b) : 0;
     *p.free_count_out = goes ? count - static_cast<int32_t>(total.b) : count;
     const int64_t lack = good ? total.b - count : total.b;
-    *p.lacking = lack > 0 ? static_cast<int32_t>(min(lack, static_cast<int64_t>(0x7FFFFFFF))) : 0;
+    // a step that did not go through has a value other than 0, whatever it failed for
+    *p.lacking = lack > 0 ? static_cast<int32_t>(min(lack, static_cast<int64_t>(0x7FFFFFFF))) : (goes ? 0 : -1);
   }
   if (inline_fill != 0) {
     __syncthreads();  // the sums are written

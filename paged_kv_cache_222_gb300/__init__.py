@@ -123,7 +123,7 @@ def append(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=N
     take them or go without; every group of 16 elements gets a scale of its own
     besides.
     """
-    if k_cache.dtype == torch.uint8 and k_cache.shape[-1] in _E2M1_ROWS:
+    if k_cache.dtype == torch.uint8 and k_cache.dim() == 4 and k_cache.shape[-1] in _E2M1_ROWS:
         _lib.check(_lib.binding().append(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale,
                                          scale_row_stride), "pkv_append")
         return

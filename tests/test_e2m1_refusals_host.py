@@ -1,0 +1,15 @@
+"""Arguments that the 4-bit caches' and the axes' helpers refuse (no GPU)."""
+
+import pytest
+import torch
+
+import paged_kv_cache_222_gb300 as pkv
+
+
+@pytest.mark.parametrize("shape", [(), (0,), (36,), (72,), (4, 72), (3, 16, 36), (2, 2, 2, 16, 72)])
+@pytest.mark.parametrize("dtype", [torch.uint8, torch.bfloat16])
+def test_append_into_what_is_no_cache(shape, dtype):
+    c = torch.zeros(shape, dtype=dtype)
+    k = torch.zeros((2, 3, 128))
+    with pytest.raises(ValueError):
+        pkv.append(k, k, torch.zeros(2, dtype=torch.int64), c, c)

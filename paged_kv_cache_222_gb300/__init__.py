@@ -445,8 +445,9 @@ def rotary_axes(sections, mixed=False, device=None):
     position along each of len(sections) axes: sections[a] pairs turn by axis a.
     One axis after another, or with `mixed` a pair of each axis in turn while it
     has any left."""
+    sections = list(sections)
     left = [int(n) for n in sections]
-    if not left or min(left) < 0 or sum(left) == 0:
+    if not left or left != sections or min(left) < 0 or sum(left) == 0:
         raise ValueError("sections must be numbers of pairs, one per axis")
     if mixed:
         axes = [a for i in range(max(left)) for a, n in enumerate(left) if i < n]

@@ -170,24 +170,20 @@ __device__ __forceinline__ void cap_scores(float* x, float w_mult, float cap_log
   }
 }
 
-// tanh(y) = y P(y^2) for |y| <= kMidLimit, off by less than 4.4e-7 with binary32's own
-// rounding: 100 times that (the largest cap of these kernels) is below 2^-13 of a
-// weight.  The coefficients of the least largest error, the last one positive so
-// that -inf, a hidden score, stays that.  Ten packed FMA-pipe operations for two
+// tanh(y) for |y| <= kMidLimit (kMidC0 ...).  Ten packed FMA-pipe operations for two
 // weights' exponents, where the exponential form takes 2.25 special-function and
 // about 15 other operations for each: E2M1 caches, whose scores the groups' largest
 // channels bring past 0.35 of a cap, 3 chunks of 2000 over 1000 of 128-wide heads
 // with cap 30 1383 -> 730 us.
-constexpr float kMidLimit = 1.25f;
 __device__ __forceinline__ float2 mid_tanh(float2 x, float y_mult) {
   const float2 u = __fmul2_rn(x, make_float2(y_mult, y_mult)), t = __fmul2_rn(u, u);
-  float2 q = make_float2(0.000525482697f, 0.000525482697f);
-  q = __ffma2_rn(q, t, make_float2(-0.00432548998f, -0.00432548998f));
-  q = __ffma2_rn(q, t, make_float2(0.0176362358f, 0.0176362358f));
-  q = __ffma2_rn(q, t, make_float2(-0.0516446903f, -0.0516446903f));
-  q = __ffma2_rn(q, t, make_float2(0.132648036f, 0.132648036f));
-  q = __ffma2_rn(q, t, make_float2(-0.333242148f, -0.333242148f));
-  q = __ffma2_rn(q, t, make_float2(0.999996483f, 0.999996483f));
+  float2 q = make_float2(kMidC6, kMidC6);
+  q = __ffma2_rn(q, t, make_float2(kMidC5, kMidC5));
+  q = __ffma2_rn(q, t, make_float2(kMidC4, kMidC4));
+  q = __ffma2_rn(q, t, make_float2(kMidC3, kMidC3));
+  q = __ffma2_rn(q, t, make_float2(kMidC2, kMidC2));
+  q = __ffma2_rn(q, t, make_float2(kMidC1, kMidC1));
+  q = __ffma2_rn(q, t, make_float2(kMidC0, kMidC0));
   return __fmul2_rn(u, q);
 }
 

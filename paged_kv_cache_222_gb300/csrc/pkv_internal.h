@@ -433,6 +433,14 @@ inline void cap_coefficients(double cap, float (&c)[3], float& y_max) {
 // by less than 4.1e-8 of itself: the least largest relative error with 1 exactly.
 constexpr float kCapC1 = -0.33332663f, kCapC2 = 0.13299825f, kCapC3 = -0.0491485f;
 
+// tanh(y) = y (kMidC0 + kMidC1 y^2 + ... + kMidC6 y^12) for |y| <= kMidLimit, off by less
+// than 4.4e-7 with binary32's own rounding: 100 times that (kCapNear) is below
+// 2^-13 of a weight.  The coefficients of the least largest error, the last one
+// positive so that -inf, a hidden score, stays that.
+constexpr float kMidLimit = 1.25f;
+constexpr float kMidC0 = 0.999996483f, kMidC1 = -0.333242148f, kMidC2 = 0.132648036f, kMidC3 = -0.0516446903f,
+                kMidC4 = 0.0176362358f, kMidC5 = -0.00432548998f, kMidC6 = 0.000525482697f;
+
 // Rows of query heads one cascade prefix CTA covers: two groups of 128 TMEM
 // lanes.
 constexpr int kCascadeRowsTc = 256;

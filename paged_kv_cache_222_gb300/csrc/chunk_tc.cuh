@@ -384,6 +384,7 @@ __global__ void __launch_bounds__(TcShape<D, KV, MODE>::THREADS, 1)
   constexpr int SCORE = MODE & ~kFar;
   constexpr bool MID = KV == kE2M1 && !FAR;  // scores past the small ones' polynomial, up to kMidLimit caps
   constexpr bool PARTS = MID && SCORE == kCapped;
+  static_assert(!(PARTS && EARLY), "scores in parts are read from S until the last P is written: S(k+1) may not come first");
   // + g * NK, + g * (EARLY ? NK / 2 : NK), + g * D
   constexpr uint32_t COL_S = 0, COL_P = EARLY ? GROUPS * NK : COL_S, COL_O = COL_P + GROUPS * (EARLY ? NK / 2 : NK);
   constexpr uint32_t P_STEP = EARLY ? NK / 2 : NK;

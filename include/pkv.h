@@ -114,18 +114,19 @@ typedef struct {
  *                  another one for each piece of the row (in an E2M1 cache for a
  *                  group's codes and its scale).
  *   k_cache, v_cache  written in place (only the addressed slots change).
- *   k_scale, v_scale  E4M3 caches only (NULL otherwise): float32, row i and
- *                  KV head h use element [i * scale_row_stride + h];
- *                  scale_row_stride 0 gives one scale per KV head.  The code is
- *                  RNE-satfinite(x / scale) with x / scale an IEEE binary32
- *                  division.  bf16 caches: bf16 sources are copied bit for bit,
- *                  f32 sources are rounded to nearest even.
- *                  E2M1 caches: both or neither (neither: 1).  With y = x / scale
- *                  (IEEE binary32), the group's scale is RNE-satfinite E4M3 of
- *                  max |y| / 6 and the code RNE-satfinite E2M1 of y over it, both
- *                  binary32 quotients.  A group whose scale rounds to zero (max
- *                  |y| up to 6 x 2^-10) is stored as zeros; a group that holds a
- *                  NaN reads as NaN; infinities saturate.
+ *   k_scale, v_scale  E4M3 caches both, E2M1 caches both or neither (neither: 1),
+ *                  bf16 caches NULL: float32, row i and KV head h use element
+ *                  [i * scale_row_stride + h]; scale_row_stride 0 gives one scale
+ *                  per KV head.
+ *                  E4M3 caches: the code is RNE-satfinite(x / scale) with x / scale
+ *                  an IEEE binary32 division.  bf16 caches: bf16 sources are copied
+ *                  bit for bit, f32 sources are rounded to nearest even.
+ *                  E2M1 caches: with y = x / scale (IEEE binary32), the group's
+ *                  scale is RNE-satfinite E4M3 of max |y| / 6 and the code
+ *                  RNE-satfinite E2M1 of y over it, both binary32 quotients.  A
+ *                  group whose scale rounds to zero (max |y| up to 6 x 2^-10) is
+ *                  stored as zeros; a group that holds a NaN reads as NaN;
+ *                  infinities saturate.
  *   n_tokens == 0 is a no-op.
  */
 pkv_status pkv_append(const void* k_new, const void* v_new, int32_t src_dtype,

@@ -13,10 +13,12 @@
 // Grid-stride, so any number of rows fits a bounded grid.
 //
 // E2M1 caches: a thread per group of 16 elements, 8 code bytes and a scale byte
-// (how codes are found without dividing: pkv_device.cuh).  Bound: the bytes, and
-// the ALU beside them (14 instructions per element): 16,384 tokens of 8 heads of 128
-// from bf16 20 us, 4.3 TB/s; 8 elements of K and of V per thread, whose group's
-// largest magnitude two lanes exchange, 26-34 us.
+// (how codes are found without dividing by it: pkv_device.cuh).  Bound: a thread's
+// loads and then its codes (14 instructions per element), so that neither HBM nor the
+// ALU (58 %) is full: 16,384 tokens of 8 heads of 128 from bf16 20 us, 4.3 TB/s; 8
+// elements of K and of V per thread, whose group's largest magnitude two lanes
+// exchange, 26-34 us.  Head scales divide every element first: 65,536 such tokens 114
+// us, without 65.
 //
 // read_kernel is the way back: a thread per 8 elements of a (token, head) row
 // widens them (codes times scales; every code and code-times-scale product is
